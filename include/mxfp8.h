@@ -70,6 +70,18 @@ typedef enum { MX_ROPE_INTERLEAVED = 0, MX_ROPE_NEOX = 1 } mx_rope_style;
 /* Element type of checkpoint scales given to mx_woa_expand_scales. */
 typedef enum { MX_SCALE_E8M0 = 0, MX_SCALE_F32 = 1 } mx_scale_kind;
 
+/* Score of a router logit (mx_moe_route). */
+typedef enum { MX_ROUTE_SOFTMAX = 0, MX_ROUTE_SIGMOID = 1 } mx_route_score;
+
+/* What mx_grouped_linear applies to its input before it is quantised. */
+typedef enum { MX_ACT_NONE = 0, MX_ACT_SWIGLU = 1 } mx_act;
+
+/* Limits of mx_moe_route. */
+#define MX_ROUTE_MAX_EXPERTS 1024
+#define MX_ROUTE_MAX_K 32
+/* Block along N and K of FP32 weight scales (mx_linear_block128, mx_grouped_linear). */
+#define MX_BLOCK128 128
+
 /* ------------------------------------------------------------------ status */
 
 /* Static text for a status code. */
@@ -92,9 +104,10 @@ void mx_set_dry_run(int on);
  * dequant, linear BF16 branch (prepared weight), linear FP8 branch, linear
  * per-call-dequant branch, f32->e8m0 device, e4m3 encode device, inverse RoPE
  * to BF16, BF16 bmm (large tiles), BF16 bmm (small T), wo_a scale expansion,
- * single-kernel wo_a.
+ * single-kernel wo_a, expert router, grouped linear, join of the experts'
+ * rows, block-128 linear.
  * `out` gets min(n, MX_NUM_COUNTERS) values; returns MX_NUM_COUNTERS. */
-#define MX_NUM_COUNTERS 14
+#define MX_NUM_COUNTERS 18
 int mx_get_counters(uint64_t* out, int n);
 void mx_reset_counters(void);
 
@@ -321,6 +334,128 @@ mx_status mx_linear(const void* x, int64_t M, int64_t K, const void* w,
 mx_status mx_linear_noalloc(const void* x, int64_t M, int64_t K, const void* w,
                             const uint8_t* w_scale, int32_t w_elem_bytes, int64_t N, void* out,
                             void* stream);
+
+/* ------------------------------------- linear with FP32 block-128 scales */
+
+/*
+ * mx_linear_block128 -- out = x @ W^T for an FP8 weight with one FP32 scale per
+ * 128 x 128 block.  The scales are any FP32 values: a checkpoint whose scales
+ * are not powers of two, which mx_woa_expand_scales rejects, keeps its FP8
+ * weight here.
+ *
+ * x is quantised on the way, per row m and block b of 128 consecutive K (the
+ * last one short when K % 128 != 0):
+ *   amax = max |x| over the block, at least 2^-96;  sa[m,b] = amax / 448
+ *   q    = e4m3(x * 448 / amax), nearest even, saturating (OCP)
+ * out[m,n] = bf16( sum_b  sa[m,b] * sw[n/128,b] * sum_{k in b} q[m,k] * w[n,k] )
+ * with FP32 sums.  A block holding NaN/Inf makes its row of out NaN.
+ *
+ * x        device BF16 [M, K].      w  device u8 [N, K] OCP e4m3.
+ * w_scale  device FP32 [ceil(N/128), ceil(K/128)].
+ * out      device BF16 [M, N].
+ * workspace device, at least mx_linear_block128_workspace_bytes(M, N, K),
+ *          16-byte aligned: the quantised x, written before it is read.  Calls
+ *          that may overlap need one each.
+ * Requires: M >= 0 (0 is a no-op), N, K >= 16, N % 16 == 0, K % 16 == 0,
+ * K < 2^22, M * (K rounded up to 128) < 2^32, x, w and out 16-byte aligned,
+ * w_scale 4-byte aligned; out overlaps no input and not the workspace.
+ */
+size_t mx_linear_block128_workspace_bytes(int64_t M, int64_t N, int64_t K);
+mx_status mx_linear_block128(const void* x, int64_t M, int64_t K, const uint8_t* w,
+                             const float* w_scale, int64_t N, void* out, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------- mixture of experts */
+
+/*
+ * mx_moe_route -- the k experts of every token, their weights, and the token
+ * slots grouped by expert.
+ *
+ * l' = l with NaN taken as -inf and +inf as the largest finite FP32; an expert
+ * with l' = -inf is masked out.
+ * p  = softmax(l') over the experts (MX_ROUTE_SOFTMAX) or 1 / (1 + exp(-l'))
+ *      (MX_ROUTE_SIGMOID); 0 for masked experts.
+ * The k experts of largest key are chosen, largest first, equal keys by the
+ * lower index: key = l' without a bias, p + bias (in FP64) with one, -inf for a
+ * masked expert or a NaN key.  Masked experts are only chosen when fewer than
+ * k are left; their weight is 0.
+ * weight_j = p_j (renormalize: over sum_j p_j, 0 when that is 0) * scale.
+ *
+ * logits   device [T, E], FP32 (logits_f32 = 1) or BF16 (0).
+ * bias     device FP32 [E] or NULL.
+ * ids      device int32 [T, k].      weights  device FP32 [T, k].
+ * offsets  device int32 [E + 1]: expert e owns rows [offsets[e], offsets[e+1]).
+ * row_slot device int32 [T * k]: the flat slot t * k + j that row r holds, rows
+ *          in ascending slot order within an expert.
+ * slot_row device int32 [T, k]: the row of each slot (row_slot's inverse).
+ * workspace device, at least mx_moe_route_workspace_bytes(T, E), 4-byte aligned
+ *          (may be NULL when that is 0).  Calls that may overlap need one each.
+ * The result does not depend on timing (no position comes from an atomic).
+ * Requires: T >= 0 (0 writes offsets of zero), 1 <= E <= MX_ROUTE_MAX_EXPERTS,
+ * 1 <= k <= min(E, MX_ROUTE_MAX_K), T * k < 2^31; FP32 and int32 tensors 4-byte,
+ * BF16 logits 2-byte aligned.
+ */
+size_t mx_moe_route_workspace_bytes(int64_t T, int32_t E);
+mx_status mx_moe_route(const void* logits, int32_t logits_f32, const float* bias, int64_t T,
+                       int32_t E, int32_t k, int32_t score, int32_t renormalize, float scale,
+                       int32_t* ids, float* weights, int32_t* offsets, int32_t* row_slot,
+                       int32_t* slot_row, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mx_grouped_linear -- every row times its own expert's FP8 weight: S rows
+ * sorted by expert, expert e owning rows [offsets[e], offsets[e+1]).
+ *
+ * out[r,:] = W[e(r)] @ Q(x[src(r),:]),  src(r) = row_slot[r] / k with row_slot
+ * (the slots of mx_moe_route: x is the tokens' tensor, read through the index,
+ * and k the router's), r without.
+ * act      MX_ACT_NONE: x is BF16 [rows, K].  MX_ACT_SWIGLU: x is BF16
+ *          [rows, 2K] = gate | up and silu(gate) * up, formed in FP32 and
+ *          rounded to BF16, takes its place.
+ * scale_kind  MX_SCALE_E8M0: w_scale u8 [E, N, K/32] (MXFP8) and Q the MXFP8
+ *          quantiser of mx_linear (OCP, block 32).  K % 32 == 0; K need not be a
+ *          multiple of 128.  MX_SCALE_F32: w_scale FP32
+ *          [E, ceil(N/128), ceil(K/128)] and Q that of mx_linear_block128.
+ * w        device u8 [E, N, K] OCP e4m3.
+ * offsets  device int32 [E + 1], ascending.  Rows are cut to [0, S); rows that
+ *          no expert owns (behind offsets[E], before offsets[0]) keep what out
+ *          held.  An expert may own no row.
+ * row_slot device int32 [S] or NULL (then rows == S).  A row whose source is
+ *          outside x (a negative slot as padding) has NaN outputs.  Several rows
+ *          may read one x row.
+ * out      device BF16 [S, N], FP32 accumulation, nearest even.
+ * workspace device, at least mx_grouped_linear_workspace_bytes(rows, S, E, N, K),
+ *          16-byte aligned: the quantised x and the list of row tiles, written
+ *          before they are read.  Calls that may overlap need one each.
+ * Requires: S >= 0 (0 is a no-op), rows >= 1 for S > 0, E >= 1, k >= 1,
+ * N, K >= 16, N % 16 == 0, K % 32 == 0 (E8M0) or K % 16 == 0 (FP32), K < 2^22,
+ * rows * (K rounded up to 128) < 2^32, S < 2^31, E < 2^20, x, w and out 16-byte
+ * aligned, FP32 scales, offsets and row_slot 4-byte aligned; out overlaps no
+ * input and not the workspace.
+ */
+size_t mx_grouped_linear_workspace_bytes(int64_t rows, int64_t S, int64_t E, int64_t N, int64_t K);
+mx_status mx_grouped_linear(const void* x, int64_t rows, int64_t K, const uint8_t* w,
+                            const void* w_scale, int32_t scale_kind, int64_t E, int64_t N,
+                            const int32_t* offsets, const int32_t* row_slot, int32_t k, int64_t S,
+                            int32_t act, void* out, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/*
+ * mx_moe_combine -- the experts' rows joined per token:
+ * out[t,:] = bf16( shared[t,:] + sum_j weights[t,j] * y[slot_row[t,j],:] ), FP32
+ * sums over j in order, rounded once.
+ * y        device BF16 [rows, N].    slot_row  device int32 [T, k].
+ * weights  device FP32 [T, k].
+ * shared   device BF16 [T, N] (a shared expert's output) or NULL.
+ * out      device BF16 [T, N]; may be `shared`, overlaps y nowhere.
+ * A slot whose row is outside [0, rows) (a dropped token) or whose weight is 0
+ * adds nothing, whatever y holds.
+ * Requires: T >= 0 (0 is a no-op), N >= 8, N % 8 == 0, 1 <= k <= 1024, rows >= 0
+ * and < 2^31, T * N < 2^39, y, shared and out 16-byte, slot_row and weights
+ * 4-byte aligned.
+ */
+mx_status mx_moe_combine(const void* y, int64_t rows, int64_t N, const int32_t* slot_row,
+                         const float* weights, int64_t T, int32_t k, const void* shared, void* out,
+                         void* stream);
 
 /* ---------------------------------------------------- format converters */
 

@@ -28,18 +28,25 @@ __all__ = [
     "mx_f32_pow2_to_e8m0", "mx_f32_pow2_to_e8m0_device", "mx_f32_to_e4m3_ocp",
     "mx_f32_to_e4m3_fnuz", "mx_f32_to_e4m3_device", "mx_e4m3_to_f32", "mx_e8m0_to_f32",
     "mx_stream_read", "COUNTER_NAMES",
+    "MX_ROUTE_SOFTMAX", "MX_ROUTE_SIGMOID", "MX_ACT_NONE", "MX_ACT_SWIGLU", "MX_BLOCK128",
+    "mx_moe_route", "mx_moe_route_workspace_bytes", "mx_grouped_linear", "mx_grouped_linear_workspace_bytes",
+    "mx_moe_combine", "mx_linear_block128", "mx_linear_block128_workspace_bytes",
 ]
 
 MX_OK, MX_ERR_INVALID_ARG, MX_ERR_UNSUPPORTED, MX_ERR_NOT_LOSSLESS, MX_ERR_HIP = range(5)
 MX_FP8_E4M3_OCP, MX_FP8_E4M3_FNUZ = 0, 1
 MX_ROPE_INTERLEAVED, MX_ROPE_NEOX = 0, 1
 MX_SCALE_E8M0, MX_SCALE_F32 = 0, 1
+MX_ROUTE_SOFTMAX, MX_ROUTE_SIGMOID = 0, 1
+MX_ACT_NONE, MX_ACT_SWIGLU = 0, 1
+MX_BLOCK128 = 128
 MX_LINEAR_K_ALIGN = 128
 MX_LINEAR_BLOCK = 32
 MX_LINEAR_NOALLOC_SCRATCH_BYTES = 32 << 20
 COUNTER_NAMES = ("quant", "bmm_large", "bmm_small", "dequant", "linear_bf16", "linear_fp8",
                  "linear_percall_dequant", "f32_to_e8m0_device", "f32_to_e4m3_device", "rope_bf16",
-                 "bmm_bf16_large", "bmm_bf16_small", "expand_scales", "wo_a_fused")
+                 "bmm_bf16_large", "bmm_bf16_small", "expand_scales", "wo_a_fused", "moe_route",
+                 "grouped_linear", "moe_combine", "linear_block128")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libmxfp8.so")
@@ -83,6 +90,14 @@ def lib():
             "mx_linear_workspace_bytes": (SZ, [I64, I64, I64, I32]),
             "mx_linear": (ctypes.c_int, [P, I64, I64, P, P, I32, I64, P, P, SZ, P]),
             "mx_linear_noalloc": (ctypes.c_int, [P, I64, I64, P, P, I32, I64, P, P]),
+            "mx_linear_block128_workspace_bytes": (SZ, [I64, I64, I64]),
+            "mx_linear_block128": (ctypes.c_int, [P, I64, I64, P, P, I64, P, P, SZ, P]),
+            "mx_moe_route_workspace_bytes": (SZ, [I64, I32]),
+            "mx_moe_route": (ctypes.c_int, [P, I32, P, I64, I32, I32, I32, I32, ctypes.c_float, P, P, P, P, P, P, SZ,
+                                            P]),
+            "mx_grouped_linear_workspace_bytes": (SZ, [I64, I64, I64, I64, I64]),
+            "mx_grouped_linear": (ctypes.c_int, [P, I64, I64, P, P, I32, I64, I64, P, P, I32, I64, I32, P, P, SZ, P]),
+            "mx_moe_combine": (ctypes.c_int, [P, I64, I64, P, P, I64, I32, P, P, P]),
             "mx_stream_read": (ctypes.c_int, [P, I64, P, P]),
             "mx_f32_pow2_to_e8m0": (ctypes.c_int, [P, P, I64]),
             "mx_f32_pow2_to_e8m0_device": (ctypes.c_int, [P, P, I64, P, P]),
@@ -416,6 +431,165 @@ def mx_linear_noalloc(x, w, w_scale=None, out=None):
     _check(lib().mx_linear_noalloc(_dev(x, "x", 2), M, K, _dev(w, "w"),
                                    _dev(w_scale, "w_scale", 1) if w_scale is not None else None, eb, N,
                                    _dev(out, "out", 2), _stream(x)))
+    return out
+
+
+# ------------------------------------- linear with FP32 block-128 scales
+
+def _dtype(t, dtypes, name):
+    if t is not None and t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)} (got {t.dtype})")
+
+
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+
+
+def _workspace(ws, need, device):
+    """(tensor or None, pointer, bytes) of a workspace of at least `need` bytes."""
+    if ws is None:
+        if not need:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    return ws, _dev(ws, "workspace"), ws.numel() * ws.element_size()
+
+
+def mx_linear_block128_workspace_bytes(M, N, K):
+    return int(lib().mx_linear_block128_workspace_bytes(M, N, K))
+
+
+def mx_linear_block128(x, w, w_scale, out=None, workspace=None):
+    """x BF16 [M,K] @ W^T; W FP8 uint8 [N,K] with float32 scales [ceil(N/128), ceil(K/128)] -> BF16 [M,N]."""
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError(f"x must be [M,K] and w [N,K] (got {tuple(x.shape)} and {tuple(w.shape)})")
+    M, K = x.shape
+    N = w.shape[0]
+    _shape(w, (N, K), "w")
+    _dtype(x, _BF16, "x")
+    _dtype(w_scale, (torch.float32,), "w_scale")
+    _shape(w_scale, (-(-N // MX_BLOCK128), -(-K // MX_BLOCK128)), "w_scale")
+    _numel(out, M * N, "out")
+    _same_device(x, ("w", w), ("w_scale", w_scale), ("out", out), ("workspace", workspace))
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    args = (_dev(x, "x", 2), M, K, _dev(w, "w", 1), _dev(w_scale, "w_scale", 4), N, _dev(out, "out", 2))
+    workspace, wp, wb = _workspace(workspace, mx_linear_block128_workspace_bytes(M, N, K), x.device)
+    with torch.cuda.device(x.device):
+        _check(lib().mx_linear_block128(*args, wp, wb, _stream(x)))
+    return out
+
+
+# ------------------------------------------------- mixture of experts
+
+def mx_moe_route_workspace_bytes(T, E):
+    return int(lib().mx_moe_route_workspace_bytes(T, E))
+
+
+def mx_moe_route(logits, k, bias=None, score=MX_ROUTE_SOFTMAX, renormalize=True, scale=1.0, ids=None, weights=None,
+                 offsets=None, row_slot=None, slot_row=None, workspace=None):
+    """logits BF16 or float32 [T,E], bias float32 [E] -> (ids int32 [T,k], weights float32 [T,k],
+    offsets int32 [E+1], row_slot int32 [T*k], slot_row int32 [T,k]): the k experts of every token, their
+    weights, and the token slots t*k + j grouped by expert."""
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [T, E] (got shape {tuple(logits.shape)})")
+    T, E = logits.shape
+    _dtype(logits, (torch.float32,) + _BF16, "logits")
+    _dtype(bias, (torch.float32,), "bias")
+    _dtype(weights, (torch.float32,), "weights")
+    for name, t in (("ids", ids), ("offsets", offsets), ("row_slot", row_slot), ("slot_row", slot_row)):
+        _dtype(t, (torch.int32,), name)
+    if k < 1:
+        raise ValueError(f"k = {k} must be positive")
+    _numel(bias, E, "bias")
+    _numel(ids, T * k, "ids")
+    _numel(weights, T * k, "weights")
+    _numel(offsets, E + 1, "offsets")
+    _numel(row_slot, T * k, "row_slot")
+    _numel(slot_row, T * k, "slot_row")
+    _same_device(logits, ("bias", bias), ("ids", ids), ("weights", weights), ("offsets", offsets),
+                 ("row_slot", row_slot), ("slot_row", slot_row), ("workspace", workspace))
+    lp = _dev(logits, "logits")
+    bp = _dev(bias, "bias", 4) if bias is not None else None
+    dev = logits.device
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    if offsets is None:
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    if row_slot is None:
+        row_slot = torch.empty(T * k, dtype=torch.int32, device=dev)
+    if slot_row is None:
+        slot_row = torch.empty((T, k), dtype=torch.int32, device=dev)
+    workspace, wp, wb = _workspace(workspace, mx_moe_route_workspace_bytes(T, E), dev)
+    with torch.cuda.device(dev):
+        _check(lib().mx_moe_route(lp, int(logits.dtype == torch.float32), bp, T, E, k, score, int(bool(renormalize)),
+                                  scale, _dev(ids, "ids", 4), _dev(weights, "weights", 4),
+                                  _dev(offsets, "offsets", 4), _dev(row_slot, "row_slot", 4),
+                                  _dev(slot_row, "slot_row", 4), wp, wb, _stream(logits)))
+    return ids, weights, offsets, row_slot, slot_row
+
+
+def mx_grouped_linear_workspace_bytes(rows, S, E, N, K):
+    return int(lib().mx_grouped_linear_workspace_bytes(rows, S, E, N, K))
+
+
+def mx_grouped_linear(x, w, w_scale, offsets, row_slot=None, k=1, act=MX_ACT_NONE, out=None, workspace=None):
+    """x BF16 [rows,K] (or [rows,2K] = gate | up with MX_ACT_SWIGLU), w FP8 uint8 [E,N,K] with w_scale uint8
+    [E,N,K/32] (MXFP8) or float32 [E,ceil(N/128),ceil(K/128)], offsets int32 [E+1] -> BF16 [S,N]: row r of expert e
+    (offsets[e] <= r < offsets[e+1]) is x[row_slot[r] // k] @ w[e]^T, or x[r] @ w[e]^T without row_slot."""
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError(f"x must be [rows,K] and w [E,N,K] (got {tuple(x.shape)} and {tuple(w.shape)})")
+    E, N, K = w.shape
+    rows = x.shape[0]
+    _shape(x, (rows, 2 * K if act == MX_ACT_SWIGLU else K), "x")
+    _dtype(x, _BF16, "x")
+    _dtype(w_scale, (torch.uint8, torch.float32), "w_scale")
+    kind = MX_SCALE_F32 if w_scale.dtype == torch.float32 else MX_SCALE_E8M0
+    if kind == MX_SCALE_F32:
+        _shape(w_scale, (E, -(-N // MX_BLOCK128), -(-K // MX_BLOCK128)), "w_scale")
+    else:
+        if K % MX_LINEAR_BLOCK:
+            raise ValueError(f"K = {K} is not a multiple of {MX_LINEAR_BLOCK}")
+        _shape(w_scale, (E, N, K // MX_LINEAR_BLOCK), "w_scale")
+    for name, t in (("offsets", offsets), ("row_slot", row_slot)):
+        _dtype(t, (torch.int32,), name)
+    _numel(offsets, E + 1, "offsets")
+    S = rows if row_slot is None else row_slot.numel()
+    _numel(out, S * N, "out")
+    _same_device(x, ("w", w), ("w_scale", w_scale), ("offsets", offsets), ("row_slot", row_slot), ("out", out),
+                 ("workspace", workspace))
+    if out is None:
+        out = torch.empty((S, N), dtype=torch.bfloat16, device=x.device)
+    args = (_dev(x, "x", 2), rows, K, _dev(w, "w", 1), _dev(w_scale, "w_scale"), kind, E, N,
+            _dev(offsets, "offsets", 4), _dev(row_slot, "row_slot", 4) if row_slot is not None else None, k, S, act,
+            _dev(out, "out", 2))
+    workspace, wp, wb = _workspace(workspace, mx_grouped_linear_workspace_bytes(rows, S, E, N, K), x.device)
+    with torch.cuda.device(x.device):
+        _check(lib().mx_grouped_linear(*args, wp, wb, _stream(x)))
+    return out
+
+
+def mx_moe_combine(y, slot_row, weights, shared=None, out=None):
+    """y BF16 [rows,N], slot_row int32 [T,k], weights float32 [T,k], shared BF16 [T,N] ->
+    BF16 [T,N] = shared + sum_j weights[:,j] * y[slot_row[:,j]]; ``out=shared`` adds in place."""
+    if y.dim() != 2 or slot_row.dim() != 2:
+        raise ValueError(f"y must be [rows,N] and slot_row [T,k] (got {tuple(y.shape)} and {tuple(slot_row.shape)})")
+    rows, N = y.shape
+    T, k = slot_row.shape
+    _dtype(y, _BF16, "y")
+    _dtype(shared, _BF16, "shared")
+    _dtype(slot_row, (torch.int32,), "slot_row")
+    _dtype(weights, (torch.float32,), "weights")
+    _shape(weights, (T, k), "weights")
+    _numel(shared, T * N, "shared")
+    _numel(out, T * N, "out")
+    _same_device(y, ("slot_row", slot_row), ("weights", weights), ("shared", shared), ("out", out))
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=y.device)
+    args = (_dev(y, "y", 2), rows, N, _dev(slot_row, "slot_row", 4), _dev(weights, "weights", 4), T, k,
+            _dev(shared, "shared", 2) if shared is not None else None, _dev(out, "out", 2))
+    with torch.cuda.device(y.device):
+        _check(lib().mx_moe_combine(*args, _stream(y)))
     return out
 
 

@@ -9,7 +9,7 @@
 #include <cstring>
 #include <mutex>
 
-#include "common.hpp"
+#include "api_checks.hpp"
 
 namespace mx {
 
@@ -125,19 +125,6 @@ mx_status require_gfx950() {
 }  // namespace mx
 
 using namespace mx;
-
-#define MX_CHECK(cond, ...)                                       \
-  do {                                                            \
-    if (!(cond)) return fail(MX_ERR_INVALID_ARG, __VA_ARGS__);    \
-  } while (0)
-
-// Validation done, dry-run honoured, device checked: the common preamble.
-#define MX_PREAMBLE()                                   \
-  do {                                                  \
-    if (dry_run()) { clear_error(); return MX_OK; }     \
-    const mx_status st_ = require_gfx950();             \
-    if (st_ != MX_OK) return st_;                       \
-  } while (0)
 
 extern "C" {
 

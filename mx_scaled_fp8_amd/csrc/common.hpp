@@ -39,6 +39,10 @@ enum Counter {
   C_BMM_BF16_SMALL,
   C_EXPAND_SCALES,
   C_WOA_FUSED,
+  C_MOE_ROUTE,
+  C_GROUPED_LINEAR,
+  C_MOE_COMBINE,
+  C_LINEAR_BLOCK128,
 };
 void count(Counter c);
 

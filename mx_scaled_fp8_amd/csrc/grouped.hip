@@ -1,0 +1,629 @@
+// Products of BF16 rows with FP8 weights, grouped by expert or dense, on block-scaled FP8 MFMA (gfx950):
+// mx_grouped_linear (MXFP8 or FP32 block-128 weights) and mx_linear_block128.
+//
+//   out[r, n] = bf16( sum_k  Q(x[src(r), k]) * W[e(r), n, k] )
+//
+// The rows r are sorted by expert: expert e owns rows [offsets[e], offsets[e+1]), known on the device alone.  Q rounds
+// the activation to e4m3 with one scale per row and K block, the weight's own block length along K:
+//   MXFP8   block 32, E8M0 on both sides: the scaled MFMA applies both scales.
+//   FP32    block 128 on the activation, 128 x 128 on the weight.  Such scales are no powers of two, so the MFMA cannot
+//           apply them: each 128-K block's partial sum P (two chained 32x32x64 MFMAs from zero) joins the running sum
+//           as acc += P * (sa * sw), one fma per element and 128 K on the vector unit beside the matrix unit.
+//
+// Two launches:
+//  * quant_rows_kernel: every activation row once (not once per expert that reads it): codes [rows, Kp] and one 4-byte
+//    scale word per 128 K [rows, Kp / 128] (four E8M0 bytes, or one FP32) into the workspace, Kp = K rounded up to 128
+//    with zero codes behind K.  With act = SwiGLU it reads [gate | up] and rounds silu(gate) * up to BF16 first.  One
+//    more workgroup turns the offsets into a list of row tiles.
+//  * grouped_gemm_kernel: one workgroup per BM x BN tile.  Rows of the activation are gathered by their index as the
+//    LDS-DMA reads them, so no copy per expert is written.
+#include <type_traits>
+
+#include "common.hpp"
+
+namespace mx {
+
+namespace {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef short v2s __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+constexpr int kStageK = 128;   // K per stage: one 128-byte line of every operand row
+
+// One row tile of an expert.
+struct RowTile {
+  int32_t expert;
+  int32_t first;       // list index of the expert's first row tile
+  int32_t count;       // row tiles of the expert
+  int32_t row_lo;      // the expert's rows
+  int32_t row_hi;
+  int32_t pad[3];
+};
+static_assert(sizeof(RowTile) == 32, "workspace layout");
+
+// ------------------------------------------------------------------ quantiser
+
+struct QuantRowsArgs {
+  const uint16_t* x;          // BF16 [rows, K], or [rows, 2K] = gate | up
+  uint8_t* xq;                // [rows, Kp] e4m3 codes
+  uint32_t* xs;               // [rows, KB] scale words
+  uint32_t rows, K, KB;
+  uint32_t units;             // rows * KB
+  DivU32 kb_div;
+  // row tiles (workgroup 0 when offsets is set)
+  const int32_t* offsets;     // [E + 1] or null
+  RowTile* tiles;             // tiles[0].count = number of tiles, the tiles from 1 on
+  int32_t E, S, BM, max_tiles;
+};
+
+// Expert e owns rows [offsets[e], offsets[e+1]) cut to [0, S); an interval that runs backwards is empty.  The list is
+// cut at max_tiles, so offsets that overlap cannot make it longer than its space.
+__device__ void build_row_tiles(const QuantRowsArgs& a) {
+  __shared__ int32_t part[256];
+  const int tid = threadIdx.x;
+  const int per = (a.E + 255) / 256;
+  const int e0 = min(tid * per, a.E), e1 = min(e0 + per, a.E);
+  auto bounds = [&](int e, int& lo, int& hi) {
+    lo = min(max(a.offsets[e], 0), a.S);
+    hi = min(max(a.offsets[e + 1], lo), a.S);
+  };
+  int n = 0;
+  for (int e = e0; e < e1; ++e) {
+    int lo, hi;
+    bounds(e, lo, hi);
+    n += (hi - lo + a.BM - 1) / a.BM;
+    n = min(n, a.max_tiles);
+  }
+  part[tid] = n;
+  __syncthreads();
+  for (int d = 1; d < 256; d *= 2) {
+    const int v = tid >= d ? part[tid - d] : 0;
+    __syncthreads();
+    part[tid] = min(part[tid] + v, a.max_tiles);
+    __syncthreads();
+  }
+  int first = tid > 0 ? part[tid - 1] : 0;
+  for (int e = e0; e < e1; ++e) {
+    int lo, hi;
+    bounds(e, lo, hi);
+    const int count = min((hi - lo + a.BM - 1) / a.BM, a.max_tiles - first);
+    for (int i = 0; i < count; ++i) a.tiles[1 + first + i] = RowTile{e, first, count, lo, hi, {0, 0, 0}};
+    first += count;
+  }
+  if (tid == 255) a.tiles[0].count = part[255];
+}
+
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  // g / (1 + 2^(-g log2 e)) * u: the approximate exponential and reciprocal are within 2^-20, rounded to BF16 after
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+
+// Sixteen lanes (a DPP row) quantise one 128-K block of one row, 8 consecutive elements each.
+template <bool F32, bool ACT>
+__global__ __launch_bounds__(256) void quant_rows_kernel(QuantRowsArgs a) {
+  uint32_t block = blockIdx.x;
+  if (a.offsets != nullptr) {
+    if (block == 0) {
+      build_row_tiles(a);
+      return;
+    }
+    --block;
+  }
+  const uint32_t raw = block * 16 + (threadIdx.x >> 4);
+  const uint32_t unit = min(raw, a.units - 1);   // every lane takes part in the reductions
+  const uint32_t row = div_u32(unit, a.kb_div), kb = unit - row * a.KB;
+  const uint32_t l = threadIdx.x & 15, k = kb * kStageK + l * 8;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (k < a.K) {                                 // K is a multiple of 16: a chunk is inside or outside
+    const uint16_t* src = a.x + static_cast<size_t>(row) * a.K * (ACT ? 2 : 1) + k;
+    v = *reinterpret_cast<const uint4*>(src);
+    if constexpr (ACT) {
+      const uint4 u = *reinterpret_cast<const uint4*>(src + a.K);
+      const uint32_t gw[4] = {v.x, v.y, v.z, v.w}, uw[4] = {u.x, u.y, u.z, u.w};
+      uint32_t h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        h[i] = pack_bf16x2(silu_mul(bf16_lo(gw[i]), bf16_lo(uw[i])), silu_mul(bf16_hi(gw[i]), bf16_hi(uw[i])));
+      v = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+  }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+  // over the 4 lanes of a 32-K block, or all 16
+  auto dpp = [](uint32_t x, auto ctrl) {
+    return static_cast<uint32_t>(
+        __builtin_amdgcn_update_dpp(0, static_cast<int>(x), decltype(ctrl)::value, 0xF, 0xF, false));
+  };
+  m = max(m, dpp(m, std::integral_constant<int, 0xB1>{}));   // quad_perm [1,0,3,2]
+  m = max(m, dpp(m, std::integral_constant<int, 0x4E>{}));   // quad_perm [2,3,0,1]
+  if constexpr (F32) {
+    m = max(m, dpp(m, std::integral_constant<int, 0x128>{}));   // row_ror:8
+    m = max(m, dpp(m, std::integral_constant<int, 0x124>{}));   // row_ror:4
+  }
+  const bool finite = m < 0x7F80u;
+  uint2 codes;
+  uint32_t word;
+  if constexpr (F32) {
+    // scale amax / 448; codes of the quotients x * 448 / amax.  They are formed from x and amax scaled by 2^-E (E the
+    // exponent of amax, so nothing overflows), and corrected by one residual step: v = x r is off by up to two
+    // roundings, which would break ties (BF16 inputs have many) either way; x * 448 - v * amax is exact in an fma.
+    const float amax = fmaxf(__uint_as_float((finite ? m : 0) << 16), 0x1p-96f);
+    const int E = min(static_cast<int>(__float_as_uint(amax) >> 23) - 127, 126);
+    const float p2 = __uint_as_float(static_cast<uint32_t>(127 - E) << 23);
+    const float am = amax * p2, rinv = 1.0f / am, r = 448.0f * rinv;
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float xl = bf16_lo(w[i]) * p2, xh = bf16_hi(w[i]) * p2;
+      const float vl = xl * r, vh = xh * r;
+      const float ql = __builtin_fmaf(__builtin_fmaf(-vl, am, xl * 448.0f), rinv, vl);
+      const float qh = __builtin_fmaf(__builtin_fmaf(-vh, am, xh * 448.0f), rinv, vh);
+      q[2 * i] = __builtin_amdgcn_fmed3f(ql, -448.0f, 448.0f);
+      q[2 * i + 1] = __builtin_amdgcn_fmed3f(qh, -448.0f, 448.0f);
+    }
+    int lo = 0, hi = 0;
+    lo = cvt_fp8x2<false>(q[0], q[1], lo);
+    lo = cvt_fp8x2<true>(q[2], q[3], lo);
+    hi = cvt_fp8x2<false>(q[4], q[5], hi);
+    hi = cvt_fp8x2<true>(q[6], q[7], hi);
+    codes = make_uint2(static_cast<uint32_t>(lo), static_cast<uint32_t>(hi));
+    word = finite ? __float_as_uint(amax / 448.0f) : 0x7FC00000u;
+  } else {
+    const int e = e8m0_exponent<8>(finite ? m : 0);
+    const float sbits = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+    v2s lo = {0, 0}, hi = {0, 0};
+    lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(lo, __builtin_bit_cast(v2bf, w[0]), sbits, false);
+    lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(lo, __builtin_bit_cast(v2bf, w[1]), sbits, true);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(hi, __builtin_bit_cast(v2bf, w[2]), sbits, false);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(hi, __builtin_bit_cast(v2bf, w[3]), sbits, true);
+    codes = make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+    // the four quads' bytes into one word, in every lane
+    word = (finite ? static_cast<uint32_t>(e + 127) : 0xFFu) << (8 * (l >> 2));
+    word |= dpp(word, std::integral_constant<int, 0x128>{});
+    word |= dpp(word, std::integral_constant<int, 0x124>{});
+  }
+  if (!finite) codes = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  if (raw >= a.units) return;
+  *reinterpret_cast<uint2*>(a.xq + static_cast<size_t>(unit) * kStageK + l * 8) = codes;
+  if (l == 0) a.xs[unit] = word;
+}
+
+// ----------------------------------------------------------------------- GEMM
+
+// 16-byte chunk c of row r of a stage lies at chunk c ^ swz8(r): the 32 rows of an operand read in distinct banks
+__device__ __forceinline__ int swz8(int r) { return ((r >> 1) ^ ((r & 1) << 2)) & 7; }
+
+struct GemmArgs {
+  const uint8_t* xq;          // [rows, KB * 128] e4m3
+  const uint32_t* xs;         // [rows, KB] scale words
+  const uint8_t* w;           // [E, N, K] e4m3
+  const void* ws;             // E8M0 [E, N, K/32], or FP32 [E, ceil(N/128), KB]
+  uint16_t* out;              // [S, N] BF16
+  const RowTile* tiles;       // null: one group of S rows
+  const int32_t* row_slot;    // [S] or null: row r reads x row row_slot[r] / k
+  DivU32 k_div;
+  int32_t rows, S, N, K, KB;
+  int32_t n_tiles;
+};
+
+template <int HALF>
+__device__ __forceinline__ v16f mfma_mx(const v8i& w, const v8i& x, const v16f& c, uint32_t sw, uint32_t sx) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, c, 0, 0, 2 * HALF, static_cast<int>(sw), 2 * HALF,
+                                                         static_cast<int>(sx));
+}
+
+// WGM x WGN waves share a BM (rows) x BN (columns) tile; with WGK > 1 that many sets of them each take every WGK-th
+// stage and their sums meet in LDS at the end.  STAGES super-stages of WGK x 128 K in LDS.
+//
+// v_mfma_scale_f32_32x32x64_f8f6f4, weight first: lane l holds row l % 32 of each operand, K [16q, 16q+16) and
+// [32+16q, 32+16q+16) of the 64 with q = l / 32, and passes the scale of 32-K block q; its 16 results are the columns
+// 8 (r / 4) + 4 q + r % 4 of activation row l % 32.
+template <bool F32, int BM, int BN, int WGM, int WGN, int WGK, int STAGES>
+__device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
+  constexpr int NW = WGM * WGN * WGK;
+  constexpr int WTM = BM / WGM, WTN = BN / WGN;        // a wave's sub-tile
+  constexpr int JT = WTM / 32, IT = WTN / 32;          // its MFMA tiles
+  constexpr int kSub = (BM + BN) * kStageK;            // bytes of one 128-K stage: W rows, then x rows
+  constexpr int kStage = kSub * WGK;
+  constexpr int A_INS = WGK * BM / 8, W_INS = WGK * BN / 8;   // DMA instructions of a super-stage (8 rows each)
+  constexpr int APW = (A_INS + NW - 1) / NW, WPW = (W_INS + NW - 1) / NW;
+  constexpr int kDma = APW + WPW;                      // per wave and super-stage
+  static_assert(STAGES == 2 || STAGES == 3, "ring");
+  static_assert(IT * JT * 16 * 256 * (WGK - 1) * WGM * WGN <= kStage, "the partial sums fit a stage buffer");
+  __shared__ __attribute__((aligned(1024))) uint8_t st0[kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t st1[kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t st2[STAGES > 2 ? kStage : 16];
+  __shared__ int32_t src_row[BM];                      // x row of each tile row; -1: outside x
+
+  // ---- the tile.  Workgroup i runs on XCD i % 8; every XCD takes a contiguous range of the tiles, ordered by expert,
+  // column tile, row tile, so that the row tiles that share a weight tile run together on one XCD's L2.
+  const int total_mt = p.tiles ? p.tiles[0].count : (p.S + BM - 1) / BM;
+  const int total = total_mt * p.n_tiles;
+  const int per_xcd = (total + 7) >> 3;
+  const int slot = blockIdx.x >> 3;
+  const int work = (blockIdx.x & 7) * per_xcd + slot;
+  if (slot >= per_xcd || work >= total) return;
+  int e = 0, row_lo = 0, row_hi = p.S, mt, nt;
+  if (p.tiles) {
+    const RowTile t = p.tiles[1 + work / p.n_tiles];
+    const int local = work - t.first * p.n_tiles;
+    e = __builtin_amdgcn_readfirstlane(t.expert);
+    row_lo = __builtin_amdgcn_readfirstlane(t.row_lo);
+    row_hi = __builtin_amdgcn_readfirstlane(t.row_hi);
+    const int count = __builtin_amdgcn_readfirstlane(t.count);
+    mt = local % count;
+    nt = local / count;
+  } else {
+    mt = work % total_mt;
+    nt = work / total_mt;
+  }
+  mt = __builtin_amdgcn_readfirstlane(mt);
+  nt = __builtin_amdgcn_readfirstlane(nt);
+  const int row0 = row_lo + mt * BM, n0 = nt * BN;
+  const int rows = min(BM, row_hi - row0), cols = min(BN, p.N - n0);
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave % WGN, wm = (wave / WGN) % WGM, wk = wave / (WGN * WGM);
+  const int r32 = lane & 31, q2 = lane >> 5;
+  const int KB = p.KB, KS = (KB + WGK - 1) / WGK;
+
+  for (int r = tid; r < BM; r += 64 * NW) {
+    const int rr = row0 + min(r, rows - 1);            // rows behind the tile's last re-read it
+    int s = rr;
+    if (p.row_slot) {
+      const int slot_id = p.row_slot[rr];
+      s = slot_id < 0 ? -1 : static_cast<int>(div_u32(static_cast<uint32_t>(slot_id), p.k_div));
+    }
+    src_row[r] = s >= p.rows ? -1 : s;
+  }
+  __syncthreads();
+
+  // ---- DMA sources.  Instruction i of an operand moves 8 rows x 128 bytes: stage i / (rows / 8) of the super-stage,
+  // rows 8 (i % (rows / 8)).. of the tile.  Where there are fewer instructions than waves some repeat another's.
+  const uint32_t Kp = static_cast<uint32_t>(KB) * kStageK;
+  const __amdgpu_buffer_rsrc_t ares = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(p.xq), 0, static_cast<int>(static_cast<uint32_t>(p.rows) * Kp), kBufferFlags);
+  const __amdgpu_buffer_rsrc_t wres = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(p.w + (static_cast<size_t>(e) * p.N + n0) * p.K), 0, cols * p.K, kBufferFlags);
+  uint32_t offA[APW], offW[WPW], chW[WPW];
+  int ldsA[APW], ldsW[WPW], subA[APW], subW[WPW];
+#pragma unroll
+  for (int u = 0; u < APW; ++u) {
+    const int i = (wave + u * NW) % A_INS, sub = i / (BM / 8), rg = i % (BM / 8);
+    const int r = rg * 8 + (lane >> 3);
+    offA[u] = static_cast<uint32_t>(max(src_row[r], 0)) * Kp + ((lane & 7) ^ swz8(r)) * 16;
+    subA[u] = sub;
+    ldsA[u] = sub * kSub + BN * kStageK + rg * 8 * kStageK;
+  }
+#pragma unroll
+  for (int u = 0; u < WPW; ++u) {
+    const int i = (wave + u * NW) % W_INS, sub = i / (BN / 8), rg = i % (BN / 8);
+    const int r = rg * 8 + (lane >> 3);
+    offW[u] = static_cast<uint32_t>(min(r, cols - 1)) * static_cast<uint32_t>(p.K);
+    chW[u] = ((lane & 7) ^ swz8(r)) * 16;
+    subW[u] = sub;
+    ldsW[u] = sub * kSub + rg * 8 * kStageK;
+  }
+  // Chunks of the weight at or behind K re-read the row's last one: the activation's codes there are zero.
+  auto issue = [&](uint8_t* buf, int ks) {
+#pragma unroll
+    for (int u = 0; u < WPW; ++u) {
+      const uint32_t k = min(static_cast<uint32_t>((ks * WGK + subW[u]) * kStageK) + chW[u],
+                             static_cast<uint32_t>(p.K - 16));
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wres, (lds_void_t*)(buf + ldsW[u]), 16, offW[u] + k, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < APW; ++u) {
+      const int kb = min(ks * WGK + subA[u], KB - 1);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ares, (lds_void_t*)(buf + ldsA[u]), 16, offA[u], kb * kStageK, 0, 0);
+    }
+  };
+
+  // ---- scales of this wave's rows for one stage, in registers one super-stage ahead
+  uint32_t soffA[JT], soffW[IT];
+  const int K32 = p.K / 32;
+  const uint8_t* const wsb = static_cast<const uint8_t*>(p.ws) + (static_cast<size_t>(e) * p.N + n0) * K32;
+  const int NB = (p.N + 127) / 128;
+  const float* const wsf = static_cast<const float*>(p.ws) +
+                           (static_cast<size_t>(e) * NB + min((n0 + wn * WTN) / 128, NB - 1)) * KB;
+#pragma unroll
+  for (int j = 0; j < JT; ++j)
+    soffA[j] = static_cast<uint32_t>(max(src_row[wm * WTM + 32 * j + r32], 0)) * static_cast<uint32_t>(KB);
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+    soffW[i] = static_cast<uint32_t>(min(wn * WTN + 32 * i + r32, cols - 1)) * static_cast<uint32_t>(K32);
+  const int tail = K32 & 3;                            // 32-K blocks of the last stage when it is not whole
+  auto load_scales = [&](int ks, uint32_t (&sw)[IT], uint32_t (&sx)[JT]) {
+    const int kb = min(ks * WGK + wk, KB - 1);
+#pragma unroll
+    for (int j = 0; j < JT; ++j) sx[j] = p.xs[soffA[j] + static_cast<uint32_t>(kb)];
+    if constexpr (F32) {
+      sw[0] = __float_as_uint(wsf[kb]);
+    } else {
+      if (tail == 0 || kb < KB - 1) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) __builtin_memcpy(&sw[i], wsb + (soffW[i] + static_cast<uint32_t>(4 * kb)), 4);
+      } else {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          sw[i] = 0x7F7F7F7Fu;
+          for (int b = 0; b < tail; ++b) {
+            const uint32_t s = wsb[soffW[i] + static_cast<uint32_t>(4 * kb + b)];
+            sw[i] = (sw[i] & ~(0xFFu << (8 * b))) | (s << (8 * b));
+          }
+        }
+      }
+    }
+  };
+
+  v16f acc[IT][JT];
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+#pragma unroll
+    for (int j = 0; j < JT; ++j) acc[i][j] = v16f{};
+
+  const int rdW = wk * kSub + (wn * WTN + r32) * kStageK;
+  const int rdA = wk * kSub + BN * kStageK + (wm * WTM + r32) * kStageK;
+  const int sz = swz8(r32);
+  auto frag = [&](const uint8_t* base, int half) {
+    const uint4 lo = *reinterpret_cast<const uint4*>(base + (((4 * half + q2) ^ sz) << 4));
+    const uint4 hi = *reinterpret_cast<const uint4*>(base + (((4 * half + q2 + 2) ^ sz) << 4));
+    v8i v;
+    v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+    v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+    return v;
+  };
+  const bool has_rows = wm * WTM < rows && wn * WTN < cols;   // a wave without output of its own only moves data
+  auto compute = [&](const uint8_t* buf, int ks, const uint32_t (&sw)[IT], const uint32_t (&sx)[JT]) {
+    if (!has_rows || ks * WGK + wk >= KB) return;
+    if constexpr (F32) {
+      v8i fw[IT][2];
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        fw[i][0] = frag(buf + rdW + 32 * i * kStageK, 0);
+        fw[i][1] = frag(buf + rdW + 32 * i * kStageK, 1);
+      }
+#pragma unroll
+      for (int j = 0; j < JT; ++j) {
+        const v8i f0 = frag(buf + rdA + 32 * j * kStageK, 0), f1 = frag(buf + rdA + 32 * j * kStageK, 1);
+        const float s = __uint_as_float(sx[j]) * __uint_as_float(sw[0]);
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          v16f part = mfma_mx<0>(fw[i][0], f0, v16f{}, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+          part = mfma_mx<0>(fw[i][1], f1, part, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(part[r], s, acc[i][j][r]);
+        }
+      }
+    } else {
+      // lane group q passes block 2 half + q of the stage: byte 0 (half 0) or 2 (half 1) of the word moved down by q
+      uint32_t swq[IT], sxq[JT];
+#pragma unroll
+      for (int i = 0; i < IT; ++i) swq[i] = sw[i] >> (8 * q2);
+#pragma unroll
+      for (int j = 0; j < JT; ++j) sxq[j] = sx[j] >> (8 * q2);
+      auto half = [&](auto H) {
+        constexpr int h = decltype(H)::value;
+        v8i fw[IT], fx[JT];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) fw[i] = frag(buf + rdW + 32 * i * kStageK, h);
+#pragma unroll
+        for (int j = 0; j < JT; ++j) fx[j] = frag(buf + rdA + 32 * j * kStageK, h);
+#pragma unroll
+        for (int j = 0; j < JT; ++j)
+#pragma unroll
+          for (int i = 0; i < IT; ++i) acc[i][j] = mfma_mx<h>(fw[i], fx[j], acc[i][j], swq[i], sxq[j]);
+      };
+      half(std::integral_constant<int, 0>{});
+      half(std::integral_constant<int, 1>{});
+    }
+  };
+
+  // ---- ring.  On entry to step ks its DMA and at most STAGES - 2 younger super-stages are in flight.
+  uint32_t sw[IT], sx[JT];
+  load_scales(0, sw, sx);
+  issue(st0, 0);
+  if (STAGES > 2 && KS > 1) issue(st1, 1);
+  auto step = [&](const uint8_t* buf, uint8_t* refill, int ks) {
+    __builtin_amdgcn_sched_barrier(0);
+    if (STAGES > 2 && ks + 1 < KS)
+      __builtin_amdgcn_s_waitcnt(wait_vm_only(kDma));
+    else
+      __builtin_amdgcn_s_waitcnt(wait_vm_only(0));
+    __builtin_amdgcn_s_barrier();                      // super-stage ks is in LDS; the buffer before it is free
+    __builtin_amdgcn_sched_barrier(0);
+    uint32_t swn[IT], sxn[JT];
+    load_scales(min(ks + 1, KS - 1), swn, sxn);
+    if (ks + STAGES - 1 < KS) issue(refill, ks + STAGES - 1);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(buf, ks, sw, sx);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(kWaitLgkmOnly);         // this wave's reads of the buffer are done
+#pragma unroll
+    for (int i = 0; i < (F32 ? 1 : IT); ++i) sw[i] = swn[i];
+#pragma unroll
+    for (int j = 0; j < JT; ++j) sx[j] = sxn[j];
+  };
+  if constexpr (STAGES == 2) {
+    for (int ks = 0; ks < KS; ks += 2) {
+      step(st0, st1, ks);
+      if (ks + 1 < KS) step(st1, st0, ks + 1);
+    }
+  } else {
+    for (int ks = 0; ks < KS; ks += 3) {
+      step(st0, st2, ks);
+      if (ks + 1 < KS) step(st1, st0, ks + 1);
+      if (ks + 2 < KS) step(st2, st1, ks + 2);
+    }
+  }
+
+  // ---- the WGK partial sums, added in order by the first set of waves
+  if constexpr (WGK > 1) {
+    __syncthreads();
+    float* const red = reinterpret_cast<float*>(st0);
+    const int set = wave % (WGM * WGN);
+    if (wk > 0) {
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int j = 0; j < JT; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            red[((((wk - 1) * WGM * WGN + set) * IT + i) * JT + j) * 1024 + r * 64 + lane] = acc[i][j][r];
+    }
+    __syncthreads();
+    if (wk > 0) return;
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+#pragma unroll
+      for (int j = 0; j < JT; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          for (int s = 0; s < WGK - 1; ++s)
+            acc[i][j][r] += red[((((s * WGM * WGN) + set) * IT + i) * JT + j) * 1024 + r * 64 + lane];
+  }
+
+  // ---- out.  The lanes l and l + 32 hold alternating groups of four columns of one row: a swap of every second
+  // register pair leaves lane l columns 16 p .. 16 p + 7 and lane l + 32 columns 16 p + 8 .. 16 p + 15.
+#pragma unroll
+  for (int j = 0; j < JT; ++j) {
+    const int m = wm * WTM + 32 * j + r32;
+    const bool bad = src_row[m] < 0;
+    uint16_t* const orow = p.out + static_cast<size_t>(row0 + m) * p.N;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const v16f& v = acc[i][j];
+#pragma unroll
+      for (int pp = 0; pp < 2; ++pp) {
+        const uint32_t x0 = pack_bf16x2(v[8 * pp + 0], v[8 * pp + 1]), x1 = pack_bf16x2(v[8 * pp + 2], v[8 * pp + 3]);
+        const uint32_t y0 = pack_bf16x2(v[8 * pp + 4], v[8 * pp + 5]), y1 = pack_bf16x2(v[8 * pp + 6], v[8 * pp + 7]);
+        const auto s0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
+        const auto s1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
+        const int n = wn * WTN + 32 * i + 16 * pp + 8 * q2;
+        uint4 o = make_uint4(s0[0], s1[0], s0[1], s1[1]);
+        if (bad) o = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+        if (m < rows && n < cols) *reinterpret_cast<uint4*>(orow + n0 + n) = o;
+      }
+    }
+  }
+}
+
+template <bool F32, int BM, int BN, int WGM, int WGN, int WGK, int STAGES>
+__global__ __launch_bounds__(64 * WGM * WGN * WGK, 1) void grouped_gemm_kernel(GemmArgs p) {
+  grouped_gemm<F32, BM, BN, WGM, WGN, WGK, STAGES>(p);
+}
+
+// ------------------------------------------------------------------- dispatch
+
+struct Shape {
+  int BM, BN;
+};
+
+Shape pick_shape(int64_t S, int64_t E, int64_t N) {
+  const int64_t per = (S + E - 1) / E;
+  if (per <= 32) return {32, 64};
+  if (per <= 64) return {64, 128};
+  auto tiles = [&](int64_t bm, int64_t bn) { return (S / bm + (S < E ? S : E)) * ((N + bn - 1) / bn); };
+  if (per <= 160 || tiles(256, 256) < 256) return tiles(128, 256) < 256 ? Shape{64, 128} : Shape{128, 256};
+  return {256, 256};
+}
+
+int64_t max_row_tiles(int64_t S, int64_t E, int BM) { return S / BM + (S < E ? S : E); }
+
+size_t align_up(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+
+template <bool F32>
+void launch_gemm(const Shape s, const GemmArgs& a, int64_t tiles, hipStream_t stream) {
+  const unsigned grid = static_cast<unsigned>((tiles + 7) / 8 * 8);
+  if (s.BM == 32)
+    grouped_gemm_kernel<F32, 32, 64, 1, 2, 4, 3><<<grid, 512, 0, stream>>>(a);
+  else if (s.BM == 64)
+    grouped_gemm_kernel<F32, 64, 128, 1, 4, 2, 3><<<grid, 512, 0, stream>>>(a);
+  else if (s.BM == 128)
+    grouped_gemm_kernel<F32, 128, 256, 2, 4, 1, 3><<<grid, 512, 0, stream>>>(a);
+  else if constexpr (F32)
+    grouped_gemm_kernel<F32, 256, 256, 2, 4, 1, 2><<<grid, 512, 0, stream>>>(a);
+  else
+    grouped_gemm_kernel<F32, 256, 256, 2, 2, 1, 2><<<grid, 256, 0, stream>>>(a);
+}
+
+}  // namespace
+
+size_t grouped_workspace_bytes(int64_t rows, int64_t S, int64_t E, int64_t N, int64_t K) {
+  if (rows <= 0 || S <= 0 || E <= 0) return 0;
+  const int64_t KB = (K + kStageK - 1) / kStageK;
+  const Shape s = pick_shape(S, E, N);
+  return align_up(sizeof(RowTile) * (1 + max_row_tiles(S, E, s.BM))) + align_up(rows * KB * kStageK) +
+         align_up(rows * KB * 4);
+}
+
+mx_status launch_grouped(const void* x, int64_t rows, const uint8_t* w, const void* ws, bool f32, bool act,
+                         const int32_t* offsets, const int32_t* row_slot, int32_t k, int64_t S, int64_t E, int64_t N,
+                         int64_t K, void* out, void* workspace, hipStream_t stream, const char* what) {
+  const int64_t KB = (K + kStageK - 1) / kStageK;
+  const Shape s = pick_shape(S, E, N);
+  const int64_t mt = max_row_tiles(S, E, s.BM);
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  RowTile* const tiles = reinterpret_cast<RowTile*>(at);
+  at += align_up(sizeof(RowTile) * (1 + mt));
+  uint8_t* const xq = at;
+  at += align_up(rows * KB * kStageK);
+  uint32_t* const xs = reinterpret_cast<uint32_t*>(at);
+
+  QuantRowsArgs q{};
+  q.x = static_cast<const uint16_t*>(x);
+  q.xq = xq;
+  q.xs = xs;
+  q.rows = static_cast<uint32_t>(rows);
+  q.K = static_cast<uint32_t>(K);
+  q.KB = static_cast<uint32_t>(KB);
+  q.units = static_cast<uint32_t>(rows * KB);
+  q.kb_div = make_div(static_cast<uint32_t>(KB));
+  q.offsets = offsets;
+  q.tiles = tiles;
+  q.E = static_cast<int32_t>(E);
+  q.S = static_cast<int32_t>(S);
+  q.BM = s.BM;
+  q.max_tiles = static_cast<int32_t>(mt);
+  const unsigned qgrid = (q.units + 15) / 16 + (offsets ? 1 : 0);
+  if (f32 && act)
+    quant_rows_kernel<true, true><<<qgrid, 256, 0, stream>>>(q);
+  else if (f32)
+    quant_rows_kernel<true, false><<<qgrid, 256, 0, stream>>>(q);
+  else if (act)
+    quant_rows_kernel<false, true><<<qgrid, 256, 0, stream>>>(q);
+  else
+    quant_rows_kernel<false, false><<<qgrid, 256, 0, stream>>>(q);
+  mx_status st = launch_status(what);
+  if (st != MX_OK) return st;
+
+  GemmArgs g{};
+  g.xq = xq;
+  g.xs = xs;
+  g.w = w;
+  g.ws = ws;
+  g.out = static_cast<uint16_t*>(out);
+  g.tiles = offsets ? tiles : nullptr;
+  g.row_slot = row_slot;
+  g.k_div = make_div(static_cast<uint32_t>(k));
+  g.rows = static_cast<int32_t>(rows);
+  g.S = static_cast<int32_t>(S);
+  g.N = static_cast<int32_t>(N);
+  g.K = static_cast<int32_t>(K);
+  g.KB = static_cast<int32_t>(KB);
+  g.n_tiles = static_cast<int32_t>((N + s.BN - 1) / s.BN);
+  const int64_t total = (offsets ? mt : (S + s.BM - 1) / s.BM) * g.n_tiles;
+  if (f32)
+    launch_gemm<true>(s, g, total, stream);
+  else
+    launch_gemm<false>(s, g, total, stream);
+  return launch_status(what);
+}
+
+}  // namespace mx

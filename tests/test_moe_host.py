@@ -1,0 +1,174 @@
+"""Argument checks of the mixture-of-experts calls and the block-128 linear, on the CPU: the C entry points in dry-run
+mode, and the binding's shape and type checks (which run before any pointer is taken)."""
+
+import os
+
+import pytest
+import torch
+
+import mx_scaled_fp8_amd as mx
+
+pytestmark = pytest.mark.skipif(not os.path.exists(mx.lib_path()), reason="libmxfp8.so not built")
+
+FAKE = 1 << 20      # a 16-byte aligned stand-in for a device pointer; nothing is read in dry-run mode
+BIG = 1 << 44       # another, far from it
+
+
+@pytest.fixture
+def dry():
+    mx.mx_set_dry_run(True)
+    yield
+    mx.mx_set_dry_run(False)
+
+
+def _route(**kw):
+    a = dict(logits=FAKE, f32=1, bias=FAKE, T=100, E=64, k=8, score=0, renorm=1, scale=1.0, ids=FAKE, weights=FAKE,
+             offsets=FAKE, row_slot=FAKE, slot_row=FAKE, ws=FAKE, wb=1 << 30)
+    a.update(kw)
+    return mx.lib().mx_moe_route(*a.values(), None)
+
+
+def test_route_validation(dry):
+    assert _route() == mx.MX_OK
+    assert _route(bias=None) == mx.MX_OK
+    assert _route(f32=0, logits=FAKE + 2) == mx.MX_OK                # BF16 logits
+    assert _route(T=0, logits=None, ids=None, weights=None, row_slot=None, slot_row=None, ws=None, wb=0) == mx.MX_OK
+    assert _route(T=64, ws=None, wb=0) == mx.MX_OK                   # one chunk needs no workspace
+    assert _route(E=1, k=1) == mx.MX_OK
+    assert _route(E=1024, k=32) == mx.MX_OK
+    need = mx.mx_moe_route_workspace_bytes(100, 64)
+    assert need == 2 * 64 * 4 and _route(wb=need) == mx.MX_OK
+    for bad in (dict(f32=2), dict(E=0), dict(E=1025), dict(k=0), dict(k=65), dict(E=4, k=5), dict(k=33), dict(T=-1),
+                dict(T=1 << 30), dict(score=2), dict(renorm=2), dict(logits=None), dict(ids=None), dict(weights=None),
+                dict(offsets=None), dict(row_slot=None), dict(slot_row=None), dict(logits=FAKE + 2),
+                dict(offsets=FAKE + 2), dict(ws=None), dict(ws=FAKE + 2), dict(wb=need - 1), dict(bias=FAKE + 1)):
+        assert _route(**bad) == mx.MX_ERR_INVALID_ARG, bad
+        assert mx.lib().mx_last_error().decode()
+
+
+def _grouped(**kw):
+    a = dict(x=FAKE, rows=100, K=576, w=BIG, ws=FAKE, kind=0, E=8, N=512, offsets=FAKE, row_slot=FAKE, k=2, S=200,
+             act=0, out=2 * BIG, work=FAKE, wb=1 << 40)
+    a.update(kw)
+    return mx.lib().mx_grouped_linear(*a.values(), None)
+
+
+def test_grouped_validation(dry):
+    assert _grouped() == mx.MX_OK
+    assert _grouped(kind=1) == mx.MX_OK
+    assert _grouped(kind=1, K=16) == mx.MX_OK
+    assert _grouped(row_slot=None, S=100) == mx.MX_OK
+    assert _grouped(S=0) == mx.MX_OK
+    assert _grouped(rows=0, S=0, x=None, w=None, out=None, work=None, wb=0) == mx.MX_OK
+    need = mx.mx_grouped_linear_workspace_bytes(100, 200, 8, 512, 576)
+    assert need >= 100 * 640 and _grouped(wb=need) == mx.MX_OK
+    for bad in (dict(kind=2), dict(act=2), dict(k=0), dict(K=0), dict(K=48), dict(kind=1, K=24), dict(K=1 << 22),
+                dict(N=0), dict(N=24), dict(E=0), dict(E=1 << 20), dict(S=-1), dict(rows=-1), dict(S=1 << 31),
+                dict(row_slot=None), dict(rows=0), dict(rows=1 << 30), dict(x=None), dict(w=None), dict(ws=None),
+                dict(offsets=None), dict(out=None), dict(x=FAKE + 8), dict(w=BIG + 4), dict(out=2 * BIG + 8),
+                dict(kind=1, ws=FAKE + 2), dict(offsets=FAKE + 2), dict(row_slot=FAKE + 1), dict(work=None),
+                dict(work=FAKE + 8), dict(wb=need - 1), dict(out=BIG + 512), dict(out=FAKE),
+                dict(S=(1 << 31) - 1, N=1 << 20)):
+        assert _grouped(**bad) == mx.MX_ERR_INVALID_ARG, bad
+        assert mx.lib().mx_last_error().decode()
+
+
+def test_block128_validation(dry):
+    def f(**kw):
+        a = dict(x=FAKE, M=65, K=144, w=BIG, ws=FAKE, N=48, out=2 * BIG, work=FAKE, wb=1 << 30)
+        a.update(kw)
+        return mx.lib().mx_linear_block128(*a.values(), None)
+    assert f() == mx.MX_OK
+    assert f(M=0, x=None, out=None, work=None, wb=0) == mx.MX_OK
+    need = mx.mx_linear_block128_workspace_bytes(65, 48, 144)
+    assert f(wb=need) == mx.MX_OK
+    for bad in (dict(M=-1), dict(K=8), dict(K=100), dict(N=8), dict(N=50), dict(x=None), dict(w=None), dict(ws=None),
+                dict(out=None), dict(x=FAKE + 2), dict(w=BIG + 8), dict(ws=FAKE + 1), dict(out=2 * BIG + 8),
+                dict(work=None), dict(wb=need - 1), dict(out=BIG), dict(M=1 << 26, K=4096)):
+        assert f(**bad) == mx.MX_ERR_INVALID_ARG, bad
+
+
+def test_combine_validation(dry):
+    def f(**kw):
+        a = dict(y=FAKE, rows=80, N=512, slot_row=FAKE, weights=FAKE, T=10, k=8, shared=BIG, out=2 * BIG)
+        a.update(kw)
+        return mx.lib().mx_moe_combine(*a.values(), None)
+    assert f() == mx.MX_OK
+    assert f(shared=None) == mx.MX_OK
+    assert f(out=BIG) == mx.MX_OK                                    # in place over the shared rows
+    assert f(T=0, y=None, out=None) == mx.MX_OK
+    assert f(rows=0, y=None) == mx.MX_OK                             # every slot dropped
+    assert f(out=FAKE + 80 * 512 * 2) == mx.MX_OK                    # behind y
+    for bad in (dict(T=-1), dict(rows=-1), dict(rows=1 << 31), dict(N=0), dict(N=12), dict(k=0), dict(k=1025),
+                dict(y=None), dict(slot_row=None), dict(weights=None), dict(out=None), dict(y=FAKE + 8),
+                dict(out=2 * BIG + 2), dict(shared=BIG + 8), dict(slot_row=FAKE + 2), dict(out=FAKE + 1024),
+                dict(out=BIG + 1024), dict(T=1 << 30, N=1 << 10)):
+        assert f(**bad) == mx.MX_ERR_INVALID_ARG, bad
+
+
+def z(*shape, dtype=torch.uint8):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def _raises(match, fn, *a, **k):
+    with pytest.raises(ValueError, match=match):
+        fn(*a, **k)
+
+
+i16, i32, f32 = torch.int16, torch.int32, torch.float32
+
+
+def test_route_binding_checks():
+    l, b = z(8, 16, dtype=f32), z(16, dtype=f32)
+    _raises("logits must be", mx.mx_moe_route, z(8, dtype=f32), 2)
+    _raises("logits must be", mx.mx_moe_route, z(8, 16, dtype=torch.float64), 2)
+    _raises("bias has", mx.mx_moe_route, l, 2, bias=z(15, dtype=f32))
+    _raises("bias must be", mx.mx_moe_route, l, 2, bias=z(16, dtype=i16))
+    _raises("k = 0", mx.mx_moe_route, l, 0)
+    _raises("ids has", mx.mx_moe_route, l, 2, ids=z(8, dtype=i32))
+    _raises("ids must be", mx.mx_moe_route, l, 2, ids=z(8, 2, dtype=torch.int64))
+    _raises("weights has", mx.mx_moe_route, l, 2, weights=z(8, 3, dtype=f32))
+    _raises("offsets has", mx.mx_moe_route, l, 2, offsets=z(16, dtype=i32))
+    _raises("row_slot has", mx.mx_moe_route, l, 2, row_slot=z(15, dtype=i32))
+    _raises("slot_row has", mx.mx_moe_route, l, 2, slot_row=z(17, dtype=i32))
+    _raises("GPU tensor", mx.mx_moe_route, l, 2, bias=b)
+
+
+def test_grouped_binding_checks():
+    E, N, K, T, k = 4, 32, 64, 6, 2
+    x, w, ws = z(T, K, dtype=i16), z(E, N, K), z(E, N, K // 32)
+    off, rs = z(E + 1, dtype=i32), z(T * k, dtype=i32)
+    g = mx.mx_grouped_linear
+    _raises("x must be", g, z(T * K, dtype=i16), w, ws, off)
+    _raises("x must be", g, z(T, K, dtype=f32), w, ws, off)
+    _raises("x has shape", g, z(T, K + 32, dtype=i16), w, ws, off)
+    _raises("x has shape", g, x, w, ws, off, act=mx.MX_ACT_SWIGLU)
+    _raises("w_scale has shape", g, x, w, z(E, N, 1), off)
+    _raises("w_scale has shape", g, x, w, z(E, 1, 2, dtype=f32), off)
+    _raises("w_scale must be", g, x, w, z(E, N, 2, dtype=i16), off)
+    _raises("multiple of 32", g, z(T, 48, dtype=i16), z(E, N, 48), z(E, N, 1), off)
+    _raises("offsets has", g, x, w, ws, z(E, dtype=i32))
+    _raises("offsets must be", g, x, w, ws, z(E + 1, dtype=torch.int64))
+    _raises("row_slot must be", g, x, w, ws, off, row_slot=z(12, dtype=torch.int64), k=k)
+    _raises("out has", g, x, w, ws, off, row_slot=rs, k=k, out=z(T, N, dtype=i16))
+    _raises("GPU tensor", g, x, w, ws, off, row_slot=rs, k=k)
+
+
+def test_combine_and_block128_binding_checks():
+    T, k, N = 6, 2, 32
+    y, sr, wt = z(T * k, N, dtype=i16), z(T, k, dtype=i32), z(T, k, dtype=f32)
+    c = mx.mx_moe_combine
+    _raises("y must be", c, z(12, dtype=i16), sr, wt)
+    _raises("slot_row must be", c, y, z(T, k, dtype=torch.int64), wt)
+    _raises("weights has", c, y, sr, z(T, 3, dtype=f32))
+    _raises("weights must be", c, y, sr, z(T, k, dtype=i16))
+    _raises("shared has", c, y, sr, wt, shared=z(T, N + 8, dtype=i16))
+    _raises("out has", c, y, sr, wt, out=z(T, N + 8, dtype=i16))
+    _raises("GPU tensor", c, y, sr, wt)
+    x, w, ws = z(5, 144, dtype=i16), z(48, 144), z(1, 2, dtype=f32)
+    b = mx.mx_linear_block128
+    _raises("w has shape", b, x, z(48, 128), ws)
+    _raises("w_scale has shape", b, x, w, z(1, 1, dtype=f32))
+    _raises("w_scale must be", b, x, w, z(1, 2))
+    _raises("out has", b, x, w, ws, out=z(5, 32, dtype=i16))
+    _raises("GPU tensor", b, x, w, ws)
