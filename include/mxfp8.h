@@ -388,7 +388,7 @@ mx_status mx_linear_block128(const void* x, int64_t M, int64_t K, const uint8_t*
  * row_slot device int32 [T * k]: the flat slot t * k + j that row r holds, rows
  *          in ascending slot order within an expert.
  * slot_row device int32 [T, k]: the row of each slot (row_slot's inverse).
- * workspace device, at least mx_moe_route_workspace_bytes(T, E), 4-byte aligned
+ * workspace device, at least mx_moe_route_workspace_bytes(T, E), 8-byte aligned
  *          (may be NULL when that is 0).  Calls that may overlap need one each.
  * The result does not depend on timing (no position comes from an atomic).
  * Requires: T >= 0 (0 writes offsets of zero), 1 <= E <= MX_ROUTE_MAX_EXPERTS,

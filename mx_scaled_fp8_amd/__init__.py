@@ -444,13 +444,28 @@ def _dtype(t, dtypes, name):
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 
 
-def _workspace(ws, need, device):
-    """(tensor or None, pointer, bytes) of a workspace of at least `need` bytes."""
+def _workspace(ws, need, like):
+    """(tensor or None, pointer, bytes) of a workspace of at least `need` bytes on the device of `like`."""
     if ws is None:
         if not need:
             return None, None, 0
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = like.new_empty(need, dtype=torch.uint8)
+        return ws, ws.data_ptr(), need
     return ws, _dev(ws, "workspace"), ws.numel() * ws.element_size()
+
+
+# torch.cuda.current_stream() builds a Stream object, 2 us of a call that takes 6; the handle alone is a lookup
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on_device(fn, ref, *args):
+    """fn(*args, stream) with the device of `ref` as the current one, on its current stream."""
+    index = ref.get_device()
+    stream = _raw_stream(index) if _raw_stream else _stream(ref)
+    if index == torch.cuda.current_device():
+        return _check(fn(*args, stream))
+    with torch.cuda.device(index):
+        return _check(fn(*args, stream))
 
 
 def mx_linear_block128_workspace_bytes(M, N, K):
@@ -472,9 +487,8 @@ def mx_linear_block128(x, w, w_scale, out=None, workspace=None):
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     args = (_dev(x, "x", 2), M, K, _dev(w, "w", 1), _dev(w_scale, "w_scale", 4), N, _dev(out, "out", 2))
-    workspace, wp, wb = _workspace(workspace, mx_linear_block128_workspace_bytes(M, N, K), x.device)
-    with torch.cuda.device(x.device):
-        _check(lib().mx_linear_block128(*args, wp, wb, _stream(x)))
+    workspace, wp, wb = _workspace(workspace, mx_linear_block128_workspace_bytes(M, N, K), x)
+    _on_device(lib().mx_linear_block128, x, *args, wp, wb)
     return out
 
 
@@ -509,23 +523,20 @@ def mx_moe_route(logits, k, bias=None, score=MX_ROUTE_SOFTMAX, renormalize=True,
                  ("row_slot", row_slot), ("slot_row", slot_row), ("workspace", workspace))
     lp = _dev(logits, "logits")
     bp = _dev(bias, "bias", 4) if bias is not None else None
-    dev = logits.device
     if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        ids = logits.new_empty((T, k), dtype=torch.int32)
     if weights is None:
-        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        weights = logits.new_empty((T, k), dtype=torch.float32)
     if offsets is None:
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        offsets = logits.new_empty(E + 1, dtype=torch.int32)
     if row_slot is None:
-        row_slot = torch.empty(T * k, dtype=torch.int32, device=dev)
+        row_slot = logits.new_empty(T * k, dtype=torch.int32)
     if slot_row is None:
-        slot_row = torch.empty((T, k), dtype=torch.int32, device=dev)
-    workspace, wp, wb = _workspace(workspace, mx_moe_route_workspace_bytes(T, E), dev)
-    with torch.cuda.device(dev):
-        _check(lib().mx_moe_route(lp, int(logits.dtype == torch.float32), bp, T, E, k, score, int(bool(renormalize)),
-                                  scale, _dev(ids, "ids", 4), _dev(weights, "weights", 4),
-                                  _dev(offsets, "offsets", 4), _dev(row_slot, "row_slot", 4),
-                                  _dev(slot_row, "slot_row", 4), wp, wb, _stream(logits)))
+        slot_row = logits.new_empty((T, k), dtype=torch.int32)
+    workspace, wp, wb = _workspace(workspace, mx_moe_route_workspace_bytes(T, E), logits)
+    _on_device(lib().mx_moe_route, logits, lp, int(logits.dtype == torch.float32), bp, T, E, k, score,
+               int(bool(renormalize)), scale, _dev(ids, "ids", 4), _dev(weights, "weights", 4),
+               _dev(offsets, "offsets", 4), _dev(row_slot, "row_slot", 4), _dev(slot_row, "slot_row", 4), wp, wb)
     return ids, weights, offsets, row_slot, slot_row
 
 
@@ -563,9 +574,8 @@ def mx_grouped_linear(x, w, w_scale, offsets, row_slot=None, k=1, act=MX_ACT_NON
     args = (_dev(x, "x", 2), rows, K, _dev(w, "w", 1), _dev(w_scale, "w_scale"), kind, E, N,
             _dev(offsets, "offsets", 4), _dev(row_slot, "row_slot", 4) if row_slot is not None else None, k, S, act,
             _dev(out, "out", 2))
-    workspace, wp, wb = _workspace(workspace, mx_grouped_linear_workspace_bytes(rows, S, E, N, K), x.device)
-    with torch.cuda.device(x.device):
-        _check(lib().mx_grouped_linear(*args, wp, wb, _stream(x)))
+    workspace, wp, wb = _workspace(workspace, mx_grouped_linear_workspace_bytes(rows, S, E, N, K), x)
+    _on_device(lib().mx_grouped_linear, x, *args, wp, wb)
     return out
 
 
@@ -588,8 +598,7 @@ def mx_moe_combine(y, slot_row, weights, shared=None, out=None):
         out = torch.empty((T, N), dtype=torch.bfloat16, device=y.device)
     args = (_dev(y, "y", 2), rows, N, _dev(slot_row, "slot_row", 4), _dev(weights, "weights", 4), T, k,
             _dev(shared, "shared", 2) if shared is not None else None, _dev(out, "out", 2))
-    with torch.cuda.device(y.device):
-        _check(lib().mx_moe_combine(*args, _stream(y)))
+    _on_device(lib().mx_moe_combine, y, *args)
     return out
 
 

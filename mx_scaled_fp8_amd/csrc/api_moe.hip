@@ -49,8 +49,8 @@ mx_status mx_moe_route(const void* logits, int32_t logits_f32, const float* bias
                  aligned(row_slot, 4) && aligned(slot_row, 4),
              "%s: logits must be aligned to their element, the other tensors to 4 bytes", fn);
     const size_t need = mx_moe_route_workspace_bytes(T, E);
-    MX_CHECK(workspace_bytes >= need && (need == 0 || (workspace && aligned(workspace, 4))),
-             "%s: workspace of %zu bytes (4-byte aligned) needed, got %zu", fn, need, workspace_bytes);
+    MX_CHECK(workspace_bytes >= need && (need == 0 || (workspace && aligned(workspace, 8))),
+             "%s: workspace of %zu bytes (8-byte aligned) needed, got %zu", fn, need, workspace_bytes);
   }
   MX_PREAMBLE();
   count(C_MOE_ROUTE);

@@ -207,7 +207,7 @@ struct GemmArgs {
   const RowTile* tiles;       // null: one group of S rows
   const int32_t* row_slot;    // [S] or null: row r reads x row row_slot[r] / k
   DivU32 k_div;
-  int32_t rows, S, N, K, KB;
+  int32_t rows, S, E, N, K, KB;
   int32_t n_tiles;
 };
 
@@ -238,6 +238,11 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   __shared__ __attribute__((aligned(1024))) uint8_t st0[kStage];
   __shared__ __attribute__((aligned(1024))) uint8_t st1[kStage];
   __shared__ __attribute__((aligned(1024))) uint8_t st2[STAGES > 2 ? kStage : 16];
+  // scale words of two windows of four stages.  MXFP8: W rows, then x rows, four E8M0 bytes each.  FP32: the products of
+  // an x row's scale with the column block's, for each of the tile's column blocks.
+  constexpr int kCB = (BN + 127) / 128;
+  constexpr int kScRows = F32 ? BM * kCB : BN + BM;
+  __shared__ __attribute__((aligned(16))) uint32_t sc[2][4][kScRows];
   __shared__ int32_t src_row[BM];                      // x row of each tile row; -1: outside x
 
   // ---- the tile.  Workgroup i runs on XCD i % 8; every XCD takes a contiguous range of the tiles, ordered by expert,
@@ -297,7 +302,8 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   for (int u = 0; u < APW; ++u) {
     const int i = (wave + u * NW) % A_INS, sub = i / (BM / 8), rg = i % (BM / 8);
     const int r = rg * 8 + (lane >> 3);
-    offA[u] = static_cast<uint32_t>(max(src_row[r], 0)) * Kp + ((lane & 7) ^ swz8(r)) * 16;
+    // rows behind the tile's last are not fetched (an offset behind the resource): an MFMA's rows are independent
+    offA[u] = r < rows ? static_cast<uint32_t>(max(src_row[r], 0)) * Kp + ((lane & 7) ^ swz8(r)) * 16 : 0xFFFFFFF0u;
     subA[u] = sub;
     ldsA[u] = sub * kSub + BN * kStageK + rg * 8 * kStageK;
   }
@@ -310,55 +316,112 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
     subW[u] = sub;
     ldsW[u] = sub * kSub + rg * 8 * kStageK;
   }
-  // Chunks of the weight at or behind K re-read the row's last one: the activation's codes there are zero.
+  // Chunks of the weight at or behind K re-read the row's last one: the activation's codes there are zero.  A super-stage
+  // behind the last is asked for all the same, at offsets behind the resources: nothing is fetched, and the number of
+  // instructions in flight stays the same for every step.
   auto issue = [&](uint8_t* buf, int ks) {
+    uint32_t behind = ks < KS ? 0u : 0xFFFFFFF0u;
+    asm("" : "+s"(behind));                           // or-ed in: as a choice of offsets it became branches
 #pragma unroll
     for (int u = 0; u < WPW; ++u) {
       const uint32_t k = min(static_cast<uint32_t>((ks * WGK + subW[u]) * kStageK) + chW[u],
                              static_cast<uint32_t>(p.K - 16));
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wres, (lds_void_t*)(buf + ldsW[u]), 16, offW[u] + k, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wres, (lds_void_t*)(buf + ldsW[u]), 16, (offW[u] + k) | behind, 0, 0, 0);
     }
 #pragma unroll
     for (int u = 0; u < APW; ++u) {
       const int kb = min(ks * WGK + subA[u], KB - 1);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ares, (lds_void_t*)(buf + ldsA[u]), 16, offA[u], kb * kStageK, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ares, (lds_void_t*)(buf + ldsA[u]), 16, offA[u] | behind,
+                                               kb * kStageK, 0, 0);
     }
   };
 
-  // ---- scales of this wave's rows for one stage, in registers one super-stage ahead
-  uint32_t soffA[JT], soffW[IT];
-  const int K32 = p.K / 32;
-  const uint8_t* const wsb = static_cast<const uint8_t*>(p.ws) + (static_cast<size_t>(e) * p.N + n0) * K32;
-  const int NB = (p.N + 127) / 128;
-  const float* const wsf = static_cast<const float*>(p.ws) +
-                           (static_cast<size_t>(e) * NB + min((n0 + wn * WTN) / 128, NB - 1)) * KB;
+  // ---- scales: thread t owns rows t, t + threads, .. of the tile's operands (W rows, then x rows; FP32: x rows alone)
+  // and brings four stages' words at a time, one window ahead.  (One word per row, lane and stage, gathered by every
+  // wave for itself, took the address unit longer than the operands: 1945 against 1607 us for 65536 rows, N = 4608,
+  // K = 5120 without any scale loads.)
+  constexpr int kScOwn = F32 ? BM : BN + BM;
+  constexpr int SPT = (kScOwn + 64 * NW - 1) / (64 * NW);
+  const int K32 = p.K / 32, NB = (p.N + 127) / 128;
+  struct Words { uint32_t v[4]; };
+  Words own[SPT], colw[F32 ? kCB : 1];
+  // A thread's row of scale words, 4 bytes a stage for either operand.  A window is one 16-byte load, unconditional, so
+  // that nothing waits for it before it is stored a window later.  It may reach behind the row: behind the last x row
+  // lies workspace, and a W row's load is moved back to end with the tensor (`back` bytes, undone when it is stored).
+  const uint8_t* rowp[SPT];
+  int room[SPT];                                       // bytes from the row's begin to the last place a load may start
 #pragma unroll
-  for (int j = 0; j < JT; ++j)
-    soffA[j] = static_cast<uint32_t>(max(src_row[wm * WTM + 32 * j + r32], 0)) * static_cast<uint32_t>(KB);
-#pragma unroll
-  for (int i = 0; i < IT; ++i)
-    soffW[i] = static_cast<uint32_t>(min(wn * WTN + 32 * i + r32, cols - 1)) * static_cast<uint32_t>(K32);
-  const int tail = K32 & 3;                            // 32-K blocks of the last stage when it is not whole
-  auto load_scales = [&](int ks, uint32_t (&sw)[IT], uint32_t (&sx)[JT]) {
-    const int kb = min(ks * WGK + wk, KB - 1);
-#pragma unroll
-    for (int j = 0; j < JT; ++j) sx[j] = p.xs[soffA[j] + static_cast<uint32_t>(kb)];
-    if constexpr (F32) {
-      sw[0] = __float_as_uint(wsf[kb]);
+  for (int u = 0; u < SPT; ++u) {
+    const int t = min(tid + u * 64 * NW, kScOwn - 1);
+    if (!F32 && t < BN) {
+      const size_t row = static_cast<size_t>(e) * p.N + n0 + min(t, cols - 1);
+      rowp[u] = static_cast<const uint8_t*>(p.ws) + row * K32;
+      room[u] = static_cast<int>(min(static_cast<size_t>(p.E) * p.N * K32 - row * K32, static_cast<size_t>(1) << 30)) - 16;
     } else {
-      if (tail == 0 || kb < KB - 1) {
+      rowp[u] = reinterpret_cast<const uint8_t*>(p.xs + static_cast<size_t>(max(src_row[F32 ? t : t - BN], 0)) * KB);
+      room[u] = 1 << 30;
+    }
+  }
+  auto load_scales = [&](int win) {
+    const int kb = min(4 * win, KB - 1);               // a window behind the last is never used
 #pragma unroll
-        for (int i = 0; i < IT; ++i) __builtin_memcpy(&sw[i], wsb + (soffW[i] + static_cast<uint32_t>(4 * kb)), 4);
-      } else {
+    for (int u = 0; u < SPT; ++u) __builtin_memcpy(&own[u], rowp[u] + min(4 * kb, room[u]), 16);
+    if constexpr (F32) {
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          sw[i] = 0x7F7F7F7Fu;
-          for (int b = 0; b < tail; ++b) {
-            const uint32_t s = wsb[soffW[i] + static_cast<uint32_t>(4 * kb + b)];
-            sw[i] = (sw[i] & ~(0xFFu << (8 * b))) | (s << (8 * b));
+      for (int c = 0; c < kCB; ++c) {
+        const float* src = static_cast<const float*>(p.ws) +
+                           (static_cast<size_t>(e) * NB + min(n0 / 128 + c, NB - 1)) * KB + kb;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) colw[c].v[q] = __float_as_uint(src[min(q, KB - 1 - kb)]);
+      }
+    }
+  };
+  auto store_scales = [&](int win) {
+    const int left = K32 - 16 * win;                   // 32-K blocks of the row from this window on
+#pragma unroll
+    for (int u = 0; u < SPT; ++u) {
+      const int t = tid + u * 64 * NW;
+      if constexpr (!F32) {
+        const int back = 16 * win - room[u];
+        if (back > 0) {                                // the tensor's last rows
+          uint64_t v[2];
+          __builtin_memcpy(v, &own[u], 16);
+          const int sh = 8 * back;
+          v[0] = sh < 64 ? v[0] >> sh | v[1] << (64 - sh) : v[1] >> (sh - 64);
+          v[1] = sh < 64 ? v[1] >> sh : 0;
+          __builtin_memcpy(&own[u], v, 16);
+        }
+        // blocks behind K: 2^-127, not the next row's scale (which may be NaN); their codes are zero
+        if (left < 16) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int b = left - 4 * q;
+            own[u].v[q] &= b >= 4 ? 0xFFFFFFFFu : b <= 0 ? 0u : (1u << (8 * b)) - 1;
           }
         }
       }
+      if (t >= kScOwn) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if constexpr (F32) {
+#pragma unroll
+          for (int c = 0; c < kCB; ++c)
+            sc[win & 1][q][c * BM + t] = __float_as_uint(__uint_as_float(own[u].v[q]) * __uint_as_float(colw[c].v[q]));
+        } else {
+          sc[win & 1][q][t] = own[u].v[q];
+        }
+      }
+    }
+  };
+  // scale words of this wave's MFMA tiles for stage kb
+  auto read_scales = [&](int kb, uint32_t (&sw)[IT], uint32_t (&sx)[JT]) {
+    const uint32_t* const row = sc[(kb >> 2) & 1][kb & 3];
+#pragma unroll
+    for (int j = 0; j < JT; ++j)
+      sx[j] = row[(F32 ? wn * WTN / 128 * BM : BN) + wm * WTM + 32 * j + r32];
+    if constexpr (!F32) {
+#pragma unroll
+      for (int i = 0; i < IT; ++i) sw[i] = row[wn * WTN + 32 * i + r32];
     }
   };
 
@@ -392,7 +455,7 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
 #pragma unroll
       for (int j = 0; j < JT; ++j) {
         const v8i f0 = frag(buf + rdA + 32 * j * kStageK, 0), f1 = frag(buf + rdA + 32 * j * kStageK, 1);
-        const float s = __uint_as_float(sx[j]) * __uint_as_float(sw[0]);
+        const float s = __uint_as_float(sx[j]);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
           v16f part = mfma_mx<0>(fw[i][0], f0, v16f{}, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
@@ -425,30 +488,26 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
     }
   };
 
-  // ---- ring.  On entry to step ks its DMA and at most STAGES - 2 younger super-stages are in flight.
-  uint32_t sw[IT], sx[JT];
-  load_scales(0, sw, sx);
+  // ---- ring.  At the top of step ks its DMA and that of the STAGES - 2 super-stages behind it are in flight.
   issue(st0, 0);
-  if (STAGES > 2 && KS > 1) issue(st1, 1);
+  load_scales(0);
+  if constexpr (STAGES > 2) issue(st1, 1);
   auto step = [&](const uint8_t* buf, uint8_t* refill, int ks) {
+    const bool window = (ks * WGK) % 4 == 0;
     __builtin_amdgcn_sched_barrier(0);
-    if (STAGES > 2 && ks + 1 < KS)
-      __builtin_amdgcn_s_waitcnt(wait_vm_only(kDma));
-    else
-      __builtin_amdgcn_s_waitcnt(wait_vm_only(0));
+    __builtin_amdgcn_s_waitcnt(wait_vm_only((STAGES - 2) * kDma));
+    if (window) store_scales(ks * WGK / 4);
+    __builtin_amdgcn_s_waitcnt(kWaitLgkmOnly);         // the scales are written; reads of the buffer before are done
     __builtin_amdgcn_s_barrier();                      // super-stage ks is in LDS; the buffer before it is free
     __builtin_amdgcn_sched_barrier(0);
-    uint32_t swn[IT], sxn[JT];
-    load_scales(min(ks + 1, KS - 1), swn, sxn);
-    if (ks + STAGES - 1 < KS) issue(refill, ks + STAGES - 1);
+    uint32_t sw[IT], sx[JT];
+    read_scales(ks * WGK + wk, sw, sx);
+    if (window) load_scales(ks * WGK / 4 + 1);
+    __builtin_amdgcn_sched_barrier(0);                 // the loads go out before the DMA, and are waited for before it
+    issue(refill, ks + STAGES - 1);
     __builtin_amdgcn_sched_barrier(0);
     compute(buf, ks, sw, sx);
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(kWaitLgkmOnly);         // this wave's reads of the buffer are done
-#pragma unroll
-    for (int i = 0; i < (F32 ? 1 : IT); ++i) sw[i] = swn[i];
-#pragma unroll
-    for (int j = 0; j < JT; ++j) sx[j] = sxn[j];
   };
   if constexpr (STAGES == 2) {
     for (int ks = 0; ks < KS; ks += 2) {
@@ -462,6 +521,8 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
       if (ks + 2 < KS) step(st2, st1, ks + 2);
     }
   }
+
+  __builtin_amdgcn_s_waitcnt(wait_vm_only(0));         // no DMA outlives the tile or meets the sums below
 
   // ---- the WGK partial sums, added in order by the first set of waves
   if constexpr (WGK > 1) {
@@ -560,7 +621,7 @@ size_t grouped_workspace_bytes(int64_t rows, int64_t S, int64_t E, int64_t N, in
   const int64_t KB = (K + kStageK - 1) / kStageK;
   const Shape s = pick_shape(S, E, N);
   return align_up(sizeof(RowTile) * (1 + max_row_tiles(S, E, s.BM))) + align_up(rows * KB * kStageK) +
-         align_up(rows * KB * 4);
+         align_up(rows * KB * 4 + 12);
 }
 
 mx_status launch_grouped(const void* x, int64_t rows, const uint8_t* w, const void* ws, bool f32, bool act,
@@ -614,6 +675,7 @@ mx_status launch_grouped(const void* x, int64_t rows, const uint8_t* w, const vo
   g.k_div = make_div(static_cast<uint32_t>(k));
   g.rows = static_cast<int32_t>(rows);
   g.S = static_cast<int32_t>(S);
+  g.E = static_cast<int32_t>(E);
   g.N = static_cast<int32_t>(N);
   g.K = static_cast<int32_t>(K);
   g.KB = static_cast<int32_t>(KB);

@@ -62,9 +62,9 @@ def test_route(T, E, k, score, bias):
     _check_route(F.bf16_to_f64(lb), dev_u16(lb), k, b, score, False)
 
 
-@pytest.mark.parametrize("T", [16384, 16385, 40000])
+@pytest.mark.parametrize("T", [16384, 16385, 32769, 40000])
 def test_route_many_tokens(T):
-    """Chunks of more than 64 tokens (over 256 chunks of 64) and several LDS rounds of a chunk."""
+    """Both block lengths, and more blocks than workgroups of the grouping."""
     rng = np.random.default_rng(T)
     l = rng.standard_normal((T, 16)).astype(np.float32)
     say("route many", T)
@@ -88,6 +88,9 @@ def test_route_masks_nan_and_equal_logits(score, bias):
     l[8, :] = np.finfo(np.float32).min
     l[8, 5] = 1.0
     l[9, ::3] = -inf
+    l[10], l[11] = -5.0, -5.0                  # scores that FP32 cannot tell apart, few and many of them
+    l[10, :20] = 15.0 + 0.01 * rng.permutation(20)
+    l[11, :60] = 15.0 + 0.01 * rng.permutation(60)
     b = np.zeros(E, dtype=np.float32) if bias else None
     if bias:
         b[4], b[11], b[12] = np.nan, inf, -inf

@@ -33,15 +33,15 @@ def test_route_validation(dry):
     assert _route(bias=None) == mx.MX_OK
     assert _route(f32=0, logits=FAKE + 2) == mx.MX_OK                # BF16 logits
     assert _route(T=0, logits=None, ids=None, weights=None, row_slot=None, slot_row=None, ws=None, wb=0) == mx.MX_OK
-    assert _route(T=64, ws=None, wb=0) == mx.MX_OK                   # one chunk needs no workspace
+    assert _route(T=64, ws=None, wb=0) == mx.MX_OK                   # one block of tokens needs no workspace
     assert _route(E=1, k=1) == mx.MX_OK
     assert _route(E=1024, k=32) == mx.MX_OK
     need = mx.mx_moe_route_workspace_bytes(100, 64)
-    assert need == 2 * 64 * 4 and _route(wb=need) == mx.MX_OK
+    assert need == 4 * 64 * (8 + 1) and _route(wb=need) == mx.MX_OK
     for bad in (dict(f32=2), dict(E=0), dict(E=1025), dict(k=0), dict(k=65), dict(E=4, k=5), dict(k=33), dict(T=-1),
                 dict(T=1 << 30), dict(score=2), dict(renorm=2), dict(logits=None), dict(ids=None), dict(weights=None),
                 dict(offsets=None), dict(row_slot=None), dict(slot_row=None), dict(logits=FAKE + 2),
-                dict(offsets=FAKE + 2), dict(ws=None), dict(ws=FAKE + 2), dict(wb=need - 1), dict(bias=FAKE + 1)):
+                dict(offsets=FAKE + 2), dict(ws=None), dict(ws=FAKE + 4), dict(wb=need - 1), dict(bias=FAKE + 1)):
         assert _route(**bad) == mx.MX_ERR_INVALID_ARG, bad
         assert mx.lib().mx_last_error().decode()
 
