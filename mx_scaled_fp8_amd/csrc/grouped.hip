@@ -11,44 +11,28 @@
 //           as acc += P * (sa * sw), one fma per element and 128 K on the vector unit beside the matrix unit.
 //
 // Two launches:
-//  * quant_rows_kernel: every activation row once (not once per expert that reads it): codes [rows, Kp] and one 4-byte
-//    scale word per 128 K [rows, Kp / 128] (four E8M0 bytes, or one FP32) into the workspace, Kp = K rounded up to 128
-//    with zero codes behind K.  With act = SwiGLU it reads [gate | up] and rounds silu(gate) * up to BF16 first.  One
+//  * quant_rows_kernel: every activation row once (not once per expert that reads it): codes [KB, rows, 128] and one
+//    4-byte scale word per 128 K [rows, KB] (four E8M0 bytes, or one FP32) into the workspace, KB = K / 128 rounded up,
+//    with zero codes behind K.  The codes lie by K block first: row by row, the rows of a tile, a multiple of 512 bytes
+//    apart as a rule, would meet in a few of the memory channels at every stage.  With act = SwiGLU it reads [gate | up] and rounds silu(gate) * up to BF16 first.  One
 //    more workgroup turns the offsets into a list of row tiles.
 //  * grouped_gemm_kernel: one workgroup per BM x BN tile.  Rows of the activation are gathered by their index as the
 //    LDS-DMA reads them, so no copy per expert is written.
 #include <type_traits>
 
-#include "common.hpp"
+#include "grouped.hpp"
 
 namespace mx {
 
 namespace {
 
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef short v2s __attribute__((ext_vector_type(2)));
-typedef __attribute__((address_space(3))) void lds_void_t;
-
-constexpr int kStageK = 128;   // K per stage: one 128-byte line of every operand row
-
-// One row tile of an expert.
-struct RowTile {
-  int32_t expert;
-  int32_t first;       // list index of the expert's first row tile
-  int32_t count;       // row tiles of the expert
-  int32_t row_lo;      // the expert's rows
-  int32_t row_hi;
-  int32_t pad[3];
-};
-static_assert(sizeof(RowTile) == 32, "workspace layout");
-
 // ------------------------------------------------------------------ quantiser
 
 struct QuantRowsArgs {
   const uint16_t* x;          // BF16 [rows, K], or [rows, 2K] = gate | up
-  uint8_t* xq;                // [rows, Kp] e4m3 codes
+  uint8_t* xq;                // [KB, rows, 128] e4m3 codes
   uint32_t* xs;               // [rows, KB] scale words
   uint32_t rows, K, KB;
   uint32_t units;             // rows * KB
@@ -189,27 +173,11 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(QuantRowsArgs a) {
   }
   if (!finite) codes = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
   if (raw >= a.units) return;
-  *reinterpret_cast<uint2*>(a.xq + static_cast<size_t>(unit) * kStageK + l * 8) = codes;
+  *reinterpret_cast<uint2*>(a.xq + (static_cast<size_t>(kb) * a.rows + row) * kStageK + l * 8) = codes;
   if (l == 0) a.xs[unit] = word;
 }
 
 // ----------------------------------------------------------------------- GEMM
-
-// 16-byte chunk c of row r of a stage lies at chunk c ^ swz8(r): the 32 rows of an operand read in distinct banks
-__device__ __forceinline__ int swz8(int r) { return ((r >> 1) ^ ((r & 1) << 2)) & 7; }
-
-struct GemmArgs {
-  const uint8_t* xq;          // [rows, KB * 128] e4m3
-  const uint32_t* xs;         // [rows, KB] scale words
-  const uint8_t* w;           // [E, N, K] e4m3
-  const void* ws;             // E8M0 [E, N, K/32], or FP32 [E, ceil(N/128), KB]
-  uint16_t* out;              // [S, N] BF16
-  const RowTile* tiles;       // null: one group of S rows
-  const int32_t* row_slot;    // [S] or null: row r reads x row row_slot[r] / k
-  DivU32 k_div;
-  int32_t rows, S, E, N, K, KB;
-  int32_t n_tiles;
-};
 
 template <int HALF>
 __device__ __forceinline__ v16f mfma_mx(const v8i& w, const v8i& x, const v16f& c, uint32_t sw, uint32_t sx) {
@@ -291,9 +259,9 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
 
   // ---- DMA sources.  Instruction i of an operand moves 8 rows x 128 bytes: stage i / (rows / 8) of the super-stage,
   // rows 8 (i % (rows / 8)).. of the tile.  Where there are fewer instructions than waves some repeat another's.
-  const uint32_t Kp = static_cast<uint32_t>(KB) * kStageK;
+  const uint32_t slab = static_cast<uint32_t>(p.rows) * kStageK;   // bytes of a K block of the activation
   const __amdgpu_buffer_rsrc_t ares = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(p.xq), 0, static_cast<int>(static_cast<uint32_t>(p.rows) * Kp), kBufferFlags);
+      const_cast<uint8_t*>(p.xq), 0, static_cast<int>(static_cast<uint32_t>(KB) * slab), kBufferFlags);
   const __amdgpu_buffer_rsrc_t wres = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(p.w + (static_cast<size_t>(e) * p.N + n0) * p.K), 0, cols * p.K, kBufferFlags);
   uint32_t offA[APW], offW[WPW], chW[WPW];
@@ -303,7 +271,7 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
     const int i = (wave + u * NW) % A_INS, sub = i / (BM / 8), rg = i % (BM / 8);
     const int r = rg * 8 + (lane >> 3);
     // rows behind the tile's last are not fetched (an offset behind the resource): an MFMA's rows are independent
-    offA[u] = r < rows ? static_cast<uint32_t>(max(src_row[r], 0)) * Kp + ((lane & 7) ^ swz8(r)) * 16 : 0xFFFFFFF0u;
+    offA[u] = r < rows ? static_cast<uint32_t>(max(src_row[r], 0)) * kStageK + ((lane & 7) ^ swz8(r)) * 16 : 0xFFFFFFF0u;
     subA[u] = sub;
     ldsA[u] = sub * kSub + BN * kStageK + rg * 8 * kStageK;
   }
@@ -316,11 +284,18 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
     subW[u] = sub;
     ldsW[u] = sub * kSub + rg * 8 * kStageK;
   }
+  // The tiles start at different windows of K and go round: started at the same one, the workgroups read the same 512
+  // bytes of rows that lie a multiple of 256 bytes apart, which meet in a few memory channels.
+  constexpr int kWindow = 4 / WGK;                     // super-stages whose scales are brought together
+  const int windows = (KS + kWindow - 1) / kWindow;
+  const int turn = (mt + nt + e) % windows * kWindow;
+  auto turned = [&](int ks) { return ks + turn < KS ? ks + turn : ks + turn - KS; };   // ks < 2 KS - turn
   // Chunks of the weight at or behind K re-read the row's last one: the activation's codes there are zero.  A super-stage
   // behind the last is asked for all the same, at offsets behind the resources: nothing is fetched, and the number of
   // instructions in flight stays the same for every step.
   auto issue = [&](uint8_t* buf, int ks) {
     uint32_t behind = ks < KS ? 0u : 0xFFFFFFF0u;
+    ks = turned(ks);
     asm("" : "+s"(behind));                           // or-ed in: as a choice of offsets it became branches
 #pragma unroll
     for (int u = 0; u < WPW; ++u) {
@@ -332,7 +307,7 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
     for (int u = 0; u < APW; ++u) {
       const int kb = min(ks * WGK + subA[u], KB - 1);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ares, (lds_void_t*)(buf + ldsA[u]), 16, offA[u] | behind,
-                                               kb * kStageK, 0, 0);
+                                               static_cast<int>(static_cast<uint32_t>(kb) * slab), 0, 0);
     }
   };
 
@@ -363,7 +338,7 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
     }
   }
   auto load_scales = [&](int win) {
-    const int kb = min(4 * win, KB - 1);               // a window behind the last is never used
+    const int kb = 4 * win;
 #pragma unroll
     for (int u = 0; u < SPT; ++u) __builtin_memcpy(&own[u], rowp[u] + min(4 * kb, room[u]), 16);
     if constexpr (F32) {
@@ -376,7 +351,7 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
       }
     }
   };
-  auto store_scales = [&](int win) {
+  auto store_scales = [&](int win, int buf) {
     const int left = K32 - 16 * win;                   // 32-K blocks of the row from this window on
 #pragma unroll
     for (int u = 0; u < SPT; ++u) {
@@ -406,16 +381,16 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
         if constexpr (F32) {
 #pragma unroll
           for (int c = 0; c < kCB; ++c)
-            sc[win & 1][q][c * BM + t] = __float_as_uint(__uint_as_float(own[u].v[q]) * __uint_as_float(colw[c].v[q]));
+            sc[buf][q][c * BM + t] = __float_as_uint(__uint_as_float(own[u].v[q]) * __uint_as_float(colw[c].v[q]));
         } else {
-          sc[win & 1][q][t] = own[u].v[q];
+          sc[buf][q][t] = own[u].v[q];
         }
       }
     }
   };
-  // scale words of this wave's MFMA tiles for stage kb
-  auto read_scales = [&](int kb, uint32_t (&sw)[IT], uint32_t (&sx)[JT]) {
-    const uint32_t* const row = sc[(kb >> 2) & 1][kb & 3];
+  // scale words of this wave's MFMA tiles for stage q of the window in a buffer
+  auto read_scales = [&](int buf, int q, uint32_t (&sw)[IT], uint32_t (&sx)[JT]) {
+    const uint32_t* const row = sc[buf][q];
 #pragma unroll
     for (int j = 0; j < JT; ++j)
       sx[j] = row[(F32 ? wn * WTN / 128 * BM : BN) + wm * WTM + 32 * j + r32];
@@ -490,23 +465,29 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
 
   // ---- ring.  At the top of step ks its DMA and that of the STAGES - 2 super-stages behind it are in flight.
   issue(st0, 0);
-  load_scales(0);
+  int win = turn / kWindow, wbuf = 1;                  // window in use, and its buffer
+  load_scales(win);
   if constexpr (STAGES > 2) issue(st1, 1);
   auto step = [&](const uint8_t* buf, uint8_t* refill, int ks) {
-    const bool window = (ks * WGK) % 4 == 0;
+    const int at = turned(ks);
+    const bool window = at % kWindow == 0;
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(wait_vm_only((STAGES - 2) * kDma));
-    if (window) store_scales(ks * WGK / 4);
+    if (window) {
+      win = at / kWindow;
+      wbuf ^= 1;
+      store_scales(win, wbuf);
+    }
     __builtin_amdgcn_s_waitcnt(kWaitLgkmOnly);         // the scales are written; reads of the buffer before are done
     __builtin_amdgcn_s_barrier();                      // super-stage ks is in LDS; the buffer before it is free
     __builtin_amdgcn_sched_barrier(0);
     uint32_t sw[IT], sx[JT];
-    read_scales(ks * WGK + wk, sw, sx);
-    if (window) load_scales(ks * WGK / 4 + 1);
+    read_scales(wbuf, (at * WGK + wk) & 3, sw, sx);
+    if (window) load_scales(win + 1 < windows ? win + 1 : 0);
     __builtin_amdgcn_sched_barrier(0);                 // the loads go out before the DMA, and are waited for before it
     issue(refill, ks + STAGES - 1);
     __builtin_amdgcn_sched_barrier(0);
-    compute(buf, ks, sw, sx);
+    compute(buf, at, sw, sx);
     __builtin_amdgcn_sched_barrier(0);
   };
   if constexpr (STAGES == 2) {
@@ -681,7 +662,9 @@ mx_status launch_grouped(const void* x, int64_t rows, const uint8_t* w, const vo
   g.KB = static_cast<int32_t>(KB);
   g.n_tiles = static_cast<int32_t>((N + s.BN - 1) / s.BN);
   const int64_t total = (offsets ? mt : (S + s.BM - 1) / s.BM) * g.n_tiles;
-  if (f32)
+  if (!f32 && s.BM == 256 && offsets && KB >= kLargeMinStages)
+    launch_grouped_large(g, stream);
+  else if (f32)
     launch_gemm<true>(s, g, total, stream);
   else
     launch_gemm<false>(s, g, total, stream);

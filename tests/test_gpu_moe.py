@@ -195,7 +195,7 @@ def test_grouped_small(fmt, K, counts, N):
     _run_grouped(K + N, fmt, counts, N, K)
 
 
-@pytest.mark.parametrize("fmt,K", [("mx", 160), ("mx", 512), ("f32", 144), ("f32", 640)])
+@pytest.mark.parametrize("fmt,K", [("mx", 160), ("mx", 512), ("mx", 1056), ("mx", 1184), ("mx", 1280), ("f32", 144), ("f32", 640)])
 @pytest.mark.parametrize("act", [False, True])
 @pytest.mark.parametrize("counts,N", [([129, 300, 0, 131, 128], 4112), ([1025, 40, 257, 256], 4400), ([2600], 7696),
                                       ([700, 0, 1300, 257], 8208)])
