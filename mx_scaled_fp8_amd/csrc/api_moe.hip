@@ -124,8 +124,8 @@ mx_status grouped_sizes(const char* fn, int64_t rows, int64_t K, bool f32, int64
   const int64_t Kp = (K + 127) / 128 * 128;
   MX_CHECK(rows < (int64_t(1) << 31) && rows * Kp < (int64_t(1) << 32) - 256,
            "%s: rows * K = %lld x %lld too large for 32-bit row offsets", fn, (long long)rows, (long long)K);
-  // workgroups of the smallest tile
-  MX_CHECK((S / 32 + std::min(S, E)) * ((N + 63) / 64) < (int64_t(1) << 30), "%s: S = %lld x N = %lld too large", fn,
+  // 16-column units of the smallest tile's rows, which the kernels number with 31 bits
+  MX_CHECK((S / 32 + std::min(S, E)) * (N / 16) < (int64_t(1) << 31), "%s: S = %lld x N = %lld too large", fn,
            (long long)S, (long long)N);
   return MX_OK;
 }

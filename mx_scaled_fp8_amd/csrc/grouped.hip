@@ -12,8 +12,8 @@
 //
 // Two launches:
 //  * quant_rows_kernel: every activation row once (not once per expert that reads it): codes [KB, rows, 128] and one
-//    4-byte scale word per 128 K [rows, KB] (four E8M0 bytes, or one FP32) into the workspace, KB = K / 128 rounded up,
-//    with zero codes behind K.  The codes lie by K block first: row by row, the rows of a tile, a multiple of 512 bytes
+//    4-byte scale word per 128 K [rows, KB4] (four E8M0 bytes, or one FP32) into the workspace, KB = K / 128 rounded up,
+//    KB4 = KB rounded up to 4, with zero codes behind K.  The codes lie by K block first: row by row, the rows of a tile, a multiple of 512 bytes
 //    apart as a rule, would meet in a few of the memory channels at every stage.  With act = SwiGLU it reads [gate | up] and rounds silu(gate) * up to BF16 first.  One
 //    more workgroup turns the offsets into a list of row tiles.
 //  * grouped_gemm_kernel: one workgroup per BM x BN tile.  Rows of the activation are gathered by their index as the
@@ -28,12 +28,13 @@ namespace {
 
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef short v2s __attribute__((ext_vector_type(2)));
+typedef const __attribute__((address_space(4))) uint32_t* const_u32;   // read through the scalar cache
 // ------------------------------------------------------------------ quantiser
 
 struct QuantRowsArgs {
   const uint16_t* x;          // BF16 [rows, K], or [rows, 2K] = gate | up
   uint8_t* xq;                // [KB, rows, 128] e4m3 codes
-  uint32_t* xs;               // [rows, KB] scale words
+  uint32_t* xs;               // [rows, KB4] scale words, KB4 = KB rounded up to 4
   uint32_t rows, K, KB;
   uint32_t units;             // rows * KB
   DivU32 kb_div;
@@ -174,10 +175,12 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(QuantRowsArgs a) {
   if (!finite) codes = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
   if (raw >= a.units) return;
   *reinterpret_cast<uint2*>(a.xq + (static_cast<size_t>(kb) * a.rows + row) * kStageK + l * 8) = codes;
-  if (l == 0) a.xs[unit] = word;
+  if (l == 0) a.xs[row * ((a.KB + 3) & ~3u) + kb] = word;
 }
 
 // ----------------------------------------------------------------------- GEMM
+
+constexpr uint32_t kNone = 0xFFFFFFF0u;    // an offset behind every resource
 
 template <int HALF>
 __device__ __forceinline__ v16f mfma_mx(const v8i& w, const v8i& x, const v16f& c, uint32_t sw, uint32_t sx) {
@@ -218,8 +221,7 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   const int total_mt = p.tiles ? p.tiles[0].count : (p.S + BM - 1) / BM;
   const int total = total_mt * p.n_tiles;
   const int per_xcd = (total + 7) >> 3;
-  const int slot = blockIdx.x >> 3;
-  const int work = (blockIdx.x & 7) * per_xcd + slot;
+  const int slot = blockIdx.x >> 3, work = (blockIdx.x & 7) * per_xcd + slot;
   if (slot >= per_xcd || work >= total) return;
   int e = 0, row_lo = 0, row_hi = p.S, mt, nt;
   if (p.tiles) {
@@ -264,23 +266,29 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
       const_cast<uint8_t*>(p.xq), 0, static_cast<int>(static_cast<uint32_t>(KB) * slab), kBufferFlags);
   const __amdgpu_buffer_rsrc_t wres = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(p.w + (static_cast<size_t>(e) * p.N + n0) * p.K), 0, cols * p.K, kBufferFlags);
-  uint32_t offA[APW], offW[WPW], chW[WPW];
-  int ldsA[APW], ldsW[WPW], subA[APW], subW[WPW];
+  // The rows of an instruction are a scalar offset in the weight (a tile's rows begin at a multiple of 16, so a lane's chunk
+  // is the same for all of them), and gathered ones in the activation.
+  uint32_t offA[APW], noneW[WPW];
+  int ldsA[APW], ldsW[WPW], subA[APW], subW[WPW], rowW[WPW];
 #pragma unroll
   for (int u = 0; u < APW; ++u) {
     const int i = (wave + u * NW) % A_INS, sub = i / (BM / 8), rg = i % (BM / 8);
     const int r = rg * 8 + (lane >> 3);
     // rows behind the tile's last are not fetched (an offset behind the resource): an MFMA's rows are independent
-    offA[u] = r < rows ? static_cast<uint32_t>(max(src_row[r], 0)) * kStageK + ((lane & 7) ^ swz8(r)) * 16 : 0xFFFFFFF0u;
+    offA[u] = r < rows ? static_cast<uint32_t>(max(src_row[r], 0)) * kStageK + ((lane & 7) ^ swz8(r)) * 16 : kNone;
     subA[u] = sub;
     ldsA[u] = sub * kSub + BN * kStageK + rg * 8 * kStageK;
   }
+  static_assert(NW % 2 == 0 && BN % 16 == 0, "every instruction of a wave begins at the same row of 16");
+  const uint32_t dmaW = static_cast<uint32_t>(lane >> 3) * static_cast<uint32_t>(p.K);
+  const uint32_t chW = ((lane & 7) ^ swz8((wave & 1) * 8 + (lane >> 3))) * 16;
 #pragma unroll
   for (int u = 0; u < WPW; ++u) {
     const int i = (wave + u * NW) % W_INS, sub = i / (BN / 8), rg = i % (BN / 8);
-    const int r = rg * 8 + (lane >> 3);
-    offW[u] = static_cast<uint32_t>(min(r, cols - 1)) * static_cast<uint32_t>(p.K);
-    chW[u] = ((lane & 7) ^ swz8(r)) * 16;
+    // so are columns behind the tile's last (the bounds are checked against the bytes less the scalar offset, which must
+    // not exceed them)
+    rowW[u] = rg * 8 < cols ? rg * 8 * p.K : 0;
+    noneW[u] = rg * 8 < cols ? 0u : kNone;
     subW[u] = sub;
     ldsW[u] = sub * kSub + rg * 8 * kStageK;
   }
@@ -294,14 +302,14 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   // behind the last is asked for all the same, at offsets behind the resources: nothing is fetched, and the number of
   // instructions in flight stays the same for every step.
   auto issue = [&](uint8_t* buf, int ks) {
-    uint32_t behind = ks < KS ? 0u : 0xFFFFFFF0u;
+    uint32_t behind = ks < KS ? 0u : kNone;
     ks = turned(ks);
     asm("" : "+s"(behind));                           // or-ed in: as a choice of offsets it became branches
 #pragma unroll
     for (int u = 0; u < WPW; ++u) {
-      const uint32_t k = min(static_cast<uint32_t>((ks * WGK + subW[u]) * kStageK) + chW[u],
-                             static_cast<uint32_t>(p.K - 16));
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wres, (lds_void_t*)(buf + ldsW[u]), 16, (offW[u] + k) | behind, 0, 0, 0);
+      const uint32_t k = min(static_cast<uint32_t>((ks * WGK + subW[u]) * kStageK) + chW, static_cast<uint32_t>(p.K - 16));
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wres, (lds_void_t*)(buf + ldsW[u]), 16, (dmaW + k) | noneW[u] | behind,
+                                               rowW[u], 0, 0);
     }
 #pragma unroll
     for (int u = 0; u < APW; ++u) {
@@ -321,8 +329,8 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   struct Words { uint32_t v[4]; };
   Words own[SPT], colw[F32 ? kCB : 1];
   // A thread's row of scale words, 4 bytes a stage for either operand.  A window is one 16-byte load, unconditional, so
-  // that nothing waits for it before it is stored a window later.  It may reach behind the row: behind the last x row
-  // lies workspace, and a W row's load is moved back to end with the tensor (`back` bytes, undone when it is stored).
+  // that nothing waits for it before it is stored a window later.  An x row is whole windows; a W row's load may reach behind the
+  // row, and is moved back to end with the tensor (`back` bytes, undone when it is stored).
   const uint8_t* rowp[SPT];
   int room[SPT];                                       // bytes from the row's begin to the last place a load may start
 #pragma unroll
@@ -333,7 +341,7 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
       rowp[u] = static_cast<const uint8_t*>(p.ws) + row * K32;
       room[u] = static_cast<int>(min(static_cast<size_t>(p.E) * p.N * K32 - row * K32, static_cast<size_t>(1) << 30)) - 16;
     } else {
-      rowp[u] = reinterpret_cast<const uint8_t*>(p.xs + static_cast<size_t>(max(src_row[F32 ? t : t - BN], 0)) * KB);
+      rowp[u] = reinterpret_cast<const uint8_t*>(p.xs + static_cast<size_t>(max(src_row[F32 ? t : t - BN], 0)) * ((KB + 3) & ~3));
       room[u] = 1 << 30;
     }
   }
@@ -344,10 +352,10 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
     if constexpr (F32) {
 #pragma unroll
       for (int c = 0; c < kCB; ++c) {
-        const float* src = static_cast<const float*>(p.ws) +
-                           (static_cast<size_t>(e) * NB + min(n0 / 128 + c, NB - 1)) * KB + kb;
+        const const_u32 src = (const_u32)(uintptr_t)(static_cast<const uint32_t*>(p.ws) +
+                                                     (static_cast<size_t>(e) * NB + min(n0 / 128 + c, NB - 1)) * KB + kb);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) colw[c].v[q] = __float_as_uint(src[min(q, KB - 1 - kb)]);
+        for (int q = 0; q < 4; ++q) colw[c].v[q] = src[min(q, KB - 1 - kb)];
       }
     }
   };
@@ -421,24 +429,40 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   auto compute = [&](const uint8_t* buf, int ks, const uint32_t (&sw)[IT], const uint32_t (&sx)[JT]) {
     if (!has_rows || ks * WGK + wk >= KB) return;
     if constexpr (F32) {
-      v8i fw[IT][2];
-#pragma unroll
-      for (int i = 0; i < IT; ++i) {
+      // A tile's fma's are issued under the next one's MFMAs, and the reads of the next x rows between two MFMAs (the order
+      // in the source let one wait for the other: @ORD@).
+      v8i fw[IT][2], fx[2][2];
+      v16f part[2];
+      auto read_w = [&](int i) {
         fw[i][0] = frag(buf + rdW + 32 * i * kStageK, 0);
         fw[i][1] = frag(buf + rdW + 32 * i * kStageK, 1);
+      };
+      auto read_x = [&](int j) {
+        fx[j & 1][0] = frag(buf + rdA + 32 * j * kStageK, 0);
+        fx[j & 1][1] = frag(buf + rdA + 32 * j * kStageK, 1);
+      };
+      auto add = [&](int t) {
+        const float s = __uint_as_float(sx[t / IT]);
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          acc[t % IT][t / IT][r] = __builtin_fmaf(part[t & 1][r], s, acc[t % IT][t / IT][r]);
+      };
+      read_w(0);
+      read_x(0);
+#pragma unroll
+      for (int t = 0; t < IT * JT; ++t) {
+        const int i = t % IT, j = t / IT;
+        __builtin_amdgcn_sched_barrier(0);
+        part[t & 1] = mfma_mx<0>(fw[i][0], fx[j & 1][0], v16f{}, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        if (j == 0 && i + 1 < IT) read_w(i + 1);
+        if (i == IT - 1 && j + 1 < JT) read_x(j + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        part[t & 1] = mfma_mx<0>(fw[i][1], fx[j & 1][1], part[t & 1], 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        __builtin_amdgcn_sched_barrier(0);
+        if (t > 0) add(t - 1);
       }
-#pragma unroll
-      for (int j = 0; j < JT; ++j) {
-        const v8i f0 = frag(buf + rdA + 32 * j * kStageK, 0), f1 = frag(buf + rdA + 32 * j * kStageK, 1);
-        const float s = __uint_as_float(sx[j]);
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          v16f part = mfma_mx<0>(fw[i][0], f0, v16f{}, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-          part = mfma_mx<0>(fw[i][1], f1, part, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-#pragma unroll
-          for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(part[r], s, acc[i][j][r]);
-        }
-      }
+      __builtin_amdgcn_sched_barrier(0);
+      add(IT * JT - 1);
     } else {
       // lane group q passes block 2 half + q of the stage: byte 0 (half 0) or 2 (half 1) of the word moved down by q
       uint32_t swq[IT], sxq[JT];
@@ -567,13 +591,20 @@ struct Shape {
   int BM, BN;
 };
 
+// The tile for S rows of E groups, by the rows of an average group (the groups' sizes are known on the device alone).
+// Measured on one MI355X, whole calls, us:
+//   <= 32 rows: grouped_stream.hip.
+//   More: 128 x 128 with two workgroups per compute unit, whose pauses cover each other (48 rows a group, 32 groups, N =
+//   5120, K = 2304: 98; 64 x 128 with three 106, 128 x 256 with one 109), unless that leaves compute units without a
+//   tile: then 64 x 64 with the waves split over K (777 rows, N = 1040, K = 4112, FP32 scales: 22; 128 x 128: 38).
+//   256 x 256 from 160 rows on where those tiles fill the chip (8192 rows, N = 5120, K = 4096, FP32 scales: 237; 128 x
+//   128: 271, 128 x 256: 239).
 Shape pick_shape(int64_t S, int64_t E, int64_t N) {
   const int64_t per = (S + E - 1) / E;
   if (per <= 32) return {32, 64};
-  if (per <= 64) return {64, 128};
   auto tiles = [&](int64_t bm, int64_t bn) { return (S / bm + (S < E ? S : E)) * ((N + bn - 1) / bn); };
-  if (per <= 160 || tiles(256, 256) < 256) return tiles(128, 256) < 256 ? Shape{64, 128} : Shape{128, 256};
-  return {256, 256};
+  if (per > 160 && tiles(256, 256) >= 256) return {256, 256};
+  return tiles(128, 128) >= 256 ? Shape{128, 128} : Shape{64, 64};
 }
 
 int64_t max_row_tiles(int64_t S, int64_t E, int BM) { return S / BM + (S < E ? S : E); }
@@ -582,17 +613,15 @@ size_t align_up(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
 template <bool F32>
 void launch_gemm(const Shape s, const GemmArgs& a, int64_t tiles, hipStream_t stream) {
-  const unsigned grid = static_cast<unsigned>((tiles + 7) / 8 * 8);
-  if (s.BM == 32)
-    grouped_gemm_kernel<F32, 32, 64, 1, 2, 4, 3><<<grid, 512, 0, stream>>>(a);
-  else if (s.BM == 64)
-    grouped_gemm_kernel<F32, 64, 128, 1, 4, 2, 3><<<grid, 512, 0, stream>>>(a);
+  const unsigned per_xcd = static_cast<unsigned>((tiles + 7) / 8);
+  if (s.BM == 64)
+    grouped_gemm_kernel<F32, 64, 64, 1, 2, 4, 2><<<8 * per_xcd, 512, 0, stream>>>(a);
   else if (s.BM == 128)
-    grouped_gemm_kernel<F32, 128, 256, 2, 4, 1, 3><<<grid, 512, 0, stream>>>(a);
+    grouped_gemm_kernel<F32, 128, 128, 2, 2, 1, 2><<<8 * per_xcd, 256, 0, stream>>>(a);
   else if constexpr (F32)
-    grouped_gemm_kernel<F32, 256, 256, 2, 4, 1, 2><<<grid, 512, 0, stream>>>(a);
+    grouped_gemm_kernel<F32, 256, 256, 2, 4, 1, 2><<<8 * per_xcd, 512, 0, stream>>>(a);
   else
-    grouped_gemm_kernel<F32, 256, 256, 2, 2, 1, 2><<<grid, 256, 0, stream>>>(a);
+    grouped_gemm_kernel<F32, 256, 256, 2, 2, 1, 2><<<8 * per_xcd, 256, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -602,7 +631,7 @@ size_t grouped_workspace_bytes(int64_t rows, int64_t S, int64_t E, int64_t N, in
   const int64_t KB = (K + kStageK - 1) / kStageK;
   const Shape s = pick_shape(S, E, N);
   return align_up(sizeof(RowTile) * (1 + max_row_tiles(S, E, s.BM))) + align_up(rows * KB * kStageK) +
-         align_up(rows * KB * 4 + 12);
+         align_up(rows * ((KB + 3) / 4 * 4) * 4);
 }
 
 mx_status launch_grouped(const void* x, int64_t rows, const uint8_t* w, const void* ws, bool f32, bool act,
@@ -660,9 +689,12 @@ mx_status launch_grouped(const void* x, int64_t rows, const uint8_t* w, const vo
   g.N = static_cast<int32_t>(N);
   g.K = static_cast<int32_t>(K);
   g.KB = static_cast<int32_t>(KB);
+  g.wg_per_xcd = device_cu_count() >= 8 ? device_cu_count() / 8 : 1;
   g.n_tiles = static_cast<int32_t>((N + s.BN - 1) / s.BN);
   const int64_t total = (offsets ? mt : (S + s.BM - 1) / s.BM) * g.n_tiles;
-  if (!f32 && s.BM == 256 && offsets && KB >= kLargeMinStages)
+  if (s.BM == 32)
+    launch_grouped_stream(f32, g, stream);
+  else if (s.BM == 256 && !f32 && offsets && KB >= kLargeMinStages)
     launch_grouped_large(g, stream);
   else if (f32)
     launch_gemm<true>(s, g, total, stream);

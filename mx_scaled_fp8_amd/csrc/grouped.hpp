@@ -27,19 +27,24 @@ __device__ __forceinline__ int swz8(int r) { return ((r >> 1) ^ ((r & 1) << 2)) 
 
 struct GemmArgs {
   const uint8_t* xq;          // [KB, rows, 128] e4m3
-  const uint32_t* xs;         // [rows, KB] scale words
+  const uint32_t* xs;         // [rows, KB4] scale words, KB4 = KB rounded up to 4
   const uint8_t* w;           // [E, N, K] e4m3
   const void* ws;             // E8M0 [E, N, K/32], or FP32 [E, ceil(N/128), KB]
   uint16_t* out;              // [S, N] BF16
   const RowTile* tiles;       // null: one group of S rows
   const int32_t* row_slot;    // [S] or null: row r reads x row row_slot[r] / k
   DivU32 k_div;
+  DivU32 nu_div;              // columns in units (grouped_stream.hip)
   int32_t rows, S, E, N, K, KB;
   int32_t n_tiles;
+  int32_t wg_per_xcd;         // compute units of an XCD
 };
 
 // The 256 x 256 MXFP8 kernel (grouped_large.hip): K of at least kLargeMinStages stages.
 constexpr int kLargeMinStages = 8;
 void launch_grouped_large(const GemmArgs& a, hipStream_t stream);
+
+// Row tiles of 32 rows (grouped_stream.hip).
+void launch_grouped_stream(bool f32, const GemmArgs& a, hipStream_t stream);
 
 }  // namespace mx

@@ -66,7 +66,7 @@ struct Tile {
   int turn;                                // the pair of stages it starts at
 };
 
-__device__ __forceinline__ void grouped_large(const GemmArgs& p, int wg_per_xcd) {
+__device__ __forceinline__ void grouped_large(const GemmArgs& p) {
   __shared__ __attribute__((aligned(1024))) uint8_t st0[2 * kOp];
   __shared__ __attribute__((aligned(1024))) uint8_t st1[2 * kOp];
   // scale words of two windows of four stages: [stage][block][W | x][half of the tile][row % 32], a byte per 32-row tile
@@ -91,7 +91,7 @@ __device__ __forceinline__ void grouped_large(const GemmArgs& p, int wg_per_xcd)
   const int total = list[2] * p.n_tiles;               // tiles[0].count
   const int per_xcd = (total + 7) >> 3;
   auto tile_at = [&](int r, Tile& t) {
-    const int li = (slot + r * 11) % wg_per_xcd + r * wg_per_xcd;
+    const int li = (slot + r * 11) % p.wg_per_xcd + r * p.wg_per_xcd;
     const int work = xcd * per_xcd + li;
     if (li >= per_xcd || work >= total) return false;
     const const_i32 d = list + 8 * (1 + work / p.n_tiles);
@@ -117,7 +117,7 @@ __device__ __forceinline__ void grouped_large(const GemmArgs& p, int wg_per_xcd)
     const bool bad = row < 0 || row >= p.rows;
     const uint32_t at = bad ? 0u : static_cast<uint32_t>(row);
     xq_off = r < t.rows ? at * kStageK : kNoRow;
-    xs_off = bad ? 0xFFFFFFFFu : at * static_cast<uint32_t>(KB) * 4;
+    xs_off = bad ? 0xFFFFFFFFu : at * static_cast<uint32_t>((KB + 3) & ~3) * 4;
   };
 
   // ---- DMA: wave `wave` fills rows it*32 + wave*8 + lane/8 of each operand, lane i -> physical chunk i % 8
@@ -478,16 +478,14 @@ __device__ __forceinline__ void grouped_large(const GemmArgs& p, int wg_per_xcd)
   __builtin_amdgcn_s_waitcnt(wait_vm(0));              // no DMA outlives the workgroup
 }
 
-__global__ __launch_bounds__(256, 1) void grouped_large_kernel(GemmArgs p, int wg_per_xcd) {
-  grouped_large(p, wg_per_xcd);
+__global__ __launch_bounds__(256, 1) void grouped_large_kernel(GemmArgs p) {
+  grouped_large(p);
 }
 
 }  // namespace
 
 void launch_grouped_large(const GemmArgs& a, hipStream_t stream) {
-  const int cus = device_cu_count();
-  const int wg_per_xcd = cus >= 8 ? cus / 8 : 1;
-  grouped_large_kernel<<<8 * wg_per_xcd, 256, 0, stream>>>(a, wg_per_xcd);
+  grouped_large_kernel<<<8 * a.wg_per_xcd, 256, 0, stream>>>(a);
 }
 
 }  // namespace mx

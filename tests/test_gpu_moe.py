@@ -218,6 +218,15 @@ def test_grouped_gathers_router_slots(fmt, T, E, k, N, K):
     _close(host_u16(out), M.grouped_linear(x, w, ws, off.cpu().numpy(), rs.cpu().numpy(), k))
 
 
+@pytest.mark.parametrize("fmt,K", [("mx", 288), ("mx", 384), ("f32", 272), ("f32", 384)])
+@pytest.mark.parametrize("counts,N", [([5, 0, 31, 9], 8208), ([60, 3, 64, 0, 40], 8208), ([100, 128, 70], 8208),
+                                      ([1] * 64, 2320), ([200, 10, 90, 0, 300, 65], 5136)])
+def test_grouped_shares_of_many_columns(fmt, K, counts, N):
+    """Enough columns that a workgroup's share holds several tiles, begins inside a block of 128 columns and ends in
+    another expert's, with groups of several row tiles."""
+    _run_grouped(3 * K + N, fmt, counts, N, K)
+
+
 @pytest.mark.parametrize("fmt", ["mx", "f32"])
 def test_grouped_bad_slots_and_nonfinite_inputs(fmt):
     def spoil(x, w, ws, slots):
@@ -297,7 +306,7 @@ def test_grouped_equal_tokens_are_equal(fmt):
 # ---------------------------------------------------------------- block 128
 
 @pytest.mark.parametrize("Mr,N,K", [(1, 16, 16), (1, 5120, 2304), (2, 144, 144), (17, 272, 1040), (33, 1024, 4096),
-                                    (64, 4096, 576), (65, 80, 2304), (129, 1040, 4112), (513, 2064, 272),
+                                    (64, 4096, 576), (65, 80, 2304), (129, 1040, 4112), (30, 16400, 144), (100, 16400, 272), (513, 2064, 272),
                                     (2100, 2320, 272), (4200, 5136, 144)])
 def test_block128(Mr, N, K):
     rng = np.random.default_rng(Mr + N + K)
