@@ -292,18 +292,13 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
     subW[u] = sub;
     ldsW[u] = sub * kSub + rg * 8 * kStageK;
   }
-  // The tiles start at different windows of K and go round: started at the same one, the workgroups read the same 512
-  // bytes of rows that lie a multiple of 256 bytes apart, which meet in a few memory channels.
   constexpr int kWindow = 4 / WGK;                     // super-stages whose scales are brought together
   const int windows = (KS + kWindow - 1) / kWindow;
-  const int turn = (mt + nt + e) % windows * kWindow;
-  auto turned = [&](int ks) { return ks + turn < KS ? ks + turn : ks + turn - KS; };   // ks < 2 KS - turn
   // Chunks of the weight at or behind K re-read the row's last one: the activation's codes there are zero.  A super-stage
   // behind the last is asked for all the same, at offsets behind the resources: nothing is fetched, and the number of
   // instructions in flight stays the same for every step.
   auto issue = [&](uint8_t* buf, int ks) {
     uint32_t behind = ks < KS ? 0u : kNone;
-    ks = turned(ks);
     asm("" : "+s"(behind));                           // or-ed in: as a choice of offsets it became branches
 #pragma unroll
     for (int u = 0; u < WPW; ++u) {
@@ -329,26 +324,30 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   struct Words { uint32_t v[4]; };
   Words own[SPT], colw[F32 ? kCB : 1];
   // A thread's row of scale words, 4 bytes a stage for either operand.  A window is one 16-byte load, unconditional, so
-  // that nothing waits for it before it is stored a window later.  An x row is whole windows; a W row's load may reach behind the
-  // row, and is moved back to end with the tensor (`back` bytes, undone when it is stored).
-  const uint8_t* rowp[SPT];
-  int room[SPT];                                       // bytes from the row's begin to the last place a load may start
+  // that nothing waits for it before it is stored a window later.  An x row is whole windows; a W row's load may reach
+  // behind the row, and is moved back to end with the tensor (undone when it is stored).
+  const size_t wrow = static_cast<size_t>(e) * p.N + n0;               // the tile's first W row
+  const uint8_t* const wsp = static_cast<const uint8_t*>(p.ws) + wrow * K32;
+  const uint32_t room = F32 ? 0 : static_cast<uint32_t>(min((static_cast<size_t>(p.E) * p.N - wrow) * K32,
+                                                            static_cast<size_t>(1) << 31)) - 16;   // last place of a load
+  uint32_t soff[SPT];                                                  // the row's offset from wsp, or from xs
 #pragma unroll
   for (int u = 0; u < SPT; ++u) {
     const int t = min(tid + u * 64 * NW, kScOwn - 1);
-    if (!F32 && t < BN) {
-      const size_t row = static_cast<size_t>(e) * p.N + n0 + min(t, cols - 1);
-      rowp[u] = static_cast<const uint8_t*>(p.ws) + row * K32;
-      room[u] = static_cast<int>(min(static_cast<size_t>(p.E) * p.N * K32 - row * K32, static_cast<size_t>(1) << 30)) - 16;
-    } else {
-      rowp[u] = reinterpret_cast<const uint8_t*>(p.xs + static_cast<size_t>(max(src_row[F32 ? t : t - BN], 0)) * ((KB + 3) & ~3));
-      room[u] = 1 << 30;
-    }
+    if (!F32 && t < BN)
+      soff[u] = static_cast<uint32_t>(min(t, cols - 1)) * static_cast<uint32_t>(K32);
+    else
+      soff[u] = static_cast<uint32_t>(max(src_row[F32 ? t : t - BN], 0)) * static_cast<uint32_t>((KB + 3) & ~3) * 4;
   }
   auto load_scales = [&](int win) {
     const int kb = 4 * win;
+    const uint8_t* const xsp = reinterpret_cast<const uint8_t*>(p.xs);
 #pragma unroll
-    for (int u = 0; u < SPT; ++u) __builtin_memcpy(&own[u], rowp[u] + min(4 * kb, room[u]), 16);
+    for (int u = 0; u < SPT; ++u) {
+      const uint32_t at = soff[u] + static_cast<uint32_t>(16 * win);
+      const bool is_w = !F32 && tid + u * 64 * NW < BN;
+      __builtin_memcpy(&own[u], is_w ? wsp + min(at, room) : xsp + at, 16);
+    }
     if constexpr (F32) {
 #pragma unroll
       for (int c = 0; c < kCB; ++c) {
@@ -365,8 +364,8 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
     for (int u = 0; u < SPT; ++u) {
       const int t = tid + u * 64 * NW;
       if constexpr (!F32) {
-        const int back = 16 * win - room[u];
-        if (back > 0) {                                // the tensor's last rows
+        const int back = static_cast<int>(soff[u] + static_cast<uint32_t>(16 * win) - room);
+        if (t < BN && back > 0) {                      // the tensor's last rows
           uint64_t v[2];
           __builtin_memcpy(v, &own[u], 16);
           const int sh = 8 * back;
@@ -414,12 +413,14 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
 #pragma unroll
     for (int j = 0; j < JT; ++j) acc[i][j] = v16f{};
 
-  const int rdW = wk * kSub + (wn * WTN + r32) * kStageK;
-  const int rdA = wk * kSub + BN * kStageK + (wm * WTM + r32) * kStageK;
+  // A lane's 16-byte chunks of a row, 4 half + q and 4 half + q + 2, at chunk ^ sz: their places differ in bits 5 and 6
+  // alone.
   const int sz = swz8(r32);
+  const int rd0 = wk * kSub + r32 * kStageK + ((q2 ^ sz) << 4);
+  const int rdW = wn * WTN * kStageK, rdA = (BN + wm * WTM) * kStageK;
   auto frag = [&](const uint8_t* base, int half) {
-    const uint4 lo = *reinterpret_cast<const uint4*>(base + (((4 * half + q2) ^ sz) << 4));
-    const uint4 hi = *reinterpret_cast<const uint4*>(base + (((4 * half + q2 + 2) ^ sz) << 4));
+    const uint4 lo = *reinterpret_cast<const uint4*>(base + (rd0 ^ (64 * half)));
+    const uint4 hi = *reinterpret_cast<const uint4*>(base + (rd0 ^ (64 * half + 32)));
     v8i v;
     v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
     v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
@@ -489,29 +490,24 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
 
   // ---- ring.  At the top of step ks its DMA and that of the STAGES - 2 super-stages behind it are in flight.
   issue(st0, 0);
-  int win = turn / kWindow, wbuf = 1;                  // window in use, and its buffer
-  load_scales(win);
+  load_scales(0);
   if constexpr (STAGES > 2) issue(st1, 1);
   auto step = [&](const uint8_t* buf, uint8_t* refill, int ks) {
-    const int at = turned(ks);
-    const bool window = at % kWindow == 0;
+    const int win = ks / kWindow, wbuf = win & 1;
+    const bool window = ks % kWindow == 0;
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(wait_vm_only((STAGES - 2) * kDma));
-    if (window) {
-      win = at / kWindow;
-      wbuf ^= 1;
-      store_scales(win, wbuf);
-    }
+    if (window) store_scales(win, wbuf);
     __builtin_amdgcn_s_waitcnt(kWaitLgkmOnly);         // the scales are written; reads of the buffer before are done
     __builtin_amdgcn_s_barrier();                      // super-stage ks is in LDS; the buffer before it is free
     __builtin_amdgcn_sched_barrier(0);
     uint32_t sw[IT], sx[JT];
-    read_scales(wbuf, (at * WGK + wk) & 3, sw, sx);
-    if (window) load_scales(win + 1 < windows ? win + 1 : 0);
+    read_scales(wbuf, (ks * WGK + wk) & 3, sw, sx);
+    if (window) load_scales(min(win + 1, windows - 1));
     __builtin_amdgcn_sched_barrier(0);                 // the loads go out before the DMA, and are waited for before it
     issue(refill, ks + STAGES - 1);
     __builtin_amdgcn_sched_barrier(0);
-    compute(buf, at, sw, sx);
+    compute(buf, ks, sw, sx);
     __builtin_amdgcn_sched_barrier(0);
   };
   if constexpr (STAGES == 2) {
