@@ -188,6 +188,10 @@ __device__ __forceinline__ v16f mfma_mx(const v8i& w, const v8i& x, const v16f& 
                                                          static_cast<int>(sx));
 }
 
+// Whether the tiles of a last, mostly empty round are cut into parts.
+template <bool F32, int BM>
+constexpr bool kParts = F32 && BM == 256;
+
 // WGM x WGN waves share a BM (rows) x BN (columns) tile; with WGK > 1 that many sets of them each take every WGK-th
 // stage and their sums meet in LDS at the end.  STAGES super-stages of WGK x 128 K in LDS.
 //
@@ -221,8 +225,28 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   const int total_mt = p.tiles ? p.tiles[0].count : (p.S + BM - 1) / BM;
   const int total = total_mt * p.n_tiles;
   const int per_xcd = (total + 7) >> 3;
-  const int slot = blockIdx.x >> 3, work = (blockIdx.x & 7) * per_xcd + slot;
-  if (slot >= per_xcd || work >= total) return;
+  const int first_work = (blockIdx.x & 7) * per_xcd, mine = min(per_xcd, total - first_work);
+  int slot = blockIdx.x >> 3;
+  // Tiles of 256 rows come one to a compute unit, in rounds.  Where the last round would leave half of the compute units
+  // idle, or three quarters, its tiles are cut into two or four parts of fewer rows, with fewer MFMAs for every wave (640
+  // tiles on 256 compute units, K = 4096: 223 -> 213 us; 576 tiles: 223 -> 217.  Halves that leave every second wave
+  // without rows gained nothing).
+  int part = 0, parts = 1;
+  if constexpr (kParts<F32, BM>) {
+    const int rem = mine > 0 ? mine % p.wg_per_xcd : 0, cut = mine - rem;
+    if (4 * rem <= p.wg_per_xcd)
+      parts = 4;
+    else if (2 * rem <= p.wg_per_xcd)
+      parts = 2;
+    if (slot >= cut) {
+      part = (slot - cut) & (parts - 1);
+      slot = cut + (slot - cut) / parts;
+    } else {
+      parts = 1;
+    }
+  }
+  if (slot >= mine) return;
+  const int work = first_work + slot;
   int e = 0, row_lo = 0, row_hi = p.S, mt, nt;
   if (p.tiles) {
     const RowTile t = p.tiles[1 + work / p.n_tiles];
@@ -239,14 +263,17 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   }
   mt = __builtin_amdgcn_readfirstlane(mt);
   nt = __builtin_amdgcn_readfirstlane(nt);
-  const int row0 = row_lo + mt * BM, n0 = nt * BN;
-  const int rows = min(BM, row_hi - row0), cols = min(BN, p.N - n0);
+  const int bm = BM / __builtin_amdgcn_readfirstlane(parts);           // rows of the tile, or of its part
+  const int row0 = row_lo + mt * BM + __builtin_amdgcn_readfirstlane(part) * bm, n0 = nt * BN;
+  const int rows = min(bm, row_hi - row0), cols = min(BN, p.N - n0);
+  if (rows <= 0) return;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave % WGN, wm = (wave / WGN) % WGM, wk = wave / (WGN * WGM);
   const int r32 = lane & 31, q2 = lane >> 5;
   const int KB = p.KB, KS = (KB + WGK - 1) / WGK;
+  const int wtm = kParts<F32, BM> ? bm / WGM : WTM, jt = wtm / 32;     // a wave's rows, and their MFMA tiles
 
   for (int r = tid; r < BM; r += 64 * NW) {
     const int rr = row0 + min(r, rows - 1);            // rows behind the tile's last re-read it
@@ -400,7 +427,7 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
     const uint32_t* const row = sc[buf][q];
 #pragma unroll
     for (int j = 0; j < JT; ++j)
-      sx[j] = row[(F32 ? wn * WTN / 128 * BM : BN) + wm * WTM + 32 * j + r32];
+      sx[j] = row[(F32 ? wn * WTN / 128 * BM : BN) + wm * wtm + 32 * j + r32];
     if constexpr (!F32) {
 #pragma unroll
       for (int i = 0; i < IT; ++i) sw[i] = row[wn * WTN + 32 * i + r32];
@@ -417,7 +444,7 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   // alone.
   const int sz = swz8(r32);
   const int rd0 = wk * kSub + r32 * kStageK + ((q2 ^ sz) << 4);
-  const int rdW = wn * WTN * kStageK, rdA = (BN + wm * WTM) * kStageK;
+  const int rdW = wn * WTN * kStageK, rdA = (BN + wm * wtm) * kStageK;
   auto frag = [&](const uint8_t* base, int half) {
     const uint4 lo = *reinterpret_cast<const uint4*>(base + (rd0 ^ (64 * half)));
     const uint4 hi = *reinterpret_cast<const uint4*>(base + (rd0 ^ (64 * half + 32)));
@@ -426,12 +453,13 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
     v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
     return v;
   };
-  const bool has_rows = wm * WTM < rows && wn * WTN < cols;   // a wave without output of its own only moves data
-  auto compute = [&](const uint8_t* buf, int ks, const uint32_t (&sw)[IT], const uint32_t (&sx)[JT]) {
+  const bool has_rows = wm * wtm < rows && wn * WTN < cols;   // a wave without output of its own only moves data
+  // over the wave's first J row tiles
+  auto compute = [&](auto J, const uint8_t* buf, int ks, const uint32_t (&sw)[IT], const uint32_t (&sx)[JT]) {
     if (!has_rows || ks * WGK + wk >= KB) return;
     if constexpr (F32) {
-      // A tile's fma's are issued under the next one's MFMAs, and the reads of the next x rows between two MFMAs (the order
-      // in the source let one wait for the other: @ORD@).
+      // A tile's fma's are issued under the next one's MFMAs, and the reads of the next x rows between two MFMAs (one
+      // after the other: 245 us against 228 at 16384 rows, N = 2304, K = 4096).
       v8i fw[IT][2], fx[2][2];
       v16f part[2];
       auto read_w = [&](int i) {
@@ -448,22 +476,23 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
         for (int r = 0; r < 16; ++r)
           acc[t % IT][t / IT][r] = __builtin_fmaf(part[t & 1][r], s, acc[t % IT][t / IT][r]);
       };
+      constexpr int n = decltype(J)::value;
       read_w(0);
       read_x(0);
 #pragma unroll
-      for (int t = 0; t < IT * JT; ++t) {
+      for (int t = 0; t < IT * n; ++t) {
         const int i = t % IT, j = t / IT;
         __builtin_amdgcn_sched_barrier(0);
         part[t & 1] = mfma_mx<0>(fw[i][0], fx[j & 1][0], v16f{}, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
         if (j == 0 && i + 1 < IT) read_w(i + 1);
-        if (i == IT - 1 && j + 1 < JT) read_x(j + 1);
+        if (i == IT - 1 && j + 1 < n) read_x(j + 1);
         __builtin_amdgcn_sched_barrier(0);
         part[t & 1] = mfma_mx<0>(fw[i][1], fx[j & 1][1], part[t & 1], 0x7F7F7F7Fu, 0x7F7F7F7Fu);
         __builtin_amdgcn_sched_barrier(0);
         if (t > 0) add(t - 1);
       }
       __builtin_amdgcn_sched_barrier(0);
-      add(IT * JT - 1);
+      add(IT * n - 1);
     } else {
       // lane group q passes block 2 half + q of the stage: byte 0 (half 0) or 2 (half 1) of the word moved down by q
       uint32_t swq[IT], sxq[JT];
@@ -492,36 +521,44 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   issue(st0, 0);
   load_scales(0);
   if constexpr (STAGES > 2) issue(st1, 1);
-  auto step = [&](const uint8_t* buf, uint8_t* refill, int ks) {
-    const int win = ks / kWindow, wbuf = win & 1;
-    const bool window = ks % kWindow == 0;
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(wait_vm_only((STAGES - 2) * kDma));
-    if (window) store_scales(win, wbuf);
-    __builtin_amdgcn_s_waitcnt(kWaitLgkmOnly);         // the scales are written; reads of the buffer before are done
-    __builtin_amdgcn_s_barrier();                      // super-stage ks is in LDS; the buffer before it is free
-    __builtin_amdgcn_sched_barrier(0);
-    uint32_t sw[IT], sx[JT];
-    read_scales(wbuf, (ks * WGK + wk) & 3, sw, sx);
-    if (window) load_scales(min(win + 1, windows - 1));
-    __builtin_amdgcn_sched_barrier(0);                 // the loads go out before the DMA, and are waited for before it
-    issue(refill, ks + STAGES - 1);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(buf, ks, sw, sx);
-    __builtin_amdgcn_sched_barrier(0);
+  auto ring = [&](auto J) {
+    auto step = [&](const uint8_t* buf, uint8_t* refill, int ks) {
+      const int win = ks / kWindow, wbuf = win & 1;
+      const bool window = ks % kWindow == 0;
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(wait_vm_only((STAGES - 2) * kDma));
+      if (window) store_scales(win, wbuf);
+      __builtin_amdgcn_s_waitcnt(kWaitLgkmOnly);         // the scales are written; reads of the buffer before are done
+      __builtin_amdgcn_s_barrier();                      // super-stage ks is in LDS; the buffer before it is free
+      __builtin_amdgcn_sched_barrier(0);
+      uint32_t sw[IT], sx[JT];
+      read_scales(wbuf, (ks * WGK + wk) & 3, sw, sx);
+      if (window) load_scales(min(win + 1, windows - 1));
+      __builtin_amdgcn_sched_barrier(0);                 // the loads go out before the DMA, and are waited for before it
+      issue(refill, ks + STAGES - 1);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(J, buf, ks, sw, sx);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    if constexpr (STAGES == 2) {
+      for (int ks = 0; ks < KS; ks += 2) {
+        step(st0, st1, ks);
+        if (ks + 1 < KS) step(st1, st0, ks + 1);
+      }
+    } else {
+      for (int ks = 0; ks < KS; ks += 3) {
+        step(st0, st2, ks);
+        if (ks + 1 < KS) step(st1, st0, ks + 1);
+        if (ks + 2 < KS) step(st2, st1, ks + 2);
+      }
+    }
   };
-  if constexpr (STAGES == 2) {
-    for (int ks = 0; ks < KS; ks += 2) {
-      step(st0, st1, ks);
-      if (ks + 1 < KS) step(st1, st0, ks + 1);
-    }
-  } else {
-    for (int ks = 0; ks < KS; ks += 3) {
-      step(st0, st2, ks);
-      if (ks + 1 < KS) step(st1, st0, ks + 1);
-      if (ks + 2 < KS) step(st2, st1, ks + 2);
-    }
-  }
+  if (!kParts<F32, BM> || jt == JT)
+    ring(std::integral_constant<int, JT>{});
+  else if (jt == JT / 2)
+    ring(std::integral_constant<int, (JT + 1) / 2>{});
+  else
+    ring(std::integral_constant<int, (JT + 3) / 4>{});
 
   __builtin_amdgcn_s_waitcnt(wait_vm_only(0));         // no DMA outlives the tile or meets the sums below
 
@@ -555,7 +592,8 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   // register pair leaves lane l columns 16 p .. 16 p + 7 and lane l + 32 columns 16 p + 8 .. 16 p + 15.
 #pragma unroll
   for (int j = 0; j < JT; ++j) {
-    const int m = wm * WTM + 32 * j + r32;
+    if (kParts<F32, BM> && j >= jt) break;
+    const int m = wm * wtm + 32 * j + r32;
     const bool bad = src_row[m] < 0;
     uint16_t* const orow = p.out + static_cast<size_t>(row0 + m) * p.N;
 #pragma unroll
@@ -615,7 +653,8 @@ void launch_gemm(const Shape s, const GemmArgs& a, int64_t tiles, hipStream_t st
   else if (s.BM == 128)
     grouped_gemm_kernel<F32, 128, 128, 2, 2, 1, 2><<<8 * per_xcd, 256, 0, stream>>>(a);
   else if constexpr (F32)
-    grouped_gemm_kernel<F32, 256, 256, 2, 4, 1, 2><<<8 * per_xcd, 512, 0, stream>>>(a);
+    // up to one more round of parts
+    grouped_gemm_kernel<F32, 256, 256, 2, 4, 1, 2><<<8 * (per_xcd + a.wg_per_xcd), 512, 0, stream>>>(a);
   else
     grouped_gemm_kernel<F32, 256, 256, 2, 2, 1, 2><<<8 * per_xcd, 256, 0, stream>>>(a);
 }

@@ -195,6 +195,13 @@ def test_grouped_small(fmt, K, counts, N):
     _run_grouped(K + N, fmt, counts, N, K)
 
 
+@pytest.mark.parametrize("fmt", ["mx", "f32"])
+@pytest.mark.parametrize("counts,N", [([2600], 6656), ([2343, 7], 6944), ([0, 2560, 0], 9472)])
+def test_grouped_last_round(fmt, counts, N):
+    """Counts of 256-row tiles a little, a quarter and a half above what the compute units hold at once."""
+    _run_grouped(N, fmt, counts, N, 160 if fmt == "mx" else 272)
+
+
 @pytest.mark.parametrize("fmt,K", [("mx", 160), ("mx", 512), ("mx", 1056), ("mx", 1184), ("mx", 1280), ("f32", 144), ("f32", 640)])
 @pytest.mark.parametrize("act", [False, True])
 @pytest.mark.parametrize("counts,N", [([129, 300, 0, 131, 128], 4112), ([1025, 40, 257, 256], 4400), ([2600], 7696),
