@@ -357,8 +357,8 @@ mx_status mx_linear_noalloc(const void* x, int64_t M, int64_t K, const void* w,
  *          16-byte aligned: the quantised x, written before it is read.  Calls
  *          that may overlap need one each.
  * Requires: M >= 0 (0 is a no-op), N, K >= 16, N % 16 == 0, K % 16 == 0,
- * K < 2^22, M * (K rounded up to 128) < 2^32, x, w and out 16-byte aligned,
- * w_scale 4-byte aligned; out overlaps no input and not the workspace.
+ * K < 2^22, M * (K rounded up to 128) < 2^32, (M/128 + 1) * ceil(N/128) < 2^23 - 512,
+ * x, w and out 16-byte aligned, w_scale 4-byte aligned; out overlaps no input and not the workspace.
  */
 size_t mx_linear_block128_workspace_bytes(int64_t M, int64_t N, int64_t K);
 mx_status mx_linear_block128(const void* x, int64_t M, int64_t K, const uint8_t* w,
@@ -428,9 +428,9 @@ mx_status mx_moe_route(const void* logits, int32_t logits_f32, const float* bias
  *          before they are read.  Calls that may overlap need one each.
  * Requires: S >= 0 (0 is a no-op), rows >= 1 for S > 0, E >= 1, k >= 1,
  * N, K >= 16, N % 16 == 0, K % 32 == 0 (E8M0) or K % 16 == 0 (FP32), K < 2^22,
- * rows * (K rounded up to 128) < 2^32, S < 2^31, E < 2^20, x, w and out 16-byte
- * aligned, FP32 scales, offsets and row_slot 4-byte aligned; out overlaps no
- * input and not the workspace.
+ * rows * (K rounded up to 128) < 2^32, S < 2^31, E < 2^20, (S/128 + min(S, E)) *
+ * ceil(N/128) < 2^23 - 512, x, w and out 16-byte aligned, FP32 scales, offsets and
+ * row_slot 4-byte aligned; out overlaps no input and not the workspace.
  */
 size_t mx_grouped_linear_workspace_bytes(int64_t rows, int64_t S, int64_t E, int64_t N, int64_t K);
 mx_status mx_grouped_linear(const void* x, int64_t rows, int64_t K, const uint8_t* w,
@@ -450,7 +450,7 @@ mx_status mx_grouped_linear(const void* x, int64_t rows, int64_t K, const uint8_
  * A slot whose row is outside [0, rows) (a dropped token) or whose weight is 0
  * adds nothing, whatever y holds.
  * Requires: T >= 0 (0 is a no-op), N >= 8, N % 8 == 0, 1 <= k <= 1024, rows >= 0
- * and < 2^31, T * N < 2^39, y, shared and out 16-byte, slot_row and weights
+ * and < 2^31, T * N <= 2^35 - 2048, y, shared and out 16-byte, slot_row and weights
  * 4-byte aligned.
  */
 mx_status mx_moe_combine(const void* y, int64_t rows, int64_t N, const int32_t* slot_row,

@@ -68,7 +68,9 @@ mx_status mx_moe_combine(const void* y, int64_t rows, int64_t N, const int32_t* 
   MX_CHECK(N >= 8 && N % 8 == 0 && N < (int64_t(1) << 31), "%s: N = %lld is not a positive multiple of 8", fn,
            (long long)N);
   MX_CHECK(k >= 1 && k <= 1024, "%s: k = %d (1 to 1024)", fn, k);
-  MX_CHECK(T < (int64_t(1) << 31) && T * N < (int64_t(1) << 39), "%s: T * N too large", fn);
+  // a thread takes 8 elements, and a launch is below 2^32 threads
+  MX_CHECK(T < (int64_t(1) << 31) && T * N <= (int64_t(1) << 35) - 2048, "%s: T = %lld x N = %lld too large", fn,
+           (long long)T, (long long)N);
   if (T == 0) { clear_error(); return MX_OK; }
   MX_CHECK((y || rows == 0) && slot_row && weights && out, "%s: null tensor pointer", fn);
   MX_CHECK(aligned(y, 16) && aligned(shared, 16) && aligned(out, 16) && aligned(slot_row, 4) && aligned(weights, 4),
@@ -124,8 +126,9 @@ mx_status grouped_sizes(const char* fn, int64_t rows, int64_t K, bool f32, int64
   const int64_t Kp = (K + 127) / 128 * 128;
   MX_CHECK(rows < (int64_t(1) << 31) && rows * Kp < (int64_t(1) << 32) - 256,
            "%s: rows * K = %lld x %lld too large for 32-bit row offsets", fn, (long long)rows, (long long)K);
-  // 16-column units of the smallest tile's rows, which the kernels number with 31 bits
-  MX_CHECK((S / 32 + std::min(S, E)) * (N / 16) < (int64_t(1) << 31), "%s: S = %lld x N = %lld too large", fn,
+  // A launch of the tiles (256 threads for 128 x 128, 512 for 256 x 256) is below 2^32 threads, and the 32 x 16 units that
+  // the smallest tiles are cut into are numbered with 31 bits.
+  MX_CHECK((S / 128 + std::min(S, E)) * ((N + 127) / 128) < (int64_t(1) << 23) - 512, "%s: S = %lld x N = %lld too large", fn,
            (long long)S, (long long)N);
   return MX_OK;
 }

@@ -451,6 +451,44 @@ def test_layer_on_two_streams():
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("fmt", ["mx", "f32"])
+@pytest.mark.parametrize("rows", [3, 300, 600])
+def test_grouped_weight_behind_4_gb(fmt, rows):
+    """The last expert's weight lies behind 2^32 bytes: its last columns equal those of an expert of their own, for 32-,
+    128- and 256-row tiles.  x is 0 or +-448 (one power of two as its scale, or 1), the codes are +-1 and +-2 and the
+    weight's scales powers of two within 2^3 of each other: every sum is an integer below 448 * 2^20 in steps of 448, exact
+    in any order."""
+    E, N, K = 3, 65552, 23040
+    say("grouped behind 4 GB", fmt, rows)
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    w = torch.randint(0, 4, (E, N, K), generator=gen, dtype=torch.uint8, device="cuda")
+    w = (w & 1).mul_(8).add_(0x38).bitwise_or_((w & 2).mul_(64))
+    if fmt == "mx":
+        ws = torch.randint(124, 128, (E, N, K // 32), generator=gen, dtype=torch.uint8, device="cuda")
+    else:
+        ws = 2.0 ** torch.randint(-3, 1, (E, -(-N // 128), K // 128), generator=gen, device="cuda").float()
+    x = (448 * torch.randint(-1, 2, (rows, K), generator=gen, device="cuda")).bfloat16()
+    out = mx.mx_grouped_linear(x, w, ws, _i32([0, 0, 0, rows]))
+    n0 = N - 272
+    part = mx.mx_grouped_linear(x, w[2, n0:].contiguous()[None], ws[2:, n0 if fmt == "mx" else n0 // 128:].contiguous(),
+                                _i32([0, rows]))
+    torch.cuda.synchronize()
+    assert part.abs().max() > 0 and torch.equal(out[:, n0:], part)
+
+
+def test_combine_behind_4_gb():
+    """Rows of y and out behind 2^32 bytes and 2^31 elements."""
+    T, N = 70001, 32768
+    say("combine behind 4 GB")
+    y = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    y.copy_((torch.arange(T, device="cuda") % 251).bfloat16()[:, None].expand(T, N))
+    row = torch.arange(T, dtype=torch.int32, device="cuda").flip(0)[:, None].contiguous()
+    out = mx.mx_moe_combine(y, row, torch.full((T, 1), 2.0, device="cuda"))
+    torch.cuda.synchronize()
+    for t in (0, 1, 32767, 32768, 65535, 65536, T - 1):
+        assert (out[t] == 2 * ((T - 1 - t) % 251)).all(), t
+
+
 def test_launch_counters():
     mx.mx_reset_counters()
     off = _i32([0, 4])

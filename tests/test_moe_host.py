@@ -68,7 +68,7 @@ def test_grouped_validation(dry):
                 dict(offsets=None), dict(out=None), dict(x=FAKE + 8), dict(w=BIG + 4), dict(out=2 * BIG + 8),
                 dict(kind=1, ws=FAKE + 2), dict(offsets=FAKE + 2), dict(row_slot=FAKE + 1), dict(work=None),
                 dict(work=FAKE + 8), dict(wb=need - 1), dict(out=BIG + 512), dict(out=FAKE),
-                dict(S=(1 << 31) - 1, N=1 << 20)):
+                dict(S=(1 << 31) - 1, N=1 << 20), dict(S=1 << 29, N=256), dict(S=1 << 28, N=512)):
         assert _grouped(**bad) == mx.MX_ERR_INVALID_ARG, bad
         assert mx.lib().mx_last_error().decode()
 
@@ -102,7 +102,7 @@ def test_combine_validation(dry):
     for bad in (dict(T=-1), dict(rows=-1), dict(rows=1 << 31), dict(N=0), dict(N=12), dict(k=0), dict(k=1025),
                 dict(y=None), dict(slot_row=None), dict(weights=None), dict(out=None), dict(y=FAKE + 8),
                 dict(out=2 * BIG + 2), dict(shared=BIG + 8), dict(slot_row=FAKE + 2), dict(out=FAKE + 1024),
-                dict(out=BIG + 1024), dict(T=1 << 30, N=1 << 10)):
+                dict(out=BIG + 1024), dict(T=1 << 30, N=1 << 10), dict(T=1 << 30, N=32)):
         assert f(**bad) == mx.MX_ERR_INVALID_ARG, bad
 
 
