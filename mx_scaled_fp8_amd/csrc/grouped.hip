@@ -188,9 +188,9 @@ __device__ __forceinline__ v16f mfma_mx(const v8i& w, const v8i& x, const v16f& 
                                                          static_cast<int>(sx));
 }
 
-// Whether the tiles of a last, mostly empty round are cut into parts.
-template <bool F32, int BM>
-constexpr bool kParts = F32 && BM == 256;
+// Tiles of 256 rows take fewer MFMAs where they have fewer rows.
+template <int BM>
+constexpr bool kParts = BM == 256;
 
 // WGM x WGN waves share a BM (rows) x BN (columns) tile; with WGK > 1 that many sets of them each take every WGK-th
 // stage and their sums meet in LDS at the end.  STAGES super-stages of WGK x 128 K in LDS.
@@ -232,7 +232,7 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   // tiles on 256 compute units, K = 4096: 223 -> 213 us; 576 tiles: 223 -> 217.  Halves that leave every second wave
   // without rows gained nothing).
   int part = 0, parts = 1;
-  if constexpr (kParts<F32, BM>) {
+  if constexpr (kParts<BM>) {
     const int rem = mine > 0 ? mine % p.wg_per_xcd : 0, cut = mine - rem;
     if (4 * rem <= p.wg_per_xcd)
       parts = 4;
@@ -273,7 +273,7 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   const int wn = wave % WGN, wm = (wave / WGN) % WGM, wk = wave / (WGN * WGM);
   const int r32 = lane & 31, q2 = lane >> 5;
   const int KB = p.KB, KS = (KB + WGK - 1) / WGK;
-  const int wtm = kParts<F32, BM> ? bm / WGM : WTM, jt = wtm / 32;     // a wave's rows, and their MFMA tiles
+  const int jt = kParts<BM> ? (rows + 32 * WGM - 1) / (32 * WGM) : JT, wtm = 32 * jt;   // a wave's MFMA tiles, its rows
 
   for (int r = tid; r < BM; r += 64 * NW) {
     const int rr = row0 + min(r, rows - 1);            // rows behind the tile's last re-read it
@@ -457,6 +457,7 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   // over the wave's first J row tiles
   auto compute = [&](auto J, const uint8_t* buf, int ks, const uint32_t (&sw)[IT], const uint32_t (&sx)[JT]) {
     if (!has_rows || ks * WGK + wk >= KB) return;
+    constexpr int n = decltype(J)::value;
     if constexpr (F32) {
       // A tile's fma's are issued under the next one's MFMAs, and the reads of the next x rows between two MFMAs (one
       // after the other: 245 us against 228 at 16384 rows, N = 2304, K = 4096).
@@ -476,7 +477,6 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
         for (int r = 0; r < 16; ++r)
           acc[t % IT][t / IT][r] = __builtin_fmaf(part[t & 1][r], s, acc[t % IT][t / IT][r]);
       };
-      constexpr int n = decltype(J)::value;
       read_w(0);
       read_x(0);
 #pragma unroll
@@ -502,13 +502,13 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
       for (int j = 0; j < JT; ++j) sxq[j] = sx[j] >> (8 * q2);
       auto half = [&](auto H) {
         constexpr int h = decltype(H)::value;
-        v8i fw[IT], fx[JT];
+        v8i fw[IT], fx[n];
 #pragma unroll
         for (int i = 0; i < IT; ++i) fw[i] = frag(buf + rdW + 32 * i * kStageK, h);
 #pragma unroll
-        for (int j = 0; j < JT; ++j) fx[j] = frag(buf + rdA + 32 * j * kStageK, h);
+        for (int j = 0; j < n; ++j) fx[j] = frag(buf + rdA + 32 * j * kStageK, h);
 #pragma unroll
-        for (int j = 0; j < JT; ++j)
+        for (int j = 0; j < n; ++j)
 #pragma unroll
           for (int i = 0; i < IT; ++i) acc[i][j] = mfma_mx<h>(fw[i], fx[j], acc[i][j], swq[i], sxq[j]);
       };
@@ -553,12 +553,19 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
       }
     }
   };
-  if (!kParts<F32, BM> || jt == JT)
+  if constexpr (kParts<BM>) {
+    static_assert(JT == 4, "the cases");
+    if (jt == 1)
+      ring(std::integral_constant<int, 1>{});
+    else if (jt == 2)
+      ring(std::integral_constant<int, 2>{});
+    else if (jt == 3)
+      ring(std::integral_constant<int, 3>{});
+    else
+      ring(std::integral_constant<int, 4>{});
+  } else {
     ring(std::integral_constant<int, JT>{});
-  else if (jt == JT / 2)
-    ring(std::integral_constant<int, (JT + 1) / 2>{});
-  else
-    ring(std::integral_constant<int, (JT + 3) / 4>{});
+  }
 
   __builtin_amdgcn_s_waitcnt(wait_vm_only(0));         // no DMA outlives the tile or meets the sums below
 
@@ -592,7 +599,7 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   // register pair leaves lane l columns 16 p .. 16 p + 7 and lane l + 32 columns 16 p + 8 .. 16 p + 15.
 #pragma unroll
   for (int j = 0; j < JT; ++j) {
-    if (kParts<F32, BM> && j >= jt) break;
+    if (kParts<BM> && j >= jt) break;
     const int m = wm * wtm + 32 * j + r32;
     const bool bad = src_row[m] < 0;
     uint16_t* const orow = p.out + static_cast<size_t>(row0 + m) * p.N;
@@ -652,11 +659,8 @@ void launch_gemm(const Shape s, const GemmArgs& a, int64_t tiles, hipStream_t st
     grouped_gemm_kernel<F32, 64, 64, 1, 2, 4, 2><<<8 * per_xcd, 512, 0, stream>>>(a);
   else if (s.BM == 128)
     grouped_gemm_kernel<F32, 128, 128, 2, 2, 1, 2><<<8 * per_xcd, 256, 0, stream>>>(a);
-  else if constexpr (F32)
-    // up to one more round of parts
+  else                                                 // and up to one more round of parts
     grouped_gemm_kernel<F32, 256, 256, 2, 4, 1, 2><<<8 * (per_xcd + a.wg_per_xcd), 512, 0, stream>>>(a);
-  else
-    grouped_gemm_kernel<F32, 256, 256, 2, 2, 1, 2><<<8 * per_xcd, 256, 0, stream>>>(a);
 }
 
 }  // namespace
