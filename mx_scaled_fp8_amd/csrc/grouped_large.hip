@@ -23,6 +23,13 @@
 //    built four stages (a window) at a time, 8 bytes per row and thread, transposed with v_perm, one window ahead.
 //  * K need not be a multiple of 128: the weight's chunks behind K re-read the row's last one, whose products with the
 //    activation's zero codes vanish, and scale bytes behind K are cleared.
+//
+// Measured (one MI355X, whole calls): 65536 rows of 32 groups of about 2048, N = 4608, K = 5120: 1460 us, 2.1 PFLOP/s;
+// with groups of exactly 2048 rows 1330 (a group's last, ragged tile takes a whole tile's time).  What bounds it is the way
+// of the operands to LDS as much as the MFMAs: a 256 x 256 tile takes 64 KiB per 128 K, and a kernel of such tiles took
+// 1285 us for the DMA alone (580 when every tile reads the same lines) and 1130 without any.  Half of the L2's requests
+// miss.  Where tiles begin in K decides what they share there: turned by the row tile, so that the tiles that read the same
+// activation rows are at the same K, 1460; by row and column tile 1490, by the column tile 1505, not at all 1490.
 #include <type_traits>
 
 #include "grouped.hpp"
@@ -85,13 +92,13 @@ __device__ __forceinline__ void grouped_large(const GemmArgs& p) {
   const int pairs = KE / 2;
 
   // ---- tiles of this workgroup: every XCD takes a contiguous range of the list, its workgroups one tile of each round
-  // of wg_per_xcd tiles, rotated by 11 from round to round so that no compute unit leads in all of them
+  // of wg_per_xcd tiles, rotated by 8 from round to round so that no compute unit leads in all of them
   const const_i32 list = (const_i32)(uintptr_t)p.tiles;
   const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
   const int total = list[2] * p.n_tiles;               // tiles[0].count
   const int per_xcd = (total + 7) >> 3;
   auto tile_at = [&](int r, Tile& t) {
-    const int li = (slot + r * 11) % p.wg_per_xcd + r * p.wg_per_xcd;
+    const int li = (slot + r * 8) % p.wg_per_xcd + r * p.wg_per_xcd;
     const int work = xcd * per_xcd + li;
     if (li >= per_xcd || work >= total) return false;
     const const_i32 d = list + 8 * (1 + work / p.n_tiles);
@@ -101,7 +108,7 @@ __device__ __forceinline__ void grouped_large(const GemmArgs& p) {
     t.rows = uniform(min(kT, d[4] - t.row0));
     t.n0 = uniform(local / count * kT);
     t.cols = uniform(min(kT, p.N - t.n0));
-    t.turn = uniform((local % count + local / count) % pairs);
+    t.turn = uniform(local % count % pairs);
     return true;
   };
   // rows of round r only: where a workgroup's rounds have a gap there are no later tiles either (li grows with r)

@@ -17,8 +17,12 @@
 //    the blocks before (sums of the masks' bit counts), plus the bits below t in its own block's mask.  So the rows of
 //    an expert are in slot order, and nothing is placed by the order of atomics.
 // A single block does the second's work in the first launch.
+// Measured (one MI355X, kernel times): 4 tokens, 64 experts, k = 6, BF16 logits: 4 us.  8192 tokens, 256 experts, k = 8,
+// sigmoid with a bias: 12 and 6 us; the logits alone would take 2.  The rest is the scores (FP64 only for experts that an
+// FP32 bound leaves in question: 83 us for all of them), k rounds of maxima, and the masks' way through memory.
 //
-// Join.  out[t] = shared[t] + sum_j w[t, j] * y[slot_row[t, j]] in FP32, rounded once; bound by HBM.
+// Join.  out[t] = shared[t] + sum_j w[t, j] * y[slot_row[t, j]] in FP32, rounded once; bound by HBM: 8192 tokens, k = 8,
+// N = 5120 (839 MB) 140 us, 6.0 TB/s, with the loads of eight rows in flight and past the caches (one row at a time 186).
 #include "common.hpp"
 
 namespace mx {
