@@ -454,6 +454,22 @@ def _workspace(ws, need, like):
     return ws, _dev(ws, "workspace"), ws.numel() * ws.element_size()
 
 
+def _result(t, name, shape, dtype, like, dtypes=None):
+    """(tensor, pointer) of an output on the device of `like`: a new one, or the caller's, of any shape with as many
+    elements.  A new one needs none of the checks, which take longer than a small call's kernel."""
+    if t is None:
+        t = like.new_empty(shape, dtype=dtype)
+        return t, t.data_ptr()
+    if dtypes is not None:
+        _dtype(t, dtypes, name)
+    n = 1
+    for d in shape:
+        n *= d
+    _numel(t, n, name)
+    _same_device(like, (name, t))
+    return t, _dev(t, name, dtype.itemsize)
+
+
 # torch.cuda.current_stream() builds a Stream object, 2 us of a call that takes 6; the handle alone is a lookup
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -482,11 +498,9 @@ def mx_linear_block128(x, w, w_scale, out=None, workspace=None):
     _dtype(x, _BF16, "x")
     _dtype(w_scale, (torch.float32,), "w_scale")
     _shape(w_scale, (-(-N // MX_BLOCK128), -(-K // MX_BLOCK128)), "w_scale")
-    _numel(out, M * N, "out")
-    _same_device(x, ("w", w), ("w_scale", w_scale), ("out", out), ("workspace", workspace))
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    args = (_dev(x, "x", 2), M, K, _dev(w, "w", 1), _dev(w_scale, "w_scale", 4), N, _dev(out, "out", 2))
+    _same_device(x, ("w", w), ("w_scale", w_scale), ("workspace", workspace))
+    out, op = _result(out, "out", (M, N), torch.bfloat16, x)
+    args = (_dev(x, "x", 2), M, K, _dev(w, "w", 1), _dev(w_scale, "w_scale", 4), N, op)
     workspace, wp, wb = _workspace(workspace, mx_linear_block128_workspace_bytes(M, N, K), x)
     _on_device(lib().mx_linear_block128, x, *args, wp, wb)
     return out
@@ -508,35 +522,20 @@ def mx_moe_route(logits, k, bias=None, score=MX_ROUTE_SOFTMAX, renormalize=True,
     T, E = logits.shape
     _dtype(logits, (torch.float32,) + _BF16, "logits")
     _dtype(bias, (torch.float32,), "bias")
-    _dtype(weights, (torch.float32,), "weights")
-    for name, t in (("ids", ids), ("offsets", offsets), ("row_slot", row_slot), ("slot_row", slot_row)):
-        _dtype(t, (torch.int32,), name)
     if k < 1:
         raise ValueError(f"k = {k} must be positive")
     _numel(bias, E, "bias")
-    _numel(ids, T * k, "ids")
-    _numel(weights, T * k, "weights")
-    _numel(offsets, E + 1, "offsets")
-    _numel(row_slot, T * k, "row_slot")
-    _numel(slot_row, T * k, "slot_row")
-    _same_device(logits, ("bias", bias), ("ids", ids), ("weights", weights), ("offsets", offsets),
-                 ("row_slot", row_slot), ("slot_row", slot_row), ("workspace", workspace))
-    lp = _dev(logits, "logits")
-    bp = _dev(bias, "bias", 4) if bias is not None else None
-    if ids is None:
-        ids = logits.new_empty((T, k), dtype=torch.int32)
-    if weights is None:
-        weights = logits.new_empty((T, k), dtype=torch.float32)
-    if offsets is None:
-        offsets = logits.new_empty(E + 1, dtype=torch.int32)
-    if row_slot is None:
-        row_slot = logits.new_empty(T * k, dtype=torch.int32)
-    if slot_row is None:
-        slot_row = logits.new_empty((T, k), dtype=torch.int32)
+    _same_device(logits, ("bias", bias), ("workspace", workspace))
+    i32, f32 = torch.int32, torch.float32
+    ids, ip = _result(ids, "ids", (T, k), i32, logits, (i32,))
+    weights, gp = _result(weights, "weights", (T, k), f32, logits, (f32,))
+    offsets, op = _result(offsets, "offsets", (E + 1,), i32, logits, (i32,))
+    row_slot, rp = _result(row_slot, "row_slot", (T * k,), i32, logits, (i32,))
+    slot_row, sp = _result(slot_row, "slot_row", (T, k), i32, logits, (i32,))
     workspace, wp, wb = _workspace(workspace, mx_moe_route_workspace_bytes(T, E), logits)
-    _on_device(lib().mx_moe_route, logits, lp, int(logits.dtype == torch.float32), bp, T, E, k, score,
-               int(bool(renormalize)), scale, _dev(ids, "ids", 4), _dev(weights, "weights", 4),
-               _dev(offsets, "offsets", 4), _dev(row_slot, "row_slot", 4), _dev(slot_row, "slot_row", 4), wp, wb)
+    _on_device(lib().mx_moe_route, logits, _dev(logits, "logits"), int(logits.dtype == f32),
+               _dev(bias, "bias", 4) if bias is not None else None, T, E, k, score, int(bool(renormalize)), scale, ip, gp,
+               op, rp, sp, wp, wb)
     return ids, weights, offsets, row_slot, slot_row
 
 
@@ -566,14 +565,11 @@ def mx_grouped_linear(x, w, w_scale, offsets, row_slot=None, k=1, act=MX_ACT_NON
         _dtype(t, (torch.int32,), name)
     _numel(offsets, E + 1, "offsets")
     S = rows if row_slot is None else row_slot.numel()
-    _numel(out, S * N, "out")
-    _same_device(x, ("w", w), ("w_scale", w_scale), ("offsets", offsets), ("row_slot", row_slot), ("out", out),
+    _same_device(x, ("w", w), ("w_scale", w_scale), ("offsets", offsets), ("row_slot", row_slot),
                  ("workspace", workspace))
-    if out is None:
-        out = torch.empty((S, N), dtype=torch.bfloat16, device=x.device)
+    out, op = _result(out, "out", (S, N), torch.bfloat16, x)
     args = (_dev(x, "x", 2), rows, K, _dev(w, "w", 1), _dev(w_scale, "w_scale"), kind, E, N,
-            _dev(offsets, "offsets", 4), _dev(row_slot, "row_slot", 4) if row_slot is not None else None, k, S, act,
-            _dev(out, "out", 2))
+            _dev(offsets, "offsets", 4), _dev(row_slot, "row_slot", 4) if row_slot is not None else None, k, S, act, op)
     workspace, wp, wb = _workspace(workspace, mx_grouped_linear_workspace_bytes(rows, S, E, N, K), x)
     _on_device(lib().mx_grouped_linear, x, *args, wp, wb)
     return out
@@ -592,12 +588,10 @@ def mx_moe_combine(y, slot_row, weights, shared=None, out=None):
     _dtype(weights, (torch.float32,), "weights")
     _shape(weights, (T, k), "weights")
     _numel(shared, T * N, "shared")
-    _numel(out, T * N, "out")
-    _same_device(y, ("slot_row", slot_row), ("weights", weights), ("shared", shared), ("out", out))
-    if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=y.device)
+    _same_device(y, ("slot_row", slot_row), ("weights", weights), ("shared", shared))
+    out, op = _result(out, "out", (T, N), torch.bfloat16, y)
     args = (_dev(y, "y", 2), rows, N, _dev(slot_row, "slot_row", 4), _dev(weights, "weights", 4), T, k,
-            _dev(shared, "shared", 2) if shared is not None else None, _dev(out, "out", 2))
+            _dev(shared, "shared", 2) if shared is not None else None, op)
     _on_device(lib().mx_moe_combine, y, *args)
     return out
 
