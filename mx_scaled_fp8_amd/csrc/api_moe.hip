@@ -95,20 +95,22 @@ namespace {
 
 // Argument checks shared by mx_grouped_linear and mx_linear_block128: `rows` rows of x, S of out.
 mx_status grouped_check(const char* fn, const void* x, int64_t rows, int64_t x_width, int64_t K, const void* w,
-                        const void* w_scale, bool f32, int64_t E, int64_t N, int64_t S, const void* out, const void* workspace,
-                        size_t workspace_bytes, size_t need) {
+                        const void* w_scale, bool f32, const int32_t* offsets, const int32_t* row_slot, int64_t E,
+                        int64_t N, int64_t S, const void* out, const void* workspace, size_t workspace_bytes,
+                        size_t need) {
   MX_CHECK(x && w && w_scale && out, "%s: null tensor pointer", fn);
   MX_CHECK(aligned(x, 16) && aligned(w, 16) && aligned(out, 16), "%s: x, w and out must be 16-byte aligned", fn);
   MX_CHECK(!f32 || aligned(w_scale, 4), "%s: FP32 w_scale must be 4-byte aligned", fn);
   MX_CHECK(workspace && aligned(workspace, 16) && workspace_bytes >= need,
            "%s: workspace of %zu bytes (16-byte aligned) needed, got %zu", fn, need, workspace_bytes);
   const uintptr_t ob = reinterpret_cast<uintptr_t>(out), obytes = static_cast<uintptr_t>(S) * N * 2;
-  auto apart = [&](const void* p, uintptr_t bytes) {
+  auto apart = [&](const void* p, int64_t bytes) {
     const uintptr_t b = reinterpret_cast<uintptr_t>(p);
-    return b + bytes <= ob || ob + obytes <= b;
+    return !p || b + bytes <= ob || ob + obytes <= b;
   };
-  MX_CHECK(apart(w, static_cast<uintptr_t>(E) * N * K) && apart(workspace, need) &&
-               apart(x, static_cast<uintptr_t>(rows) * x_width * 2),
+  const int64_t scale_bytes = f32 ? E * ((N + 127) / 128) * ((K + 127) / 128) * 4 : E * N * (K / MX_LINEAR_BLOCK);
+  MX_CHECK(apart(x, rows * x_width * 2) && apart(w, E * N * K) && apart(w_scale, scale_bytes) &&
+               apart(offsets, (E + 1) * 4) && apart(row_slot, S * 4) && apart(workspace, static_cast<int64_t>(need)),
            "%s: out overlaps an input or the workspace", fn);
   return MX_OK;
 }
@@ -159,8 +161,8 @@ mx_status mx_grouped_linear(const void* x, int64_t rows, int64_t K, const uint8_
   MX_CHECK(rows >= 1, "%s: x has no rows", fn);
   MX_CHECK(offsets && aligned(offsets, 4) && aligned(row_slot, 4),
            "%s: offsets and row_slot must be 4-byte aligned, offsets not null", fn);
-  st = grouped_check(fn, x, rows, act == MX_ACT_SWIGLU ? 2 * K : K, K, w, w_scale, f32, E, N, S, out, workspace,
-                     workspace_bytes, mx_grouped_linear_workspace_bytes(rows, S, E, N, K));
+  st = grouped_check(fn, x, rows, act == MX_ACT_SWIGLU ? 2 * K : K, K, w, w_scale, f32, offsets, row_slot, E, N, S,
+                     out, workspace, workspace_bytes, mx_grouped_linear_workspace_bytes(rows, S, E, N, K));
   if (st != MX_OK) return st;
   MX_PREAMBLE();
   count(C_GROUPED_LINEAR);
@@ -180,7 +182,7 @@ mx_status mx_linear_block128(const void* x, int64_t M, int64_t K, const uint8_t*
   mx_status st = grouped_sizes(fn, M, K, true, 1, N, M);
   if (st != MX_OK) return st;
   if (M == 0) { clear_error(); return MX_OK; }
-  st = grouped_check(fn, x, M, K, K, w, w_scale, true, 1, N, M, out, workspace, workspace_bytes,
+  st = grouped_check(fn, x, M, K, K, w, w_scale, true, nullptr, nullptr, 1, N, M, out, workspace, workspace_bytes,
                      mx_linear_block128_workspace_bytes(M, N, K));
   if (st != MX_OK) return st;
   MX_PREAMBLE();

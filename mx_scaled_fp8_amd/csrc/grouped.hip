@@ -17,8 +17,8 @@
 //    a multiple of 512 bytes apart as a rule, would meet in a few of the memory channels at every stage.  With act =
 //    SwiGLU it reads [gate | up] and rounds silu(gate) * up to BF16 first.  One more workgroup turns the offsets into a
 //    list of row tiles.  Bound by memory: 8192 x 4096 (100 MB) 20 us, 5 TB/s.
-//  * a product over tiles of 32, 64, 128 or 256 rows (pick_shape): grouped_stream.hip for 32, grouped_large.hip for 256
-//    with MXFP8 scales and 1024 K or more, and here grouped_gemm_kernel, one workgroup per BM x BN tile.  Rows of the
+//  * a product over tiles of 32, 64, 128 or 256 rows (pick_shape): grouped_stream.hip for 32, grouped_large.hip for many
+//    tiles of 256 with MXFP8 scales and 1024 K or more, and here grouped_gemm_kernel, one workgroup per BM x BN tile.  Rows of the
 //    activation are gathered by their index as the LDS-DMA reads them, so no copy per expert is written.
 //
 // What bounds grouped_gemm_kernel (one MI355X, kernel times):
@@ -640,22 +640,28 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK, 1) void grouped_gemm_kernel(G
 
 struct Shape {
   int BM, BN;
+  bool large = false;          // 256 x 256: grouped_large.hip where it can
 };
 
-// The tile for S rows of E groups, by the rows of an average group (the groups' sizes are known on the device alone).
-// Measured on one MI355X, whole calls, us:
-//   <= 32 rows: grouped_stream.hip.
-//   More: 128 x 128 with two workgroups per compute unit, whose pauses cover each other (48 rows a group, 32 groups, N =
-//   5120, K = 2304: 98; 64 x 128 with three 106, 128 x 256 with one 109), unless that leaves compute units without a
-//   tile: then 64 x 64 with the waves split over K (777 rows, N = 1040, K = 4112, FP32 scales: 22; 128 x 128: 38).
-//   256 x 256 from 160 rows on where those tiles fill the chip (8192 rows, N = 5120, K = 4096, FP32 scales: 237; 128 x
-//   128: 271, 128 x 256: 239).
+// The tile for S rows of E groups, by the rows of an average group (the groups' sizes are known on the device alone) and the
+// tiles that makes for 256 compute units.  Measured on one MI355X, whole calls, us:
+//   <= 32 rows: grouped_stream.hip (16 groups of 8 rows, N = K = 2048, MXFP8: 18.0; 128 x 128 18.9, 64 x 64 21.9).
+//   256 x 256 where it pads the average group by no more than a quarter over 128 x 128 and takes nine sixteenths of the
+//     compute units (8 groups of 192 rows, N = 5120, K = 4096, MXFP8: 54 against 62; 640 rows: 130 against 162.  Else, 320 rows: 95
+//     against 75; 128 tiles, 16 groups of 192 rows, N = K = 2048: 29.5 against 27.6).  With MXFP8 scales and groups of
+//     1024 rows or more: grouped_large.hip (32 groups, N = 4608, K = 5120, groups of 2048 rows, more or less 25: 1608 against
+//     1696; 1024 rows: 862 against 872; 512 rows: 499 against 490, its ragged tiles cost it more).
+//   128 x 128, two workgroups per compute unit, whose pauses cover each other, where it takes half of them (48 rows a group,
+//     32 groups, N = 5120, K = 2304: 98; 64 x 128 with three 106, 128 x 256 with one 109).
+//   Else 64 x 64 with the waves split over K (384 rows, N = 5120, K = 4096, FP32 scales: 28 against 34 with 128 x 128; 512
+//     rows: 39 against 35).
 Shape pick_shape(int64_t S, int64_t E, int64_t N) {
-  const int64_t per = (S + E - 1) / E;
+  const int64_t groups = S < E ? S : E, per = (S + E - 1) / E;
   if (per <= 32) return {32, 64};
-  auto tiles = [&](int64_t bm, int64_t bn) { return (S / bm + (S < E ? S : E)) * ((N + bn - 1) / bn); };
-  if (per > 160 && tiles(256, 256) >= 256) return {256, 256};
-  return tiles(128, 128) >= 256 ? Shape{128, 128} : Shape{64, 64};
+  auto padded = [&](int64_t m) { return (per + m - 1) / m * m; };
+  auto tiles = [&](int64_t m) { return groups * (padded(m) / m) * ((N + m - 1) / m); };
+  if (4 * padded(256) <= 5 * padded(128) && tiles(256) >= 144) return {256, 256, per >= 1024};
+  return tiles(128) >= 128 ? Shape{128, 128} : Shape{64, 64};
 }
 
 int64_t max_row_tiles(int64_t S, int64_t E, int BM) { return S / BM + (S < E ? S : E); }
@@ -743,7 +749,7 @@ mx_status launch_grouped(const void* x, int64_t rows, const uint8_t* w, const vo
   const int64_t total = (offsets ? mt : (S + s.BM - 1) / s.BM) * g.n_tiles;
   if (s.BM == 32)
     launch_grouped_stream(f32, g, stream);
-  else if (s.BM == 256 && !f32 && offsets && KB >= kLargeMinStages)
+  else if (s.large && !f32 && KB >= kLargeMinStages)
     launch_grouped_large(g, stream);
   else if (f32)
     launch_gemm<true>(s, g, total, stream);

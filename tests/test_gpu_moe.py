@@ -142,12 +142,14 @@ def _close(got_bits, ref, extra=None, what=""):
     assert not bad.any(), f"{what}: {bad.sum()} of {ref.size} outside, first at {np.argwhere(bad)[0]}"
 
 
-def _swiglu_extra(x_bits, w, ws, offsets):
+def _swiglu_extra(x_bits, w, ws, offsets, slots=None, k=1):
     """|Q(h-) - Q(h+)| @ |W|^T, h-+ the BF16 roundings of silu(gate) * up moved by its FP32 evaluation's error, below
     2^-16 relative: the exponent's rounding moves the exponential by |gate| 2^-24 <= 2^-17 (|gate| <= 128: beyond, the
     result is 0 or gate * up), and the exponential, an addition, a reciprocal and two products by at most 8 steps of
     2^-24."""
     h = M.swiglu(x_bits)
+    if slots is not None:
+        h = h[slots // k]
     lo, hi = F.f64_to_bf16_rne(h * (1 - 2.0 ** -16)), F.f64_to_bf16_rne(h * (1 + 2.0 ** -16))
     out = np.zeros((h.shape[0], w.shape[1]))
     for e in range(w.shape[0]):
@@ -179,7 +181,7 @@ def _run_grouped(seed, fmt, counts, N, K, act=False, gather=None, k=1, spoil=Non
                                act=mx.MX_ACT_SWIGLU if act else mx.MX_ACT_NONE)
     torch.cuda.synchronize()
     ref = M.grouped_linear(x, w, ws, off, slots, k, act)
-    extra = _swiglu_extra(x, w, ws, off) if act else None
+    extra = _swiglu_extra(x, w, ws, off, slots, k) if act else None
     _close(host_u16(out), ref, extra, f"{fmt} {counts} N={N} K={K}")
     return out
 
@@ -209,6 +211,20 @@ def test_grouped_last_round(fmt, counts, N):
 def test_grouped_large_tiles(fmt, K, act, counts, N):
     """Tiles of 128 and 256 rows, ragged in both directions."""
     _run_grouped(7 * K + N, fmt, counts, N, K, act=act)
+
+
+@pytest.mark.parametrize("K", [1056, 1184, 1280])
+@pytest.mark.parametrize("act,gather", [(False, None), (True, None), (False, 900), (True, 900)])
+def test_grouped_large_groups(K, act, gather):
+    """Groups of a thousand rows and more on average, some empty or small, from x or gathered from fewer rows of it."""
+    _run_grouped(K, "mx", [1300, 0, 2700, 257], 4112, K, act=act, gather=gather, k=3)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "f32"])
+@pytest.mark.parametrize("counts,N,K", [([4, 0, 2], 80, 288), ([40, 90], 144, 160), ([150, 100], 8208, 160), ([700, 500], 5136, 160)])
+def test_grouped_gathers_gate_and_up(fmt, counts, N, K):
+    """SwiGLU of gathered rows, for each size of tile."""
+    _run_grouped(N + K, fmt, counts, N, K, act=True, gather=37, k=2)
 
 
 @pytest.mark.parametrize("fmt", ["mx", "f32"])

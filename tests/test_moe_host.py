@@ -68,7 +68,8 @@ def test_grouped_validation(dry):
                 dict(offsets=None), dict(out=None), dict(x=FAKE + 8), dict(w=BIG + 4), dict(out=2 * BIG + 8),
                 dict(kind=1, ws=FAKE + 2), dict(offsets=FAKE + 2), dict(row_slot=FAKE + 1), dict(work=None),
                 dict(work=FAKE + 8), dict(wb=need - 1), dict(out=BIG + 512), dict(out=FAKE),
-                dict(S=(1 << 31) - 1, N=1 << 20), dict(S=1 << 29, N=256), dict(S=1 << 28, N=512)):
+                dict(S=(1 << 31) - 1, N=1 << 20), dict(S=1 << 29, N=256), dict(S=1 << 28, N=512),
+                dict(ws=2 * BIG + 64), dict(offsets=2 * BIG + 64), dict(row_slot=2 * BIG + 64), dict(work=2 * BIG + 64)):
         assert _grouped(**bad) == mx.MX_ERR_INVALID_ARG, bad
         assert mx.lib().mx_last_error().decode()
 
