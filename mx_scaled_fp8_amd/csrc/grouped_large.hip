@@ -376,7 +376,7 @@ __device__ __forceinline__ void grouped_large(const GemmArgs& p) {
           "ds_read_b128 %0, %4\n"
           "ds_read_b128 %1, %4 offset:1024\n"
           "ds_read_b128 %2, %4 offset:2048\n"
-          "ds_read_b128 %3, %4 offset:3072\n"
+          "ds_read_b128 %3, %4 offset:0xc00\n"
           "s_waitcnt lgkmcnt(0)"
           : "=&v"(d0), "=&v"(d1), "=&v"(d2), "=&v"(d3)
           : "v"(wa + er * 128 + ((ec ^ er) << 4))

@@ -368,7 +368,7 @@ __device__ __forceinline__ void grouped_stream(const GemmArgs& p) {
         v4u v0, v1, v2, v3;
         asm volatile(
             "ds_read_b128 %0, %4\nds_read_b128 %1, %4 offset:1024\nds_read_b128 %2, %4 offset:2048\n"
-            "ds_read_b128 %3, %4 offset:3072\ns_waitcnt lgkmcnt(0)"
+            "ds_read_b128 %3, %4 offset:0xc00\ns_waitcnt lgkmcnt(0)"
             : "=&v"(v0), "=&v"(v1), "=&v"(v2), "=&v"(v3)
             : "v"(at + s * kSet)
             : "memory");
