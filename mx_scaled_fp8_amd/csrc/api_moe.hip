@@ -38,7 +38,8 @@ mx_status mx_moe_route(const void* logits, int32_t logits_f32, const float* bias
   MX_CHECK(E >= 1 && E <= MX_ROUTE_MAX_EXPERTS, "%s: E = %d (1 to %d)", fn, E, MX_ROUTE_MAX_EXPERTS);
   MX_CHECK(k >= 1 && k <= std::min(E, MX_ROUTE_MAX_K), "%s: k = %d (1 to min(E = %d, %d))", fn, k, E,
            MX_ROUTE_MAX_K);
-  MX_CHECK(T >= 0 && T < (int64_t(1) << 31) && T * k < (int64_t(1) << 31), "%s: T = %lld out of range", fn,
+  // a workgroup of 512 threads takes 64 tokens, and a launch is below 2^32 threads
+  MX_CHECK(T >= 0 && T < (int64_t(1) << 29) - 64 && T * k < (int64_t(1) << 31), "%s: T = %lld out of range", fn,
            (long long)T);
   MX_CHECK(score == MX_ROUTE_SOFTMAX || score == MX_ROUTE_SIGMOID, "%s: unknown score %d", fn, score);
   MX_CHECK(renormalize == 0 || renormalize == 1, "%s: renormalize = %d (0 or 1)", fn, renormalize);

@@ -10,15 +10,15 @@
 // keys are formed in FP64, which leaves near-ties of different scores to the exact order.  Equal keys: lowest index.
 //
 // Two launches, bound by latency (a few kilobytes to a few megabytes):
-//  * route_topk_kernel: 16 lanes a token (64 for more than 256 experts or k > 16), each holding every 16th expert; k
-//    rounds of a maximum across the lanes.  A workgroup takes a block of up to 64 tokens and notes in LDS, per expert, which
+//  * route_topk_kernel: 16 or 64 lanes a token, each holding every 16th or 64th expert; k rounds of a maximum across the
+//    lanes.  A workgroup takes a block of up to 64 tokens and notes in LDS, per expert, which
 //    of them picked it: a 64-bit mask.
 //  * route_scatter_kernel: the row of slot (t, j) is the number of slots of lower experts, plus those of its expert in
 //    the blocks before (sums of the masks' bit counts), plus the bits below t in its own block's mask.  So the rows of
 //    an expert are in slot order, and nothing is placed by the order of atomics.
 // A single block does the second's work in the first launch.
 // Measured (one MI355X, kernel times): 4 tokens, 64 experts, k = 6, BF16 logits: 4 us.  8192 tokens, 256 experts, k = 8,
-// sigmoid with a bias: 12 and 6 us; the logits alone would take 2.  The rest is the scores (FP64 only for experts that an
+// sigmoid with a bias: 10 and 6 us; the logits alone would take 2.  The rest is the scores (FP64 only for experts that an
 // FP32 bound leaves in question: 83 us for all of them), k rounds of maxima, and the masks' way through memory.
 //
 // Join.  out[t] = shared[t] + sum_j w[t, j] * y[slot_row[t, j]] in FP32, rounded once; bound by HBM: 8192 tokens, k = 8,
@@ -270,42 +270,53 @@ __device__ __forceinline__ void route_token_biased(const RouteArgs& a, bool f32,
   }
 }
 
-// Sigmoid scores with a bias, without an FP64 exponential for every expert.  FP32 keys find the k-th largest; an FP32
-// key is within 2^-20 (1 + |key|) of its FP64 one (an exponential, an addition, a reciprocal of values up to 1, the
-// bias's addition: a few 2^-24 each), so the k largest are among the experts whose FP32 key is at least the k-th one's
-// less 2^-18 (1 + |key|).  Those, k and rarely one more, get FP64 keys and are ordered by counting, for each, the ones
-// before it.  Returns false, nothing written, if they do not fit (many equal keys, or fewer than k experts left).
-constexpr int kCandidates = 32;
+// Sigmoid scores with a bias, without an FP64 exponential for every expert.  FP32 keys find the k-th largest of different
+// ones, which is at most the k-th largest; an FP32 key is within 2^-20 (1 + |key|) of its FP64 one (an exponential, an
+// addition, a reciprocal of values up to 1, the bias's addition: a few 2^-24 each), so the k largest are among the experts
+// whose FP32 key is at least that one's less 2^-18 (1 + |key|).  Those, k and rarely more, get FP64 keys and are ordered by
+// counting, for each, the ones before it.  Returns false, nothing written, if they do not fit (many equal keys, or fewer
+// than k different ones left).
+template <int LANES>
 struct Candidates {
-  double key[kCandidates], p[kCandidates], sorted[16];
-  int32_t id[kCandidates];
+  static constexpr int kMost = LANES == 16 ? 32 : 64;
+  double key[kMost], p[kMost], sorted[LANES == 16 ? 16 : MX_ROUTE_MAX_K];
+  int32_t id[kMost];
   int32_t count;
 };
 
-template <int EI>
+template <int LANES, int EI>
 __device__ __forceinline__ bool route_token_preselected(const RouteArgs& a, bool f32, int64_t t, int sub,
-                                                        uint32_t* mask, uint32_t bit, Candidates& c) {
+                                                        uint32_t* mask, uint32_t bit, Candidates<LANES>& c) {
   float l[EI], bias[EI], key[EI];
   uint32_t left[EI];
 #pragma unroll
-  for (int i = 0; i < EI; ++i) bias[i] = a.bias[min(i * 16 + sub, a.E - 1)];
-  load_logits<16>(a, f32, t, sub, l);
+  for (int i = 0; i < EI; ++i) bias[i] = a.bias[min(i * LANES + sub, a.E - 1)];
+  load_logits<LANES, EI>(a, f32, t, sub, l);
   if (sub == 0) c.count = 0;
 #pragma unroll
   for (int i = 0; i < EI; ++i) {
     const float v = __builtin_amdgcn_rcpf(1.0f + __expf(-l[i])) + bias[i];
     key[i] = l[i] == -__builtin_inff() || v != v ? -__builtin_inff() : v;
-    left[i] = i * 16 + sub < a.E ? key_of(key[i]) : taken_key<uint32_t>();
+    left[i] = i * LANES + sub < a.E ? key_of(key[i]) : 0u;
   }
+  // the next smaller key is `most` plus the largest difference modulo 2^32: of the smaller ones those are the largest
   uint32_t most = 0;
-  for (int j = 0; j < a.k; ++j) take_largest<uint32_t, 16>(left, sub, most);
+  bool below = true;
+  for (int j = 0; j < a.k; ++j) {
+    uint32_t d = left[0] - most;
+#pragma unroll
+    for (int i = 1; i < EI; ++i) d = max(d, left[i] - most);
+    d = across<LANES>(d, Max()) + most;
+    below = below && (j == 0 || d < most);
+    most = d;
+  }
   const float kth = value_of(most);
   const float least = kth - 0x1p-18f * (1.0f + fabsf(kth));   // NaN or infinite where kth is
   uint32_t mine = 0;
 #pragma unroll
-  for (int i = 0; i < EI; ++i) mine |= (i * 16 + sub < a.E && key[i] >= least ? 1u : 0u) << i;
-  const int total = across<16>(static_cast<int>(__popc(mine)), Sum());
-  if (!(fabsf(kth) <= __FLT_MAX__) || total > kCandidates) return false;
+  for (int i = 0; i < EI; ++i) mine |= (i * LANES + sub < a.E && key[i] >= least ? 1u : 0u) << i;
+  const int total = across<LANES>(static_cast<int>(__popc(mine)), Sum());
+  if (!below || !(fabsf(kth) <= __FLT_MAX__) || total > c.kMost) return false;
 
   while (mine != 0) {
     const int i = __ffs(mine) - 1;
@@ -320,11 +331,11 @@ __device__ __forceinline__ bool route_token_preselected(const RouteArgs& a, bool
     const int at = atomicAdd(&c.count, 1);       // any order: the ranks below do not depend on it
     c.key[at] = p + static_cast<double>(b);
     c.p[at] = p;
-    c.id[at] = i * 16 + sub;
+    c.id[at] = i * LANES + sub;
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
-  for (int n = sub; n < total; n += 16) {
+  for (int n = sub; n < total; n += LANES) {
     const double mykey = c.key[n];
     const int id = c.id[n];
     int rank = 0;
@@ -377,7 +388,7 @@ template <bool BIAS, int LANES, int EI>
 __global__ __launch_bounds__(kTopkThreads) void route_topk_kernel(RouteArgs a, int f32) {
   __shared__ uint32_t mask[2][kMaxExperts];      // tokens 0..31 and 32..63 of the block
   __shared__ int32_t start[kMaxExperts];
-  __shared__ Candidates cand[BIAS && LANES == 16 ? kTopkThreads / 16 : 1];
+  __shared__ Candidates<LANES> cand[BIAS ? kTopkThreads / LANES : 1];
   const int tid = threadIdx.x;
   const int sub = tid & (LANES - 1), group = tid / LANES;
   constexpr int threads = kTopkThreads, groups = threads / LANES;
@@ -388,8 +399,9 @@ __global__ __launch_bounds__(kTopkThreads) void route_topk_kernel(RouteArgs a, i
   for (int q = group; q < a.block_tokens && t0 + q < a.T; q += groups) {
     uint32_t* const m = mask[q >> 5];
     const uint32_t bit = 1u << (q & 31);
-    if constexpr (BIAS && LANES == 16) {
-      if (a.score == MX_ROUTE_SIGMOID && route_token_preselected<EI>(a, f32 != 0, t0 + q, sub, m, bit, cand[group]))
+    if constexpr (BIAS) {
+      if (a.score == MX_ROUTE_SIGMOID &&
+          route_token_preselected<LANES, EI>(a, f32 != 0, t0 + q, sub, m, bit, cand[group]))
         continue;
     }
     if constexpr (BIAS)
@@ -559,21 +571,33 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
   reinterpret_cast<v4u*>(a.out)[i] = o;
 }
 
-// One block takes up to 64 tokens, in one launch.  More are cut into blocks of 32, which use twice the compute units
-// (8192 tokens, 256 experts, sigmoid with a bias: 30 against 35 us when this was measured), until longer blocks fill
-// the chip too and halve the masks that the second launch reads.
-int route_block_tokens(int64_t T) { return T <= kBlockTokens || T > 32 * 1024 ? kBlockTokens : 32; }
-int route_blocks(int64_t T) {
-  const int b = route_block_tokens(T);
+// 16 lanes a token while its experts' scores and keys fit the registers and k the lanes, and 64 lanes else, or where there
+// are several experts a lane and few tokens, so that latency counts (256 experts, k = 8, kernels of a call, us: 64 tokens,
+// softmax with a bias 11.6 against 30.1, without 8.9 against 12.0; 2048 tokens 14.2 against 21.9 and 11.3 against 12.2; 64
+// experts, 500 tokens 8.6 against 7.6).
+bool route_wide(int64_t T, int32_t E, int32_t k) { return k > 16 || E > 256 || (E > 128 && T > 32 && T <= 8 * 256); }
+// Tokens of a block.  One block takes up to 64, in one launch.  More are cut into blocks of 32, the tokens that a workgroup
+// works on at once with 16 lanes each (8192 tokens, 256 experts, sigmoid with a bias: 30 against 35 us with 64 when this was
+// measured), until longer blocks fill the chip too and halve the masks that the second launch reads.  With 64 lanes a token
+// a workgroup works on 8 at once: blocks of 8 then, while they are no more than the compute units (450 experts, 79 tokens:
+// 11 to 16 us by the score, 23 to 41 with blocks of 32).
+int route_block_tokens(int64_t T, int32_t E) {
+  if (T > 32 * 1024) return kBlockTokens;
+  if (T <= (E > 256 ? 16 : E > 128 ? 32 : kBlockTokens)) return kBlockTokens;
+  if (E > 128 && T <= 8 * 256) return 8;
+  return E > 256 && T <= 16 * 256 ? 16 : 32;
+}
+int route_blocks(int64_t T, int32_t E) {
+  const int b = route_block_tokens(T, E);
   return T > 0 ? static_cast<int>((T + b - 1) / b) : 1;
 }
 
 template <bool BIAS>
 void launch_topk(const RouteArgs& a, int32_t f32, hipStream_t stream) {
-  // 16 lanes a token while their experts' scores and keys fit the registers and k the lanes
 #define MX_TOPK(LANES, EI) route_topk_kernel<BIAS, LANES, EI><<<a.blocks, kTopkThreads, 0, stream>>>(a, f32)
-  if (a.k > 16 || a.E > 256) {
+  if (route_wide(a.T, a.E, a.k)) {
     if (a.E <= 64) MX_TOPK(64, 1);
+    else if (a.E <= 128) MX_TOPK(64, 2);
     else if (a.E <= 256) MX_TOPK(64, 4);
     else if (a.E <= 512) MX_TOPK(64, 8);
     else MX_TOPK(64, 16);
@@ -588,7 +612,7 @@ void launch_topk(const RouteArgs& a, int32_t f32, hipStream_t stream) {
 }  // namespace
 
 size_t route_workspace_bytes(int64_t T, int32_t E) {
-  const int64_t blocks = route_blocks(T);
+  const int64_t blocks = route_blocks(T, E);
   return blocks > 1 ? static_cast<size_t>(blocks) * (8 * static_cast<size_t>(E) + (E + 3) / 4 * 4) : 0;
 }
 
@@ -608,8 +632,8 @@ mx_status launch_moe_route(const void* logits, int32_t f32, const float* bias, i
   a.E = E;
   a.k = k;
   a.E4 = (E + 3) / 4 * 4;
-  a.block_tokens = route_block_tokens(T);
-  a.blocks = route_blocks(T);
+  a.block_tokens = route_block_tokens(T, E);
+  a.blocks = route_blocks(T, E);
   a.masks = static_cast<uint64_t*>(workspace);
   a.counts = reinterpret_cast<uint32_t*>(a.masks + static_cast<int64_t>(a.blocks) * E);
   a.span = (a.blocks + kMaxSpans - 1) / kMaxSpans;

@@ -48,7 +48,9 @@ def _check_route(l64, dev_logits, k, bias=None, score=0, renorm=True, scale=1.0)
 
 
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 8), (3, 5, 2), (64, 64, 6), (65, 64, 6), (1000, 65, 4), (130, 255, 8),
-                                   (777, 256, 8), (40, 300, 32), (257, 512, 3), (100, 1000, 12), (2000, 1024, 1)])
+                                   (777, 256, 8), (40, 300, 32), (257, 512, 3), (100, 1000, 12), (2000, 1024, 1),
+                                   (16, 300, 9), (17, 257, 3), (33, 129, 5), (32, 200, 16), (2049, 130, 2), (2049, 300, 4),
+                                   (4097, 260, 2), (70, 100, 20), (9, 1024, 32)])
 @pytest.mark.parametrize("score", [mx.MX_ROUTE_SOFTMAX, mx.MX_ROUTE_SIGMOID])
 @pytest.mark.parametrize("bias", [False, True])
 def test_route(T, E, k, score, bias):

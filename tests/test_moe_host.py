@@ -39,7 +39,7 @@ def test_route_validation(dry):
     need = mx.mx_moe_route_workspace_bytes(100, 64)
     assert need == 4 * 64 * (8 + 1) and _route(wb=need) == mx.MX_OK
     for bad in (dict(f32=2), dict(E=0), dict(E=1025), dict(k=0), dict(k=65), dict(E=4, k=5), dict(k=33), dict(T=-1),
-                dict(T=1 << 30), dict(score=2), dict(renorm=2), dict(logits=None), dict(ids=None), dict(weights=None),
+                dict(T=1 << 30), dict(T=1 << 29, E=2, k=1), dict(score=2), dict(renorm=2), dict(logits=None), dict(ids=None), dict(weights=None),
                 dict(offsets=None), dict(row_slot=None), dict(slot_row=None), dict(logits=FAKE + 2),
                 dict(offsets=FAKE + 2), dict(ws=None), dict(ws=FAKE + 4), dict(wb=need - 1), dict(bias=FAKE + 1)):
         assert _route(**bad) == mx.MX_ERR_INVALID_ARG, bad
