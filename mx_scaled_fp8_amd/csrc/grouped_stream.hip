@@ -74,17 +74,19 @@ struct Tile {
   int e, row0, rows, n0, cols, turn;
 };
 
-// ODD: K is no multiple of 128 (the last stage is short), or the MXFP8 weight's scale words are not 4-byte aligned (each
-// then comes as the two aligned words around it).
+// ODD: K is no multiple of 128 (the last stage is short), or the MXFP8 weight's scale words are not 4-byte aligned (a row's
+// four of a super-stage then lie in the five aligned words around them: 46 rows of 8 groups, N = 3584, K = 4448: 38.5 us
+// against 56.5 with two words for each of the four; K = 4480: 36).
 template <bool F32, bool ODD>
 __device__ __forceinline__ void grouped_stream(const GemmArgs& p) {
   constexpr int BM = 32, BN = 64, WGN = 2, WGK = 4, S = 3;
   constexpr int kWaves = WGN * WGK;
   constexpr int kSub = (BN + BM) * kStageK;            // one 128-K stage: W rows, then x rows
   constexpr int kSlot = kSub * WGK;
-  constexpr int kScW = ODD && !F32 ? 2 : 1;            // words of a W row's scale
+  constexpr bool kTail = ODD && !F32;
+  constexpr int kScW = WGK + (kTail ? 1 : 0);          // words of a W row's scales; unaligned, they lie in one more
   constexpr int kScX = WGK * BM;                       // words of the x rows' scales
-  constexpr int kScWords = kScX + WGK * kScW * BN;
+  constexpr int kScWords = kScX + kScW * BN;
   constexpr int kScIns = kScWords / 64;                // DMA instructions of a super-stage's scales
   constexpr int kXIns = WGK * BM / 8, kWIns = WGK * BN / 8;
   constexpr int XPW = (kXIns + kWaves - 1) / kWaves, WPW = kWIns / kWaves, SPW = (kScIns + kWaves - 1) / kWaves;
@@ -207,8 +209,7 @@ __device__ __forceinline__ void grouped_stream(const GemmArgs& p) {
         sptr[u] = reinterpret_cast<const uint8_t*>(p.xs);
         sbytes[u] = static_cast<uint32_t>(p.rows) * static_cast<uint32_t>((KB + 3) & ~3) * 4;
       } else {
-        const int j = i - kScX / 64, part = j / (BN / 64) % kScW, r = j % (BN / 64) * 64 + lane;
-        const int sub = j / (BN / 64 * kScW);
+        const int j = i - kScX / 64, r = j % (BN / 64) * 64 + lane, sub = j / (BN / 64);
         if constexpr (F32) {
           // the columns' 128-blocks: two in a tile of 256 (which may begin inside one)
           const float* const at = static_cast<const float*>(p.ws) + static_cast<size_t>(t.e) * NB * KB;
@@ -223,7 +224,7 @@ __device__ __forceinline__ void grouped_stream(const GemmArgs& p) {
           sptr[u] = at - mis;
           // up to the aligned word that holds the tensor's last byte
           sbytes[u] = static_cast<uint32_t>(min(static_cast<size_t>(end - sptr[u]) + 3, static_cast<size_t>(1) << 30)) & ~3u;
-          offS[u] = ((mis + static_cast<uint32_t>(min(r, t.cols - 1)) * static_cast<uint32_t>(K32)) & ~3u) + 4 * part + 4 * sub;
+          offS[u] = ((mis + static_cast<uint32_t>(min(r, t.cols - 1)) * static_cast<uint32_t>(K32)) & ~3u) + 4 * sub;
         }
       }
     }
@@ -288,14 +289,14 @@ __device__ __forceinline__ void grouped_stream(const GemmArgs& p) {
     rdX[c] = ring0 + wk * kSub + (BN + r32) * kStageK + chunk;
   }
   const uint32_t rdSx = scales0 + (wk * BM + r32) * 4;
-  const uint32_t rdSw = scales0 + (kScX + wk * kScW * BN + wn * 32 + r32) * 4;
+  const uint32_t rdSw = scales0 + (kScX + wk * BN + wn * 32 + r32) * 4;
   v16f acc = {};
   int cslot = 0;
   auto compute = [&](int kb, uint32_t misalign) {
     const uint32_t so = static_cast<uint32_t>(cslot) * kSlot, co = static_cast<uint32_t>(cslot) * kScWords * 4;
     const uint32_t sx = lds_read(rdSx + co);
     uint32_t sw = lds_read(rdSw + co);
-    if constexpr (kScW == 2) {
+    if constexpr (kTail) {
       sw = __builtin_amdgcn_alignbyte(lds_read(rdSw + co + BN * 4), sw, misalign);
       // blocks behind K: 2^-127, not what follows the row (which may be a NaN scale); their codes are zero
       if (kb == KB - 1 && (K32 & 3) != 0) sw &= (1u << (8 * (K32 & 3))) - 1;
