@@ -640,6 +640,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * WGK, 1) void grouped_gemm_kernel(G
 
 struct Shape {
   int BM, BN;
+  bool split = false;          // the waves split over K
   bool large = false;          // 256 x 256: grouped_large.hip where it can
 };
 
@@ -651,17 +652,20 @@ struct Shape {
 //     against 75; 128 tiles, 16 groups of 192 rows, N = K = 2048: 29.5 against 27.6).  With MXFP8 scales and groups of
 //     1024 rows or more: grouped_large.hip (32 groups, N = 4608, K = 5120, groups of 2048 rows, more or less 25: 1608 against
 //     1696; 1024 rows: 862 against 872; 512 rows: 499 against 490, its ragged tiles cost it more).
-//   128 x 128, two workgroups per compute unit, whose pauses cover each other, where it takes half of them (48 rows a group,
-//     32 groups, N = 5120, K = 2304: 98; 64 x 128 with three 106, 128 x 256 with one 109).
-//   Else 64 x 64 with the waves split over K (384 rows, N = 5120, K = 4096, FP32 scales: 28 against 34 with 128 x 128; 512
-//     rows: 39 against 35).
+//   While the tiles are no more than the compute units: 64 x 64, 64 x 128 or 128 x 128 (the first that are), with the waves
+//     split over K, four, two and two ways (FP32 scales, N = 5120, K = 4096, 256 rows: 27.6, 21.7, 26.3; 512 rows: 39.7,
+//     39.2, 29.1; 128 x 128 with one set of waves 35.5; 8 groups of 100 rows, N = K = 2048, MXFP8: 20.5, 16.3, 17.9).
+//   Else 128 x 128, two workgroups per compute unit, whose pauses cover each other (800 rows: 44 against 52 split; 48 rows a
+//     group, 32 groups, N = 5120, K = 2304: 98; 64 x 128 with three workgroups 106, 128 x 256 with one 109).
 Shape pick_shape(int64_t S, int64_t E, int64_t N) {
   const int64_t groups = S < E ? S : E, per = (S + E - 1) / E;
   if (per <= 32) return {32, 64};
-  auto padded = [&](int64_t m) { return (per + m - 1) / m * m; };
-  auto tiles = [&](int64_t m) { return groups * (padded(m) / m) * ((N + m - 1) / m); };
-  if (4 * padded(256) <= 5 * padded(128) && tiles(256) >= 144) return {256, 256, per >= 1024};
-  return tiles(128) >= 128 ? Shape{128, 128} : Shape{64, 64};
+  auto ceil_to = [](int64_t v, int64_t m) { return (v + m - 1) / m * m; };
+  auto tiles = [&](int64_t bm, int64_t bn) { return groups * (ceil_to(per, bm) / bm) * (ceil_to(N, bn) / bn); };
+  if (4 * ceil_to(per, 256) <= 5 * ceil_to(per, 128) && tiles(256, 256) >= 144) return {256, 256, false, per >= 1024};
+  if (tiles(64, 64) <= 256) return {64, 64, true};
+  if (tiles(64, 128) <= 256) return {64, 128, true};
+  return {128, 128, tiles(128, 128) <= 256};
 }
 
 int64_t max_row_tiles(int64_t S, int64_t E, int BM) { return S / BM + (S < E ? S : E); }
@@ -671,8 +675,12 @@ size_t align_up(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 template <bool F32>
 void launch_gemm(const Shape s, const GemmArgs& a, int64_t tiles, hipStream_t stream) {
   const unsigned per_xcd = static_cast<unsigned>((tiles + 7) / 8);
-  if (s.BM == 64)
+  if (s.BM == 64 && s.BN == 64)
     grouped_gemm_kernel<F32, 64, 64, 1, 2, 4, 2><<<8 * per_xcd, 512, 0, stream>>>(a);
+  else if (s.BM == 64)
+    grouped_gemm_kernel<F32, 64, 128, 2, 2, 2, 2><<<8 * per_xcd, 512, 0, stream>>>(a);
+  else if (s.BM == 128 && s.split)
+    grouped_gemm_kernel<F32, 128, 128, 2, 2, 2, 2><<<8 * per_xcd, 512, 0, stream>>>(a);
   else if (s.BM == 128)
     grouped_gemm_kernel<F32, 128, 128, 2, 2, 1, 2><<<8 * per_xcd, 256, 0, stream>>>(a);
   else                                                 // and up to one more round of parts

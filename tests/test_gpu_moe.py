@@ -215,6 +215,14 @@ def test_grouped_large_tiles(fmt, K, act, counts, N):
     _run_grouped(7 * K + N, fmt, counts, N, K, act=act)
 
 
+@pytest.mark.parametrize("fmt,K", [("mx", 32), ("mx", 160), ("mx", 288), ("mx", 1152), ("f32", 16), ("f32", 144), ("f32", 272),
+                                   ("f32", 1040)])
+@pytest.mark.parametrize("counts,N", [([60, 100, 0, 90], 4112), ([150, 200, 170], 4112), ([700], 4112), ([250], 5136)])
+def test_grouped_waves_split_over_k(fmt, K, counts, N):
+    """Tiles of 64 x 128 and 128 x 128, fewer than compute units: every K tail, K of one stage among them."""
+    _run_grouped(5 * K + N, fmt, counts, N, K)
+
+
 @pytest.mark.parametrize("K", [1056, 1184, 1280])
 @pytest.mark.parametrize("act,gather", [(False, None), (True, None), (False, 900), (True, 900)])
 def test_grouped_large_groups(K, act, gather):
