@@ -270,12 +270,12 @@ __device__ __forceinline__ void route_token_biased(const RouteArgs& a, bool f32,
   }
 }
 
-// Sigmoid scores with a bias, without an FP64 exponential for every expert.  FP32 keys find the k-th largest of different
-// ones, which is at most the k-th largest; an FP32 key is within 2^-20 (1 + |key|) of its FP64 one (an exponential, an
-// addition, a reciprocal of values up to 1, the bias's addition: a few 2^-24 each), so the k largest are among the experts
-// whose FP32 key is at least that one's less 2^-18 (1 + |key|).  Those, k and rarely more, get FP64 keys and are ordered by
-// counting, for each, the ones before it.  Returns false, nothing written, if they do not fit (many equal keys, or fewer
-// than k different ones left).
+// Scores with a bias, without FP64 keys for every expert (a softmax's sum takes their FP64 exponentials all the same).  FP32
+// keys find the k-th largest of different ones, which is at most the k-th largest; an FP32 key is within 2^-20 (1 + |key|)
+// of its FP64 one (an exponential, a reciprocal or a product of values up to 1, the bias's addition: a few 2^-24 each), so
+// the k largest are among the experts whose FP32 key is at least that one's less 2^-18 (1 + |key|).  Those, k and rarely
+// more, get FP64 keys and are ordered by counting, for each, the ones before it.  Returns false, nothing written, if they
+// do not fit (many equal keys, or fewer than k different ones left).
 template <int LANES>
 struct Candidates {
   static constexpr int kMost = LANES == 16 ? 32 : 64;
@@ -284,7 +284,7 @@ struct Candidates {
   int32_t count;
 };
 
-template <int LANES, int EI>
+template <int LANES, int EI, bool SOFT>
 __device__ __forceinline__ bool route_token_preselected(const RouteArgs& a, bool f32, int64_t t, int sub,
                                                         uint32_t* mask, uint32_t bit, Candidates<LANES>& c) {
   float l[EI], bias[EI], key[EI];
@@ -293,9 +293,28 @@ __device__ __forceinline__ bool route_token_preselected(const RouteArgs& a, bool
   for (int i = 0; i < EI; ++i) bias[i] = a.bias[min(i * LANES + sub, a.E - 1)];
   load_logits<LANES, EI>(a, f32, t, sub, l);
   if (sub == 0) c.count = 0;
+  float top = 0;
+  double inv = 1;
+  if constexpr (SOFT) {
+    top = l[0];
+#pragma unroll
+    for (int i = 1; i < EI; ++i) top = fmaxf(top, l[i]);
+    top = across<LANES>(top, Max());
+    double sum = 0;
+#pragma unroll 1
+    for (int n = 0; n < EI; ++n) {               // the logits rotate: see route_token_biased
+      const float x = l[0];
+      sum += exp(static_cast<double>(x) - static_cast<double>(top));
+#pragma unroll
+      for (int i = 0; i + 1 < EI; ++i) l[i] = l[i + 1];
+      l[EI - 1] = x;
+    }
+    inv = 1.0 / across<LANES>(sum, Sum());       // NaN if every expert is masked, and so are the keys
+  }
+  const float finv = static_cast<float>(inv);
 #pragma unroll
   for (int i = 0; i < EI; ++i) {
-    const float v = __builtin_amdgcn_rcpf(1.0f + __expf(-l[i])) + bias[i];
+    const float v = (SOFT ? __expf(l[i] - top) * finv : __builtin_amdgcn_rcpf(1.0f + __expf(-l[i]))) + bias[i];
     key[i] = l[i] == -__builtin_inff() || v != v ? -__builtin_inff() : v;
     left[i] = i * LANES + sub < a.E ? key_of(key[i]) : 0u;
   }
@@ -327,7 +346,8 @@ __device__ __forceinline__ bool route_token_preselected(const RouteArgs& a, bool
       x = q == i ? l[q] : x;
       b = q == i ? bias[q] : b;
     }
-    const double p = 1.0 / (1.0 + exp(-static_cast<double>(x)));
+    const double e = exp(SOFT ? static_cast<double>(x) - static_cast<double>(top) : -static_cast<double>(x));
+    const double p = SOFT ? e * inv : 1.0 / (1.0 + e);
     const int at = atomicAdd(&c.count, 1);       // any order: the ranks below do not depend on it
     c.key[at] = p + static_cast<double>(b);
     c.p[at] = p;
@@ -400,14 +420,14 @@ __global__ __launch_bounds__(kTopkThreads) void route_topk_kernel(RouteArgs a, i
     uint32_t* const m = mask[q >> 5];
     const uint32_t bit = 1u << (q & 31);
     if constexpr (BIAS) {
-      if (a.score == MX_ROUTE_SIGMOID &&
-          route_token_preselected<LANES, EI>(a, f32 != 0, t0 + q, sub, m, bit, cand[group]))
-        continue;
-    }
-    if constexpr (BIAS)
-      route_token_biased<LANES, EI>(a, f32 != 0, t0 + q, sub, m, bit);
-    else
+      const bool done = a.score == MX_ROUTE_SOFTMAX
+                            ? route_token_preselected<LANES, EI, true>(a, f32 != 0, t0 + q, sub, m, bit, cand[group])
+                            : route_token_preselected<LANES, EI, false>(a, f32 != 0, t0 + q, sub, m, bit, cand[group]);
+      if (!done)
+        route_token_biased<LANES, EI>(a, f32 != 0, t0 + q, sub, m, bit);
+    } else {
       route_token_plain<LANES, EI>(a, f32 != 0, t0 + q, sub, m, bit);
+    }
   }
   __syncthreads();
   if (a.blocks > 1) {
