@@ -12,21 +12,23 @@
 //
 // Two launches:
 //  * quant_rows_kernel: every activation row once (not once per expert that reads it): codes [KB, rows, 128] and one
-//    4-byte scale word per 128 K [rows, KB4] (four E8M0 bytes, or one FP32) into the workspace, KB = K / 128 rounded up,
-//    KB4 = KB rounded up to 4, with zero codes behind K.  The codes lie by K block first: row by row, the rows of a tile,
-//    a multiple of 512 bytes apart as a rule, would meet in a few of the memory channels at every stage.  With act =
-//    SwiGLU it reads [gate | up] and rounds silu(gate) * up to BF16 first.  One more workgroup turns the offsets into a
-//    list of row tiles.  Bound by memory: 8192 x 4096 (100 MB) 20 us, 5 TB/s.
-//  * a product over tiles of 32, 64, 128 or 256 rows (pick_shape): grouped_stream.hip for 32, grouped_large.hip for many
-//    tiles of 256 with MXFP8 scales and 1024 K or more, and here grouped_gemm_kernel, one workgroup per BM x BN tile.  Rows of the
-//    activation are gathered by their index as the LDS-DMA reads them, so no copy per expert is written.
+//    4-byte scale word per 128 K [rows, KB4] (four E8M0 bytes, or one FP32) into the workspace, KB = K / 128 rounded
+//    up, KB4 = KB rounded up to 4, with zero codes behind K.  The codes lie by K block first: row by row, the rows of a
+//    tile, a multiple of 512 bytes apart as a rule, would meet in a few of the memory channels at every stage.  With
+//    act = SwiGLU it reads [gate | up] and rounds silu(gate) * up to BF16 first.  One more workgroup turns the offsets
+//    into a list of row tiles.  Bound by memory: 8192 x 4096 (100 MB) 20 us, 5 TB/s.
+//  * a product over tiles of 32, 64, 128 or 256 rows (pick_shape): grouped_stream.hip for 32, grouped_large.hip for
+//    many tiles of 256 with MXFP8 scales and 1024 K or more, and here grouped_gemm_kernel, one workgroup per BM x BN
+//    tile.  Rows of the activation are gathered by their index as the LDS-DMA reads them, so no copy per expert is
+//    written.
 //
 // What bounds grouped_gemm_kernel (one MI355X, kernel times):
-//   128 x 128, 1544 rows of 32 groups, N = 5120, K = 2304, MXFP8: 95 us for 377 MB of weights, 4.0 TB/s.  The same without
-//     MFMAs takes as long, with every tile on the same weight rows 52, without the x rows 88, without stores 86: the
-//     weights' stream, and the tiles' other traffic in its gaps.
-//   256 x 256, 8192 rows, N = 5120, K = 4096, FP32 scales: 185 to 200 us, 1.7 to 1.9 PFLOP/s.  Without the fma's 6 % less,
-//     with no DMA 20 % less, with operands of zeros 12 % less (the clock follows the power that the operands' bits draw).
+//   128 x 128, 1544 rows of 32 groups, N = 5120, K = 2304, MXFP8: 95 us for 377 MB of weights, 4.0 TB/s.  The same
+//     without MFMAs takes as long, with every tile on the same weight rows 52, without the x rows 88, without stores 86:
+//     the weights' stream, and the tiles' other traffic in its gaps.
+//   256 x 256, 8192 rows, N = 5120, K = 4096, FP32 scales: 185 to 200 us, 1.7 to 1.9 PFLOP/s.  Without the fma's 6 %
+//     less, with no DMA 20 % less, with operands of zeros 12 % less (the clock follows the power that the operands' bits
+//     draw).
 #include <type_traits>
 
 #include "grouped.hpp"
@@ -222,8 +224,8 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   __shared__ __attribute__((aligned(1024))) uint8_t st0[kStage];
   __shared__ __attribute__((aligned(1024))) uint8_t st1[kStage];
   __shared__ __attribute__((aligned(1024))) uint8_t st2[STAGES > 2 ? kStage : 16];
-  // scale words of two windows of four stages.  MXFP8: W rows, then x rows, four E8M0 bytes each.  FP32: the products of
-  // an x row's scale with the column block's, for each of the tile's column blocks.
+  // scale words of two windows of four stages.  MXFP8: W rows, then x rows, four E8M0 bytes each.  FP32: the products
+  // of an x row's scale with the column block's, for each of the tile's column blocks.
   constexpr int kCB = (BN + 127) / 128;
   constexpr int kScRows = F32 ? BM * kCB : BN + BM;
   __shared__ __attribute__((aligned(16))) uint32_t sc[2][4][kScRows];
@@ -236,10 +238,10 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   const int per_xcd = (total + 7) >> 3;
   const int first_work = (blockIdx.x & 7) * per_xcd, mine = min(per_xcd, total - first_work);
   int slot = blockIdx.x >> 3;
-  // Tiles of 256 rows come one to a compute unit, in rounds.  Where the last round would leave half of the compute units
-  // idle, or three quarters, its tiles are cut into two or four parts of fewer rows, with fewer MFMAs for every wave (640
-  // tiles on 256 compute units, K = 4096: 223 -> 213 us; 576 tiles: 223 -> 217.  Halves that leave every second wave
-  // without rows gained nothing).
+  // Tiles of 256 rows come one to a compute unit, in rounds.  Where the last round would leave half of the compute
+  // units idle, or three quarters, its tiles are cut into two or four parts of fewer rows, with fewer MFMAs for every
+  // wave (640 tiles on 256 compute units, K = 4096: 223 -> 213 us; 576 tiles: 223 -> 217.  Halves that leave every
+  // second wave without rows gained nothing).
   int part = 0, parts = 1;
   if constexpr (kParts<BM>) {
     const int rem = mine > 0 ? mine % p.wg_per_xcd : 0, cut = mine - rem;
@@ -303,8 +305,8 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
       const_cast<uint8_t*>(p.xq), 0, static_cast<int>(static_cast<uint32_t>(KB) * slab), kBufferFlags);
   const __amdgpu_buffer_rsrc_t wres = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(p.w + (static_cast<size_t>(e) * p.N + n0) * p.K), 0, cols * p.K, kBufferFlags);
-  // The rows of an instruction are a scalar offset in the weight (a tile's rows begin at a multiple of 16, so a lane's chunk
-  // is the same for all of them), and gathered ones in the activation.
+  // The rows of an instruction are a scalar offset in the weight (a tile's rows begin at a multiple of 16, so a lane's
+  // chunk is the same for all of them), and gathered ones in the activation.
   uint32_t offA[APW], noneW[WPW];
   int ldsA[APW], ldsW[WPW], subA[APW], subW[WPW], rowW[WPW];
 #pragma unroll
@@ -322,8 +324,8 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
 #pragma unroll
   for (int u = 0; u < WPW; ++u) {
     const int i = (wave + u * NW) % W_INS, sub = i / (BN / 8), rg = i % (BN / 8);
-    // so are columns behind the tile's last (the bounds are checked against the bytes less the scalar offset, which must
-    // not exceed them)
+    // so are columns behind the tile's last (the bounds are checked against the bytes less the scalar offset, which
+    // must not exceed them)
     rowW[u] = rg * 8 < cols ? rg * 8 * p.K : 0;
     noneW[u] = rg * 8 < cols ? 0u : kNone;
     subW[u] = sub;
@@ -331,9 +333,9 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   }
   constexpr int kWindow = 4 / WGK;                     // super-stages whose scales are brought together
   const int windows = (KS + kWindow - 1) / kWindow;
-  // Chunks of the weight at or behind K re-read the row's last one: the activation's codes there are zero.  A super-stage
-  // behind the last is asked for all the same, at offsets behind the resources: nothing is fetched, and the number of
-  // instructions in flight stays the same for every step.
+  // Chunks of the weight at or behind K re-read the row's last one: the activation's codes there are zero.  A
+  // super-stage behind the last is asked for all the same, at offsets behind the resources: nothing is fetched, and the
+  // number of instructions in flight stays the same for every step.
   auto issue = [&](uint8_t* buf, int ks) {
     uint32_t behind = ks < KS ? 0u : kNone;
     asm("" : "+s"(behind));                           // or-ed in: as a choice of offsets it became branches
@@ -644,19 +646,21 @@ struct Shape {
   bool large = false;          // 256 x 256: grouped_large.hip where it can
 };
 
-// The tile for S rows of E groups, by the rows of an average group (the groups' sizes are known on the device alone) and the
-// tiles that makes for 256 compute units.  Measured on one MI355X, whole calls, us:
+// The tile for S rows of E groups, by the rows of an average group (the groups' sizes are known on the device alone)
+// and the tiles that makes for 256 compute units.  Measured on one MI355X, whole calls, us:
 //   <= 32 rows: grouped_stream.hip (16 groups of 8 rows, N = K = 2048, MXFP8: 18.0; 128 x 128 18.9, 64 x 64 21.9).
 //   256 x 256 where it pads the average group by no more than a quarter over 128 x 128 and takes nine sixteenths of the
-//     compute units (8 groups of 192 rows, N = 5120, K = 4096, MXFP8: 54 against 62; 640 rows: 130 against 162.  Else, 320 rows: 95
-//     against 75; 128 tiles, 16 groups of 192 rows, N = K = 2048: 29.5 against 27.6).  With MXFP8 scales and groups of
-//     1024 rows or more: grouped_large.hip (32 groups, N = 4608, K = 5120, groups of 2048 rows, more or less 25: 1608 against
-//     1696; 1024 rows: 862 against 872; 512 rows: 499 against 490, its ragged tiles cost it more).
-//   While the tiles are no more than the compute units: 64 x 64, 64 x 128 or 128 x 128 (the first that are), with the waves
-//     split over K, four, two and two ways (FP32 scales, N = 5120, K = 4096, 256 rows: 27.6, 21.7, 26.3; 512 rows: 39.7,
-//     39.2, 29.1; 128 x 128 with one set of waves 35.5; 8 groups of 100 rows, N = K = 2048, MXFP8: 20.5, 16.3, 17.9).
-//   Else 128 x 128, two workgroups per compute unit, whose pauses cover each other (800 rows: 44 against 52 split; 48 rows a
-//     group, 32 groups, N = 5120, K = 2304: 98; 64 x 128 with three workgroups 106, 128 x 256 with one 109).
+//     compute units (8 groups of 192 rows, N = 5120, K = 4096, MXFP8: 54 against 62; 640 rows: 130 against 162.  Else,
+//     320 rows: 95 against 75; 128 tiles, 16 groups of 192 rows, N = K = 2048: 29.5 against 27.6).  With MXFP8 scales
+//     and groups of 1024 rows or more: grouped_large.hip (32 groups, N = 4608, K = 5120, groups of 2048 rows, more or
+//     less 25: 1608 against 1696; 1024 rows: 862 against 872; 512 rows: 499 against 490, its ragged tiles cost it
+//     more).
+//   While the tiles are no more than the compute units: 64 x 64, 64 x 128 or 128 x 128 (the first that are), with the
+//     waves split over K, four, two and two ways (FP32 scales, N = 5120, K = 4096, 256 rows: 27.6, 21.7, 26.3; 512 rows:
+//     39.7, 39.2, 29.1; 128 x 128 with one set of waves 35.5; 8 groups of 100 rows, N = K = 2048, MXFP8: 20.5, 16.3,
+//     17.9).
+//   Else 128 x 128, two workgroups per compute unit, whose pauses cover each other (800 rows: 44 against 52 split; 48
+//     rows a group, 32 groups, N = 5120, K = 2304: 98; 64 x 128 with three workgroups 106, 128 x 256 with one 109).
 Shape pick_shape(int64_t S, int64_t E, int64_t N) {
   const int64_t groups = S < E ? S : E, per = (S + E - 1) / E;
   if (per <= 32) return {32, 64};

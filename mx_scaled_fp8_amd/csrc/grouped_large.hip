@@ -25,11 +25,12 @@
 //    activation's zero codes vanish, and scale bytes behind K are cleared.
 //
 // Measured (one MI355X, whole calls): 65536 rows of 32 groups of about 2048, N = 4608, K = 5120: 1460 us, 2.1 PFLOP/s;
-// with groups of exactly 2048 rows 1330 (a group's last, ragged tile takes a whole tile's time).  What bounds it is the way
-// of the operands to LDS as much as the MFMAs: a 256 x 256 tile takes 64 KiB per 128 K, and a kernel of such tiles took
-// 1285 us for the DMA alone (580 when every tile reads the same lines) and 1130 without any.  Half of the L2's requests
-// miss.  Where tiles begin in K decides what they share there: turned by the row tile, so that the tiles that read the same
-// activation rows are at the same K, 1460; by row and column tile 1490, by the column tile 1505, not at all 1490.
+// with groups of exactly 2048 rows 1330 (a group's last, ragged tile takes a whole tile's time).  What bounds it is the
+// way of the operands to LDS as much as the MFMAs: a 256 x 256 tile takes 64 KiB per 128 K, and a kernel of such tiles
+// took 1285 us for the DMA alone (580 when every tile reads the same lines) and 1130 without any.  Half of the L2's
+// requests miss.  Where tiles begin in K decides what they share there: turned by the row tile, so that the tiles that
+// read the same activation rows are at the same K, 1460; by row and column tile 1490, by the column tile 1505, not at
+// all 1490.
 #include <type_traits>
 
 #include "grouped.hpp"
@@ -76,7 +77,8 @@ struct Tile {
 __device__ __forceinline__ void grouped_large(const GemmArgs& p) {
   __shared__ __attribute__((aligned(1024))) uint8_t st0[2 * kOp];
   __shared__ __attribute__((aligned(1024))) uint8_t st1[2 * kOp];
-  // scale words of two windows of four stages: [stage][block][W | x][half of the tile][row % 32], a byte per 32-row tile
+  // scale words of two windows of four stages: [stage][block][W | x][half of the tile][row % 32], a byte per 32-row
+  // tile
   __shared__ __attribute__((aligned(16))) uint32_t sc[2][4][4][2][2][32];
   // 4 KiB per wave: the epilogue's staging; between epilogues the next tile's row offsets in xq (256 words) and in xs
   __shared__ __attribute__((aligned(16))) uint32_t stage_lds[4096];

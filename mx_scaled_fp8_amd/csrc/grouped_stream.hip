@@ -6,24 +6,24 @@
 // What costs here is everything that lets the stream pause: tiles that end at different times, a pipeline that fills
 // and drains for each of them, and scales that arrive by loads of their own.  So
 //  * one resident workgroup per compute unit takes an equal share of the whole product: the (expert, 16 or 32 columns)
-//    units are numbered through and cut into as many ranges as there are workgroups.  A range is walked in tiles of up to 64
-//    columns (an expert's row tiles one after the other on the same columns: the weight comes from HBM once).
-//  * the pipeline runs on through the tile boundaries: a ring of S super-stages of WGK x 128 K in LDS, filled by LDS-DMA
-//    S - 1 super-stages ahead of the MFMAs, whatever tile those belong to.
+//    units are numbered through and cut into as many ranges as there are workgroups.  A range is walked in tiles of up
+//    to 64 columns (an expert's row tiles one after the other on the same columns: the weight comes from HBM once).
+//  * the pipeline runs on through the tile boundaries: a ring of S super-stages of WGK x 128 K in LDS, filled by
+//    LDS-DMA S - 1 super-stages ahead of the MFMAs, whatever tile those belong to.
 //  * the scale words (and the row indices of the next tile) come by LDS-DMA too, so one count of vector-memory
 //    instructions orders everything, and nothing else waits for memory.  LDS is read and written in inline asm with its
 //    own waits: the compiler, which cannot tell the slots of a ring apart, would drain the DMA before each access.
-//  * rows behind the group's last and columns behind the tile's last are not fetched: their offsets lie behind the buffer
-//    resource.
-// Eight waves: two share a tile's 64 columns, and four such pairs each take every fourth 128 K; their sums meet in the slot
-// that was multiplied last.  A step is short, so its instructions count: DMA offsets are registers fixed per tile, the
-// place in K a scalar offset, and what is not to be fetched has a resource of no bytes (and a scalar offset of 0: the bounds
-// are checked against the bytes less that offset).
+//  * rows behind the group's last and columns behind the tile's last are not fetched: their offsets lie behind the
+//    buffer resource.
+// Eight waves: two share a tile's 64 columns, and four such pairs each take every fourth 128 K; their sums meet in the
+// slot that was multiplied last.  A step is short, so its instructions count: DMA offsets are registers fixed per tile,
+// the place in K a scalar offset, and what is not to be fetched has a resource of no bytes (and a scalar offset of 0:
+// the bounds are checked against the bytes less that offset).
 //
 // Measured (one MI355X): one token of 8 experts, N = 4608, K = 5120 (195 MB): 39 us, 5.0 TB/s (whole
-// call 44; with a workgroup per tile 55).  512 bytes of a row at a time is what HBM wants: the pattern alone reads 5.7 TB/s, with 128 bytes 4.2 by way
-// of LDS.  For 64 or 128 rows the same ring lost against plain tiles (48 rows a group: 117 against 99 us): the scale words
-// and the steps' control are not hidden there.
+// call 44; with a workgroup per tile 55).  512 bytes of a row at a time is what HBM wants: the pattern alone reads 5.7
+// TB/s, with 128 bytes 4.2 by way of LDS.  For 64 or 128 rows the same ring lost against plain tiles (48 rows a group:
+// 117 against 99 us): the scale words and the steps' control are not hidden there.
 #include "grouped.hpp"
 
 namespace mx {
@@ -33,8 +33,8 @@ namespace {
 typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 typedef const __attribute__((address_space(4))) int32_t* const_i32;
 
-// Columns of a unit of work.  With FP32 scales the 32 columns of an MFMA tile share one, so they may not straddle a block
-// of 128.
+// Columns of a unit of work.  With FP32 scales the 32 columns of an MFMA tile share one, so they may not straddle a
+// block of 128.
 constexpr int unit_columns(bool f32) { return f32 ? 32 : 16; }
 constexpr uint32_t kNone = 0xFFFFFF80u;    // an offset behind every resource
 constexpr int kSlotBufs = 8;               // tiles whose row indices are held in LDS
@@ -74,9 +74,9 @@ struct Tile {
   int e, row0, rows, n0, cols, turn;
 };
 
-// ODD: K is no multiple of 128 (the last stage is short), or the MXFP8 weight's scale words are not 4-byte aligned (a row's
-// four of a super-stage then lie in the five aligned words around them: 46 rows of 8 groups, N = 3584, K = 4448: 38.5 us
-// against 56.5 with two words for each of the four; K = 4480: 36).
+// ODD: K is no multiple of 128 (the last stage is short), or the MXFP8 weight's scale words are not 4-byte aligned (a
+// row's four of a super-stage then lie in the five aligned words around them: 46 rows of 8 groups, N = 3584, K = 4448:
+// 38.5 us against 56.5 with two words for each of the four; K = 4480: 36).
 template <bool F32, bool ODD>
 __device__ __forceinline__ void grouped_stream(const GemmArgs& p) {
   constexpr int BM = 32, BN = 64, WGN = 2, WGK = 4, S = 3;
@@ -115,8 +115,8 @@ __device__ __forceinline__ void grouped_stream(const GemmArgs& p) {
   const int share = units / wgs, extra = units - share * wgs;
   const int u0 = share * wg + min(wg, extra), u1 = u0 + share + (wg < extra ? 1 : 0);
   if (u0 >= u1) return;
-  // The tile that begins with unit u; moves u behind it.  Tiles start at different places of K and go round, so that they
-  // do not all read the same few channels' lines: `turn` is the last tile's start.
+  // The tile that begins with unit u; moves u behind it.  Tiles start at different places of K and go round, so that
+  // they do not all read the same few channels' lines: `turn` is the last tile's start.
   auto tile_at = [&](int& u, int turn) {
     Tile t;
     int first = 0, count = total_mt, lo = 0, hi = p.S;
@@ -199,15 +199,15 @@ __device__ __forceinline__ void grouped_stream(const GemmArgs& p) {
       // chunks behind K re-read the row's last one: the activation's codes there are zero
       offT[u] = r < t.cols ? at + min(chunk, static_cast<uint32_t>(p.K - 16 - (KB - 1) * kStageK)) : kNone;
     }
+    const uint32_t row_bytes = static_cast<uint32_t>((KB + 3) & ~3) * 4;
 #pragma unroll
     for (int u = 0; u < SPW; ++u) {
       const int i = (wave + u * kWaves) % kScIns;
       if (i < kScX / 64) {
         const int word = (i * 64 + lane) % (WGK * BM), r = word % BM;
-        offS[u] = static_cast<uint32_t>(max(x_row(t, idx, min(r, t.rows - 1)), 0)) * static_cast<uint32_t>((KB + 3) & ~3) * 4 +
-                  word / BM * 4;
+        offS[u] = static_cast<uint32_t>(max(x_row(t, idx, min(r, t.rows - 1)), 0)) * row_bytes + word / BM * 4;
         sptr[u] = reinterpret_cast<const uint8_t*>(p.xs);
-        sbytes[u] = static_cast<uint32_t>(p.rows) * static_cast<uint32_t>((KB + 3) & ~3) * 4;
+        sbytes[u] = static_cast<uint32_t>(p.rows) * row_bytes;
       } else {
         const int j = i - kScX / 64, r = j % (BN / 64) * 64 + lane, sub = j / (BN / 64);
         if constexpr (F32) {
@@ -223,7 +223,8 @@ __device__ __forceinline__ void grouped_stream(const GemmArgs& p) {
           const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at) & 3);
           sptr[u] = at - mis;
           // up to the aligned word that holds the tensor's last byte
-          sbytes[u] = static_cast<uint32_t>(min(static_cast<size_t>(end - sptr[u]) + 3, static_cast<size_t>(1) << 30)) & ~3u;
+          const size_t left = static_cast<size_t>(end - sptr[u]) + 3;
+          sbytes[u] = static_cast<uint32_t>(min(left, static_cast<size_t>(1) << 30)) & ~3u;
           offS[u] = ((mis + static_cast<uint32_t>(min(r, t.cols - 1)) * static_cast<uint32_t>(K32)) & ~3u) + 4 * sub;
         }
       }

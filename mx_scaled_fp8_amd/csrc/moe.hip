@@ -10,19 +10,20 @@
 // keys are formed in FP64, which leaves near-ties of different scores to the exact order.  Equal keys: lowest index.
 //
 // Two launches, bound by latency (a few kilobytes to a few megabytes):
-//  * route_topk_kernel: 16 or 64 lanes a token, each holding every 16th or 64th expert; k rounds of a maximum across the
-//    lanes.  A workgroup takes a block of up to 64 tokens and notes in LDS, per expert, which
+//  * route_topk_kernel: 16 or 64 lanes a token, each holding every 16th or 64th expert; k rounds of a maximum across
+//    the lanes.  A workgroup takes a block of up to 64 tokens and notes in LDS, per expert, which
 //    of them picked it: a 64-bit mask.
 //  * route_scatter_kernel: the row of slot (t, j) is the number of slots of lower experts, plus those of its expert in
 //    the blocks before (sums of the masks' bit counts), plus the bits below t in its own block's mask.  So the rows of
 //    an expert are in slot order, and nothing is placed by the order of atomics.
 // A single block does the second's work in the first launch.
-// Measured (one MI355X, kernel times): 4 tokens, 64 experts, k = 6, BF16 logits: 4 us.  8192 tokens, 256 experts, k = 8,
-// sigmoid with a bias: 10 and 6 us; the logits alone would take 2.  The rest is the scores (FP64 only for experts that an
-// FP32 bound leaves in question: 83 us for all of them), k rounds of maxima, and the masks' way through memory.
+// Measured (one MI355X, kernel times): 4 tokens, 64 experts, k = 6, BF16 logits: 4 us.  8192 tokens, 256 experts, k =
+// 8, sigmoid with a bias: 10 and 6 us; the logits alone would take 2.  The rest is the scores (FP64 only for experts
+// that an FP32 bound leaves in question: 83 us for all of them), k rounds of maxima, and the masks' way through memory.
 //
-// Join.  out[t] = shared[t] + sum_j w[t, j] * y[slot_row[t, j]] in FP32, rounded once; bound by HBM: 8192 tokens, k = 8,
-// N = 5120 (839 MB) 140 us, 6.0 TB/s, with the loads of eight rows in flight and past the caches (one row at a time 186).
+// Join.  out[t] = shared[t] + sum_j w[t, j] * y[slot_row[t, j]] in FP32, rounded once; bound by HBM: 8192 tokens, k =
+// 8, N = 5120 (839 MB) 140 us, 6.0 TB/s, with the loads of eight rows in flight and past the caches (one row at a time
+// 186).
 #include "common.hpp"
 
 namespace mx {
@@ -136,8 +137,8 @@ __device__ __forceinline__ void load_logits(const RouteArgs& a, bool f32, int64_
   }
 }
 
-// One round of the choice: the largest key over a token's lanes and its expert (the lowest index of equal keys), known to
-// every lane; the key is marked as taken.
+// One round of the choice: the largest key over a token's lanes and its expert (the lowest index of equal keys), known
+// to every lane; the key is marked as taken.
 template <typename K, int LANES, int EI>
 __device__ __forceinline__ int take_largest(K (&key)[EI], int sub, K& most) {
   K best = key[0];
@@ -270,12 +271,12 @@ __device__ __forceinline__ void route_token_biased(const RouteArgs& a, bool f32,
   }
 }
 
-// Scores with a bias, without FP64 keys for every expert (a softmax's sum takes their FP64 exponentials all the same).  FP32
-// keys find the k-th largest of different ones, which is at most the k-th largest; an FP32 key is within 2^-20 (1 + |key|)
-// of its FP64 one (an exponential, a reciprocal or a product of values up to 1, the bias's addition: a few 2^-24 each), so
-// the k largest are among the experts whose FP32 key is at least that one's less 2^-18 (1 + |key|).  Those, k and rarely
-// more, get FP64 keys and are ordered by counting, for each, the ones before it.  Returns false, nothing written, if they
-// do not fit (many equal keys, or fewer than k different ones left).
+// Scores with a bias, without FP64 keys for every expert (a softmax's sum takes their FP64 exponentials all the same).
+// FP32 keys find the k-th largest of different ones, which is at most the k-th largest; an FP32 key is within 2^-20 (1
+// + |key|) of its FP64 one (an exponential, a reciprocal or a product of values up to 1, the bias's addition: a few
+// 2^-24 each), so the k largest are among the experts whose FP32 key is at least that one's less 2^-18 (1 + |key|).
+// Those, k and rarely more, get FP64 keys and are ordered by counting, for each, the ones before it.  Returns false,
+// nothing written, if they do not fit (many equal keys, or fewer than k different ones left).
 template <int LANES>
 struct Candidates {
   static constexpr int kMost = LANES == 16 ? 32 : 64;
@@ -543,8 +544,8 @@ struct CombineArgs {
   uint64_t total;             // T * N8
 };
 
-// A thread owns 8 consecutive columns of one token.  Eight slots' rows are in flight at a time; a dropped slot reads row
-// 0 and is left out of the sum (a select, so that what the row holds does not matter).
+// A thread owns 8 consecutive columns of one token.  Eight slots' rows are in flight at a time; a dropped slot reads
+// row 0 and is left out of the sum (a select, so that what the row holds does not matter).
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
   typedef unsigned v4u __attribute__((ext_vector_type(4)));
   const uint64_t i = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -591,16 +592,16 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
   reinterpret_cast<v4u*>(a.out)[i] = o;
 }
 
-// 16 lanes a token while its experts' scores and keys fit the registers and k the lanes, and 64 lanes else, or where there
-// are several experts a lane and few tokens, so that latency counts (256 experts, k = 8, kernels of a call, us: 64 tokens,
-// softmax with a bias 11.6 against 30.1, without 8.9 against 12.0; 2048 tokens 14.2 against 21.9 and 11.3 against 12.2; 64
-// experts, 500 tokens 8.6 against 7.6).
+// 16 lanes a token while its experts' scores and keys fit the registers and k the lanes, and 64 lanes else, or where
+// there are several experts a lane and few tokens, so that latency counts (256 experts, k = 8, kernels of a call, us:
+// 64 tokens, softmax with a bias 11.6 against 30.1, without 8.9 against 12.0; 2048 tokens 14.2 against 21.9 and 11.3
+// against 12.2; 64 experts, 500 tokens 8.6 against 7.6).
 bool route_wide(int64_t T, int32_t E, int32_t k) { return k > 16 || E > 256 || (E > 128 && T > 32 && T <= 8 * 256); }
-// Tokens of a block.  One block takes up to 64, in one launch.  More are cut into blocks of 32, the tokens that a workgroup
-// works on at once with 16 lanes each (8192 tokens, 256 experts, sigmoid with a bias: 30 against 35 us with 64 when this was
-// measured), until longer blocks fill the chip too and halve the masks that the second launch reads.  With 64 lanes a token
-// a workgroup works on 8 at once: blocks of 8 then, while they are no more than the compute units (450 experts, 79 tokens:
-// 11 to 16 us by the score, 23 to 41 with blocks of 32).
+// Tokens of a block.  One block takes up to 64, in one launch.  More are cut into blocks of 32, the tokens that a
+// workgroup works on at once with 16 lanes each (8192 tokens, 256 experts, sigmoid with a bias: 30 against 35 us with
+// 64 when this was measured), until longer blocks fill the chip too and halve the masks that the second launch reads.
+// With 64 lanes a token a workgroup works on 8 at once: blocks of 8 then, while they are no more than the compute units
+// (450 experts, 79 tokens: 11 to 16 us by the score, 23 to 41 with blocks of 32).
 int route_block_tokens(int64_t T, int32_t E) {
   if (T > 32 * 1024) return kBlockTokens;
   if (T <= (E > 256 ? 16 : E > 128 ? 32 : kBlockTokens)) return kBlockTokens;
