@@ -24,11 +24,11 @@
 //
 // What bounds grouped_gemm_kernel (one MI355X, kernel times):
 //   128 x 128, 1544 rows of 32 groups, N = 5120, K = 2304, MXFP8: 95 us for 377 MB of weights, 4.0 TB/s.  The same
-//     without MFMAs takes as long, with every tile on the same weight rows 52, without the x rows 88, without stores 86:
-//     the weights' stream, and the tiles' other traffic in its gaps.
+//     without MFMAs takes as long, with every tile on the same weight rows 52, without the x rows 88, without stores
+//     86: the weights' stream, and the tiles' other traffic in its gaps.
 //   256 x 256, 8192 rows, N = 5120, K = 4096, FP32 scales: 185 to 200 us, 1.7 to 1.9 PFLOP/s.  Without the fma's 6 %
-//     less, with no DMA 20 % less, with operands of zeros 12 % less (the clock follows the power that the operands' bits
-//     draw).
+//     less, with no DMA 20 % less, with operands of zeros 12 % less (the clock follows the power that the operands'
+//     bits draw).
 #include <type_traits>
 
 #include "grouped.hpp"
@@ -648,25 +648,28 @@ struct Shape {
 
 // The tile for S rows of E groups, by the rows of an average group (the groups' sizes are known on the device alone)
 // and the tiles that makes for 256 compute units.  Measured on one MI355X, whole calls, us:
-//   <= 32 rows: grouped_stream.hip (16 groups of 8 rows, N = K = 2048, MXFP8: 18.0; 128 x 128 18.9, 64 x 64 21.9).
+//   <= 32 rows: grouped_stream.hip (32 groups of a row, N = 4608, K = 2304, MXFP8: 69 against 79 with 128 x 128; 16
+//     groups of 8 rows, N = K = 2048: 18.0 against 18.9), but for few stages and many tiles: its tiles are short then,
+//     and 128 x 128 as below (K = 1152: 43, 43; K = 576: 32, 26; 8 groups, K = 576: 14.7, 11.7).
 //   256 x 256 where it pads the average group by no more than a quarter over 128 x 128 and takes nine sixteenths of the
-//     compute units (8 groups of 192 rows, N = 5120, K = 4096, MXFP8: 54 against 62; 640 rows: 130 against 162.  Else,
-//     320 rows: 95 against 75; 128 tiles, 16 groups of 192 rows, N = K = 2048: 29.5 against 27.6).  With MXFP8 scales
-//     and groups of 1024 rows or more: grouped_large.hip (32 groups, N = 4608, K = 5120, groups of 2048 rows, more or
-//     less 25: 1608 against 1696; 1024 rows: 862 against 872; 512 rows: 499 against 490, its ragged tiles cost it
-//     more).
+//     compute units, or 128 x 128 would not fit them in one round of two (8 groups of 192 rows, N = 5120, K = 4096,
+//     MXFP8: 54 against 62; 640 rows: 130 against 162.  Else, 320 rows: 95 against 75; 128 tiles, 16 groups of 192
+//     rows, N = K = 2048: 29.5 against 27.6).  With MXFP8 scales and groups of 1024 rows or more: grouped_large.hip (32
+//     groups, N = 4608, K = 5120, groups of 2048 rows, more or less 25: 1608 against 1696; 1024 rows: 862 against 872;
+//     512 rows: 499 against 490, its ragged tiles cost it more).
 //   While the tiles are no more than the compute units: 64 x 64, 64 x 128 or 128 x 128 (the first that are), with the
-//     waves split over K, four, two and two ways (FP32 scales, N = 5120, K = 4096, 256 rows: 27.6, 21.7, 26.3; 512 rows:
-//     39.7, 39.2, 29.1; 128 x 128 with one set of waves 35.5; 8 groups of 100 rows, N = K = 2048, MXFP8: 20.5, 16.3,
-//     17.9).
+//     waves split over K, four, two and two ways (FP32 scales, N = 5120, K = 4096, 256 rows: 27.6, 21.7, 26.3; 512
+//     rows: 39.7, 39.2, 29.1; 128 x 128 with one set of waves 35.5; 8 groups of 100 rows, N = K = 2048, MXFP8: 20.5,
+//     16.3, 17.9).
 //   Else 128 x 128, two workgroups per compute unit, whose pauses cover each other (800 rows: 44 against 52 split; 48
 //     rows a group, 32 groups, N = 5120, K = 2304: 98; 64 x 128 with three workgroups 106, 128 x 256 with one 109).
-Shape pick_shape(int64_t S, int64_t E, int64_t N) {
+Shape pick_shape(int64_t S, int64_t E, int64_t N, int64_t K) {
   const int64_t groups = S < E ? S : E, per = (S + E - 1) / E;
-  if (per <= 32) return {32, 64};
   auto ceil_to = [](int64_t v, int64_t m) { return (v + m - 1) / m * m; };
   auto tiles = [&](int64_t bm, int64_t bn) { return groups * (ceil_to(per, bm) / bm) * (ceil_to(N, bn) / bn); };
-  if (4 * ceil_to(per, 256) <= 5 * ceil_to(per, 128) && tiles(256, 256) >= 144) return {256, 256, false, per >= 1024};
+  if (per <= 32) return K <= 1152 && tiles(128, 128) >= 256 ? Shape{128, 128} : Shape{32, 64};
+  if (4 * ceil_to(per, 256) <= 5 * ceil_to(per, 128) && (tiles(256, 256) >= 144 || tiles(128, 128) > 512))
+    return {256, 256, false, per >= 1024};
   if (tiles(64, 64) <= 256) return {64, 64, true};
   if (tiles(64, 128) <= 256) return {64, 128, true};
   return {128, 128, tiles(128, 128) <= 256};
@@ -696,7 +699,7 @@ void launch_gemm(const Shape s, const GemmArgs& a, int64_t tiles, hipStream_t st
 size_t grouped_workspace_bytes(int64_t rows, int64_t S, int64_t E, int64_t N, int64_t K) {
   if (rows <= 0 || S <= 0 || E <= 0) return 0;
   const int64_t KB = (K + kStageK - 1) / kStageK;
-  const Shape s = pick_shape(S, E, N);
+  const Shape s = pick_shape(S, E, N, K);
   return align_up(sizeof(RowTile) * (1 + max_row_tiles(S, E, s.BM))) + align_up(rows * KB * kStageK) +
          align_up(rows * ((KB + 3) / 4 * 4) * 4);
 }
@@ -705,7 +708,7 @@ mx_status launch_grouped(const void* x, int64_t rows, const uint8_t* w, const vo
                          const int32_t* offsets, const int32_t* row_slot, int32_t k, int64_t S, int64_t E, int64_t N,
                          int64_t K, void* out, void* workspace, hipStream_t stream, const char* what) {
   const int64_t KB = (K + kStageK - 1) / kStageK;
-  const Shape s = pick_shape(S, E, N);
+  const Shape s = pick_shape(S, E, N, K);
   const int64_t mt = max_row_tiles(S, E, s.BM);
   uint8_t* at = static_cast<uint8_t*>(workspace);
   RowTile* const tiles = reinterpret_cast<RowTile*>(at);

@@ -260,6 +260,14 @@ def test_grouped_shares_of_many_columns(fmt, K, counts, N):
     _run_grouped(3 * K + N, fmt, counts, N, K)
 
 
+@pytest.mark.parametrize("fmt,K", [("mx", 1184), ("mx", 1280), ("f32", 1168), ("f32", 1280)])
+@pytest.mark.parametrize("counts,N,gather", [([5, 0, 31, 9], 8208, None), ([1] * 64, 2320, None), ([40, 0, 20, 3], 4112, 7),
+                                             ([0, 32, 1, 33, 0, 2], 5136, 50)])
+def test_grouped_shares_of_long_rows(fmt, K, counts, N, gather):
+    """The same for rows of more stages, which small groups take there."""
+    _run_grouped(2 * K + N, fmt, counts, N, K, gather=gather, k=2)
+
+
 @pytest.mark.parametrize("fmt", ["mx", "f32"])
 def test_grouped_bad_slots_and_nonfinite_inputs(fmt):
     def spoil(x, w, ws, slots):
