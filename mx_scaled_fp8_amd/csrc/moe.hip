@@ -544,8 +544,10 @@ struct CombineArgs {
   uint64_t total;             // T * N8
 };
 
-// A thread owns 8 consecutive columns of one token.  Eight slots' rows are in flight at a time; a dropped slot reads
-// row 0 and is left out of the sum (a select, so that what the row holds does not matter).
+// A thread owns 8 consecutive columns of one token.  J slots' rows are in flight at a time, at most 8, so that the last
+// turn is full too (k = 4, 6868 x 5080: 84 us with 8, 64); a dropped slot reads row 0 and is left out of the sum (a
+// select, so that what the row holds does not matter).
+template <int J>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
   typedef unsigned v4u __attribute__((ext_vector_type(4)));
   const uint64_t i = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -556,12 +558,12 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
   if (a.shared != nullptr) sh = reinterpret_cast<const v4u*>(a.shared)[i];
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (a.rows > 0) {
-    for (int j0 = 0; j0 < a.k; j0 += 8) {
-      int r[8];
-      float w[8];
-      v4u v[8];
+    for (int j0 = 0; j0 < a.k; j0 += J) {
+      int r[J];
+      float w[J];
+      v4u v[J];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < J; ++j) {
         const uint64_t s = t * a.k + min(j0 + j, a.k - 1);
         r[j] = a.slot_row[s];
         w[j] = a.weights[s];
@@ -571,10 +573,10 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
         }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < J; ++j)
         v[j] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(a.y) + (static_cast<uint64_t>(r[j]) * a.N8 + c));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < J; ++j) {
         const bool in = w[j] != 0.f;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -685,7 +687,18 @@ mx_status launch_moe_combine(const void* y, int64_t rows, int64_t N, const int32
   a.N8 = static_cast<uint32_t>(N / 8);
   a.n8_div = make_div(a.N8);
   a.total = static_cast<uint64_t>(T) * a.N8;
-  combine_kernel<<<static_cast<unsigned>((a.total + 255) / 256), 256, 0, stream>>>(a);
+  const unsigned grid = static_cast<unsigned>((a.total + 255) / 256);
+  const int turns = (k + 7) / 8;
+  switch ((k + turns - 1) / turns) {
+    case 1: combine_kernel<1><<<grid, 256, 0, stream>>>(a); break;
+    case 2: combine_kernel<2><<<grid, 256, 0, stream>>>(a); break;
+    case 3: combine_kernel<3><<<grid, 256, 0, stream>>>(a); break;
+    case 4: combine_kernel<4><<<grid, 256, 0, stream>>>(a); break;
+    case 5: combine_kernel<5><<<grid, 256, 0, stream>>>(a); break;
+    case 6: combine_kernel<6><<<grid, 256, 0, stream>>>(a); break;
+    case 7: combine_kernel<7><<<grid, 256, 0, stream>>>(a); break;
+    default: combine_kernel<8><<<grid, 256, 0, stream>>>(a); break;
+  }
   return launch_status("mx_moe_combine");
 }
 

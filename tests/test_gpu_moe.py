@@ -374,7 +374,8 @@ def test_block128_scales_that_are_no_powers_of_two():
 
 # --------------------------------------------------------------------- join
 
-@pytest.mark.parametrize("T,k,N", [(1, 1, 8), (1, 8, 5120), (5, 3, 16), (64, 6, 1032), (1000, 8, 2304), (3, 40, 264)])
+@pytest.mark.parametrize("T,k,N", [(1, 1, 8), (1, 8, 5120), (5, 3, 16), (64, 6, 1032), (1000, 8, 2304), (3, 40, 264),
+                                   (7, 2, 40), (9, 4, 520), (6, 5, 264), (4, 7, 1032), (5, 9, 264), (3, 12, 72), (3, 17, 8)])
 @pytest.mark.parametrize("shared", [False, True])
 def test_combine(T, k, N, shared):
     rng = np.random.default_rng(T + k + N)
