@@ -649,8 +649,9 @@ struct Shape {
 // The tile for S rows of E groups, by the rows of an average group (the groups' sizes are known on the device alone)
 // and the tiles that makes for 256 compute units.  Measured on one MI355X, whole calls, us:
 //   <= 32 rows: grouped_stream.hip (32 groups of a row, N = 4608, K = 2304, MXFP8: 69 against 79 with 128 x 128; 16
-//     groups of 8 rows, N = K = 2048: 18.0 against 18.9), but for few stages and many tiles: its tiles are short then,
-//     and 128 x 128 as below (K = 1152: 43, 43; K = 576: 32, 26; 8 groups, K = 576: 14.7, 11.7).
+//     groups of 8 rows, N = K = 2048: 18.0 against 18.9), but not for short rows where a workgroup's share is more than
+//     one of its tiles, whose few stages hide nothing: there 128 x 128 as below (8 groups, N = 3584, K = 1152: 16.3
+//     against 13.7, K = 576: 14.4, 10.1; N = 2048: 10.2, 12.7 and 9.0, 9.5).
 //   256 x 256 where it pads the average group by no more than a quarter over 128 x 128 and takes nine sixteenths of the
 //     compute units, or 128 x 128 would not fit them in one round of two (8 groups of 192 rows, N = 5120, K = 4096,
 //     MXFP8: 54 against 62; 640 rows: 130 against 162.  Else, 320 rows: 95 against 75; 128 tiles, 16 groups of 192
@@ -667,7 +668,7 @@ Shape pick_shape(int64_t S, int64_t E, int64_t N, int64_t K) {
   const int64_t groups = S < E ? S : E, per = (S + E - 1) / E;
   auto ceil_to = [](int64_t v, int64_t m) { return (v + m - 1) / m * m; };
   auto tiles = [&](int64_t bm, int64_t bn) { return groups * (ceil_to(per, bm) / bm) * (ceil_to(N, bn) / bn); };
-  if (per <= 32) return K <= 1152 && tiles(128, 128) >= 256 ? Shape{128, 128} : Shape{32, 64};
+  if (per <= 32) return K <= 1152 && tiles(128, 128) > 128 ? Shape{128, 128} : Shape{32, 64};
   if (4 * ceil_to(per, 256) <= 5 * ceil_to(per, 128) && (tiles(256, 256) >= 144 || tiles(128, 128) > 512))
     return {256, 256, false, per >= 1024};
   if (tiles(64, 64) <= 256) return {64, 64, true};
