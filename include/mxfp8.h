@@ -374,7 +374,8 @@ mx_status mx_linear_block128(const void* x, int64_t M, int64_t K, const uint8_t*
  * l' = l with NaN taken as -inf and +inf as the largest finite FP32; an expert
  * with l' = -inf is masked out.
  * p  = softmax(l') over the experts (MX_ROUTE_SOFTMAX) or 1 / (1 + exp(-l'))
- *      (MX_ROUTE_SIGMOID); 0 for masked experts.
+ *      (MX_ROUTE_SIGMOID); 0 for masked experts.  A sigmoid keeps the range of FP64
+ *      (0 below l' = -709.8), so that its ratios hold where FP32 scores would be 0.
  * The k experts of largest key are chosen, largest first, equal keys by the
  * lower index: key = l' without a bias, p + bias (in FP64) with one, -inf for a
  * masked expert or a NaN key.  Masked experts are only chosen when fewer than

@@ -160,7 +160,10 @@ __device__ __forceinline__ int take_largest(K (&key)[EI], int sub, K& most) {
 
 // Token t by LANES lanes, of which this is number `sub`, without a bias: the logits are the keys, and only the chosen
 // ones' scores are needed (all of a softmax's sum unless the weights are renormalised).  Sets `bit` in the masks of the
-// token's experts.
+// token's experts.  A sigmoid far below 0 is 0 in FP32 (exp(-l) overflows at l = -88.7) while the weights, ratios of
+// such scores, are not: tokens with a chosen logit below kFarLogit, where exp(-l) and the score are far inside FP32's
+// normal range, take their k scores in FP64, as those with a bias do.
+constexpr float kFarLogit = -64.0f;
 template <int LANES, int EI>
 __device__ __forceinline__ void route_token_plain(const RouteArgs& a, bool f32, int64_t t, int sub, uint32_t* mask,
                                                   uint32_t bit) {
@@ -170,31 +173,42 @@ __device__ __forceinline__ void route_token_plain(const RouteArgs& a, bool f32, 
 #pragma unroll
   for (int i = 0; i < EI; ++i) key[i] = i * LANES + sub < a.E ? key_of(l[i]) : taken_key<uint32_t>();
   int my_id = 0;
-  uint32_t my_key = 0, top_key = 0;
+  uint32_t my_key = 0, top_key = 0, low_key = 0;
   for (int j = 0; j < a.k; ++j) {
-    uint32_t most;
-    const int id = take_largest<uint32_t, LANES>(key, sub, most);
-    top_key = j == 0 ? most : top_key;
+    const int id = take_largest<uint32_t, LANES>(key, sub, low_key);
+    top_key = j == 0 ? low_key : top_key;
     my_id = sub == j ? id : my_id;
-    my_key = sub == j ? most : my_key;
+    my_key = sub == j ? low_key : my_key;
   }
   const float ninf = -__builtin_inff();
   const float x = value_of(my_key), top = value_of(top_key);
-  float p = 0.f;
-  if (sub < a.k && x != ninf) p = a.score == MX_ROUTE_SOFTMAX ? expf(x - top) : 1.0f / (1.0f + expf(-x));
-  if (a.renormalize) {
-    const float sum = across<LANES>(p, Sum());
-    p = sum > 0.f ? p / sum : 0.f;
-  } else if (a.score == MX_ROUTE_SOFTMAX) {
-    float total = 0.f;
+  const bool chosen = sub < a.k && x != ninf;
+  float w;
+  if (a.score == MX_ROUTE_SIGMOID && value_of(low_key) < kFarLogit) {
+    double p = chosen ? 1 / (1 + exp(-static_cast<double>(x))) : 0;
+    if (a.renormalize) {
+      const double sum = across<LANES>(p, Sum());
+      p = sum > 0 ? p / sum : 0;
+    }
+    w = static_cast<float>(p * static_cast<double>(a.scale));
+  } else {
+    float p = 0.f;
+    if (chosen) p = a.score == MX_ROUTE_SOFTMAX ? expf(x - top) : 1.0f / (1.0f + expf(-x));
+    if (a.renormalize) {
+      const float sum = across<LANES>(p, Sum());
+      p = sum > 0.f ? p / sum : 0.f;
+    } else if (a.score == MX_ROUTE_SOFTMAX) {
+      float total = 0.f;
 #pragma unroll
-    for (int i = 0; i < EI; ++i) total += l[i] == ninf ? 0.f : __expf(l[i] - top);
-    total = across<LANES>(total, Sum());
-    p = total > 0.f ? p / total : 0.f;
+      for (int i = 0; i < EI; ++i) total += l[i] == ninf ? 0.f : __expf(l[i] - top);
+      total = across<LANES>(total, Sum());
+      p = total > 0.f ? p / total : 0.f;
+    }
+    w = p * a.scale;
   }
   if (sub < a.k) {
     a.ids[t * a.k + sub] = my_id;
-    a.weights[t * a.k + sub] = p * a.scale;
+    a.weights[t * a.k + sub] = w;
     atomicOr(&mask[my_id], bit);
   }
 }

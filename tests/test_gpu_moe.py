@@ -117,6 +117,28 @@ def test_route_repeats_bit_for_bit():
         assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+@pytest.mark.parametrize("E", [70, 300])
+@pytest.mark.parametrize("score", [mx.MX_ROUTE_SOFTMAX, mx.MX_ROUTE_SIGMOID])
+@pytest.mark.parametrize("bias", [False, True])
+def test_route_logits_below_the_range_of_fp32_scores(E, score, bias):
+    """exp(-l) overflows FP32 at l = -88.7 and FP64 at -709.8: between them the weights are the scores' ratios all the
+    same, with a bias of zeros or none."""
+    rows = [[-95, -96, -97, -98], [-85, -92, -92.5, -103], [-88, -88.5, -88.75, -89], [-64, -64.25, -63.75, -65],
+            [-100, -110, -120, -130], [-650, -651, -652.5, -690], [-700, -720, -800, -900], [3, -20, -70, -140],
+            [-90, -np.inf, -np.inf, -91], [-720, -721, -722, -723]]
+    l = np.full((len(rows), E), -1000.0, dtype=np.float32)
+    for t, r in enumerate(rows):
+        l[t, [5, E - 3, 17, 40]] = r
+    b = np.zeros(E, dtype=np.float32) if bias else None
+    say("route far logits", E, score, bias)
+    for k in (3, 4):
+        _check_route(l.astype(np.float64), _f32(l), k, b, score, True, 2.5)
+        # scores as they are, to FP32's smallest steps (2^-149)
+        got = mx.mx_moe_route(_f32(l), k, bias=None if b is None else _f32(b), score=score, renormalize=False)[1]
+        ref = M.route(l.astype(np.float64), k, b, score, False)[1]
+        assert np.all(np.abs(got.cpu().numpy() - ref) <= 2.0 ** -17 * ref + 2.0 ** -149)
+
+
 # ---------------------------------------------------------------- products
 
 def _weights(rng, lead, N, K, fmt):
