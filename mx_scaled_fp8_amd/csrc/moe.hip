@@ -290,7 +290,7 @@ __device__ __forceinline__ void route_token_biased(const RouteArgs& a, bool f32,
 // + |key|) of its FP64 one (an exponential, a reciprocal or a product of values up to 1, the bias's addition: a few
 // 2^-24 each), so the k largest are among the experts whose FP32 key is at least that one's less 2^-18 (1 + |key|).
 // Those, k and rarely more, get FP64 keys and are ordered by counting, for each, the ones before it.  Returns false,
-// nothing written, if they do not fit (many equal keys, or fewer than k different ones left).
+// nothing written, if they do not fit (many equal keys, or fewer than k different ones left) or the bound is not finite.
 template <int LANES>
 struct Candidates {
   static constexpr int kMost = LANES == 16 ? 32 : 64;
@@ -345,12 +345,14 @@ __device__ __forceinline__ bool route_token_preselected(const RouteArgs& a, bool
     most = d;
   }
   const float kth = value_of(most);
-  const float least = kth - 0x1p-18f * (1.0f + fabsf(kth));   // NaN or infinite where kth is
+  // NaN or -inf where kth is infinite, and -inf for a kth next to the lowest value (a bias that masks), where masked
+  // experts, whose FP32 key is -inf too, would be among the candidates
+  const float least = kth - 0x1p-18f * (1.0f + fabsf(kth));
   uint32_t mine = 0;
 #pragma unroll
   for (int i = 0; i < EI; ++i) mine |= (i * LANES + sub < a.E && key[i] >= least ? 1u : 0u) << i;
   const int total = across<LANES>(static_cast<int>(__popc(mine)), Sum());
-  if (!below || !(fabsf(kth) <= __FLT_MAX__) || total > c.kMost) return false;
+  if (!below || !(least >= -__FLT_MAX__) || total > c.kMost) return false;
 
   while (mine != 0) {
     const int i = __ffs(mine) - 1;

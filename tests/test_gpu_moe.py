@@ -139,6 +139,24 @@ def test_route_logits_below_the_range_of_fp32_scores(E, score, bias):
         assert np.all(np.abs(got.cpu().numpy() - ref) <= 2.0 ** -17 * ref + 2.0 ** -149)
 
 
+@pytest.mark.parametrize("E", [16, 300])
+@pytest.mark.parametrize("score", [mx.MX_ROUTE_SOFTMAX, mx.MX_ROUTE_SIGMOID])
+def test_route_bias_of_the_lowest_value_beside_masked_experts(E, score):
+    """A bias of the type's lowest value ranks its expert behind all others with a finite key, but before the masked."""
+    low = np.finfo(np.float32).min
+    l = np.full((4, E), -np.inf, dtype=np.float32)
+    l[0, [3, 9]] = 1.0, 2.0                    # two left, the second behind the lowest bias
+    l[1, [3, 9, 11]] = 1.0, 2.0, 0.5
+    l[2, 9] = 2.0
+    l[3] = 0.25
+    say("route lowest bias", E, score)
+    for bias in (low, np.float32(-3.4e38), np.float32(low * 0.999)):
+        b = np.zeros(E, dtype=np.float32)
+        b[9] = bias
+        for k in (1, 2, 3):
+            _check_route(l.astype(np.float64), _f32(l), k, b, score)
+
+
 # ---------------------------------------------------------------- products
 
 def _weights(rng, lead, N, K, fmt):
