@@ -394,7 +394,8 @@ mx_status mx_linear_block128(const void* x, int64_t M, int64_t K, const uint8_t*
  * The result does not depend on timing (no position comes from an atomic).
  * Requires: T >= 0 (0 writes offsets of zero), 1 <= E <= MX_ROUTE_MAX_EXPERTS,
  * 1 <= k <= min(E, MX_ROUTE_MAX_K), T < 2^29 - 64, T * k < 2^31; FP32 and int32
- * tensors 4-byte, BF16 logits 2-byte aligned.
+ * tensors 4-byte, BF16 logits 2-byte aligned; outputs and workspace overlap
+ * neither each other nor an input.
  */
 size_t mx_moe_route_workspace_bytes(int64_t T, int32_t E);
 mx_status mx_moe_route(const void* logits, int32_t logits_f32, const float* bias, int64_t T,

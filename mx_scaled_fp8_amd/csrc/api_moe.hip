@@ -53,6 +53,20 @@ mx_status mx_moe_route(const void* logits, int32_t logits_f32, const float* bias
     MX_CHECK(workspace_bytes >= need && (need == 0 || (workspace && aligned(workspace, 8))),
              "%s: workspace of %zu bytes (8-byte aligned) needed, got %zu", fn, need, workspace_bytes);
   }
+  // The kernels read ids and the workspace back as indices, so nothing may have been written over them.  (Not in a dry
+  // run, whose pointers are stand-ins.)
+  if (!dry_run()) {
+    const size_t n = static_cast<size_t>(T), slots = n * k * 4;
+    const struct { const char* name; const void* at; size_t bytes; } part[] = {
+        {"ids", ids, slots}, {"weights", weights, slots}, {"row_slot", row_slot, slots}, {"slot_row", slot_row, slots},
+        {"offsets", offsets, (static_cast<size_t>(E) + 1) * 4},
+        {"workspace", workspace, mx_moe_route_workspace_bytes(T, E)},
+        {"logits", logits, n * E * (logits_f32 ? 4 : 2)}, {"bias", bias, static_cast<size_t>(E) * 4}};
+    for (int i = 0; i < 6; ++i)
+      for (int j = i + 1; j < 8; ++j)
+        MX_CHECK(apart(part[i].at, part[i].bytes, part[j].at, part[j].bytes), "%s: %s overlaps %s", fn, part[i].name,
+                 part[j].name);
+  }
   MX_PREAMBLE();
   count(C_MOE_ROUTE);
   const mx_status st = launch_moe_route(logits, logits_f32, bias, T, E, k, score, renormalize, scale, ids, weights,

@@ -46,6 +46,32 @@ def test_route_validation(dry):
         assert mx.lib().mx_last_error().decode()
 
 
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="stand-in pointers must reach no GPU")
+
+
+@no_gpu
+def test_route_refuses_tensors_that_overlap():
+    """Outside a dry run, before any device is asked for: a call of tensors that lie apart gets as far as that."""
+    T, E, k = 100, 64, 8
+    names = ("logits", "bias", "ids", "weights", "offsets", "row_slot", "slot_row", "ws")
+    size = dict(logits=T * E * 4, bias=E * 4, offsets=(E + 1) * 4, ws=mx.mx_moe_route_workspace_bytes(T, E))
+    size.update((n, T * k * 4) for n in ("ids", "weights", "row_slot", "slot_row"))
+    at, places = FAKE, {}
+    for n in names:                                                  # back to back
+        places[n] = at
+        at += -(-size[n] // 8) * 8
+    assert _route(T=T, E=E, k=k, **places) == mx.MX_ERR_UNSUPPORTED
+    for a in names:
+        for b in names:
+            if a == b or {a, b} == {"logits", "bias"}:
+                continue
+            for place in (places[b], places[b] + (size[b] - 8) // 8 * 8):
+                assert _route(T=T, E=E, k=k, **dict(places, **{a: place})) == mx.MX_ERR_INVALID_ARG, (a, b)
+                assert "overlaps" in mx.lib().mx_last_error().decode()
+    # a bias inside the logits is read alone
+    assert _route(T=T, E=E, k=k, **dict(places, bias=places["logits"])) == mx.MX_ERR_UNSUPPORTED
+
+
 def _grouped(**kw):
     a = dict(x=FAKE, rows=100, K=576, w=BIG, ws=FAKE, kind=0, E=8, N=512, offsets=FAKE, row_slot=FAKE, k=2, S=200,
              act=0, out=2 * BIG, work=FAKE, wb=1 << 40)
