@@ -358,7 +358,8 @@ mx_status mx_linear_noalloc(const void* x, int64_t M, int64_t K, const void* w,
  *          that may overlap need one each.
  * Requires: M >= 0 (0 is a no-op), N, K >= 16, N % 16 == 0, K % 16 == 0,
  * K < 2^22, M * (K rounded up to 128) < 2^32, (M/128 + 1) * ceil(N/128) < 2^23 - 512,
- * x, w and out 16-byte aligned, w_scale 4-byte aligned; out overlaps no input and not the workspace.
+ * x, w and out 16-byte aligned, w_scale 4-byte aligned; out and the workspace overlap no input and not
+ * each other.
  */
 size_t mx_linear_block128_workspace_bytes(int64_t M, int64_t N, int64_t K);
 mx_status mx_linear_block128(const void* x, int64_t M, int64_t K, const uint8_t* w,
@@ -432,7 +433,7 @@ mx_status mx_moe_route(const void* logits, int32_t logits_f32, const float* bias
  * N, K >= 16, N % 16 == 0, K % 32 == 0 (E8M0) or K % 16 == 0 (FP32), K < 2^22,
  * rows * (K rounded up to 128) < 2^32, S < 2^31, E < 2^20, (S/128 + min(S, E)) *
  * ceil(N/128) < 2^23 - 512, x, w and out 16-byte aligned, FP32 scales, offsets and
- * row_slot 4-byte aligned; out overlaps no input and not the workspace.
+ * row_slot 4-byte aligned; out and the workspace overlap no input and not each other.
  */
 size_t mx_grouped_linear_workspace_bytes(int64_t rows, int64_t S, int64_t E, int64_t N, int64_t K);
 mx_status mx_grouped_linear(const void* x, int64_t rows, int64_t K, const uint8_t* w,

@@ -118,15 +118,17 @@ mx_status grouped_check(const char* fn, const void* x, int64_t rows, int64_t x_w
   MX_CHECK(!f32 || aligned(w_scale, 4), "%s: FP32 w_scale must be 4-byte aligned", fn);
   MX_CHECK(workspace && aligned(workspace, 16) && workspace_bytes >= need,
            "%s: workspace of %zu bytes (16-byte aligned) needed, got %zu", fn, need, workspace_bytes);
-  const uintptr_t ob = reinterpret_cast<uintptr_t>(out), obytes = static_cast<uintptr_t>(S) * N * 2;
-  auto apart = [&](const void* p, int64_t bytes) {
-    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
-    return !p || b + bytes <= ob || ob + obytes <= b;
-  };
-  const int64_t scale_bytes = f32 ? E * ((N + 127) / 128) * ((K + 127) / 128) * 4 : E * N * (K / MX_LINEAR_BLOCK);
-  MX_CHECK(apart(x, rows * x_width * 2) && apart(w, E * N * K) && apart(w_scale, scale_bytes) &&
-               apart(offsets, (E + 1) * 4) && apart(row_slot, S * 4) && apart(workspace, static_cast<int64_t>(need)),
-           "%s: out overlaps an input or the workspace", fn);
+  const struct { const char* name; const void* at; int64_t bytes; } in[] = {
+      {"x", x, rows * x_width * 2}, {"w", w, E * N * K},
+      {"w_scale", w_scale, f32 ? E * ((N + 127) / 128) * ((K + 127) / 128) * 4 : E * N * (K / MX_LINEAR_BLOCK)},
+      {"offsets", offsets, (E + 1) * 4}, {"row_slot", row_slot, S * 4}};
+  MX_CHECK(apart(out, S * N * 2, workspace, need), "%s: out overlaps the workspace", fn);
+  for (const auto& t : in) {
+    MX_CHECK(apart(out, S * N * 2, t.at, t.bytes), "%s: out overlaps %s", fn, t.name);
+    // The list of row tiles and the codes are written while the offsets and x are read.  (Not in a dry run, whose
+    // pointers are stand-ins.)
+    MX_CHECK(dry_run() || apart(workspace, need, t.at, t.bytes), "%s: the workspace overlaps %s", fn, t.name);
+  }
   return MX_OK;
 }
 

@@ -115,6 +115,31 @@ def test_block128_validation(dry):
         assert f(**bad) == mx.MX_ERR_INVALID_ARG, bad
 
 
+@no_gpu
+@pytest.mark.parametrize("kind", [0, 1])
+def test_products_refuse_a_workspace_over_an_input(kind):
+    """Outside a dry run, before any device is asked for: a call of tensors that lie apart gets as far as that."""
+    rows, S, K, E, N = 100, 200, 576, 8, 512
+    size = dict(x=rows * K * 2, w=E * N * K, ws=E * N * (K // 32) if kind == 0 else E * 4 * 5 * 4, offsets=(E + 1) * 4,
+                row_slot=S * 4, work=mx.mx_grouped_linear_workspace_bytes(rows, S, E, N, K))
+    at, places = FAKE, {}
+    for n, b in size.items():                                        # back to back
+        places[n] = at
+        at += -(-b // 16) * 16
+    assert _grouped(kind=kind, **places) == mx.MX_ERR_UNSUPPORTED
+    dense = lambda **p: mx.lib().mx_linear_block128(p["x"], rows, K, p["w"], p["ws"], N, 2 * BIG, p["work"], 1 << 30, None)
+    assert dense(**places) == mx.MX_ERR_UNSUPPORTED
+    for n in ("x", "w", "ws", "offsets", "row_slot"):
+        for work in (places[n], places[n] + (size[n] - 1) // 16 * 16):
+            p = dict(places, work=work)
+            if n == "x":
+                p["w"] = BIG                                         # so that only x is met
+            assert _grouped(kind=kind, **p) == mx.MX_ERR_INVALID_ARG, n
+            assert "workspace overlaps" in mx.lib().mx_last_error().decode()
+            if kind == 1 and n in ("x", "w", "ws") and work == places[n]:   # the dense weight is the first expert's
+                assert dense(**p) == mx.MX_ERR_INVALID_ARG, n
+
+
 def test_combine_validation(dry):
     def f(**kw):
         a = dict(y=FAKE, rows=80, N=512, slot_row=FAKE, weights=FAKE, T=10, k=8, shared=BIG, out=2 * BIG)
