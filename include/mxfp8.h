@@ -449,7 +449,7 @@ mx_status mx_grouped_linear(const void* x, int64_t rows, int64_t K, const uint8_
  * y        device BF16 [rows, N].    slot_row  device int32 [T, k].
  * weights  device FP32 [T, k].
  * shared   device BF16 [T, N] (a shared expert's output) or NULL.
- * out      device BF16 [T, N]; may be `shared`, overlaps y nowhere.
+ * out      device BF16 [T, N]; may be `shared`, overlaps no other input.
  * A slot whose row is outside [0, rows) (a dropped token) or whose weight is 0
  * adds nothing, whatever y holds.
  * Requires: T >= 0 (0 is a no-op), N >= 8, N % 8 == 0, 1 <= k <= 1024, rows >= 0

@@ -90,12 +90,11 @@ mx_status mx_moe_combine(const void* y, int64_t rows, int64_t N, const int32_t* 
   MX_CHECK((y || rows == 0) && slot_row && weights && out, "%s: null tensor pointer", fn);
   MX_CHECK(aligned(y, 16) && aligned(shared, 16) && aligned(out, 16) && aligned(slot_row, 4) && aligned(weights, 4),
            "%s: y, shared and out must be 16-byte, slot_row and weights 4-byte aligned", fn);
-  const uintptr_t yb = reinterpret_cast<uintptr_t>(y), ob = reinterpret_cast<uintptr_t>(out);
-  const uintptr_t sb = reinterpret_cast<uintptr_t>(shared);
-  const uintptr_t ybytes = static_cast<uintptr_t>(rows) * N * 2, obytes = static_cast<uintptr_t>(T) * N * 2;
-  MX_CHECK(rows == 0 || yb + ybytes <= ob || ob + obytes <= yb, "%s: out overlaps y", fn);
-  MX_CHECK(!shared || sb == ob || sb + obytes <= ob || ob + obytes <= sb, "%s: out overlaps shared without being it",
-           fn);
+  const size_t out_bytes = static_cast<size_t>(T) * N * 2, slot_bytes = static_cast<size_t>(T) * k * 4;
+  MX_CHECK(apart(out, out_bytes, y, static_cast<size_t>(rows) * N * 2), "%s: out overlaps y", fn);
+  MX_CHECK(shared == out || apart(out, out_bytes, shared, out_bytes), "%s: out overlaps shared without being it", fn);
+  MX_CHECK(apart(out, out_bytes, slot_row, slot_bytes) && apart(out, out_bytes, weights, slot_bytes),
+           "%s: out overlaps slot_row or weights", fn);
   MX_PREAMBLE();
   count(C_MOE_COMBINE);
   const mx_status st =

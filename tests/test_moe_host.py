@@ -158,6 +158,17 @@ def test_combine_validation(dry):
         assert f(**bad) == mx.MX_ERR_INVALID_ARG, bad
 
 
+def test_combine_refuses_out_over_the_slots(dry):
+    T, k, N = 10, 8, 512
+    for name in ("slot_row", "weights"):
+        for at, ok in ((BIG + T * k * 4, True), (BIG + T * k * 4 - 16, False), (BIG, False), (BIG - T * N * 2 + 16, False),
+                       (BIG - T * N * 2, True)):
+            a = dict(y=FAKE, rows=80, N=N, slot_row=2 * BIG, weights=2 * BIG, T=T, k=k, shared=None, out=at)
+            a[name] = BIG
+            st = mx.lib().mx_moe_combine(*a.values(), None)
+            assert st == (mx.MX_OK if ok else mx.MX_ERR_INVALID_ARG), (name, at - BIG)
+
+
 def z(*shape, dtype=torch.uint8):
     return torch.zeros(shape, dtype=dtype)
 
