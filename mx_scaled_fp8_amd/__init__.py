@@ -442,6 +442,7 @@ def _dtype(t, dtypes, name):
 
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_E4M3 = (torch.uint8, torch.int8, torch.float8_e4m3fn)
 
 
 def _workspace(ws, need, like):
@@ -454,14 +455,13 @@ def _workspace(ws, need, like):
     return ws, _dev(ws, "workspace"), ws.numel() * ws.element_size()
 
 
-def _result(t, name, shape, dtype, like, dtypes=None):
+def _result(t, name, shape, dtype, like, dtypes):
     """(tensor, pointer) of an output on the device of `like`: a new one, or the caller's, of any shape with as many
     elements.  A new one needs none of the checks, which take longer than a small call's kernel."""
     if t is None:
         t = like.new_empty(shape, dtype=dtype)
         return t, t.data_ptr()
-    if dtypes is not None:
-        _dtype(t, dtypes, name)
+    _dtype(t, dtypes, name)
     n = 1
     for d in shape:
         n *= d
@@ -496,10 +496,11 @@ def mx_linear_block128(x, w, w_scale, out=None, workspace=None):
     N = w.shape[0]
     _shape(w, (N, K), "w")
     _dtype(x, _BF16, "x")
+    _dtype(w, _E4M3, "w")
     _dtype(w_scale, (torch.float32,), "w_scale")
     _shape(w_scale, (-(-N // MX_BLOCK128), -(-K // MX_BLOCK128)), "w_scale")
     _same_device(x, ("w", w), ("w_scale", w_scale), ("workspace", workspace))
-    out, op = _result(out, "out", (M, N), torch.bfloat16, x)
+    out, op = _result(out, "out", (M, N), torch.bfloat16, x, _BF16)
     args = (_dev(x, "x", 2), M, K, _dev(w, "w", 1), _dev(w_scale, "w_scale", 4), N, op)
     workspace, wp, wb = _workspace(workspace, mx_linear_block128_workspace_bytes(M, N, K), x)
     _on_device(lib().mx_linear_block128, x, *args, wp, wb)
@@ -553,6 +554,7 @@ def mx_grouped_linear(x, w, w_scale, offsets, row_slot=None, k=1, act=MX_ACT_NON
     rows = x.shape[0]
     _shape(x, (rows, 2 * K if act == MX_ACT_SWIGLU else K), "x")
     _dtype(x, _BF16, "x")
+    _dtype(w, _E4M3, "w")
     _dtype(w_scale, (torch.uint8, torch.float32), "w_scale")
     kind = MX_SCALE_F32 if w_scale.dtype == torch.float32 else MX_SCALE_E8M0
     if kind == MX_SCALE_F32:
@@ -567,7 +569,7 @@ def mx_grouped_linear(x, w, w_scale, offsets, row_slot=None, k=1, act=MX_ACT_NON
     S = rows if row_slot is None else row_slot.numel()
     _same_device(x, ("w", w), ("w_scale", w_scale), ("offsets", offsets), ("row_slot", row_slot),
                  ("workspace", workspace))
-    out, op = _result(out, "out", (S, N), torch.bfloat16, x)
+    out, op = _result(out, "out", (S, N), torch.bfloat16, x, _BF16)
     args = (_dev(x, "x", 2), rows, K, _dev(w, "w", 1), _dev(w_scale, "w_scale"), kind, E, N,
             _dev(offsets, "offsets", 4), _dev(row_slot, "row_slot", 4) if row_slot is not None else None, k, S, act, op)
     workspace, wp, wb = _workspace(workspace, mx_grouped_linear_workspace_bytes(rows, S, E, N, K), x)
@@ -589,7 +591,7 @@ def mx_moe_combine(y, slot_row, weights, shared=None, out=None):
     _shape(weights, (T, k), "weights")
     _numel(shared, T * N, "shared")
     _same_device(y, ("slot_row", slot_row), ("weights", weights), ("shared", shared))
-    out, op = _result(out, "out", (T, N), torch.bfloat16, y)
+    out, op = _result(out, "out", (T, N), torch.bfloat16, y, _BF16)
     args = (_dev(y, "y", 2), rows, N, _dev(slot_row, "slot_row", 4), _dev(weights, "weights", 4), T, k,
             _dev(shared, "shared", 2) if shared is not None else None, op)
     _on_device(lib().mx_moe_combine, y, *args)

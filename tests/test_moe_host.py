@@ -235,3 +235,21 @@ def test_combine_and_block128_binding_checks():
     _raises("w_scale must be", b, x, w, z(1, 2))
     _raises("out has", b, x, w, ws, out=z(5, 32, dtype=i16))
     _raises("GPU tensor", b, x, w, ws)
+
+
+def test_types_of_the_same_width_are_refused():
+    """An output of another 16-bit type, or a weight in another FP8 format, would be read as what it is not."""
+    half = z(6, 32, dtype=torch.float16)
+    x, w, off = z(6, 64, dtype=i16), z(4, 32, 64), z(5, dtype=i32)
+    y, sr, wt = z(12, 32, dtype=i16), z(6, 2, dtype=i32), z(6, 2, dtype=f32)
+    g, b, c = mx.mx_grouped_linear, mx.mx_linear_block128, mx.mx_moe_combine
+    ws, wsf = z(4, 32, 2), z(1, 1, dtype=f32)
+    _raises("out must be", g, x, w, ws, off, out=half)
+    _raises("out must be", b, x, w[0], wsf, out=half)
+    _raises("out must be", c, y, sr, wt, out=half)
+    for t in (torch.float8_e4m3fnuz, torch.float8_e5m2, torch.bool):
+        _raises("w must be", g, x, w.to(t), ws, off)
+        _raises("w must be", b, x, w[0].to(t), wsf)
+    for t in (torch.uint8, torch.int8, torch.float8_e4m3fn):          # OCP codes: as far as the device check
+        _raises("GPU tensor", g, x, w.view(t), ws, off)
+        _raises("GPU tensor", b, x, w[0].view(t), wsf)
