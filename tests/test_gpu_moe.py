@@ -64,6 +64,15 @@ def test_route(T, E, k, score, bias):
     _check_route(F.bf16_to_f64(lb), dev_u16(lb), k, b, score, False)
 
 
+@pytest.mark.parametrize("T,E,k", [(70, 17, 3), (300, 32, 8), (5, 31, 16), (70, 32, 20), (9, 64, 32), (300, 128, 16),
+                                   (40, 100, 17)])
+@pytest.mark.parametrize("score", [mx.MX_ROUTE_SOFTMAX, mx.MX_ROUTE_SIGMOID])
+@pytest.mark.parametrize("bias", [False, True])
+def test_route_few_experts(T, E, k, score, bias):
+    """17 to 32 experts by 16 lanes a token, and k above 16 among up to 128."""
+    test_route(T, E, k, score, bias)
+
+
 @pytest.mark.parametrize("T", [16384, 16385, 32769, 40000])
 def test_route_many_tokens(T):
     """Both block lengths, and more blocks than workgroups of the grouping."""
@@ -308,6 +317,28 @@ def test_grouped_shares_of_long_rows(fmt, K, counts, N, gather):
     _run_grouped(2 * K + N, fmt, counts, N, K, gather=gather, k=2)
 
 
+def _list_bytes(BM, S, E):
+    """Bytes of the list of row tiles of BM rows in the workspace of a grouped product."""
+    return -(-32 * (1 + S // BM + min(S, E)) // 256) * 256
+
+
+@pytest.mark.parametrize("fmt,K", [("mx", 32), ("mx", 96), ("mx", 288), ("mx", 512), ("mx", 576), ("mx", 1024), ("f32", 16),
+                                   ("f32", 112), ("f32", 272), ("f32", 512), ("f32", 640), ("f32", 1024)])
+@pytest.mark.parametrize("counts", [[249, 1, 1, 1, 1, 1, 1, 1], [140, 70, 20, 20, 3, 2, 0, 1]])
+@pytest.mark.parametrize("gather,act", [(None, False), (37, False), (37, True)])
+def test_grouped_skewed_groups_of_short_rows(fmt, K, counts, gather, act):
+    """Small groups on average, one of them large: 32-row tiles, of which a workgroup's share holds two or three, each of
+    one or two super-stages of 512 K.  Some gathered rows have no source."""
+    N, E, S = 2048, len(counts), sum(counts)
+    rows = S if gather is None else gather
+    rest = sum(-(-b // 256) * 256 for b in (rows * -(-K // 128) * 128, rows * -(-K // 512) * 16))
+    assert mx.mx_grouped_linear_workspace_bytes(rows, S, E, N, K) - rest == _list_bytes(32, S, E) != _list_bytes(128, S, E)
+
+    def spoil(x, w, ws, slots):
+        slots[[0, 131, 250]] = [-1, 37 * 2, 2 ** 31 - 1]
+    _run_grouped(K + counts[0], fmt, counts, N, K, act=act, gather=gather, k=2, spoil=spoil if gather and not act else None)
+
+
 @pytest.mark.parametrize("fmt", ["mx", "f32"])
 def test_grouped_bad_slots_and_nonfinite_inputs(fmt):
     def spoil(x, w, ws, slots):
@@ -382,6 +413,22 @@ def test_grouped_equal_tokens_are_equal(fmt):
     for S in (7, 60, 1000, 9000):
         out = mx.mx_grouped_linear(dev_u16(x), dev_u8(w), _scale_dev(ws), _i32([0, S]), row_slot=_i32(np.zeros(S)))
         assert (out == out[0]).all()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "f32"])
+@pytest.mark.parametrize("counts,N,K", [([1, 0, 3], 4112, 2304), ([40, 90], 144, 160), ([150, 100], 8208, 160),
+                                        ([700, 500], 5136, 1152), ([1300, 0, 2700, 257], 4112, 1280)])
+def test_grouped_repeats_bit_for_bit(fmt, counts, N, K):
+    """Equal calls give equal bits, for each kind of tile."""
+    rng = np.random.default_rng(N + K)
+    off = _sizes(counts)
+    x = dev_u16(workloads.activations(rng, int(off[-1]), K))
+    w, ws = _weights(rng, (len(counts),), N, K, fmt)
+    w, ws, off = dev_u8(w), _scale_dev(ws), _i32(off)
+    say("grouped repeats", fmt, counts, N, K)
+    first = mx.mx_grouped_linear(x, w, ws, off)
+    for _ in range(5):
+        assert torch.equal(mx.mx_grouped_linear(x, w, ws, off).view(torch.int16), first.view(torch.int16))
 
 
 # ---------------------------------------------------------------- block 128
