@@ -204,12 +204,12 @@ template <int BM>
 constexpr bool kParts = BM == 256;
 
 // WGM x WGN waves share a BM (rows) x BN (columns) tile; with WGK > 1 that many sets of them each take every WGK-th
-// stage and their sums meet in LDS at the end.  STAGES super-stages of WGK x 128 K in LDS.
+// stage and their sums meet in LDS at the end.  Two super-stages of WGK x 128 K in LDS.
 //
 // v_mfma_scale_f32_32x32x64_f8f6f4, weight first: lane l holds row l % 32 of each operand, K [16q, 16q+16) and
 // [32+16q, 32+16q+16) of the 64 with q = l / 32, and passes the scale of 32-K block q; its 16 results are the columns
 // 8 (r / 4) + 4 q + r % 4 of activation row l % 32.
-template <bool F32, int BM, int BN, int WGM, int WGN, int WGK, int STAGES>
+template <bool F32, int BM, int BN, int WGM, int WGN, int WGK>
 __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   constexpr int NW = WGM * WGN * WGK;
   constexpr int WTM = BM / WGM, WTN = BN / WGN;        // a wave's sub-tile
@@ -218,12 +218,9 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   constexpr int kStage = kSub * WGK;
   constexpr int A_INS = WGK * BM / 8, W_INS = WGK * BN / 8;   // DMA instructions of a super-stage (8 rows each)
   constexpr int APW = (A_INS + NW - 1) / NW, WPW = (W_INS + NW - 1) / NW;
-  constexpr int kDma = APW + WPW;                      // per wave and super-stage
-  static_assert(STAGES == 2 || STAGES == 3, "ring");
   static_assert(IT * JT * 16 * 256 * (WGK - 1) * WGM * WGN <= kStage, "the partial sums fit a stage buffer");
   __shared__ __attribute__((aligned(1024))) uint8_t st0[kStage];
   __shared__ __attribute__((aligned(1024))) uint8_t st1[kStage];
-  __shared__ __attribute__((aligned(1024))) uint8_t st2[STAGES > 2 ? kStage : 16];
   // scale words of two windows of four stages.  MXFP8: W rows, then x rows, four E8M0 bytes each.  FP32: the products
   // of an x row's scale with the column block's, for each of the tile's column blocks.
   constexpr int kCB = (BN + 127) / 128;
@@ -334,8 +331,7 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   constexpr int kWindow = 4 / WGK;                     // super-stages whose scales are brought together
   const int windows = (KS + kWindow - 1) / kWindow;
   // Chunks of the weight at or behind K re-read the row's last one: the activation's codes there are zero.  A
-  // super-stage behind the last is asked for all the same, at offsets behind the resources: nothing is fetched, and the
-  // number of instructions in flight stays the same for every step.
+  // super-stage behind the last is asked for all the same, at offsets behind the resources: nothing is fetched.
   auto issue = [&](uint8_t* buf, int ks) {
     uint32_t behind = ks < KS ? 0u : kNone;
     asm("" : "+s"(behind));                           // or-ed in: as a choice of offsets it became branches
@@ -529,16 +525,15 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
     }
   };
 
-  // ---- ring.  At the top of step ks its DMA and that of the STAGES - 2 super-stages behind it are in flight.
+  // ---- ring.  At the top of step ks its DMA is in flight.
   issue(st0, 0);
   load_scales(0);
-  if constexpr (STAGES > 2) issue(st1, 1);
   auto ring = [&](auto J) {
     auto step = [&](const uint8_t* buf, uint8_t* refill, int ks) {
       const int win = ks / kWindow, wbuf = win & 1;
       const bool window = ks % kWindow == 0;
       __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_waitcnt(wait_vm_only((STAGES - 2) * kDma));
+      __builtin_amdgcn_s_waitcnt(wait_vm_only(0));
       if (window) store_scales(win, wbuf);
       __builtin_amdgcn_s_waitcnt(kWaitLgkmOnly);         // the scales are written; reads of the buffer before are done
       __builtin_amdgcn_s_barrier();                      // super-stage ks is in LDS; the buffer before it is free
@@ -547,22 +542,14 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
       read_scales(wbuf, (ks * WGK + wk) & 3, sw, sx);
       if (window) load_scales(min(win + 1, windows - 1));
       __builtin_amdgcn_sched_barrier(0);                 // the loads go out before the DMA, and are waited for before it
-      issue(refill, ks + STAGES - 1);
+      issue(refill, ks + 1);
       __builtin_amdgcn_sched_barrier(0);
       compute(J, buf, ks, sw, sx);
       __builtin_amdgcn_sched_barrier(0);
     };
-    if constexpr (STAGES == 2) {
-      for (int ks = 0; ks < KS; ks += 2) {
-        step(st0, st1, ks);
-        if (ks + 1 < KS) step(st1, st0, ks + 1);
-      }
-    } else {
-      for (int ks = 0; ks < KS; ks += 3) {
-        step(st0, st2, ks);
-        if (ks + 1 < KS) step(st1, st0, ks + 1);
-        if (ks + 2 < KS) step(st2, st1, ks + 2);
-      }
+    for (int ks = 0; ks < KS; ks += 2) {
+      step(st0, st1, ks);
+      if (ks + 1 < KS) step(st1, st0, ks + 1);
     }
   };
   if constexpr (kParts<BM>) {
@@ -633,9 +620,9 @@ __device__ __forceinline__ void grouped_gemm(const GemmArgs& p) {
   }
 }
 
-template <bool F32, int BM, int BN, int WGM, int WGN, int WGK, int STAGES>
+template <bool F32, int BM, int BN, int WGM, int WGN, int WGK>
 __global__ __launch_bounds__(64 * WGM * WGN * WGK, 1) void grouped_gemm_kernel(GemmArgs p) {
-  grouped_gemm<F32, BM, BN, WGM, WGN, WGK, STAGES>(p);
+  grouped_gemm<F32, BM, BN, WGM, WGN, WGK>(p);
 }
 
 // ------------------------------------------------------------------- dispatch
@@ -684,15 +671,15 @@ template <bool F32>
 void launch_gemm(const Shape s, const GemmArgs& a, int64_t tiles, hipStream_t stream) {
   const unsigned per_xcd = static_cast<unsigned>((tiles + 7) / 8);
   if (s.BM == 64 && s.BN == 64)
-    grouped_gemm_kernel<F32, 64, 64, 1, 2, 4, 2><<<8 * per_xcd, 512, 0, stream>>>(a);
+    grouped_gemm_kernel<F32, 64, 64, 1, 2, 4><<<8 * per_xcd, 512, 0, stream>>>(a);
   else if (s.BM == 64)
-    grouped_gemm_kernel<F32, 64, 128, 2, 2, 2, 2><<<8 * per_xcd, 512, 0, stream>>>(a);
+    grouped_gemm_kernel<F32, 64, 128, 2, 2, 2><<<8 * per_xcd, 512, 0, stream>>>(a);
   else if (s.BM == 128 && s.split)
-    grouped_gemm_kernel<F32, 128, 128, 2, 2, 2, 2><<<8 * per_xcd, 512, 0, stream>>>(a);
+    grouped_gemm_kernel<F32, 128, 128, 2, 2, 2><<<8 * per_xcd, 512, 0, stream>>>(a);
   else if (s.BM == 128)
-    grouped_gemm_kernel<F32, 128, 128, 2, 2, 1, 2><<<8 * per_xcd, 256, 0, stream>>>(a);
+    grouped_gemm_kernel<F32, 128, 128, 2, 2, 1><<<8 * per_xcd, 256, 0, stream>>>(a);
   else                                                 // and up to one more round of parts
-    grouped_gemm_kernel<F32, 256, 256, 2, 4, 1, 2><<<8 * (per_xcd + a.wg_per_xcd), 512, 0, stream>>>(a);
+    grouped_gemm_kernel<F32, 256, 256, 2, 4, 1><<<8 * (per_xcd + a.wg_per_xcd), 512, 0, stream>>>(a);
 }
 
 }  // namespace
