@@ -38,6 +38,7 @@ typedef const __attribute__((address_space(4))) int32_t* const_i32;
 constexpr int unit_columns(bool f32) { return f32 ? 32 : 16; }
 constexpr uint32_t kNone = 0xFFFFFF80u;    // an offset behind every resource
 constexpr int kSlotBufs = 8;               // tiles whose row indices are held in LDS
+constexpr int kSlotWords = 64;             // of a tile: its rows' indices, in the one word a lane that a DMA writes
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
@@ -94,9 +95,10 @@ __device__ __forceinline__ void grouped_stream(const GemmArgs& p) {
   constexpr int kUnit = unit_columns(F32), kPer = BN / kUnit;   // columns of a unit, units of a tile
   static_assert(kWIns % kWaves == 0 && (S - 2) * kDma <= 63, "instruction counts");
   static_assert((WGK - 1) * WGN * 4096 <= kSlot, "the partial sums fit a slot");
+  static_assert(BM <= kSlotWords, "the row indices fit a buffer");
   __shared__ __attribute__((aligned(1024))) uint8_t ring[S * kSlot];
   __shared__ __attribute__((aligned(256))) uint32_t scales[S * kScWords];
-  __shared__ __attribute__((aligned(256))) int32_t slots[kSlotBufs * 128];
+  __shared__ __attribute__((aligned(256))) int32_t slots[kSlotBufs * kSlotWords];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = uniform(tid >> 6);
@@ -168,17 +170,15 @@ __device__ __forceinline__ void grouped_stream(const GemmArgs& p) {
   auto x_row = [&](const Tile& t, int idx, int r) {
     int s = t.row0 + r;
     if (p.row_slot) {
-      const int id = static_cast<int>(lds_read(slots0 + static_cast<uint32_t>((idx % kSlotBufs) * 128 + r) * 4));
+      const int id = static_cast<int>(lds_read(slots0 + static_cast<uint32_t>((idx % kSlotBufs) * kSlotWords + r) * 4));
       s = id < 0 ? -1 : static_cast<int>(div_u32(static_cast<uint32_t>(id), p.k_div));
     }
     return s >= p.rows ? -1 : s;
   };
   auto fetch_slots = [&](const Tile& t, int idx) {     // row indices of a tile (every wave issues one instruction)
     if (!p.row_slot) return;
-    const int half = wave & 1;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(resource(p.row_slot + t.row0, static_cast<uint32_t>(t.rows) * 4),
-                                             (lds_void_t*)(slots + (idx % kSlotBufs) * 128 + half * 64), 4,
-                                             (half * 64 + lane) * 4, 0, 0, 0);
+                                             (lds_void_t*)(slots + (idx % kSlotBufs) * kSlotWords), 4, lane * 4, 0, 0, 0);
   };
   auto set_producer = [&](const Tile& t, int idx) {
     pks = 0;
@@ -211,7 +211,7 @@ __device__ __forceinline__ void grouped_stream(const GemmArgs& p) {
       } else {
         const int j = i - kScX / 64, r = j % (BN / 64) * 64 + lane, sub = j / (BN / 64);
         if constexpr (F32) {
-          // the columns' 128-blocks: two in a tile of 256 (which may begin inside one)
+          // every column brings its 128-block's scale (one for the whole tile, which lies inside a block)
           const float* const at = static_cast<const float*>(p.ws) + static_cast<size_t>(t.e) * NB * KB;
           sptr[u] = reinterpret_cast<const uint8_t*>(at);
           sbytes[u] = static_cast<uint32_t>(NB) * static_cast<uint32_t>(KB) * 4;
