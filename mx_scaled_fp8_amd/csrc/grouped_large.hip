@@ -24,7 +24,12 @@
 //  * K need not be a multiple of 128: the weight's chunks behind K re-read the row's last one, whose products with the
 //    activation's zero codes vanish, and scale bytes behind K are cleared.
 //
-// Measured (one MI355X, whole calls): 65536 rows of 32 groups of about 2048, N = 4608, K = 5120: 1460 us, 2.1 PFLOP/s;
+// The 512 registers of a lane do not hold it all: 23 (80 bytes of scratch a lane) are spilled, the row and column limits
+// of the epilogue and the addresses of the next tile's fetches among them.  A tile's first and last stages and a change
+// of the scale window reload some.  The fold reloads two, right behind the next stage's DMA and after the first stores,
+// and each reload waits for that DMA.
+//
+// Measured (one MI355X, whole calls): 65536 rows of 32 groups of about 2048, N = 4608, K = 5120: 1460 to 1500 us, 2.1 PFLOP/s;
 // with groups of exactly 2048 rows 1330 (a group's last, ragged tile takes a whole tile's time).  What bounds it is the
 // way of the operands to LDS as much as the MFMAs: a 256 x 256 tile takes 64 KiB per 128 K, and a kernel of such tiles
 // took 1285 us for the DMA alone (580 when every tile reads the same lines) and 1130 without any.  Half of the L2's
@@ -395,7 +400,8 @@ __device__ __forceinline__ void grouped_large(const GemmArgs& p) {
     static_for<0, 8>([&](auto KK) { read_k(KK, buf, ch10, ch11, fw[1], fx[1]); });
     pin_acc();
     __builtin_amdgcn_sched_barrier(0);
-    // a whole tile issued exactly kFoldStores stores behind the DMA that this waits for; they may stay in flight
+    // A whole tile issued kFoldStores stores behind the DMA that this waits for (and reloads of spilled registers, which
+    // have waited for that DMA already, so that as built the wait finds it done); they may stay in flight.
     if (cur.rows == kT && cur.cols == kT)
       __builtin_amdgcn_s_waitcnt(wait_vm(kFoldStores));
     else
