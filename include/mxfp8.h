@@ -82,6 +82,13 @@ typedef enum { MX_ACT_NONE = 0, MX_ACT_SWIGLU = 1 } mx_act;
 /* Block along N and K of FP32 weight scales (mx_linear_block128, mx_grouped_linear). */
 #define MX_BLOCK128 128
 
+/* Element type of a key-value cache. */
+typedef enum { MX_CACHE_MXFP8 = 0, MX_CACHE_BF16 = 1 } mx_cache_kind;
+/* Elements of a head under one E8M0 scale of an MXFP8 cache. */
+#define MX_CACHE_BLOCK 32
+/* Largest page of a cache, in tokens. */
+#define MX_CACHE_MAX_PAGE 4096
+
 /* ------------------------------------------------------------------ status */
 
 /* Static text for a status code. */
@@ -105,9 +112,10 @@ void mx_set_dry_run(int on);
  * per-call-dequant branch, f32->e8m0 device, e4m3 encode device, inverse RoPE
  * to BF16, BF16 bmm (large tiles), BF16 bmm (small T), wo_a scale expansion,
  * single-kernel wo_a, expert router, grouped linear, join of the experts'
- * rows, block-128 linear.
+ * rows, block-128 linear, cache write, cache read, attention of one token,
+ * attention of prompts.
  * `out` gets min(n, MX_NUM_COUNTERS) values; returns MX_NUM_COUNTERS. */
-#define MX_NUM_COUNTERS 18
+#define MX_NUM_COUNTERS 22
 int mx_get_counters(uint64_t* out, int n);
 void mx_reset_counters(void);
 
@@ -459,6 +467,138 @@ mx_status mx_grouped_linear(const void* x, int64_t rows, int64_t K, const uint8_
 mx_status mx_moe_combine(const void* y, int64_t rows, int64_t N, const int32_t* slot_row,
                          const float* weights, int64_t T, int32_t k, const void* shared, void* out,
                          void* stream);
+
+/* ------------------------------------- key-value cache and attention */
+
+/*
+ * The paged key-value cache of the four calls below.
+ *
+ * kind      MX_CACHE_MXFP8: k_cache, v_cache device u8 [pages, Hkv, page_size, D],
+ *           OCP e4m3 codes, and k_scale, v_scale device u8
+ *           [pages, Hkv, page_size, D/32], E8M0: an element is code * 2^(scale - 127);
+ *           a scale of 0xFF makes its 32 elements NaN.
+ *           MX_CACHE_BF16: k_cache, v_cache device BF16 of the same shape; no scales
+ *           (NULL).
+ * A head's rows of one page are contiguous, so that a sequence streams by whole
+ * pages.  v_cache (and v_scale) NULL: a latent cache, whose one tensor is both
+ * keys and values.
+ * page_size a power of two, 16 to MX_CACHE_MAX_PAGE.
+ * Token i of sequence b is row i % page_size of page
+ * block_table[b][i / page_size]; block_table is device int32 [B, max_pages],
+ * whose entries behind a sequence's last page are not read.  Sequences may
+ * share pages.
+ */
+
+/*
+ * mx_kv_cache_write -- the keys and values of T tokens into their slots.
+ *
+ * k, v      device BF16 [T, Hkv, D], token t at t * k_stride (v_stride) elements,
+ *           its heads dense: a slice of a fused projection's output will do.
+ *           v NULL with a latent cache.
+ * slots     device int64 [T]: token t goes to row slots[t] % page_size of page
+ *           slots[t] / page_size.  A slot outside [0, pages * page_size) writes
+ *           nothing (-1 as padding).  Slots are distinct: the row of a slot that
+ *           is named twice holds parts of either token.
+ * MXFP8: per 32 consecutive elements e = ceil(log2(amax / 448)), at least -127,
+ * scale e + 127, codes of x * 2^-e, nearest even, saturating; a block holding
+ * NaN/Inf gets scale 0xFF and NaN codes.  (The MXFP8 quantiser of mx_linear.)
+ * Requires: T >= 0 (0 is a no-op), Hkv >= 1, D % 32 == 0, 32 <= D <= 1024,
+ * Hkv * D <= 2^20, T * Hkv * D < 2^34, strides >= Hkv * D and multiples of 8 (below 2^31), pages
+ * >= 1 and < 2^31, k, v and the caches 16-byte, slots 8-byte aligned; caches and scales
+ * overlap neither each other nor k, v and slots.
+ */
+mx_status mx_kv_cache_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                            int64_t T, int32_t Hkv, int32_t D, const int64_t* slots, int32_t kind,
+                            void* k_cache, uint8_t* k_scale, void* v_cache, uint8_t* v_scale,
+                            int64_t pages, int32_t page_size, void* stream);
+
+/*
+ * mx_kv_cache_read -- the sequences of a cache as packed BF16 rows, the form
+ * that mx_attn_prefill takes.
+ *
+ * offsets   device int32 [B + 1], ascending: row offsets[b] + i of the outputs is
+ *           token i of sequence b.  Rows are cut to [0, rows); rows that no
+ *           sequence owns keep what the outputs held.
+ * k, v      device BF16 [rows, Hkv, D], dense (v NULL with a latent cache): the
+ *           elements, exact wherever BF16 holds them (2^-133 and above; nearest
+ *           even below).  A row whose page is outside [0, pages), or beyond
+ *           max_pages, is NaN; the cache is not read for it.
+ * Requires: B >= 0, rows >= 0 (either 0 is a no-op), rows < 2^31, max_pages >= 1, the cache's
+ * sizes as for mx_kv_cache_write, rows * Hkv * D < 2^34, tensors 16-byte, block_table and offsets
+ * 4-byte aligned; k and v overlap neither each other nor an input.
+ */
+mx_status mx_kv_cache_read(int32_t kind, const void* k_cache, const uint8_t* k_scale,
+                           const void* v_cache, const uint8_t* v_scale, int64_t pages,
+                           int32_t page_size, int32_t Hkv, int32_t D, const int32_t* block_table,
+                           int64_t B, int64_t max_pages, const int32_t* offsets, int64_t rows,
+                           void* k, void* v, void* stream);
+
+/*
+ * mx_attn_decode -- attention of one new token for each of B sequences over the
+ * cache:
+ * out[b,h] = sum_i softmax_i(scale * q[b,h] . K[b,i,g]) V[b,i,g], g = h / (H / Hkv),
+ * over the sequence's first lens[b] tokens (its own token written before).
+ *
+ * q         device BF16 [B, H, D], sequence b at b * q_stride elements.
+ * lens      device int32 [B].  lens[b] <= 0: out[b] is 0.  A sequence that is
+ *           longer than its table (lens[b] > max_pages * page_size), or with a
+ *           page outside [0, pages), has NaN outputs; the cache is not read there.
+ * scale     finite and > 0 (1 / sqrt(D) as a rule).
+ * out       device BF16 [B, H, D], FP32 scores, statistics and sums; probabilities
+ *           are rounded to BF16 for the second product.  The result does not depend
+ *           on timing, but on B and max_pages, which decide where a long sequence is
+ *           cut.
+ * workspace device, at least mx_attn_decode_workspace_bytes(B, H, Hkv, D, max_pages,
+ *           page_size), 16-byte aligned: parts of long sequences, written before
+ *           they are read.  Calls that may overlap need one each.
+ * Requires: B >= 0 (0 is a no-op), B < 2^24, D 64, 128, 256 or 512, Hkv >= 1, H % Hkv == 0, H <= 2^16,
+ * max_pages >= 1, max_pages * page_size < 2^31, pages >= 1 and < 2^31,
+ * B * Hkv * ceil(H / Hkv / 16) < 2^24, and that times ceil(max_pages * page_size / 128)
+ * < 2^31, q_stride >= H * D and a multiple of 8, q, caches and out 16-byte, scales 16-byte,
+ * block_table and lens 4-byte aligned; out and the workspace overlap no input
+ * and not each other.
+ */
+size_t mx_attn_decode_workspace_bytes(int64_t B, int32_t H, int32_t Hkv, int32_t D,
+                                      int64_t max_pages, int32_t page_size);
+mx_status mx_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t H, int32_t Hkv, int32_t D,
+                         int32_t kind, const void* k_cache, const uint8_t* k_scale,
+                         const void* v_cache, const uint8_t* v_scale, int64_t pages,
+                         int32_t page_size, const int32_t* block_table, int64_t max_pages,
+                         const int32_t* lens, float scale, void* out, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * mx_attn_prefill -- causal attention over B packed prompts.  Rows
+ * [q_offsets[b], q_offsets[b+1]) of q are the last Lq of the Lk tokens whose keys
+ * and values are rows [k_offsets[b], k_offsets[b+1]): row i of them sees keys
+ * 0 .. Lk - Lq + i (Lk == Lq for a prompt from its beginning, Lk > Lq for a
+ * later chunk over its history).
+ * out[i,h] = sum_j softmax_j(scale * q[i,h] . k[j,g]) v[j,g], g = h / (H / Hkv);
+ * 0 for a row that sees no key.
+ *
+ * q         device BF16 [Tq, H, D], row i at i * q_stride elements.
+ * k, v      device BF16 [Tk, Hkv, D], rows at k_stride and v_stride; v may be k.
+ * q_offsets, k_offsets  device int32 [B + 1], ascending; cut to [0, Tq] and
+ *           [0, Tk].  Rows of out that no prompt owns keep what out held.
+ * out       device BF16 [Tq, H, D], dense.  FP32 scores, statistics and sums;
+ *           probabilities are rounded to BF16 for the second product.  Keys and
+ *           values that a row does not see take no part in it, NaN or not.
+ * workspace device, at least mx_attn_prefill_workspace_bytes(B, Tq, Tk, H, Hkv, D),
+ *           16-byte aligned (may be NULL when that is 0): parts of rows whose keys are
+ *           split over workgroups, written before they are read.  Calls that may
+ *           overlap need one each.
+ * Requires: B, Tq, Tk >= 0 (B or Tq 0 is a no-op), B < 2^24, Tq, Tk < 2^31, D 64, 128, 256 or 512, Hkv >= 1,
+ * H % Hkv == 0, H <= 2^16, (Tq / 128 + B) * H < 2^24, q_stride, k_stride and v_stride multiples of 8 and at least a dense
+ * row, q_stride below 2^31, the others below 2^22, scale finite and > 0, q, k, v and out 16-byte, offsets 4-byte aligned;
+ * out and the workspace overlap no input and not each other.
+ */
+size_t mx_attn_prefill_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t Hkv,
+                                       int32_t D);
+mx_status mx_attn_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                          const void* v, int64_t v_stride, const int32_t* q_offsets,
+                          const int32_t* k_offsets, int64_t B, int64_t Tq, int64_t Tk, int32_t H,
+                          int32_t Hkv, int32_t D, float scale, void* out, void* workspace,
+                          size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------- format converters */
 

@@ -31,12 +31,16 @@ __all__ = [
     "MX_ROUTE_SOFTMAX", "MX_ROUTE_SIGMOID", "MX_ACT_NONE", "MX_ACT_SWIGLU", "MX_BLOCK128",
     "mx_moe_route", "mx_moe_route_workspace_bytes", "mx_grouped_linear", "mx_grouped_linear_workspace_bytes",
     "mx_moe_combine", "mx_linear_block128", "mx_linear_block128_workspace_bytes",
+    "MX_CACHE_MXFP8", "MX_CACHE_BF16", "MX_CACHE_BLOCK", "mx_kv_cache_write", "mx_kv_cache_read",
+    "mx_attn_decode", "mx_attn_decode_workspace_bytes", "mx_attn_prefill", "mx_attn_prefill_workspace_bytes",
 ]
 
 MX_OK, MX_ERR_INVALID_ARG, MX_ERR_UNSUPPORTED, MX_ERR_NOT_LOSSLESS, MX_ERR_HIP = range(5)
 MX_FP8_E4M3_OCP, MX_FP8_E4M3_FNUZ = 0, 1
 MX_ROPE_INTERLEAVED, MX_ROPE_NEOX = 0, 1
 MX_SCALE_E8M0, MX_SCALE_F32 = 0, 1
+MX_CACHE_MXFP8, MX_CACHE_BF16 = 0, 1
+MX_CACHE_BLOCK = 32
 MX_ROUTE_SOFTMAX, MX_ROUTE_SIGMOID = 0, 1
 MX_ACT_NONE, MX_ACT_SWIGLU = 0, 1
 MX_BLOCK128 = 128
@@ -46,7 +50,8 @@ MX_LINEAR_NOALLOC_SCRATCH_BYTES = 32 << 20
 COUNTER_NAMES = ("quant", "bmm_large", "bmm_small", "dequant", "linear_bf16", "linear_fp8",
                  "linear_percall_dequant", "f32_to_e8m0_device", "f32_to_e4m3_device", "rope_bf16",
                  "bmm_bf16_large", "bmm_bf16_small", "expand_scales", "wo_a_fused", "moe_route",
-                 "grouped_linear", "moe_combine", "linear_block128")
+                 "grouped_linear", "moe_combine", "linear_block128", "kv_cache_write", "kv_cache_read",
+                 "attn_decode", "attn_prefill")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libmxfp8.so")
@@ -98,6 +103,14 @@ def lib():
             "mx_grouped_linear_workspace_bytes": (SZ, [I64, I64, I64, I64, I64]),
             "mx_grouped_linear": (ctypes.c_int, [P, I64, I64, P, P, I32, I64, I64, P, P, I32, I64, I32, P, P, SZ, P]),
             "mx_moe_combine": (ctypes.c_int, [P, I64, I64, P, P, I64, I32, P, P, P]),
+            "mx_kv_cache_write": (ctypes.c_int, [P, I64, P, I64, I64, I32, I32, P, I32, P, P, P, P, I64, I32, P]),
+            "mx_kv_cache_read": (ctypes.c_int, [I32, P, P, P, P, I64, I32, I32, I32, P, I64, I64, P, I64, P, P, P]),
+            "mx_attn_decode_workspace_bytes": (SZ, [I64, I32, I32, I32, I64, I32]),
+            "mx_attn_decode": (ctypes.c_int, [P, I64, I64, I32, I32, I32, I32, P, P, P, P, I64, I32, P, I64, P,
+                                              ctypes.c_float, P, P, SZ, P]),
+            "mx_attn_prefill_workspace_bytes": (SZ, [I64, I64, I64, I32, I32, I32]),
+            "mx_attn_prefill": (ctypes.c_int, [P, I64, P, I64, P, I64, P, P, I64, I64, I64, I32, I32, I32,
+                                               ctypes.c_float, P, P, SZ, P]),
             "mx_stream_read": (ctypes.c_int, [P, I64, P, P]),
             "mx_f32_pow2_to_e8m0": (ctypes.c_int, [P, P, I64]),
             "mx_f32_pow2_to_e8m0_device": (ctypes.c_int, [P, P, I64, P, P]),
@@ -595,6 +608,148 @@ def mx_moe_combine(y, slot_row, weights, shared=None, out=None):
     args = (_dev(y, "y", 2), rows, N, _dev(slot_row, "slot_row", 4), _dev(weights, "weights", 4), T, k,
             _dev(shared, "shared", 2) if shared is not None else None, op)
     _on_device(lib().mx_moe_combine, y, *args)
+    return out
+
+
+# ------------------------------------------ key-value cache and attention
+
+def _rows(t, name, heads=None, D=None):
+    """(pointer, row stride) of a BF16 tensor [rows, heads, D] whose heads are dense; the rows may be strided."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [rows, heads, D] (got shape {tuple(t.shape)})")
+    n, h, d = t.shape
+    if (heads is not None and h != heads) or (D is not None and d != D):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [rows, {heads}, {D}]")
+    _dtype(t, _BF16, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if n == 0 or h == 0:
+        return t.data_ptr(), h * d
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name} must have dense heads (strides {t.stride()})")
+    return t.data_ptr(), t.stride(0) if n > 1 else h * d
+
+
+def _cache_args(k_cache, v_cache, k_scale, v_scale):
+    """(kind, k, k_scale, v, v_scale, pages, page_size, Hkv, D) of a paged cache."""
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache must be [pages, Hkv, page_size, D] (got shape {tuple(k_cache.shape)})")
+    pages, heads, page_size, D = k_cache.shape
+    kind = MX_CACHE_MXFP8 if k_cache.element_size() == 1 else MX_CACHE_BF16
+    _dtype(k_cache, _E4M3 + _BF16, "k_cache")
+    if v_cache is not None:
+        _shape(v_cache, k_cache.shape, "v_cache")
+        _dtype(v_cache, _E4M3 if kind == MX_CACHE_MXFP8 else _BF16, "v_cache")
+    for name, c, s in (("k_scale", k_cache, k_scale), ("v_scale", v_cache, v_scale)):
+        if (s is None) != (c is None or kind == MX_CACHE_BF16):
+            raise ValueError(f"{name}: an MXFP8 cache has scales [pages, Hkv, page_size, D/32], a BF16 cache none")
+        _shape(s, (pages, heads, page_size, D // MX_CACHE_BLOCK), name)
+        _dtype(s, (torch.uint8, torch.float8_e8m0fnu), name)
+    _same_device(k_cache, ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale))
+    at = lambda t, name: _dev(t, name) if t is not None else None  # noqa: E731
+    return (kind, at(k_cache, "k_cache"), at(k_scale, "k_scale"), at(v_cache, "v_cache"), at(v_scale, "v_scale"),
+            pages, page_size, heads, D)
+
+
+def _table_args(block_table):
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table must be [B, max_pages] (got shape {tuple(block_table.shape)})")
+    _dtype(block_table, (torch.int32,), "block_table")
+    return _dev(block_table, "block_table"), block_table.shape[0], block_table.shape[1]
+
+
+def mx_kv_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None):
+    """k, v BF16 [T,Hkv,D] (rows may be strided) into rows ``slots`` (int64 [T], page * page_size + row, -1 to skip a
+    token) of the cache [pages,Hkv,page_size,D]: MXFP8 uint8 with uint8 scales [pages,Hkv,page_size,D/32], or BF16.
+    ``v`` and ``v_cache`` None: a latent cache.  Writes the caches in place."""
+    kind, kc, ks, vc, vs, pages, page_size, heads, D = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    kp, k_stride = _rows(k, "k", heads, D)
+    T = k.shape[0]
+    if (v is None) != (v_cache is None):
+        raise ValueError("v and v_cache go together")
+    vp, v_stride = None, 0
+    if v is not None:
+        vp, v_stride = _rows(v, "v", heads, D)
+        _shape(v, k.shape, "v")
+    _dtype(slots, (torch.int64,), "slots")
+    _numel(slots, T, "slots")
+    _same_device(k, ("v", v), ("slots", slots), ("k_cache", k_cache))
+    _on_device(lib().mx_kv_cache_write, k, kp, k_stride, vp, v_stride, T, heads, D, _dev(slots, "slots"), kind, kc, ks,
+               vc, vs, pages, page_size)
+
+
+def mx_kv_cache_read(k_cache, v_cache, block_table, offsets, rows, k_scale=None, v_scale=None, k=None, v=None):
+    """The sequences of a cache as packed BF16 rows: (k [rows,Hkv,D], v [rows,Hkv,D] or None).  Token i of sequence b
+    is row offsets[b] + i (offsets int32 [B+1]), from page block_table[b, i // page_size] (int32 [B,max_pages])."""
+    kind, kc, ks, vc, vs, pages, page_size, heads, D = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    table, B, max_pages = _table_args(block_table)
+    _dtype(offsets, (torch.int32,), "offsets")
+    _numel(offsets, B + 1, "offsets")
+    _same_device(k_cache, ("block_table", block_table), ("offsets", offsets))
+    if rows < 0:
+        raise ValueError(f"rows = {rows} must not be negative")
+    k, kp = _result(k, "k", (rows, heads, D), torch.bfloat16, k_cache, _BF16)
+    vp = None
+    if v_cache is not None:
+        v, vp = _result(v, "v", (rows, heads, D), torch.bfloat16, k_cache, _BF16)
+    elif v is not None:
+        raise ValueError("a latent cache has no values of its own: v must be None")
+    _on_device(lib().mx_kv_cache_read, k_cache, kind, kc, ks, vc, vs, pages, page_size, heads, D, table, B, max_pages,
+               _dev(offsets, "offsets"), rows, kp, vp)
+    return k, v
+
+
+def mx_attn_decode_workspace_bytes(B, H, Hkv, D, max_pages, page_size):
+    return int(lib().mx_attn_decode_workspace_bytes(B, H, Hkv, D, max_pages, page_size))
+
+
+def mx_attn_decode(q, k_cache, v_cache, block_table, lens, k_scale=None, v_scale=None, scale=None, out=None,
+                   workspace=None):
+    """Attention of one new token for each sequence over its first lens[b] cached tokens: q BF16 [B,H,D] (rows may be
+    strided), cache and block_table as in mx_kv_cache_read, lens int32 [B] -> BF16 [B,H,D].  Query head h reads key
+    head h // (H // Hkv).  ``scale`` is 1 / sqrt(D) unless given."""
+    kind, kc, ks, vc, vs, pages, page_size, heads, D = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    table, B, max_pages = _table_args(block_table)
+    qp, q_stride = _rows(q, "q", None, D)
+    H = q.shape[1]
+    if q.shape[0] != B:
+        raise ValueError(f"q has {q.shape[0]} rows, block_table {B}")
+    _dtype(lens, (torch.int32,), "lens")
+    _numel(lens, B, "lens")
+    _same_device(q, ("k_cache", k_cache), ("block_table", block_table), ("lens", lens), ("workspace", workspace))
+    out, op = _result(out, "out", (B, H, D), torch.bfloat16, q, _BF16)
+    need = mx_attn_decode_workspace_bytes(B, H, heads, D, max_pages, page_size)
+    workspace, wp, wb = _workspace(workspace, need, q)
+    _on_device(lib().mx_attn_decode, q, qp, q_stride, B, H, heads, D, kind, kc, ks, vc, vs, pages, page_size, table,
+               max_pages, _dev(lens, "lens"), D ** -0.5 if scale is None else scale, op, wp, wb)
+    return out
+
+
+def mx_attn_prefill_workspace_bytes(B, Tq, Tk, H, Hkv, D):
+    return int(lib().mx_attn_prefill_workspace_bytes(B, Tq, Tk, H, Hkv, D))
+
+
+def mx_attn_prefill(q, k, v, q_offsets, k_offsets, scale=None, out=None, workspace=None):
+    """Causal attention over packed prompts: q BF16 [Tq,H,D], k and v BF16 [Tk,Hkv,D] (rows may be strided),
+    q_offsets and k_offsets int32 [B+1] -> BF16 [Tq,H,D].  Rows q_offsets[b]..q_offsets[b+1] are the last of the
+    tokens whose keys are rows k_offsets[b]..k_offsets[b+1].  ``scale`` is 1 / sqrt(D) unless given."""
+    qp, q_stride = _rows(q, "q")
+    Tq, H, D = q.shape
+    kp, k_stride = _rows(k, "k", None, D)
+    Tk, heads = k.shape[:2]
+    vp, v_stride = _rows(v, "v", heads, D)
+    _shape(v, k.shape, "v")
+    for name, t in (("q_offsets", q_offsets), ("k_offsets", k_offsets)):
+        _dtype(t, (torch.int32,), name)
+    B = q_offsets.numel() - 1
+    if B < 0:
+        raise ValueError("q_offsets must hold B + 1 values")
+    _numel(k_offsets, B + 1, "k_offsets")
+    _same_device(q, ("k", k), ("v", v), ("q_offsets", q_offsets), ("k_offsets", k_offsets), ("workspace", workspace))
+    out, op = _result(out, "out", (Tq, H, D), torch.bfloat16, q, _BF16)
+    workspace, wp, wb = _workspace(workspace, mx_attn_prefill_workspace_bytes(B, Tq, Tk, H, heads, D), q)
+    _on_device(lib().mx_attn_prefill, q, qp, q_stride, kp, k_stride, vp, v_stride, _dev(q_offsets, "q_offsets"),
+               _dev(k_offsets, "k_offsets"), B, Tq, Tk, H, heads, D, D ** -0.5 if scale is None else scale, op, wp, wb)
     return out
 
 

@@ -1,0 +1,430 @@
+// Attention of one new token for each sequence over the paged cache (gfx950).
+//
+// For a sequence of n cached tokens and up to 16 query heads that share a key head,
+//   S[t,h] = K[t,:] . Q[h,:],  P = exp2(c S - m_h),  O[h,:] = sum_t P[t,h] V[t,:] / sum_t P[t,h],  c = scale * log2(e),
+// in one pass with the running maximum m and sum of the softmax.  What bounds it is the cache, which is read once from HBM:
+// 2 D (1 + 1/32) bytes a token and head in MXFP8.
+//
+// The products run on 16x16x32 BF16 MFMAs with the tokens as rows: S^T = K Q^T leaves each lane with four tokens of one
+// head (its column), which is what the second product O^T = V^T P^T wants of P^T, its B operand, if V^T's tokens are
+// numbered the same way.  So P never leaves its lane, statistics are per column, and the rescaling of O^T too.
+// A wave takes 32 tokens at a time, straight from global memory into registers:
+//  - K: lane (c, g) = (lane % 16, lane / 16) holds 16-byte pieces of token c, the pieces of the four g side by side;
+//    the order of D inside the product follows that, for Q too.
+//  - V: lane (c, g) holds tokens 4g..4g+3 and 16 + 4g..+3 (the tokens of its P), elements c * DPL .. + DPL - 1 of each:
+//    row c of MFMA i is element c * DPL + i, so that an operand is formed by v_perm of two tokens' BF16 pairs, with
+//    no transposition through LDS.
+// Codes become BF16 (exact) by v_cvt_scalef32_pk_bf16_fp8 with their block's scale.
+//
+// Work is cut into tiles of 128 tokens (32 for each of the four waves), numbered through all sequences, and every
+// workgroup takes an equal share of consecutive tiles: a long sequence is spread over many workgroups, many short ones
+// share one.  A (sequence, head group) that a workgroup does not cover whole leaves its part (O, m, l) in the
+// workspace, at most two of them for a workgroup (where its share begins and where it ends), and a second kernel joins them.
+#include <algorithm>
+
+#include "kv_cache.hpp"
+
+namespace mx {
+
+namespace {
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
+constexpr int kThreads = 256;
+constexpr int kTile = 128;             // tokens of a tile
+constexpr int kHeads = 16;             // query heads of a stream: one (sequence, key head, group of up to 16 query heads)
+
+struct DecodeArgs {
+  KvCache c;
+  const uint16_t* q;
+  int64_t q_stride;
+  const int32_t* lens;
+  uint16_t* out;
+  float* parts;              // [groups][2][kHeads][D + 2]: O, m, l
+  uint32_t* plan;            // [0] share, [1 + b] first tile of sequence b
+  float scale;               // times log2(e)
+  uint32_t B, H, G;          // G query heads a key head
+  uint32_t streams;          // a sequence's: Hkv * head groups
+  uint32_t head_groups;
+};
+
+// Tiles of one stream of sequence b.
+__device__ __forceinline__ uint32_t tiles_of(const DecodeArgs& a, uint32_t b) {
+  const int32_t n = a.lens[b];
+  const uint32_t cap = a.c.max_pages << a.c.page_shift;
+  return (min(static_cast<uint32_t>(max(n, 0)), cap) + kTile - 1) / kTile;
+}
+
+// Sum over the workgroup of the threads' v, and the sum of those before this thread.
+__device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t* buf, uint32_t& before) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t x = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  __syncthreads();
+  if (lane == 63) buf[wave] = x;
+  __syncthreads();
+  uint32_t sum = 0, base = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) {
+    if (w < wave) base += buf[w];
+    sum += buf[w];
+  }
+  before = base + x - v;
+  return sum;
+}
+
+__device__ __forceinline__ float across_groups_max(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16));
+  return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ __forceinline__ float across_groups_sum(float x) {
+  x += __shfl_xor(x, 16);
+  return x + __shfl_xor(x, 32);
+}
+
+template <int D, bool FP8>
+__global__ __launch_bounds__(kThreads) void attn_decode_kernel(DecodeArgs a) {
+  constexpr int EB = FP8 ? 1 : 2;                       // bytes of an element
+  constexpr int KE = 16 / EB;                           // elements of a 16-byte piece of K
+  constexpr int KP = D / (4 * KE);                      // pieces of a K row in a lane
+  constexpr int KS = D / 32;                            // MFMA steps of the first product
+  constexpr int PANEL = FP8 ? (D < 256 ? D : 256) : (D < 128 ? D : 128);
+  constexpr int DPL = PANEL / 16;                       // elements of V in a lane, panel and token
+  constexpr int NP = D / PANEL;
+  constexpr int VW = DPL * EB / 4;                      // their words
+  __shared__ uint32_t sbuf[4], sfound[2];
+  __shared__ float sml[4][kHeads][2];
+  __shared__ __attribute__((aligned(16))) float sacc[4][kHeads][D + 4];   // + 4: the columns' rows in different banks
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
+
+  // this workgroup's share of the tiles, and the sequence that it begins in
+  uint32_t total = 0;
+  for (uint32_t b0 = 0; b0 < a.B; b0 += kThreads) {
+    const uint32_t b = b0 + threadIdx.x;
+    uint32_t before;
+    const uint32_t n = b < a.B ? tiles_of(a, b) : 0;
+    const uint32_t sum = scan(n, sbuf, before);
+    if (blockIdx.x == 0 && b < a.B) a.plan[1 + b] = (total + before) * a.streams;
+    total += sum;
+  }
+  const uint32_t share = max((total * a.streams + gridDim.x - 1) / gridDim.x, 1u);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.plan[0] = share;
+  const uint32_t all = total * a.streams;
+  uint32_t t = blockIdx.x * share;
+  if (t >= all) return;
+  const uint32_t end = min(t + share, all);
+  uint32_t done = 0;
+  for (uint32_t b0 = 0; b0 < a.B; b0 += kThreads) {
+    const uint32_t b = b0 + threadIdx.x;
+    uint32_t before;
+    const uint32_t n = b < a.B ? tiles_of(a, b) : 0;
+    const uint32_t sum = scan(n, sbuf, before);
+    const uint32_t first = (done + before) * a.streams;
+    if (t >= first && t < first + n * a.streams) {
+      sfound[0] = b;
+      sfound[1] = first;
+    }
+    done += sum;
+    if (t < done * a.streams) break;
+  }
+  __syncthreads();
+  uint32_t b = __builtin_amdgcn_readfirstlane(sfound[0]), first = __builtin_amdgcn_readfirstlane(sfound[1]);
+
+  while (t < end) {
+    const uint32_t nt = tiles_of(a, b);
+    const uint32_t s = (t - first) / nt, tile0 = (t - first) - s * nt, n = min(nt - tile0, end - t);
+    const bool whole = n == nt;
+    const uint32_t kvh = s / a.head_groups, h0 = kvh * a.G + (s - kvh * a.head_groups) * kHeads;
+    const uint32_t heads = min(static_cast<uint32_t>(kHeads), (kvh + 1) * a.G - h0);
+    const uint32_t cap = a.c.max_pages << a.c.page_shift;
+    const int32_t wanted = a.lens[b];
+    const uint32_t len = min(static_cast<uint32_t>(max(wanted, 0)), cap);
+    bool bad = wanted > 0 && static_cast<uint32_t>(wanted) > cap;
+
+    // Q, the B operand: column `col` is query head h0 + col (the last one again past it), D in the order of K's pieces
+    v8bf qf[KS];
+    {
+      const uint16_t* qrow = a.q + static_cast<int64_t>(b) * a.q_stride + (h0 + min(static_cast<uint32_t>(col), heads - 1)) * D;
+#pragma unroll
+      for (int j = 0; j < KS; ++j) {
+        const int d = FP8 ? (j >> 1) * 64 + g * 16 + (j & 1) * 8 : j * 32 + g * 8;
+        qf[j] = *reinterpret_cast<const v8bf*>(qrow + d);
+      }
+    }
+    float m = -INFINITY, l = 0.0f;
+    v4f acc[NP][DPL];
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int i = 0; i < DPL; ++i) acc[p][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const int32_t* table = a.c.table + static_cast<int64_t>(b) * a.c.max_pages;
+    for (uint32_t i = 0; i < n; ++i) {
+      const uint32_t tok0 = (tile0 + i) * kTile + wave * 32;
+      if (tok0 >= len) break;
+      // rows of the two groups of 16 tokens, each inside one page; a group past the end reads the first one again
+      int64_t row[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t tok = __builtin_amdgcn_readfirstlane(tok0 + u * 16);
+        if (u == 1 && tok >= len) tok = __builtin_amdgcn_readfirstlane(tok0);
+        uint32_t page = static_cast<uint32_t>(table[tok >> a.c.page_shift]);
+        if (page >= a.c.pages) {
+          bad = true;
+          page = 0;
+        }
+        row[u] = ((static_cast<int64_t>(page) * a.c.Hkv + kvh) << a.c.page_shift) + (tok & ((1u << a.c.page_shift) - 1));
+      }
+      // first product
+      v4f s2[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int64_t r = row[u] + col;
+        const uint8_t* kp = a.c.k + r * (D * EB) + g * 16;
+        v4u kw[KP];
+#pragma unroll
+        for (int j = 0; j < KP; ++j) kw[j] = *reinterpret_cast<const v4u*>(kp + j * 64);
+        v4f x = {0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (FP8) {
+          const uint8_t* sp = a.c.ks + r * (D / 32) + (g >> 1);
+#pragma unroll
+          for (int j = 0; j < KP; ++j) {
+            const uint32_t sc = sp[j * 2];
+            const float sb = __uint_as_float(sc << 23);
+            const uint32_t nan = nan_codes(sc);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t w0 = kw[j][half * 2] | nan, w1 = kw[j][half * 2 + 1] | nan;
+              const v4u op = {dequant_pair<false>(w0, sb), dequant_pair<true>(w0, sb), dequant_pair<false>(w1, sb),
+                              dequant_pair<true>(w1, sb)};
+              x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, op), qf[j * 2 + half], x, 0, 0, 0);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < KP; ++j)
+            x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, kw[j]), qf[j], x, 0, 0, 0);
+        }
+        s2[u] = x;
+      }
+      const bool tail = tok0 + 32 > len;
+      float top = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float x = s2[u][r] * a.scale;
+          if (tail && tok0 + u * 16 + g * 4 + r >= len) x = -INFINITY;
+          s2[u][r] = x;
+          top = fmaxf(top, x);
+        }
+      top = fmaxf(m, across_groups_max(top));
+      const float base = top == -INFINITY ? 0.0f : top;   // nothing but -inf so far: all weights are 0
+      if (__any(top > m)) {
+        const float f = __builtin_amdgcn_exp2f(m - base);
+        l *= f;
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+          for (int k = 0; k < DPL; ++k) acc[p][k] *= f;
+        m = top;
+      }
+      uint32_t pw[4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float w[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          w[r] = __builtin_amdgcn_exp2f(s2[u][r] - base);
+          l += w[r];
+        }
+        pw[u * 2] = pack_bf16x2(w[0], w[1]);
+        pw[u * 2 + 1] = pack_bf16x2(w[2], w[3]);
+      }
+      const v8bf pf = __builtin_bit_cast(v8bf, (v4u{pw[0], pw[1], pw[2], pw[3]}));
+      // second product, panel by panel
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        uint32_t pair[8][DPL / 2];                        // BF16 pairs of the lane's 8 tokens
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int u = j >> 2;
+          const int64_t r = row[u] + g * 4 + (j & 3);
+          const uint32_t* vp = reinterpret_cast<const uint32_t*>(a.c.v + (r * D + p * PANEL + col * DPL) * EB);
+          const bool out = tail && tok0 + u * 16 + g * 4 + (j & 3) >= len;   // whatever lies there, it counts as 0
+          uint32_t w[VW];
+#pragma unroll
+          for (int k = 0; k < VW; ++k) w[k] = vp[k];
+          if constexpr (FP8) {
+            const uint32_t sc = out ? 127u : a.c.vs[r * (D / 32) + (p * PANEL + col * DPL) / 32];
+            const float sb = __uint_as_float(sc << 23);
+            const uint32_t nan = nan_codes(sc);
+#pragma unroll
+            for (int k = 0; k < VW; ++k) {
+              const uint32_t x = out ? 0u : w[k] | nan;
+              pair[j][k * 2] = dequant_pair<false>(x, sb);
+              pair[j][k * 2 + 1] = dequant_pair<true>(x, sb);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < VW; ++k) pair[j][k] = out ? 0u : w[k];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < DPL / 2; ++k) {
+          v4u even, odd;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            even[j] = __builtin_amdgcn_perm(pair[2 * j + 1][k], pair[2 * j][k], 0x05040100u);
+            odd[j] = __builtin_amdgcn_perm(pair[2 * j + 1][k], pair[2 * j][k], 0x07060302u);
+          }
+          acc[p][2 * k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, even), pf, acc[p][2 * k], 0, 0, 0);
+          acc[p][2 * k + 1] =
+              __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, odd), pf, acc[p][2 * k + 1], 0, 0, 0);
+        }
+      }
+    }
+
+    // the four waves' parts into one
+    l = across_groups_sum(l);
+    if (bad) l = __builtin_nanf("");
+    __syncthreads();                                      // the last stream's parts have been read
+    if (g == 0) {
+      sml[wave][col][0] = m;
+      sml[wave][col][1] = l;
+    }
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int i = 0; i < DPL; i += 4)
+          *reinterpret_cast<v4f*>(&sacc[wave][col][p * PANEL + (g * 4 + r) * DPL + i]) =
+              v4f{acc[p][i][r], acc[p][i + 1][r], acc[p][i + 2][r], acc[p][i + 3][r]};
+    __syncthreads();
+    float* part = a.parts + (static_cast<size_t>(blockIdx.x) * 2 + (tile0 == 0 ? 1 : 0)) * kHeads * (D + 2);
+    for (uint32_t e = threadIdx.x * 4; e < heads * D; e += kThreads * 4) {
+      const uint32_t h = e / D, d = e % D;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) top = fmaxf(top, sml[w][h][0]);
+      const float base = top == -INFINITY ? 0.0f : top;
+      float sum = 0.0f;
+      v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = __builtin_amdgcn_exp2f(sml[w][h][0] - base);
+        sum += sml[w][h][1] * f;
+        o += *reinterpret_cast<const v4f*>(&sacc[w][h][d]) * f;
+      }
+      if (whole) {
+        const float inv = 1.0f / sum;
+        *reinterpret_cast<uint2*>(a.out + (static_cast<size_t>(b) * a.H + h0 + h) * D + d) =
+            make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+      } else {
+        *reinterpret_cast<v4f*>(part + h * D + d) = o;
+        if (d == 0) {
+          part[kHeads * D + h * 2] = top;
+          part[kHeads * D + h * 2 + 1] = sum;
+        }
+      }
+    }
+    t += n;
+    if (t == first + nt * a.streams && t < end) {
+      first = t;
+      do ++b; while (tiles_of(a, b) == 0);               // a tile is left, so a sequence that has one
+    }
+  }
+}
+
+// One workgroup a stream: joins the parts that the workgroups left of it, in their order; zeros for a sequence of no
+// tokens.  A stream that one workgroup covered is done already.
+template <int D>
+__global__ __launch_bounds__(kThreads) void attn_decode_join_kernel(DecodeArgs a) {
+  const uint32_t b = blockIdx.x / a.streams, s = blockIdx.x - b * a.streams;
+  const uint32_t nt = tiles_of(a, b), kvh = s / a.head_groups, h0 = kvh * a.G + (s - kvh * a.head_groups) * kHeads;
+  const uint32_t heads = min(static_cast<uint32_t>(kHeads), (kvh + 1) * a.G - h0);
+  uint16_t* out = a.out + (static_cast<size_t>(b) * a.H + h0) * D;
+  const uint32_t share = a.plan[0], t0 = a.plan[1 + b] + s * nt;
+  const uint32_t w0 = t0 / share, w1 = nt ? (t0 + nt - 1) / share : w0;
+  if (nt != 0 && w0 == w1) return;
+  auto part = [&](uint32_t w) {
+    return a.parts + (static_cast<size_t>(w) * 2 + (w == w0 ? 1 : 0)) * kHeads * (D + 2);
+  };
+  for (uint32_t e = threadIdx.x * 4; e < heads * D; e += kThreads * 4) {
+    const uint32_t h = e / D, d = e % D;
+    uint2 r = make_uint2(0, 0);
+    if (nt != 0) {
+      float m = -INFINITY, sum = 0.0f;
+      v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (uint32_t w = w0; w <= w1; ++w) {
+        const float* p = part(w);
+        const float x = p[kHeads * D + h * 2], top = fmaxf(m, x), base = top == -INFINITY ? 0.0f : top;
+        const float f = __builtin_amdgcn_exp2f(m - base), k = __builtin_amdgcn_exp2f(x - base);
+        sum = sum * f + p[kHeads * D + h * 2 + 1] * k;
+        o = o * f + *reinterpret_cast<const v4f*>(p + h * D + d) * k;
+        m = top;
+      }
+      const float inv = 1.0f / sum;
+      r = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    }
+    *reinterpret_cast<uint2*>(out + h * D + d) = r;
+  }
+}
+
+// Workgroups of a call: as many as run at once (by registers and LDS), and no more than there can be tiles.
+uint32_t decode_groups(int64_t B, uint32_t streams, int32_t D, int64_t max_tokens) {
+  const int64_t tiles = B * streams * ((max_tokens + kTile - 1) / kTile);
+  const int64_t most = D >= 512 ? 256 : 512;
+  return static_cast<uint32_t>(std::min<int64_t>(most, tiles));
+}
+
+template <int D, bool FP8>
+void launch(const DecodeArgs& a, uint32_t groups, hipStream_t stream) {
+  hipLaunchKernelGGL((attn_decode_kernel<D, FP8>), dim3(groups), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((attn_decode_join_kernel<D>), dim3(a.B * a.streams), dim3(kThreads), 0, stream, a);
+}
+
+size_t plan_bytes(int64_t B) { return (static_cast<size_t>(B) + 1 + 3) / 4 * 16; }
+
+}  // namespace
+
+size_t decode_workspace_bytes(int64_t B, int32_t H, int32_t Hkv, int32_t D, int64_t max_tokens) {
+  const uint32_t streams = static_cast<uint32_t>(Hkv) * ((H / Hkv + kHeads - 1) / kHeads);
+  return plan_bytes(B) + static_cast<size_t>(decode_groups(B, streams, D, max_tokens)) * 2 * kHeads * (D + 2) * 4;
+}
+
+mx_status launch_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t H, int32_t D, bool fp8,
+                             const KvCache& c, const int32_t* lens, float scale, void* out, void* workspace,
+                             hipStream_t stream) {
+  DecodeArgs a;
+  a.c = c;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_stride;
+  a.lens = lens;
+  a.out = static_cast<uint16_t*>(out);
+  a.plan = static_cast<uint32_t*>(workspace);
+  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan_bytes(B));
+  a.scale = scale * 1.44269504088896340736f;
+  a.B = static_cast<uint32_t>(B);
+  a.H = static_cast<uint32_t>(H);
+  a.G = a.H / c.Hkv;
+  a.head_groups = (a.G + kHeads - 1) / kHeads;
+  a.streams = c.Hkv * a.head_groups;
+  const uint32_t groups = decode_groups(B, a.streams, D, static_cast<int64_t>(c.max_pages) << c.page_shift);
+  switch (D) {
+    case 64: fp8 ? launch<64, true>(a, groups, stream) : launch<64, false>(a, groups, stream); break;
+    case 128: fp8 ? launch<128, true>(a, groups, stream) : launch<128, false>(a, groups, stream); break;
+    case 256: fp8 ? launch<256, true>(a, groups, stream) : launch<256, false>(a, groups, stream); break;
+    default: fp8 ? launch<512, true>(a, groups, stream) : launch<512, false>(a, groups, stream); break;
+  }
+  return launch_status("mx_attn_decode");
+}
+
+}  // namespace mx

@@ -43,6 +43,10 @@ enum Counter {
   C_GROUPED_LINEAR,
   C_MOE_COMBINE,
   C_LINEAR_BLOCK128,
+  C_CACHE_WRITE,
+  C_CACHE_READ,
+  C_ATTN_DECODE,
+  C_ATTN_PREFILL,
 };
 void count(Counter c);
 

@@ -29,4 +29,4 @@ Parity status of each function is listed in its docstring.  Functions with no
 pin independent of themselves say "parity unpinned".
 """
 
-from . import formats, rope, quant, gemm, ingest, moe  # noqa: F401
+from . import formats, rope, quant, gemm, ingest, moe, attn  # noqa: F401
