@@ -1,35 +1,24 @@
 // Causal attention over packed prompts (gfx950).
 //
-// A workgroup takes 128 query rows of one prompt and head, 32 for each of its four waves, and runs over the keys in
-// tiles of KT with the running maximum m and sum l of the softmax:
-//   S^T[t,q] = K[t,:] . Q[q,:],  P = exp2(c S - m_q),  O^T[:,q] += V^T[:,t] P^T[t,q],  c = scale * log2(e).
-// Both products run on 32x32x16 BF16 MFMAs with the query rows as columns.  S^T leaves a lane with 16 keys of one query row,
-// the two lanes of a row with all 32; that is P^T as the second product's B operand wants it, if V^T's tokens are numbered
-// the same way, so P stays in registers and m, l and the rescaling of O^T are a lane's own, but for one exchange between
-// the two lanes of a row.
-// K and V tiles go from global memory to LDS by buffer-load DMA (two buffers: the next tile is under way while this one
-// is used; rows past the end are zeros by the buffer's bound), rows in 16-byte chunks that are permuted on the way in:
-// chunk ^ row % 16 for K (its readers take one chunk of 32 rows), 64-byte groups ^ row % 4 for V (its readers are
-// ds_read_b64_tr_b16, which take 4 rows x 16 columns and transpose them).
+// A workgroup takes 128 query rows of one prompt and head, 32 for each of its four waves (attn_tile.hpp), and runs over
+// the keys in tiles of KT.  K and V tiles go from global memory to LDS by buffer-load DMA, the next one while this one is
+// used; rows past the end are zeros by the buffer's bound.  Tiles that every row sees whole run first, two to a turn of
+// the loop, so that each of the two buffers is an object of its own and the compiler waits for no DMA but what a read
+// needs; the last few, which hold the diagonal and the ragged end, go through a loop with masks.
+//
+// Few row tiles with many keys are split along the keys over `splits` workgroups, whose parts (O, m, l) a second
+// kernel joins.
 #include <algorithm>
 
-#include "common.hpp"
+#include "attn_tile.hpp"
 
 namespace mx {
 
 namespace {
 
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef float v16f __attribute__((ext_vector_type(16)));
-typedef short v4s __attribute__((ext_vector_type(4)));
-typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-typedef __attribute__((address_space(3))) void lds_void_t;
-typedef __attribute__((address_space(3))) v4s lds_v4s_t;
-typedef __attribute__((address_space(3))) uint8_t lds_u8_t;
-
 constexpr int kThreads = 256;
 constexpr int kRows = 128;             // query rows of a workgroup
+constexpr int kMinTiles = 4;           // fewest key tiles of a split
 
 struct PrefillArgs {
   const uint16_t* q;
@@ -39,272 +28,251 @@ struct PrefillArgs {
   const int32_t* q_offsets;
   const int32_t* k_offsets;
   uint16_t* out;
+  float* parts;              // [row tile, head, split][O: kRows x D, m, l: kRows each], FP32
   float scale;               // times log2(e)
   uint32_t B, Tq, Tk, H, Hkv, G;
   uint32_t tiles;            // bound on the row tiles of all prompts
+  uint32_t splits;
 };
-
-// 16 bytes a lane from the buffer to LDS, 1024 bytes in lane order.
-__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t from, uint8_t* to, uint32_t offset) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void_t*)to, 16, offset, 0, 0, 0);
-}
 
 // Offset b cut to [0, T].
 __device__ __forceinline__ uint32_t cut(const int32_t* offsets, uint32_t b, uint32_t T) {
   return min(static_cast<uint32_t>(max(offsets[b], 0)), T);
 }
 
-template <int D>
-__global__ __launch_bounds__(kThreads, D >= 256 ? 1 : 2) void attn_prefill_kernel(PrefillArgs a) {
-  constexpr int KT = D <= 128 ? 64 : 32;                // keys of a tile
-  constexpr int CH = D / 8;                             // 16-byte chunks of a row
-  constexpr int TB = KT * D * 2;                        // bytes of a tile
-  constexpr int ND = TB / 1024 / 4;                     // a wave's DMA instructions for one tile
-  constexpr int SUB = KT / 32;
-  constexpr int KS = D / 16;
-  constexpr int DT = D / 32;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * TB];   // K, V, K, V
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31, hf = lane >> 5;
+// A row tile: its prompt's rows and keys, and which of them it has.
+struct RowTile {
+  uint32_t q0, k0;           // where the prompt's rows and keys begin
+  int32_t Lq, Lk;
+  int32_t first;             // row of the prompt
+  int32_t keys;              // keys that some row of the tile sees
+  bool any;                  // the tile has rows
+};
 
-  // (row tile, head): heads of one key head side by side, key heads fastest, so that with workgroups dealt to the XCDs in
-  // turn an XCD's L2 serves few key heads; last row tiles first, which have the most keys.
-  uint32_t id = blockIdx.x;
-  const uint32_t kvh = id % a.Hkv;
-  id /= a.Hkv;
-  const uint32_t head = kvh * a.G + id % a.G;
-  const uint32_t rt = a.tiles - 1 - id / a.G;
+__device__ __forceinline__ RowTile row_tile(const PrefillArgs& a, uint32_t rt) {
   // prompt b's row tiles are numbered from offsets[b] / kRows + b, which leaves room for every ragged end
   uint32_t lo = 0, hi = a.B;
   while (hi - lo > 1) {
     const uint32_t mid = (lo + hi) >> 1;
     if (cut(a.q_offsets, mid, a.Tq) / kRows + mid <= rt) lo = mid; else hi = mid;
   }
-  const uint32_t q0 = cut(a.q_offsets, lo, a.Tq), q1 = cut(a.q_offsets, lo + 1, a.Tq);
-  const uint32_t k0 = cut(a.k_offsets, lo, a.Tk), k1 = cut(a.k_offsets, lo + 1, a.Tk);
-  const uint32_t first = (rt - (q0 / kRows + lo)) * kRows;         // of the prompt's rows
-  if (q1 <= q0 || first >= q1 - q0) return;
-  const int32_t Lq = static_cast<int32_t>(q1 - q0), Lk = k1 > k0 ? static_cast<int32_t>(k1 - k0) : 0;
-  const int32_t i0 = static_cast<int32_t>(first) + wave * 32;      // the wave's first row
-  const int32_t i = i0 + col;                                      // the lane's row
-  const int32_t seen = Lk - Lq + i;                                // its last key, below 0 if none
-  // keys that the workgroup's, the wave's rows see
-  const int32_t wg_keys = min(Lk, Lk - Lq + min(static_cast<int32_t>(first) + kRows, Lq));
-  const int32_t w_keys = i0 < Lq ? min(Lk, Lk - Lq + min(i0 + 32, Lq)) : 0;
-  const int32_t full = Lk - Lq + i0 + 1;                           // keys that each of the wave's rows sees
-  const int32_t n_tiles = wg_keys > 0 ? (wg_keys + KT - 1) / KT : 0;
+  RowTile t;
+  t.q0 = cut(a.q_offsets, lo, a.Tq);
+  t.k0 = cut(a.k_offsets, lo, a.Tk);
+  const uint32_t q1 = cut(a.q_offsets, lo + 1, a.Tq), k1 = cut(a.k_offsets, lo + 1, a.Tk);
+  t.Lq = q1 > t.q0 ? static_cast<int32_t>(q1 - t.q0) : 0;
+  t.Lk = k1 > t.k0 ? static_cast<int32_t>(k1 - t.k0) : 0;
+  const uint32_t first = (rt - (t.q0 / kRows + lo)) * kRows;
+  t.any = first < static_cast<uint32_t>(t.Lq);
+  t.first = static_cast<int32_t>(first);
+  t.keys = t.any ? max(min(t.Lk, t.Lk - t.Lq + min(t.first + kRows, t.Lq)), 0) : 0;
+  return t;
+}
 
-  v8bf qf[KS];
-  {
-    const uint16_t* row = a.q + static_cast<int64_t>(q0 + min(i, Lq - 1)) * a.q_stride + head * D + hf * 8;
-#pragma unroll
-    for (int j = 0; j < KS; ++j) qf[j] = *reinterpret_cast<const v8bf*>(row + j * 16);
-  }
+template <int D>
+constexpr int key_tile() { return D <= 128 ? 64 : 32; }
 
-  // DMA: an instruction fills 1024 bytes of LDS in lane order; instruction x of a tile holds rows from x * 1024 / (2 D)
-  const uint16_t* kbase = a.k + static_cast<int64_t>(k0) * a.k_stride + kvh * D;
-  const uint16_t* vbase = a.v + static_cast<int64_t>(k0) * a.v_stride + kvh * D;
+// Splits that a row tile with so many keys is really cut into, and the tiles of each.
+template <int D>
+__device__ __forceinline__ uint32_t split_tiles(int32_t keys, uint32_t splits, uint32_t& used) {
+  const uint32_t n = (static_cast<uint32_t>(keys) + key_tile<D>() - 1) / key_tile<D>();
+  const uint32_t per = max((n + splits - 1) / splits, static_cast<uint32_t>(kMinTiles));
+  used = max((n + per - 1) / per, 1u);
+  return per;
+}
+
+template <int D, bool SAME>
+__global__ __launch_bounds__(kThreads, D >= 512 ? 1 : 2) void attn_prefill_kernel(PrefillArgs a) {
+  constexpr int KT = key_tile<D>();
+  constexpr int CH = D / 8;                             // 16-byte chunks of a row
+  constexpr int TB = KT * D * 2;                        // bytes of a tile
+  constexpr int ND = TB / 1024 / 4;                     // a wave's DMA instructions for one tile
+  using Tile = AttnTile<D, KT>;
+  constexpr int SUB = Tile::SUB;
+  __shared__ __attribute__((aligned(1024))) uint8_t kbuf0[TB], kbuf1[TB], vbuf0[SAME ? 16 : TB], vbuf1[SAME ? 16 : TB];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31;
+
+  // (row tile, head, split): key heads fastest, so that with workgroups dealt to the XCDs in turn an XCD's L2 serves few
+  // key heads; last row tiles first, which have the most keys.
+  uint32_t id = blockIdx.x;
+  const uint32_t kvh = id % a.Hkv;
+  id /= a.Hkv;
+  const uint32_t head = kvh * a.G + id % a.G;
+  id /= a.G;
+  const uint32_t split = id % a.splits, rt = a.tiles - 1 - id / a.splits;
+  const RowTile t = row_tile(a, rt);
+  uint32_t used;
+  const uint32_t per = split_tiles<D>(t.keys, a.splits, used);
+  if (!t.any || split >= used) return;
+  const int32_t hidden = t.Lk - t.Lq;                              // row i sees keys 0 .. hidden + i
+  const int32_t i0 = t.first + wave * 32, i = i0 + col;            // the wave's first row, the lane's
+  const int32_t w_keys = i0 < t.Lq ? min(t.Lk, hidden + min(i0 + 32, t.Lq)) : 0;   // keys that some row of the wave sees
+  const int32_t n_tiles = min((t.keys + KT - 1) / KT, static_cast<int32_t>((split + 1) * per));
+  const int32_t begin = split * per;
+  // whole tiles: those that the workgroup's first row sees whole; an even number of them
+  const int32_t whole = max(min(n_tiles, (hidden + t.first + 1) / KT) - begin, 0) & ~1;
+
+  Tile w;
+  w.begin();
+  w.load_q(a.q + static_cast<int64_t>(t.q0 + min(i, t.Lq - 1)) * a.q_stride + head * D);
+
+  // DMA: an instruction fills 1024 bytes of LDS in lane order
+  const uint16_t* kbase = a.k + static_cast<int64_t>(t.k0) * a.k_stride + kvh * D;
+  const uint16_t* vbase = a.v + static_cast<int64_t>(t.k0) * a.v_stride + kvh * D;
   uint32_t koff[ND], voff[ND];
 #pragma unroll
   for (int x = 0; x < ND; ++x) {
-    const uint32_t at = (wave * ND + x) * 64 + lane, r = at / CH, c = at % CH;
-    uint32_t ck, cv;
-    if constexpr (D >= 128) {
-      ck = c ^ (r & 15);
-      cv = c ^ ((r & 3) << 2);
-    } else {                                            // two rows in the 256 bytes of all banks
-      ck = c ^ ((r >> 1) & 7);
-      cv = c ^ (((r >> 1) & 1) << 2);
-    }
-    koff[x] = r * static_cast<uint32_t>(a.k_stride) * 2 + ck * 16;
-    voff[x] = r * static_cast<uint32_t>(a.v_stride) * 2 + cv * 16;
+    const uint32_t at = (wave * ND + x) * 64 + lane, r = at / CH, c = swizzled<D>(at % CH, r);
+    koff[x] = r * static_cast<uint32_t>(a.k_stride) * 2 + c * 16;
+    voff[x] = r * static_cast<uint32_t>(a.v_stride) * 2 + c * 16;
   }
-  auto dma = [&](int32_t tile, int buf) {
-    const int32_t r0 = tile * KT, rows = min(KT, Lk - r0);
+  auto dma = [&](int32_t tile, uint8_t* kto, uint8_t* vto) {
+    const int32_t r0 = tile * KT, rows = min(KT, t.Lk - r0);
     const __amdgpu_buffer_rsrc_t kr = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<uint16_t*>(kbase + r0 * a.k_stride), 0,
         (rows - 1) * static_cast<int>(a.k_stride) * 2 + D * 2, kBufferFlags);
-    const __amdgpu_buffer_rsrc_t vr = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t*>(vbase + r0 * a.v_stride), 0,
-        (rows - 1) * static_cast<int>(a.v_stride) * 2 + D * 2, kBufferFlags);
-    uint8_t* to = lds + buf * 2 * TB;
 #pragma unroll
-    for (int x = 0; x < ND; ++x) dma16(kr, to + (wave * ND + x) * 1024, koff[x]);
+    for (int x = 0; x < ND; ++x) dma16(kr, kto + (wave * ND + x) * 1024, koff[x]);
+    if constexpr (!SAME) {
+      const __amdgpu_buffer_rsrc_t vr = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint16_t*>(vbase + r0 * a.v_stride), 0,
+          (rows - 1) * static_cast<int>(a.v_stride) * 2 + D * 2, kBufferFlags);
 #pragma unroll
-    for (int x = 0; x < ND; ++x) dma16(vr, to + TB + (wave * ND + x) * 1024, voff[x]);
+      for (int x = 0; x < ND; ++x) dma16(vr, vto + (wave * ND + x) * 1024, voff[x]);
+    }
+  };
+  // this wave's part of the tile is in LDS, and after the barrier everyone's; everyone has read the other buffer
+  auto turn = [&]() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+  auto step = [&](int32_t tile, const uint8_t* kt, const uint8_t* vt, uint8_t* knext, uint8_t* vnext) {
+    turn();
+    if (tile + 1 < n_tiles) dma(tile + 1, knext, vnext);
+    v16f s[SUB];
+    v8bf pf[SUB][2];
+    w.scores(kt, s);
+    w.weights(s, a.scale, pf);
+    w.values(SAME ? kt : vt, pf);
   };
 
-  // where a lane reads: K row col of a group of 32, chunk 2 kk + hf; V rows 4 hf + (lane % 16) / 4 of a group of 8,
-  // columns 16 ((lane / 16) % 2) + 4 (lane % 4) of 32
-  const uint32_t kswz = D >= 128 ? col & 15 : (col >> 1) & 7;
-  const uint32_t krow = col * (D * 2);
-  const uint32_t vr4 = (lane & 15) >> 2, vswz = D >= 128 ? vr4 : vr4 >> 1;
-  const uint32_t vrow = (hf * 4 + vr4) * (D * 2) + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
-
-  float m = -INFINITY, l = 0.0f;
-  v16f acc[DT];
-#pragma unroll
-  for (int d = 0; d < DT; ++d)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) acc[d][r] = 0.0f;
-
-  if (n_tiles > 0) dma(0, 0);
-  for (int32_t tile = 0; tile < n_tiles; ++tile) {
-    // this wave's part of the tile is in LDS, and after the barrier everyone's; everyone has read the other buffer
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (tile + 1 < n_tiles) dma(tile + 1, (tile + 1) & 1);
+  int32_t tile = begin;
+  if (tile < n_tiles) dma(tile, kbuf0, vbuf0);
+  for (; tile < begin + whole; tile += 2) {
+    step(tile, kbuf0, vbuf0, kbuf1, vbuf1);
+    step(tile + 1, kbuf1, vbuf1, kbuf0, vbuf0);
+  }
+#pragma unroll 1
+  for (; tile < n_tiles; ++tile) {
+    const bool second = ((tile - begin) & 1) != 0;
+    turn();
+    if (tile + 1 < n_tiles) dma(tile + 1, second ? kbuf0 : kbuf1, second ? vbuf0 : vbuf1);
     const int32_t t0 = tile * KT;
     if (t0 >= w_keys) continue;
-    const uint8_t* kt = lds + (tile & 1) * 2 * TB;
-    const uint8_t* vt = kt + TB;
+    const uint8_t* kt = second ? kbuf1 : kbuf0;
+    const uint8_t* vt = SAME ? kt : second ? vbuf1 : vbuf0;
+    const int32_t seen = hidden + i + 1 - t0;           // keys of the tile that the lane's row sees (rows past Lq: more than
+                                                        // there are, zeros; nobody reads their results)
     v16f s[SUB];
-#pragma unroll
-    for (int u = 0; u < SUB; ++u)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[u][r] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < KS; ++j)
-#pragma unroll
-      for (int u = 0; u < SUB; ++u) {
-        const v8bf kf = *reinterpret_cast<const v8bf*>(kt + u * 32 * D * 2 + krow + (((2 * j + hf) ^ kswz) << 4));
-        s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[j], s[u], 0, 0, 0);
-      }
-    const bool masked = t0 + KT > full;                 // some row of the wave does not see all of the tile
-    float top = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < SUB; ++u)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        if (masked && t0 + u * 32 + (r >> 2) * 8 + hf * 4 + (r & 3) > seen) s[u][r] = -INFINITY;
-        top = fmaxf(top, s[u][r]);
-      }
-    top = fmaxf(top, __shfl_xor(top, 32)) * a.scale;
-    top = fmaxf(m, top);
-    const float base = top == -INFINITY ? 0.0f : top;   // nothing but -inf so far: all weights are 0
-    if (__any(top > m)) {
-      const float f = __builtin_amdgcn_exp2f(m - base);
-      l *= f;
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[d][r] *= f;
-      m = top;
-    }
     v8bf pf[SUB][2];
+    w.scores(kt, s);
 #pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-      float w[16];
+    for (int u = 0; u < SUB; ++u)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][r], a.scale, -base));
-        l += w[r];
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const v4u x = {pack_bf16x2(w[8 * h], w[8 * h + 1]), pack_bf16x2(w[8 * h + 2], w[8 * h + 3]),
-                       pack_bf16x2(w[8 * h + 4], w[8 * h + 5]), pack_bf16x2(w[8 * h + 6], w[8 * h + 7])};
-        pf[u][h] = __builtin_bit_cast(v8bf, x);
-      }
-    }
-    auto v_frag = [&](int d, int u, int h) {            // tokens 16 (2 u + h) + .. of the tile, columns 32 d + ..
-      const uint8_t* at = vt + (u * 32 + h * 16) * D * 2 + vrow + ((d ^ vswz) << 6);
-      const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)at);
-      const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)(at + 8 * D * 2));
-      const v2u xu = __builtin_bit_cast(v2u, x), yu = __builtin_bit_cast(v2u, y);
-      return v4u{xu[0], xu[1], yu[0], yu[1]};
-    };
-    if (!masked) {
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int u = 0; u < SUB; ++u)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, v_frag(d, u, h)), pf[u][h], acc[d], 0, 0, 0);
-    } else {
-      // A hidden key's weight is 0, but 0 * Inf is not: values that are not finite go into the product as 0, and the
-      // rows that see one get it back by a product of its own, of what is seen (0 or 1) with 1 for +Inf, 2^8 for -Inf and
-      // 2^16 for NaN, whose sums over at most 64 keys tell the three apart.
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        uint32_t odd = 0;
-#pragma unroll
-        for (int u = 0; u < SUB; ++u)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            v4u x = v_frag(d, u, h);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const bool b0 = (x[k] & 0x7F80u) == 0x7F80u, b1 = (x[k] & 0x7F800000u) == 0x7F800000u;
-              x[k] &= (b0 ? 0xFFFF0000u : ~0u) & (b1 ? 0xFFFFu : ~0u);
-              odd |= static_cast<uint32_t>(b0 | b1);
-            }
-            acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, x), pf[u][h], acc[d], 0, 0, 0);
-          }
-        if (__any(odd != 0)) {
-          v16f found;
-#pragma unroll
-          for (int r = 0; r < 16; ++r) found[r] = 0.0f;
-#pragma unroll
-          for (int u = 0; u < SUB; ++u)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const v4u x = v_frag(d, u, h);
-              v4u what, see;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                what[k] = see[k] = 0;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const uint32_t y = (x[k] >> (16 * e)) & 0xFFFFu;
-                  const uint32_t kind = y == 0x7F80u ? 0x3F80u : y == 0xFF80u ? 0x4380u : (y & 0x7F80u) == 0x7F80u ? 0x4780u : 0u;
-                  const int j = k * 2 + e;              // key of element j: 4 hf + j, then 8 + 4 hf + (j - 4)
-                  const int32_t t = t0 + u * 32 + h * 16 + (j >> 2) * 8 + hf * 4 + (j & 3);
-                  what[k] |= kind << (16 * e);
-                  see[k] |= (t <= seen ? 0x3F80u : 0u) << (16 * e);
-                }
-              }
-              found = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, what), __builtin_bit_cast(v8bf, see),
-                                                             found, 0, 0, 0);
-            }
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const uint32_t n = static_cast<uint32_t>(found[r]);
-            if (n & 0xFFu) acc[d][r] += INFINITY;
-            if (n & 0xFF00u) acc[d][r] -= INFINITY;
-            if (n >> 16) acc[d][r] = __builtin_nanf("");
-          }
-        }
-      }
-    }
+      for (int x = 0; x < 16; ++x) s[u][x] = u * 32 + w.key_of(x) < seen ? s[u][x] : -INFINITY;
+    w.weights(s, a.scale, pf);
+    w.values_masked(vt, pf, seen);
   }
 
-  if (i >= Lq) return;
-  l += __shfl_xor(l, 32);
-  const float inv = seen >= 0 && Lk > 0 ? 1.0f / l : 0.0f;
-  uint16_t* row = a.out + (static_cast<int64_t>(q0 + i) * a.H + head) * D + hf * 4;
+  w.l += __shfl_xor(w.l, 32);
+  if (used > 1) {
+    float* part = a.parts + (static_cast<size_t>(rt * a.H + head) * a.splits + split) * kRows * (D + 2);
+    float* row = part + (wave * 32 + col) * D + w.hf * 4;
 #pragma unroll
-  for (int d = 0; d < DT; ++d)
+    for (int d = 0; d < Tile::DT; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<float4*>(row + d * 32 + r * 8) =
+            make_float4(w.acc[d][4 * r], w.acc[d][4 * r + 1], w.acc[d][4 * r + 2], w.acc[d][4 * r + 3]);
+    if (w.hf == 0) {
+      part[kRows * D + wave * 32 + col] = w.m;
+      part[kRows * D + kRows + wave * 32 + col] = w.l;
+    }
+    return;
+  }
+  if (i >= t.Lq) return;
+  const float inv = t.Lk > 0 && hidden + i >= 0 ? 1.0f / w.l : 0.0f;
+  uint16_t* row = a.out + (static_cast<int64_t>(t.q0 + i) * a.H + head) * D + w.hf * 4;
+#pragma unroll
+  for (int d = 0; d < Tile::DT; ++d)
 #pragma unroll
     for (int r = 0; r < 4; ++r)
       *reinterpret_cast<uint2*>(row + d * 32 + r * 8) =
-          make_uint2(pack_bf16x2(acc[d][4 * r] * inv, acc[d][4 * r + 1] * inv),
-                     pack_bf16x2(acc[d][4 * r + 2] * inv, acc[d][4 * r + 3] * inv));
+          make_uint2(pack_bf16x2(w.acc[d][4 * r] * inv, w.acc[d][4 * r + 1] * inv),
+                     pack_bf16x2(w.acc[d][4 * r + 2] * inv, w.acc[d][4 * r + 3] * inv));
+}
+
+// A workgroup takes kJoinRows rows of a row tile and head: the splits' parts joined in their order.
+constexpr int kJoinRows = 16;
+template <int D>
+__global__ __launch_bounds__(kThreads) void attn_prefill_join_kernel(PrefillArgs a) {
+  uint32_t id = blockIdx.x;
+  const uint32_t r0 = id % (kRows / kJoinRows) * kJoinRows;
+  id /= kRows / kJoinRows;
+  const uint32_t head = id % a.H, rt = id / a.H;
+  const RowTile t = row_tile(a, rt);
+  uint32_t used;
+  split_tiles<D>(t.keys, a.splits, used);
+  if (!t.any || used == 1) return;
+  const float* parts = a.parts + static_cast<size_t>(rt * a.H + head) * a.splits * kRows * (D + 2);
+  for (uint32_t e = threadIdx.x * 4; e < kJoinRows * D; e += kThreads * 4) {
+    const uint32_t r = r0 + e / D, d = e % D;
+    const int32_t i = t.first + static_cast<int32_t>(r);
+    if (i >= t.Lq) break;
+    float m = -INFINITY, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (uint32_t s = 0; s < used; ++s) {
+      const float* p = parts + static_cast<size_t>(s) * kRows * (D + 2);
+      const float x = p[kRows * D + r], top = fmaxf(m, x), base = top == -INFINITY ? 0.0f : top;
+      const float f = __builtin_amdgcn_exp2f(m - base), g = __builtin_amdgcn_exp2f(x - base);
+      const float4 v = *reinterpret_cast<const float4*>(p + r * D + d);
+      l = l * f + p[kRows * D + kRows + r] * g;
+      o = make_float4(o.x * f + v.x * g, o.y * f + v.y * g, o.z * f + v.z * g, o.w * f + v.w * g);
+      m = top;
+    }
+    const float inv = t.Lk - t.Lq + i >= 0 ? 1.0f / l : 0.0f;
+    *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(t.q0 + i) * a.H + head) * D + d) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  }
+}
+
+uint32_t row_tiles(int64_t B, int64_t Tq) { return static_cast<uint32_t>(Tq / kRows + B); }
+
+// How many workgroups share the keys of one row tile and head.  `slots` run at once; with fewer (row tile, head) pairs
+// than that, a split leaves fewer of them idle, as long as every part has some tiles of keys.
+uint32_t split_count(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t D) {
+  const int64_t units = static_cast<int64_t>(row_tiles(B, Tq)) * H, slots = D >= 512 ? 256 : 512;
+  const int64_t tiles = (Tk / B + 63) / 64;             // of an average prompt
+  return static_cast<uint32_t>(std::max<int64_t>(1, std::min(slots / units, tiles / kMinTiles)));
 }
 
 template <int D>
 void launch(const PrefillArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL(attn_prefill_kernel<D>, dim3(a.tiles * a.H), dim3(kThreads), 0, stream, a);
+  const dim3 grid(a.tiles * a.H * a.splits);
+  if (a.k == a.v && a.k_stride == a.v_stride) hipLaunchKernelGGL((attn_prefill_kernel<D, true>), grid, dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL((attn_prefill_kernel<D, false>), grid, dim3(kThreads), 0, stream, a);
+  if (a.splits > 1)
+    hipLaunchKernelGGL(attn_prefill_join_kernel<D>, dim3(a.tiles * a.H * (kRows / kJoinRows)), dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace
 
-size_t prefill_workspace_bytes(int64_t, int64_t, int64_t, int32_t, int32_t, int32_t) { return 0; }
+size_t prefill_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t, int32_t D) {
+  const size_t splits = split_count(B, Tq, Tk, H, D);
+  return splits == 1 ? 0 : splits * row_tiles(B, Tq) * H * kRows * (D + 2) * 4;
+}
 
 mx_status launch_attn_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                               int64_t v_stride, const int32_t* q_offsets, const int32_t* k_offsets, int64_t B,
                               int64_t Tq, int64_t Tk, int32_t H, int32_t Hkv, int32_t D, float scale, void* out,
                               void* workspace, hipStream_t stream) {
-  (void)workspace;
   PrefillArgs a;
   a.q = static_cast<const uint16_t*>(q);
   a.k = static_cast<const uint16_t*>(k);
@@ -315,6 +283,7 @@ mx_status launch_attn_prefill(const void* q, int64_t q_stride, const void* k, in
   a.q_offsets = q_offsets;
   a.k_offsets = k_offsets;
   a.out = static_cast<uint16_t*>(out);
+  a.parts = static_cast<float*>(workspace);
   a.scale = scale * 1.44269504088896340736f;
   a.B = static_cast<uint32_t>(B);
   a.Tq = static_cast<uint32_t>(Tq);
@@ -322,7 +291,8 @@ mx_status launch_attn_prefill(const void* q, int64_t q_stride, const void* k, in
   a.H = static_cast<uint32_t>(H);
   a.Hkv = static_cast<uint32_t>(Hkv);
   a.G = a.H / a.Hkv;
-  a.tiles = static_cast<uint32_t>(Tq / kRows + B);
+  a.tiles = row_tiles(B, Tq);
+  a.splits = split_count(B, Tq, Tk, H, D);
   switch (D) {
     case 64: launch<64>(a, stream); break;
     case 128: launch<128>(a, stream); break;
