@@ -44,10 +44,16 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t c, uint32_t row) {
   else return c ^ ((((row >> 1) & 1) << 2) | ((row >> 2) & 3));
 }
 
-// N pairs of an LDS read for each MFMA, the reads `AHEAD` MFMAs before their use.
-template <int READS, int MFMAS, int AHEAD>
+// The value of the other half of the wave beside the lane's own: {lanes 0..31's, lanes 32..63's}, in every lane.
+__device__ __forceinline__ float2 halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// The schedule of MFMAS matrix instructions with PER LDS reads each: the reads of one come AHEAD instructions before it,
+// so that their latency passes under the others.  (Left alone, the compiler puts them right before their use.)
+template <int PER, int MFMAS, int AHEAD>
 __device__ __forceinline__ void read_ahead() {
-  constexpr int PER = READS / MFMAS;
   __builtin_amdgcn_sched_group_barrier(0x100, PER * AHEAD, 0);
 #pragma unroll
   for (int i = 0; i < MFMAS - AHEAD; ++i) {
@@ -113,6 +119,7 @@ struct AttnTile {
         const v8bf kf = *reinterpret_cast<const v8bf*>(kt + kaddr[j % KA] + u * 32 * D * 2 + (j / KA) * 256);
         s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[j], s[u], 0, 0, 0);
       }
+    read_ahead<1, KS * SUB, 4>();
   }
 
   // Scores to weights: the new maximum, O and l rescaled if it is much larger, P in BF16.
@@ -122,7 +129,8 @@ struct AttnTile {
     for (int u = 0; u < SUB; ++u)
 #pragma unroll
       for (int i = 0; i < 16; i += 2) top = fmaxf(fmaxf(top, s[u][i]), s[u][i + 1]);
-    top = fmaxf(top, __shfl_xor(top, 32)) * scale;
+    const float2 both = halves(top);
+    top = fmaxf(both.x, both.y) * scale;
     if (__any(top > m + kSlack)) {
       const float to = fmaxf(m, top), f = __builtin_amdgcn_exp2f(m - (to == -INFINITY ? 0.0f : to));
       l *= f;
@@ -158,11 +166,12 @@ struct AttnTile {
 
   __device__ __forceinline__ void values(const uint8_t* vt, const v8bf (&pf)[SUB][2]) {
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
+    for (int n = 0; n < 2 * SUB; ++n)
 #pragma unroll
-      for (int n = 0; n < 2 * SUB; ++n)
+      for (int d = 0; d < DT; ++d)
         acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, v_operand(vt, d, n)), pf[n / 2][n % 2],
                                                          acc[d], 0, 0, 0);
+    read_ahead<2, 2 * SUB * DT, 3>();
   }
 
   // As values(), where the lane's row sees only the first `seen` keys of the tile.  A hidden key's weight is 0, but
