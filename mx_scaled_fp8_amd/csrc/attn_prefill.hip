@@ -1,7 +1,7 @@
 // Causal attention over packed prompts (gfx950).
 //
-// A workgroup takes 128 query rows of one prompt and head, 32 for each of its four waves (attn_tile.hpp), and runs over
-// the keys in tiles of KT.  K and V tiles go from global memory to LDS by buffer-load DMA, the next one while this one is
+// A workgroup takes 128 query rows of one prompt and head, 32 for each of its four waves (attn_tile.hpp; for rows of 512
+// there are eight, two of which share 32 rows), and runs over the keys in tiles of KT.  K and V tiles go from global memory to LDS by buffer-load DMA, the next one while this one is
 // used; rows past the end are zeros by the buffer's bound.  Tiles that every row sees whole run first, two to a turn of
 // the loop, so that each of the two buffers is an object of its own and the compiler waits for no DMA but what a read
 // needs; the last few, which hold the diagonal and the ragged end, go through a loop with masks.
@@ -16,7 +16,6 @@ namespace mx {
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kRows = 128;             // query rows of a workgroup
 constexpr int kMinTiles = 4;           // fewest key tiles of a split
 
@@ -81,16 +80,22 @@ __device__ __forceinline__ uint32_t split_tiles(int32_t keys, uint32_t splits, u
   return per;
 }
 
+template <int D>
+constexpr int halves_of() { return D >= 512 ? 2 : 1; }
+
 template <int D, bool SAME>
-__global__ __launch_bounds__(kThreads, D >= 512 ? 1 : 2) void attn_prefill_kernel(PrefillArgs a) {
+__global__ __launch_bounds__(256 * halves_of<D>(), 2) void attn_prefill_kernel(PrefillArgs a) {
+  constexpr int HALVES = halves_of<D>(), WAVES = 4 * HALVES;
   constexpr int KT = key_tile<D>();
   constexpr int CH = D / 8;                             // 16-byte chunks of a row
   constexpr int TB = KT * D * 2;                        // bytes of a tile
-  constexpr int ND = TB / 1024 / 4;                     // a wave's DMA instructions for one tile
-  using Tile = AttnTile<D, KT>;
+  constexpr int ND = TB / 1024 / WAVES;                 // a wave's DMA instructions for one tile
+  using Tile = AttnTile<D, KT, HALVES>;
   constexpr int SUB = Tile::SUB;
   __shared__ __attribute__((aligned(1024))) uint8_t kbuf0[TB], kbuf1[TB], vbuf0[SAME ? 16 : TB], vbuf1[SAME ? 16 : TB];
+  __shared__ __attribute__((aligned(16))) uint8_t partial[HALVES == 1 ? 16 : WAVES * SUB * 4096];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31;
+  const int group = wave & 3, half = wave >> 2;         // which 32 rows, which half of D
 
   // (row tile, head, split): key heads fastest, so that with workgroups dealt to the XCDs in turn an XCD's L2 serves few
   // key heads; last row tiles first, which have the most keys.
@@ -105,7 +110,7 @@ __global__ __launch_bounds__(kThreads, D >= 512 ? 1 : 2) void attn_prefill_kerne
   const uint32_t per = split_tiles<D>(t.keys, a.splits, used);
   if (!t.any || split >= used) return;
   const int32_t hidden = t.Lk - t.Lq;                              // row i sees keys 0 .. hidden + i
-  const int32_t i0 = t.first + wave * 32, i = i0 + col;            // the wave's first row, the lane's
+  const int32_t i0 = t.first + group * 32, i = i0 + col;            // the wave's first row, the lane's
   const int32_t w_keys = i0 < t.Lq ? min(t.Lk, hidden + min(i0 + 32, t.Lq)) : 0;   // keys that some row of the wave sees
   const int32_t n_tiles = min((t.keys + KT - 1) / KT, static_cast<int32_t>((split + 1) * per));
   const int32_t begin = split * per;
@@ -113,42 +118,54 @@ __global__ __launch_bounds__(kThreads, D >= 512 ? 1 : 2) void attn_prefill_kerne
   const int32_t whole = max(min(n_tiles, (hidden + t.first + 1) / KT) - begin, 0) & ~1;
 
   Tile w;
-  w.begin();
-  w.load_q(a.q + static_cast<int64_t>(t.q0 + min(i, t.Lq - 1)) * a.q_stride + head * D);
+  w.begin(half);
+  w.load_q(a.q + static_cast<int64_t>(t.q0 + min(i, t.Lq - 1)) * a.q_stride + head * D + half * Tile::DH);
 
-  // DMA: an instruction fills 1024 bytes of LDS in lane order
+  // DMA: an instruction fills 1024 bytes of LDS, RPI rows, in lane order.  The swizzle repeats after 16 rows, so that a
+  // wave's PAT instructions of one PERIOD of rows serve all of them.
+  constexpr int RPI = 512 / D, PERIOD = RPI * WAVES > 16 ? RPI * WAVES : 16, PAT = PERIOD / RPI / WAVES;
   const uint16_t* kbase = a.k + static_cast<int64_t>(t.k0) * a.k_stride + kvh * D;
   const uint16_t* vbase = a.v + static_cast<int64_t>(t.k0) * a.v_stride + kvh * D;
-  uint32_t koff[ND], voff[ND];
+  const uint32_t ks2 = static_cast<uint32_t>(a.k_stride) * 2, vs2 = static_cast<uint32_t>(a.v_stride) * 2;
+  uint32_t koff[PAT], voff[PAT];
 #pragma unroll
-  for (int x = 0; x < ND; ++x) {
-    const uint32_t at = (wave * ND + x) * 64 + lane, r = at / CH, c = swizzled<D>(at % CH, r);
-    koff[x] = r * static_cast<uint32_t>(a.k_stride) * 2 + c * 16;
-    voff[x] = r * static_cast<uint32_t>(a.v_stride) * 2 + c * 16;
+  for (int x = 0; x < PAT; ++x) {
+    const uint32_t r = (wave * PAT + x) * RPI + lane / CH, c = swizzled<D>(lane % CH, r);
+    koff[x] = r * ks2 + c * 16;
+    voff[x] = r * vs2 + c * 16;
   }
-  auto dma = [&](int32_t tile, uint8_t* kto, uint8_t* vto) {
-    const int32_t r0 = tile * KT, rows = min(KT, t.Lk - r0);
-    const __amdgpu_buffer_rsrc_t kr = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t*>(kbase + r0 * a.k_stride), 0,
-        (rows - 1) * static_cast<int>(a.k_stride) * 2 + D * 2, kBufferFlags);
+  auto dma_rows = [&](int32_t tile, const uint16_t* base, int64_t stride, uint32_t s2, const uint32_t (&off)[PAT], uint8_t* to) {
 #pragma unroll
-    for (int x = 0; x < ND; ++x) dma16(kr, kto + (wave * ND + x) * 1024, koff[x]);
-    if constexpr (!SAME) {
-      const __amdgpu_buffer_rsrc_t vr = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<uint16_t*>(vbase + r0 * a.v_stride), 0,
-          (rows - 1) * static_cast<int>(a.v_stride) * 2 + D * 2, kBufferFlags);
-#pragma unroll
-      for (int x = 0; x < ND; ++x) dma16(vr, vto + (wave * ND + x) * 1024, voff[x]);
+    for (int x = 0; x < ND; ++x) {
+      const int32_t r0 = tile * KT + (x / PAT) * PERIOD, rows = min(PERIOD, t.Lk - r0);   // of this period
+      const __amdgpu_buffer_rsrc_t from = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint16_t*>(base + r0 * stride), 0, rows > 0 ? (rows - 1) * static_cast<int>(s2) + D * 2 : 0,
+          kBufferFlags);
+      dma16(from, to + ((x / PAT) * PERIOD + (wave * PAT + x % PAT) * RPI) * D * 2, off[x % PAT]);
     }
   };
+  auto dma = [&](int32_t tile, uint8_t* kto, uint8_t* vto) {
+    dma_rows(tile, kbase, a.k_stride, ks2, koff, kto);
+    if constexpr (!SAME) dma_rows(tile, vbase, a.v_stride, vs2, voff, vto);
+  };
   // this wave's part of the tile is in LDS, and after the barrier everyone's; everyone has read the other buffer
-  auto turn = [&]() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+  auto turn = [&]() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));
+    asm volatile("s_barrier" ::: "memory");
+  };
+  auto scores = [&](const uint8_t* kt, v16f (&s)[SUB], bool active) {
+    w.hide_bases();
+    if (active) w.scores(kt, s);
+    if constexpr (HALVES == 2)
+      Tile::exchange(s, partial + wave * SUB * 4096, partial + (wave ^ 4) * SUB * 4096, active);
+  };
   auto step = [&](int32_t tile, const uint8_t* kt, const uint8_t* vt, uint8_t* knext, uint8_t* vnext) {
     turn();
     if (tile + 1 < n_tiles) dma(tile + 1, knext, vnext);
     v16f s[SUB];
     v8bf pf[SUB][2];
-    w.scores(kt, s);
+    scores(kt, s, true);
     w.weights(s, a.scale, pf);
     w.values(SAME ? kt : vt, pf);
   };
@@ -165,14 +182,16 @@ __global__ __launch_bounds__(kThreads, D >= 512 ? 1 : 2) void attn_prefill_kerne
     turn();
     if (tile + 1 < n_tiles) dma(tile + 1, second ? kbuf0 : kbuf1, second ? vbuf0 : vbuf1);
     const int32_t t0 = tile * KT;
-    if (t0 >= w_keys) continue;
+    const bool active = t0 < w_keys;
+    if (HALVES == 1 && !active) continue;
     const uint8_t* kt = second ? kbuf1 : kbuf0;
     const uint8_t* vt = SAME ? kt : second ? vbuf1 : vbuf0;
     const int32_t seen = hidden + i + 1 - t0;           // keys of the tile that the lane's row sees (rows past Lq: more than
                                                         // there are, zeros; nobody reads their results)
     v16f s[SUB];
     v8bf pf[SUB][2];
-    w.scores(kt, s);
+    scores(kt, s, active);
+    if (!active) continue;
 #pragma unroll
     for (int u = 0; u < SUB; ++u)
 #pragma unroll
@@ -184,22 +203,22 @@ __global__ __launch_bounds__(kThreads, D >= 512 ? 1 : 2) void attn_prefill_kerne
   w.l += __shfl_xor(w.l, 32);
   if (used > 1) {
     float* part = a.parts + (static_cast<size_t>(rt * a.H + head) * a.splits + split) * kRows * (D + 2);
-    float* row = part + (wave * 32 + col) * D + w.hf * 4;
+    float* row = part + (group * 32 + col) * D + half * Tile::DH + w.hf * 4;
 #pragma unroll
     for (int d = 0; d < Tile::DT; ++d)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         *reinterpret_cast<float4*>(row + d * 32 + r * 8) =
             make_float4(w.acc[d][4 * r], w.acc[d][4 * r + 1], w.acc[d][4 * r + 2], w.acc[d][4 * r + 3]);
-    if (w.hf == 0) {
-      part[kRows * D + wave * 32 + col] = w.m;
-      part[kRows * D + kRows + wave * 32 + col] = w.l;
+    if (w.hf == 0 && half == 0) {
+      part[kRows * D + group * 32 + col] = w.m;
+      part[kRows * D + kRows + group * 32 + col] = w.l;
     }
     return;
   }
   if (i >= t.Lq) return;
   const float inv = t.Lk > 0 && hidden + i >= 0 ? 1.0f / w.l : 0.0f;
-  uint16_t* row = a.out + (static_cast<int64_t>(t.q0 + i) * a.H + head) * D + w.hf * 4;
+  uint16_t* row = a.out + (static_cast<int64_t>(t.q0 + i) * a.H + head) * D + half * Tile::DH + w.hf * 4;
 #pragma unroll
   for (int d = 0; d < Tile::DT; ++d)
 #pragma unroll
@@ -210,9 +229,9 @@ __global__ __launch_bounds__(kThreads, D >= 512 ? 1 : 2) void attn_prefill_kerne
 }
 
 // A workgroup takes kJoinRows rows of a row tile and head: the splits' parts joined in their order.
-constexpr int kJoinRows = 16;
+constexpr int kJoinRows = 16, kJoinThreads = 256;
 template <int D>
-__global__ __launch_bounds__(kThreads) void attn_prefill_join_kernel(PrefillArgs a) {
+__global__ __launch_bounds__(kJoinThreads) void attn_prefill_join_kernel(PrefillArgs a) {
   uint32_t id = blockIdx.x;
   const uint32_t r0 = id % (kRows / kJoinRows) * kJoinRows;
   id /= kRows / kJoinRows;
@@ -222,7 +241,7 @@ __global__ __launch_bounds__(kThreads) void attn_prefill_join_kernel(PrefillArgs
   split_tiles<D>(t.keys, a.splits, used);
   if (!t.any || used == 1) return;
   const float* parts = a.parts + static_cast<size_t>(rt * a.H + head) * a.splits * kRows * (D + 2);
-  for (uint32_t e = threadIdx.x * 4; e < kJoinRows * D; e += kThreads * 4) {
+  for (uint32_t e = threadIdx.x * 4; e < kJoinRows * D; e += kJoinThreads * 4) {
     const uint32_t r = r0 + e / D, d = e % D;
     const int32_t i = t.first + static_cast<int32_t>(r);
     if (i >= t.Lq) break;
@@ -255,11 +274,11 @@ uint32_t split_count(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t D) {
 
 template <int D>
 void launch(const PrefillArgs& a, hipStream_t stream) {
-  const dim3 grid(a.tiles * a.H * a.splits);
-  if (a.k == a.v && a.k_stride == a.v_stride) hipLaunchKernelGGL((attn_prefill_kernel<D, true>), grid, dim3(kThreads), 0, stream, a);
-  else hipLaunchKernelGGL((attn_prefill_kernel<D, false>), grid, dim3(kThreads), 0, stream, a);
+  const dim3 grid(a.tiles * a.H * a.splits), block(256 * halves_of<D>());
+  if (a.k == a.v && a.k_stride == a.v_stride) hipLaunchKernelGGL((attn_prefill_kernel<D, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((attn_prefill_kernel<D, false>), grid, block, 0, stream, a);
   if (a.splits > 1)
-    hipLaunchKernelGGL(attn_prefill_join_kernel<D>, dim3(a.tiles * a.H * (kRows / kJoinRows)), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL(attn_prefill_join_kernel<D>, dim3(a.tiles * a.H * (kRows / kJoinRows)), dim3(kJoinThreads), 0, stream, a);
 }
 
 }  // namespace

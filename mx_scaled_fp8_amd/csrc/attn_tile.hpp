@@ -63,33 +63,33 @@ __device__ __forceinline__ void read_ahead() {
   __builtin_amdgcn_sched_group_barrier(0x008, AHEAD, 0);
 }
 
-template <int D, int KT>
+// HALVES 2: two waves share 32 rows, each with half of D: O's and, in the first product, Q's and K's, whose partial scores
+// they exchange (a row of 512 is too much for one wave's registers).
+template <int D, int KT, int HALVES>
 struct AttnTile {
   static constexpr int SUB = KT / 32;
-  static constexpr int KS = D / 16;
-  static constexpr int DT = D / 32;
-  static constexpr int KA = KS < 8 ? KS : 8;            // places of K's chunks in a row that differ by more than 256 bytes n
+  static constexpr int DH = D / HALVES;
+  static constexpr int KS = DH / 16;
+  static constexpr int DT = DH / 32;
+  static constexpr int KA = KS < 8 ? KS : 8;            // chunks of K, groups of V within 256 bytes
   static constexpr int VA = DT < 4 ? DT : 4;
   v8bf qf[KS];
   v16f acc[DT];
   float m, l;
-  uint32_t kaddr[KA], vaddr[2][VA];
+  uint32_t kbase, vbase[2];
   int hf;
 
-  __device__ __forceinline__ void begin() {
+  __device__ __forceinline__ void begin(int half) {
     const uint32_t lane = threadIdx.x & 63, col = lane & 31;
     hf = lane >> 5;
-    // K: row col of 32, chunk 2 j + hf
-#pragma unroll
-    for (int j = 0; j < KA; ++j) kaddr[j] = col * (D * 2) + (swizzled<D>(2 * j + hf, col) << 4);
+    // K: row col of 32, chunk 2 j + hf, whose place differs from chunk hf's by the exclusive or of 2 j
+    kbase = col * (D * 2) + half * (DH * 2) + (swizzled<D>(hf, col) << 4);
     // V: row 8 n + 4 hf + (lane % 16) / 4, columns 16 ((lane / 16) % 2) + 4 (lane % 4) of 32; n odd and even apart, since
     // the swizzle has row / 4 % 4
     const uint32_t r = hf * 4 + ((lane & 15) >> 2), c = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
 #pragma unroll
     for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int d = 0; d < VA; ++d)
-        vaddr[n][d] = (n * 8 + r) * (D * 2) + (swizzled<D>(d * 4 + c, n * 8 + r) << 4) + (lane & 1) * 8;
+      vbase[n] = (n * 8 + r) * (D * 2) + half * (DH * 2) + (swizzled<D>(c, n * 8 + r) << 4) + (lane & 1) * 8;
     m = -INFINITY;
     l = 0.0f;
 #pragma unroll
@@ -98,7 +98,7 @@ struct AttnTile {
       for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
   }
 
-  // The lane's query row, D elements in global memory.
+  // The lane's query row, in global memory (its half, if shared).
   __device__ __forceinline__ void load_q(const uint16_t* row) {
 #pragma unroll
     for (int j = 0; j < KS; ++j) qf[j] = *reinterpret_cast<const v8bf*>(row + j * 16 + hf * 8);
@@ -116,10 +116,43 @@ struct AttnTile {
     for (int j = 0; j < KS; ++j)
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
-        const v8bf kf = *reinterpret_cast<const v8bf*>(kt + kaddr[j % KA] + u * 32 * D * 2 + (j / KA) * 256);
+        const v8bf kf = *reinterpret_cast<const v8bf*>(kt + (kbase ^ (j % KA << 5)) + u * 32 * D * 2 + (j / KA) * 256);
         s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[j], s[u], 0, 0, 0);
       }
     read_ahead<1, KS * SUB, 4>();
+  }
+
+  // Partial scores summed with those of the wave that has the other half of D: `mine` and `other` are places of
+  // SUB * 4096 bytes.  All waves of the workgroup come here.
+  __device__ __forceinline__ static void exchange(v16f (&s)[SUB], uint8_t* mine, const uint8_t* other, bool active) {
+    const uint32_t lane = threadIdx.x & 63;
+    if (active) {
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<float4*>(mine + (u * 4 + c) * 1024 + lane * 16) =
+              make_float4(s[u][4 * c], s[u][4 * c + 1], s[u][4 * c + 2], s[u][4 * c + 3]);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (active) {
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float4 x = *reinterpret_cast<const float4*>(other + (u * 4 + c) * 1024 + lane * 16);
+          s[u][4 * c] += x.x;
+          s[u][4 * c + 1] += x.y;
+          s[u][4 * c + 2] += x.z;
+          s[u][4 * c + 3] += x.w;
+        }
+    }
+  }
+
+  // The bases as the compiler cannot see through, so that it forms the addresses where they are used and does not hold
+  // them all in registers that a wide row needs.
+  __device__ __forceinline__ void hide_bases() {
+    if constexpr (D >= 256) asm volatile("" : "+v"(kbase), "+v"(vbase[0]), "+v"(vbase[1]));
   }
 
   // Scores to weights: the new maximum, O and l rescaled if it is much larger, P in BF16.
@@ -160,7 +193,7 @@ struct AttnTile {
   // V^T's operand: tokens 16 n .. + 15 of the tile in the order of P, columns 32 d .. + 31.
   __device__ __forceinline__ v4u v_operand(const uint8_t* vt, int d, int n) const {
     const uint32_t at = n * 16 * D * 2 + (d / VA) * 256;
-    const v2u x = read_transposed(vt + vaddr[0][d % VA] + at), y = read_transposed(vt + vaddr[1][d % VA] + at);
+    const v2u x = read_transposed(vt + (vbase[0] ^ (d % VA << 6)) + at), y = read_transposed(vt + (vbase[1] ^ (d % VA << 6)) + at);
     return v4u{x[0], x[1], y[0], y[1]};
   }
 
