@@ -194,7 +194,7 @@ mx_status mx_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t H, 
   MX_CHECK(max_pages >= 1 && max_pages < k31 && max_pages * page_size < k31, "%s: max_pages = %lld of %d tokens out of range",
            fn, (long long)max_pages, page_size);
   const int64_t streams = B * Hkv * ((H / Hkv + 15) / 16);
-  MX_CHECK(streams < (int64_t(1) << 24) && streams * ((max_pages * page_size + 127) / 128) < k31,
+  MX_CHECK(streams < (int64_t(1) << 24) && streams * ((max_pages * page_size + 31) / 32) < k31,
            "%s: B = %lld x Hkv = %d x %lld tokens too large", fn, (long long)B, Hkv, (long long)(max_pages * page_size));
   if (B == 0) { clear_error(); return MX_OK; }
   MX_CHECK(q && block_table && lens && out, "%s: null tensor pointer", fn);

@@ -16,13 +16,8 @@
 //    no transposition through LDS.
 // Codes become BF16 (exact) by v_cvt_scalef32_pk_bf16_fp8 with their block's scale.
 //
-// Work is cut into tiles of 128 tokens (32 for each of the four waves), numbered through all sequences, and every
-// workgroup takes an equal share of consecutive tiles: a long sequence is spread over many workgroups, many short ones
-// share one.  A (sequence, head group) that a workgroup does not cover whole leaves its part (O, m, l) in the
-// workspace, at most two of them for a workgroup (where its share begins and where it ends), and a second kernel joins them.
-#include <algorithm>
-
-#include "kv_cache.hpp"
+// Work is shared as attn_plan.hpp says, in tiles of 128 tokens, 32 for each of the four waves.
+#include "attn_decode.hpp"
 
 namespace mx {
 
@@ -35,49 +30,6 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256;
 constexpr int kTile = 128;             // tokens of a tile
 constexpr int kHeads = 16;             // query heads of a stream: one (sequence, key head, group of up to 16 query heads)
-
-struct DecodeArgs {
-  KvCache c;
-  const uint16_t* q;
-  int64_t q_stride;
-  const int32_t* lens;
-  uint16_t* out;
-  float* parts;              // [groups][2][kHeads][D + 2]: O, m, l
-  uint32_t* plan;            // [0] share, [1 + b] first tile of sequence b
-  float scale;               // times log2(e)
-  uint32_t B, H, G;          // G query heads a key head
-  uint32_t streams;          // a sequence's: Hkv * head groups
-  uint32_t head_groups;
-};
-
-// Tiles of one stream of sequence b.
-__device__ __forceinline__ uint32_t tiles_of(const DecodeArgs& a, uint32_t b) {
-  const int32_t n = a.lens[b];
-  const uint32_t cap = a.c.max_pages << a.c.page_shift;
-  return (min(static_cast<uint32_t>(max(n, 0)), cap) + kTile - 1) / kTile;
-}
-
-// Sum over the workgroup of the threads' v, and the sum of those before this thread.
-__device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t* buf, uint32_t& before) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t x = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t y = __shfl_up(x, d);
-    if (lane >= d) x += y;
-  }
-  __syncthreads();
-  if (lane == 63) buf[wave] = x;
-  __syncthreads();
-  uint32_t sum = 0, base = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 64; ++w) {
-    if (w < wave) base += buf[w];
-    sum += buf[w];
-  }
-  before = base + x - v;
-  return sum;
-}
 
 __device__ __forceinline__ float across_groups_max(float x) {
   x = fmaxf(x, __shfl_xor(x, 16));
@@ -98,54 +50,17 @@ __global__ __launch_bounds__(kThreads) void attn_decode_kernel(DecodeArgs a) {
   constexpr int DPL = PANEL / 16;                       // elements of V in a lane, panel and token
   constexpr int NP = D / PANEL;
   constexpr int VW = DPL * EB / 4;                      // their words
-  __shared__ uint32_t sbuf[4], sfound[2];
   __shared__ float sml[4][kHeads][2];
   __shared__ __attribute__((aligned(16))) float sacc[4][kHeads][D + 4];   // + 4: the columns' rows in different banks
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
 
-  // this workgroup's share of the tiles, and the sequence that it begins in
-  uint32_t total = 0;
-  for (uint32_t b0 = 0; b0 < a.B; b0 += kThreads) {
-    const uint32_t b = b0 + threadIdx.x;
-    uint32_t before;
-    const uint32_t n = b < a.B ? tiles_of(a, b) : 0;
-    const uint32_t sum = scan(n, sbuf, before);
-    if (blockIdx.x == 0 && b < a.B) a.plan[1 + b] = (total + before) * a.streams;
-    total += sum;
-  }
-  const uint32_t share = max((total * a.streams + gridDim.x - 1) / gridDim.x, 1u);
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.plan[0] = share;
-  const uint32_t all = total * a.streams;
-  uint32_t t = blockIdx.x * share;
-  if (t >= all) return;
-  const uint32_t end = min(t + share, all);
-  uint32_t done = 0;
-  for (uint32_t b0 = 0; b0 < a.B; b0 += kThreads) {
-    const uint32_t b = b0 + threadIdx.x;
-    uint32_t before;
-    const uint32_t n = b < a.B ? tiles_of(a, b) : 0;
-    const uint32_t sum = scan(n, sbuf, before);
-    const uint32_t first = (done + before) * a.streams;
-    if (t >= first && t < first + n * a.streams) {
-      sfound[0] = b;
-      sfound[1] = first;
-    }
-    done += sum;
-    if (t < done * a.streams) break;
-  }
-  __syncthreads();
-  uint32_t b = __builtin_amdgcn_readfirstlane(sfound[0]), first = __builtin_amdgcn_readfirstlane(sfound[1]);
-
-  while (t < end) {
-    const uint32_t nt = tiles_of(a, b);
-    const uint32_t s = (t - first) / nt, tile0 = (t - first) - s * nt, n = min(nt - tile0, end - t);
-    const bool whole = n == nt;
-    const uint32_t kvh = s / a.head_groups, h0 = kvh * a.G + (s - kvh * a.head_groups) * kHeads;
-    const uint32_t heads = min(static_cast<uint32_t>(kHeads), (kvh + 1) * a.G - h0);
-    const uint32_t cap = a.c.max_pages << a.c.page_shift;
-    const int32_t wanted = a.lens[b];
-    const uint32_t len = min(static_cast<uint32_t>(max(wanted, 0)), cap);
-    bool bad = wanted > 0 && static_cast<uint32_t>(wanted) > cap;
+  Share sh = find_share<kTile, kThreads>(a);
+  while (sh.t < sh.end) {
+    const Piece pc = piece_of<kTile, kHeads>(a, sh);
+    const uint32_t b = sh.b, kvh = pc.kvh, h0 = pc.h0, heads = pc.heads, tile0 = pc.tile0, n = pc.tiles;
+    const bool whole = n == pc.of;
+    const uint32_t len = tokens_of(a, b);
+    bool bad = a.lens[b] > static_cast<int32_t>(len);   // longer than its table
 
     // Q, the B operand: column `col` is query head h0 + col (the last one again past it), D in the order of K's pieces
     v8bf qf[KS];
@@ -308,7 +223,7 @@ __global__ __launch_bounds__(kThreads) void attn_decode_kernel(DecodeArgs a) {
           *reinterpret_cast<v4f*>(&sacc[wave][col][p * PANEL + (g * 4 + r) * DPL + i]) =
               v4f{acc[p][i][r], acc[p][i + 1][r], acc[p][i + 2][r], acc[p][i + 3][r]};
     __syncthreads();
-    float* part = a.parts + (static_cast<size_t>(blockIdx.x) * 2 + (tile0 == 0 ? 1 : 0)) * kHeads * (D + 2);
+    float* part = part_of(a, blockIdx.x, tile0 == 0, kHeads * (D + 2));
     for (uint32_t e = threadIdx.x * 4; e < heads * D; e += kThreads * 4) {
       const uint32_t h = e / D, d = e % D;
       float top = -INFINITY;
@@ -335,11 +250,7 @@ __global__ __launch_bounds__(kThreads) void attn_decode_kernel(DecodeArgs a) {
         }
       }
     }
-    t += n;
-    if (t == first + nt * a.streams && t < end) {
-      first = t;
-      do ++b; while (tiles_of(a, b) == 0);               // a tile is left, so a sequence that has one
-    }
+    advance(a, sh, pc);
   }
 }
 
@@ -348,15 +259,13 @@ __global__ __launch_bounds__(kThreads) void attn_decode_kernel(DecodeArgs a) {
 template <int D>
 __global__ __launch_bounds__(kThreads) void attn_decode_join_kernel(DecodeArgs a) {
   const uint32_t b = blockIdx.x / a.streams, s = blockIdx.x - b * a.streams;
-  const uint32_t nt = tiles_of(a, b), kvh = s / a.head_groups, h0 = kvh * a.G + (s - kvh * a.head_groups) * kHeads;
+  const uint32_t nt = (tokens_of(a, b) + kTile - 1) / kTile;
+  const uint32_t kvh = s / a.head_blocks, h0 = kvh * a.G + (s - kvh * a.head_blocks) * kHeads;
   const uint32_t heads = min(static_cast<uint32_t>(kHeads), (kvh + 1) * a.G - h0);
   uint16_t* out = a.out + (static_cast<size_t>(b) * a.H + h0) * D;
   const uint32_t share = a.plan[0], t0 = a.plan[1 + b] + s * nt;
   const uint32_t w0 = t0 / share, w1 = nt ? (t0 + nt - 1) / share : w0;
   if (nt != 0 && w0 == w1) return;
-  auto part = [&](uint32_t w) {
-    return a.parts + (static_cast<size_t>(w) * 2 + (w == w0 ? 1 : 0)) * kHeads * (D + 2);
-  };
   for (uint32_t e = threadIdx.x * 4; e < heads * D; e += kThreads * 4) {
     const uint32_t h = e / D, d = e % D;
     uint2 r = make_uint2(0, 0);
@@ -364,7 +273,7 @@ __global__ __launch_bounds__(kThreads) void attn_decode_join_kernel(DecodeArgs a
       float m = -INFINITY, sum = 0.0f;
       v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
       for (uint32_t w = w0; w <= w1; ++w) {
-        const float* p = part(w);
+        const float* p = part_of(a, w, w == w0, kHeads * (D + 2));
         const float x = p[kHeads * D + h * 2], top = fmaxf(m, x), base = top == -INFINITY ? 0.0f : top;
         const float f = __builtin_amdgcn_exp2f(m - base), k = __builtin_amdgcn_exp2f(x - base);
         sum = sum * f + p[kHeads * D + h * 2 + 1] * k;
@@ -379,11 +288,13 @@ __global__ __launch_bounds__(kThreads) void attn_decode_join_kernel(DecodeArgs a
 }
 
 // Workgroups of a call: as many as run at once (by registers and LDS), and no more than there can be tiles.
-uint32_t decode_groups(int64_t B, uint32_t streams, int32_t D, int64_t max_tokens) {
+uint32_t groups_of(int64_t B, uint32_t streams, int32_t D, int64_t max_tokens) {
   const int64_t tiles = B * streams * ((max_tokens + kTile - 1) / kTile);
   const int64_t most = D >= 512 ? 256 : 512;
   return static_cast<uint32_t>(std::min<int64_t>(most, tiles));
 }
+
+uint32_t head_blocks_of(int32_t G) { return static_cast<uint32_t>((G + kHeads - 1) / kHeads); }
 
 template <int D, bool FP8>
 void launch(const DecodeArgs& a, uint32_t groups, hipStream_t stream) {
@@ -396,8 +307,9 @@ size_t plan_bytes(int64_t B) { return (static_cast<size_t>(B) + 1 + 3) / 4 * 16;
 }  // namespace
 
 size_t decode_workspace_bytes(int64_t B, int32_t H, int32_t Hkv, int32_t D, int64_t max_tokens) {
-  const uint32_t streams = static_cast<uint32_t>(Hkv) * ((H / Hkv + kHeads - 1) / kHeads);
-  return plan_bytes(B) + static_cast<size_t>(decode_groups(B, streams, D, max_tokens)) * 2 * kHeads * (D + 2) * 4;
+  const uint32_t streams = static_cast<uint32_t>(Hkv) * head_blocks_of(H / Hkv);
+  const size_t few = static_cast<size_t>(groups_of(B, streams, D, max_tokens)) * 2 * kHeads * (D + 2) * 4;
+  return plan_bytes(B) + std::max(few, decode_rows_part_bytes(B, H, Hkv, D, max_tokens));
 }
 
 mx_status launch_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t H, int32_t D, bool fp8,
@@ -415,14 +327,19 @@ mx_status launch_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t
   a.B = static_cast<uint32_t>(B);
   a.H = static_cast<uint32_t>(H);
   a.G = a.H / c.Hkv;
-  a.head_groups = (a.G + kHeads - 1) / kHeads;
-  a.streams = c.Hkv * a.head_groups;
-  const uint32_t groups = decode_groups(B, a.streams, D, static_cast<int64_t>(c.max_pages) << c.page_shift);
-  switch (D) {
-    case 64: fp8 ? launch<64, true>(a, groups, stream) : launch<64, false>(a, groups, stream); break;
-    case 128: fp8 ? launch<128, true>(a, groups, stream) : launch<128, false>(a, groups, stream); break;
-    case 256: fp8 ? launch<256, true>(a, groups, stream) : launch<256, false>(a, groups, stream); break;
-    default: fp8 ? launch<512, true>(a, groups, stream) : launch<512, false>(a, groups, stream); break;
+  const int64_t max_tokens = static_cast<int64_t>(c.max_pages) << c.page_shift;
+  if (decode_by_rows(static_cast<int32_t>(a.G), D, c.k == c.v && c.ks == c.vs)) {
+    launch_decode_rows(a, D, fp8, max_tokens, stream);
+  } else {
+    a.head_blocks = head_blocks_of(static_cast<int32_t>(a.G));
+    a.streams = c.Hkv * a.head_blocks;
+    const uint32_t groups = groups_of(B, a.streams, D, max_tokens);
+    switch (D) {
+      case 64: fp8 ? launch<64, true>(a, groups, stream) : launch<64, false>(a, groups, stream); break;
+      case 128: fp8 ? launch<128, true>(a, groups, stream) : launch<128, false>(a, groups, stream); break;
+      case 256: fp8 ? launch<256, true>(a, groups, stream) : launch<256, false>(a, groups, stream); break;
+      default: fp8 ? launch<512, true>(a, groups, stream) : launch<512, false>(a, groups, stream); break;
+    }
   }
   return launch_status("mx_attn_decode");
 }

@@ -152,10 +152,17 @@ def test_decode(lens, Hkv, G, page, D, fp8):
     _decode(np.random.default_rng(sum(lens) + G + D), lens, Hkv, G, D, page, fp8)
 
 
-@pytest.mark.parametrize("lens,G,D,page", [([700, 33, 129], 128, 512, 64), ([64], 16, 512, 16), ([90, 1], 3, 128, 16)])
+@pytest.mark.parametrize("lens,G,D,page", [([700, 33, 129], 128, 512, 64), ([64], 16, 512, 16), ([90, 1], 3, 128, 16), ([0, 31, 32, 65], 32, 512, 16),
+                                           ([1500, 0, 2], 130, 512, 128), ([200], 33, 64, 32), ([64, 63, 1], 100, 256, 16), ([300, 5], 64, 128, 16)])
 @KINDS
 def test_decode_latent(lens, G, D, page, fp8):
     _decode(np.random.default_rng(G), lens, 1, G, D, page, fp8, latent=True, scale=0.11)
+
+
+@pytest.mark.parametrize("lens,Hkv,G,D", [([130, 63, 0, 64], 2, 32, 64), ([257, 7], 1, 71, 128), ([33, 500], 1, 128, 256), ([70], 2, 40, 512)])
+@KINDS
+def test_decode_many_heads_a_key_head(lens, Hkv, G, D, fp8):
+    _decode(np.random.default_rng(G), lens, Hkv, G, D, 32, fp8)
 
 
 @pytest.mark.parametrize("B", [300, 1030])
