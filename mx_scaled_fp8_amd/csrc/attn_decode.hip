@@ -26,6 +26,7 @@ namespace {
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
 constexpr int kTile = 128;             // tokens of a tile
@@ -40,19 +41,92 @@ __device__ __forceinline__ float across_groups_sum(float x) {
   return x + __shfl_xor(x, 32);
 }
 
+// Shapes of a wave's 32 tokens in registers.
 template <int D, bool FP8>
-__global__ __launch_bounds__(kThreads) void attn_decode_kernel(DecodeArgs a) {
-  constexpr int EB = FP8 ? 1 : 2;                       // bytes of an element
-  constexpr int KE = 16 / EB;                           // elements of a 16-byte piece of K
-  constexpr int KP = D / (4 * KE);                      // pieces of a K row in a lane
-  constexpr int KS = D / 32;                            // MFMA steps of the first product
-  constexpr int PANEL = FP8 ? (D < 256 ? D : 256) : (D < 128 ? D : 128);
-  constexpr int DPL = PANEL / 16;                       // elements of V in a lane, panel and token
-  constexpr int NP = D / PANEL;
-  constexpr int VW = DPL * EB / 4;                      // their words
+struct Shape {
+  static constexpr int EB = FP8 ? 1 : 2;                // bytes of an element
+  static constexpr int KP = D * EB / 64;                // 16-byte pieces of a K row in a lane
+  static constexpr int KS = D / 32;                     // MFMA steps of the first product
+  static constexpr int PANEL = FP8 ? (D < 256 ? D : 256) : (D < 128 ? D : 128);
+  static constexpr int NP = D / PANEL;
+  static constexpr int DPL = PANEL / 16;                // elements of V in a lane, panel and token
+  static constexpr int VW = DPL * EB / 4;               // their words
+  static constexpr int SB = D / 32;                     // scale bytes of a row
+  static constexpr int SW = (SB + 3) / 4;               // their words
+  static constexpr bool WIDE = SB <= 4;                 // V's scales of 4 tokens by one load of all their bytes
+  // As many registers as one wave's loads of a tile take; two tiles are held where two waves a SIMD still have room.
+  static constexpr int REGS = 2 * 4 * KP + 8 * NP * VW + (FP8 ? 2 * SW + (WIDE ? 2 * SB : 8 * NP) : 0);
+  static constexpr bool AHEAD = 2 * REGS + D / 4 + D / 8 <= 190;
+};
+
+// What a wave reads of 32 tokens.
+template <int D, bool FP8>
+struct Tokens {
+  using S = Shape<D, FP8>;
+  v4u k[2][S::KP];
+  uint32_t ks[2][FP8 ? S::SW : 1];
+  uint32_t v[8][S::NP][S::VW];
+  uint32_t vs[FP8 ? (S::WIDE ? 2 * S::SB : 8 * S::NP) : 1];
+  int64_t rows[2];           // the cache row of token 16 u
+};
+
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t* to, const uint8_t* from) {
+  if constexpr (N == 4) *reinterpret_cast<v4u*>(to) = *reinterpret_cast<const v4u*>(from);
+  else if constexpr (N == 2) *reinterpret_cast<v2u*>(to) = *reinterpret_cast<const v2u*>(from);
+  else if constexpr (N == 1) *to = *reinterpret_cast<const uint32_t*>(from);
+  else {
+    load_words<4>(to, from);
+    load_words<N - 4>(to + 4, from + 16);
+  }
+}
+
+template <int D, bool FP8>
+__device__ __forceinline__ void load_k(const KvCache& c, Tokens<D, FP8>& x) {
+  using S = Shape<D, FP8>;
+  const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const uint8_t* kp = c.k + (x.rows[u] + col) * (D * S::EB) + g * 16;
+#pragma unroll
+    for (int j = 0; j < S::KP; ++j) x.k[u][j] = *reinterpret_cast<const v4u*>(kp + j * 64);
+    if constexpr (FP8) {
+      const uint8_t* sp = c.ks + (x.rows[u] + col) * S::SB;
+      if constexpr (S::SB == 2) x.ks[u][0] = *reinterpret_cast<const uint16_t*>(sp);
+      else load_words<S::SW>(x.ks[u], sp);
+    }
+  }
+}
+
+template <int D, bool FP8>
+__device__ __forceinline__ void load_v(const KvCache& c, int p, Tokens<D, FP8>& x) {
+  using S = Shape<D, FP8>;
+  const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int64_t row = x.rows[u] + g * 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      load_words<S::VW>(x.v[u * 4 + j][p], c.v + ((row + j) * D + p * S::PANEL + col * S::DPL) * S::EB);
+    if constexpr (FP8) {
+      if constexpr (S::WIDE) {
+        load_words<S::SB>(&x.vs[u * S::SB], c.vs + row * S::SB);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          x.vs[(u * 4 + j) * S::NP + p] = c.vs[(row + j) * S::SB + (p * S::PANEL + col * S::DPL) / 32];
+      }
+    }
+  }
+}
+
+template <int D, bool FP8>
+__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_decode_kernel(DecodeArgs a) {
+  using S = Shape<D, FP8>;
+  constexpr int DPL = S::DPL, NP = S::NP, PANEL = S::PANEL;
   __shared__ float sml[4][kHeads][2];
   __shared__ __attribute__((aligned(16))) float sacc[4][kHeads][D + 4];   // + 4: the columns' rows in different banks
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
 
   Share sh = find_share<kTile, kThreads>(a);
   while (sh.t < sh.end) {
@@ -63,11 +137,11 @@ __global__ __launch_bounds__(kThreads) void attn_decode_kernel(DecodeArgs a) {
     bool bad = a.lens[b] > static_cast<int32_t>(len);   // longer than its table
 
     // Q, the B operand: column `col` is query head h0 + col (the last one again past it), D in the order of K's pieces
-    v8bf qf[KS];
+    v8bf qf[S::KS];
     {
       const uint16_t* qrow = a.q + static_cast<int64_t>(b) * a.q_stride + (h0 + min(static_cast<uint32_t>(col), heads - 1)) * D;
 #pragma unroll
-      for (int j = 0; j < KS; ++j) {
+      for (int j = 0; j < S::KS; ++j) {
         const int d = FP8 ? (j >> 1) * 64 + g * 16 + (j & 1) * 8 : j * 32 + g * 8;
         qf[j] = *reinterpret_cast<const v8bf*>(qrow + d);
       }
@@ -80,53 +154,55 @@ __global__ __launch_bounds__(kThreads) void attn_decode_kernel(DecodeArgs a) {
       for (int i = 0; i < DPL; ++i) acc[p][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
     const int32_t* table = a.c.table + static_cast<int64_t>(b) * a.c.max_pages;
-    for (uint32_t i = 0; i < n; ++i) {
-      const uint32_t tok0 = (tile0 + i) * kTile + wave * 32;
-      if (tok0 >= len) break;
-      // rows of the two groups of 16 tokens, each inside one page; a group past the end reads the first one again
-      int64_t row[2];
+    // The wave's tokens of tile i of the piece, if there are any, and the rows of its two groups of 16, each inside one
+    // page; a group past the end reads the first one again.
+    auto token = [&](uint32_t i) { return (tile0 + i) * kTile + static_cast<uint32_t>(wave) * 32; };
+    auto some = [&](uint32_t i) { return i < n && token(i) < len; };
+    uint32_t page[2] = {0, 0};
+    auto find_pages = [&](uint32_t i) {
+      if (!some(i)) return;
+      const uint32_t t0 = token(i), t1 = t0 + 16 < len ? t0 + 16 : t0;
+      page[0] = static_cast<uint32_t>(table[t0 >> a.c.page_shift]);
+      page[1] = static_cast<uint32_t>(table[t1 >> a.c.page_shift]);
+    };
+    auto load = [&](uint32_t i, Tokens<D, FP8>& x) {
+      if (!some(i)) return;
+      const uint32_t t0 = token(i), t1 = t0 + 16 < len ? t0 + 16 : t0;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        uint32_t tok = __builtin_amdgcn_readfirstlane(tok0 + u * 16);
-        if (u == 1 && tok >= len) tok = __builtin_amdgcn_readfirstlane(tok0);
-        uint32_t page = static_cast<uint32_t>(table[tok >> a.c.page_shift]);
-        if (page >= a.c.pages) {
+        if (page[u] >= a.c.pages) {
           bad = true;
-          page = 0;
+          page[u] = 0;
         }
-        row[u] = ((static_cast<int64_t>(page) * a.c.Hkv + kvh) << a.c.page_shift) + (tok & ((1u << a.c.page_shift) - 1));
+        x.rows[u] = ((static_cast<int64_t>(page[u]) * a.c.Hkv + kvh) << a.c.page_shift) + ((u ? t1 : t0) & ((1u << a.c.page_shift) - 1));
       }
-      // first product
+      load_k<D, FP8>(a.c, x);
+      load_v<D, FP8>(a.c, 0, x);
+    };
+    auto compute = [&](uint32_t i, Tokens<D, FP8>& x) {
+      const uint32_t tok0 = token(i);
       v4f s2[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int64_t r = row[u] + col;
-        const uint8_t* kp = a.c.k + r * (D * EB) + g * 16;
-        v4u kw[KP];
+        v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < KP; ++j) kw[j] = *reinterpret_cast<const v4u*>(kp + j * 64);
-        v4f x = {0.0f, 0.0f, 0.0f, 0.0f};
-        if constexpr (FP8) {
-          const uint8_t* sp = a.c.ks + r * (D / 32) + (g >> 1);
-#pragma unroll
-          for (int j = 0; j < KP; ++j) {
-            const uint32_t sc = sp[j * 2];
+        for (int j = 0; j < S::KP; ++j) {
+          if constexpr (FP8) {
+            const uint32_t byte = 2 * j + (g >> 1), sc = (x.ks[u][j / 2] >> (8 * (byte & 3))) & 0xFFu;
             const float sb = __uint_as_float(sc << 23);
             const uint32_t nan = nan_codes(sc);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              const uint32_t w0 = kw[j][half * 2] | nan, w1 = kw[j][half * 2 + 1] | nan;
+              const uint32_t w0 = x.k[u][j][half * 2] | nan, w1 = x.k[u][j][half * 2 + 1] | nan;
               const v4u op = {dequant_pair<false>(w0, sb), dequant_pair<true>(w0, sb), dequant_pair<false>(w1, sb),
                               dequant_pair<true>(w1, sb)};
-              x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, op), qf[j * 2 + half], x, 0, 0, 0);
+              y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, op), qf[j * 2 + half], y, 0, 0, 0);
             }
+          } else {
+            y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x.k[u][j]), qf[j], y, 0, 0, 0);
           }
-        } else {
-#pragma unroll
-          for (int j = 0; j < KP; ++j)
-            x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, kw[j]), qf[j], x, 0, 0, 0);
         }
-        s2[u] = x;
+        s2[u] = y;
       }
       const bool tail = tok0 + 32 > len;
       float top = -INFINITY;
@@ -134,10 +210,10 @@ __global__ __launch_bounds__(kThreads) void attn_decode_kernel(DecodeArgs a) {
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          float x = s2[u][r] * a.scale;
-          if (tail && tok0 + u * 16 + g * 4 + r >= len) x = -INFINITY;
-          s2[u][r] = x;
-          top = fmaxf(top, x);
+          float y = s2[u][r] * a.scale;
+          if (tail && tok0 + u * 16 + g * 4 + r >= len) y = -INFINITY;
+          s2[u][r] = y;
+          top = fmaxf(top, y);
         }
       top = fmaxf(m, across_groups_max(top));
       const float base = top == -INFINITY ? 0.0f : top;   // nothing but -inf so far: all weights are 0
@@ -163,32 +239,34 @@ __global__ __launch_bounds__(kThreads) void attn_decode_kernel(DecodeArgs a) {
         pw[u * 2 + 1] = pack_bf16x2(w[2], w[3]);
       }
       const v8bf pf = __builtin_bit_cast(v8bf, (v4u{pw[0], pw[1], pw[2], pw[3]}));
-      // second product, panel by panel
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
+        if (p + 1 < NP) load_v<D, FP8>(a.c, p + 1, x);
         uint32_t pair[8][DPL / 2];                        // BF16 pairs of the lane's 8 tokens
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int u = j >> 2;
-          const int64_t r = row[u] + g * 4 + (j & 3);
-          const uint32_t* vp = reinterpret_cast<const uint32_t*>(a.c.v + (r * D + p * PANEL + col * DPL) * EB);
-          const bool out = tail && tok0 + u * 16 + g * 4 + (j & 3) >= len;   // whatever lies there, it counts as 0
-          uint32_t w[VW];
-#pragma unroll
-          for (int k = 0; k < VW; ++k) w[k] = vp[k];
+          const bool out = tail && tok0 + (j >> 2) * 16 + g * 4 + (j & 3) >= len;   // whatever lies there, it counts as 0
           if constexpr (FP8) {
-            const uint32_t sc = out ? 127u : a.c.vs[r * (D / 32) + (p * PANEL + col * DPL) / 32];
+            uint32_t sc;
+            if constexpr (S::WIDE) {                      // byte `at` of row j % 4
+              const uint32_t at = col * DPL / 32;
+              if constexpr (S::SB == 4) sc = (x.vs[j] >> (8 * at)) & 0xFFu;
+              else sc = (x.vs[j >> 1] >> (8 * ((j & 1) * 2 + at))) & 0xFFu;
+            } else {
+              sc = x.vs[j * NP + p];
+            }
+            if (out) sc = 127;
             const float sb = __uint_as_float(sc << 23);
             const uint32_t nan = nan_codes(sc);
 #pragma unroll
-            for (int k = 0; k < VW; ++k) {
-              const uint32_t x = out ? 0u : w[k] | nan;
-              pair[j][k * 2] = dequant_pair<false>(x, sb);
-              pair[j][k * 2 + 1] = dequant_pair<true>(x, sb);
+            for (int k = 0; k < S::VW; ++k) {
+              const uint32_t w = out ? 0u : x.v[j][p][k] | nan;
+              pair[j][k * 2] = dequant_pair<false>(w, sb);
+              pair[j][k * 2 + 1] = dequant_pair<true>(w, sb);
             }
           } else {
 #pragma unroll
-            for (int k = 0; k < VW; ++k) pair[j][k] = out ? 0u : w[k];
+            for (int k = 0; k < S::VW; ++k) pair[j][k] = out ? 0u : x.v[j][p][k];
           }
         }
 #pragma unroll
@@ -203,6 +281,28 @@ __global__ __launch_bounds__(kThreads) void attn_decode_kernel(DecodeArgs a) {
           acc[p][2 * k + 1] =
               __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, odd), pf, acc[p][2 * k + 1], 0, 0, 0);
         }
+      }
+    };
+
+    find_pages(0);
+    if constexpr (S::AHEAD) {
+      Tokens<D, FP8> x, y;
+      load(0, x);
+      find_pages(1);
+      for (uint32_t i = 0; some(i); i += 2) {
+        load(i + 1, y);
+        find_pages(i + 2);
+        compute(i, x);
+        load(i + 2, x);
+        find_pages(i + 3);
+        if (some(i + 1)) compute(i + 1, y);
+      }
+    } else {
+      Tokens<D, FP8> x;
+      for (uint32_t i = 0; some(i); ++i) {
+        load(i, x);
+        find_pages(i + 1);
+        compute(i, x);
       }
     }
 
