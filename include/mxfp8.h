@@ -553,7 +553,7 @@ mx_status mx_kv_cache_read(int32_t kind, const void* k_cache, const uint8_t* k_s
  *           they are read.  Calls that may overlap need one each.
  * Requires: B >= 0 (0 is a no-op), B < 2^24, D 64, 128, 256 or 512, Hkv >= 1, H % Hkv == 0, H <= 2^16,
  * max_pages >= 1, max_pages * page_size < 2^31, pages >= 1 and < 2^31,
- * B * Hkv * ceil(H / Hkv / 16) < 2^24, and that times ceil(max_pages * page_size / 32)
+ * B * H < 2^24, B * Hkv * ceil(H / Hkv / 16) times ceil(max_pages * page_size / 32)
  * < 2^31, q_stride >= H * D and a multiple of 8, q, caches and out 16-byte, scales 16-byte,
  * block_table and lens 4-byte aligned; out and the workspace overlap no input
  * and not each other.

@@ -196,6 +196,7 @@ mx_status mx_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t H, 
   const int64_t streams = B * Hkv * ((H / Hkv + 15) / 16);
   MX_CHECK(streams < (int64_t(1) << 24) && streams * ((max_pages * page_size + 31) / 32) < k31,
            "%s: B = %lld x Hkv = %d x %lld tokens too large", fn, (long long)B, Hkv, (long long)(max_pages * page_size));
+  MX_CHECK(B * H < (int64_t(1) << 24), "%s: B = %lld x H = %d too large", fn, (long long)B, H);
   if (B == 0) { clear_error(); return MX_OK; }
   MX_CHECK(q && block_table && lens && out, "%s: null tensor pointer", fn);
   MX_CHECK(q_stride >= int64_t(H) * D && q_stride % 8 == 0 && q_stride < k31,

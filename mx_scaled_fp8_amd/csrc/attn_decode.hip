@@ -128,7 +128,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_decode_kernel
   __shared__ __attribute__((aligned(16))) float sacc[4][kHeads][D + 4];   // + 4: the columns' rows in different banks
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
 
-  Share sh = find_share<kTile, kThreads>(a);
+  Share sh = find_share<kTile, 1>(a);
   while (sh.t < sh.end) {
     const Piece pc = piece_of<kTile, kHeads>(a, sh);
     const uint32_t b = sh.b, kvh = pc.kvh, h0 = pc.h0, heads = pc.heads, tile0 = pc.tile0, n = pc.tiles;
@@ -345,45 +345,12 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_decode_kernel
       } else {
         *reinterpret_cast<v4f*>(part + h * D + d) = o;
         if (d == 0) {
-          part[kHeads * D + h * 2] = top;
-          part[kHeads * D + h * 2 + 1] = sum;
+          part[kHeads * D + h] = top;
+          part[kHeads * D + kHeads + h] = sum;
         }
       }
     }
     advance(a, sh, pc);
-  }
-}
-
-// One workgroup a stream: joins the parts that the workgroups left of it, in their order; zeros for a sequence of no
-// tokens.  A stream that one workgroup covered is done already.
-template <int D>
-__global__ __launch_bounds__(kThreads) void attn_decode_join_kernel(DecodeArgs a) {
-  const uint32_t b = blockIdx.x / a.streams, s = blockIdx.x - b * a.streams;
-  const uint32_t nt = (tokens_of(a, b) + kTile - 1) / kTile;
-  const uint32_t kvh = s / a.head_blocks, h0 = kvh * a.G + (s - kvh * a.head_blocks) * kHeads;
-  const uint32_t heads = min(static_cast<uint32_t>(kHeads), (kvh + 1) * a.G - h0);
-  uint16_t* out = a.out + (static_cast<size_t>(b) * a.H + h0) * D;
-  const uint32_t share = a.plan[0], t0 = a.plan[1 + b] + s * nt;
-  const uint32_t w0 = t0 / share, w1 = nt ? (t0 + nt - 1) / share : w0;
-  if (nt != 0 && w0 == w1) return;
-  for (uint32_t e = threadIdx.x * 4; e < heads * D; e += kThreads * 4) {
-    const uint32_t h = e / D, d = e % D;
-    uint2 r = make_uint2(0, 0);
-    if (nt != 0) {
-      float m = -INFINITY, sum = 0.0f;
-      v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (uint32_t w = w0; w <= w1; ++w) {
-        const float* p = part_of(a, w, w == w0, kHeads * (D + 2));
-        const float x = p[kHeads * D + h * 2], top = fmaxf(m, x), base = top == -INFINITY ? 0.0f : top;
-        const float f = __builtin_amdgcn_exp2f(m - base), k = __builtin_amdgcn_exp2f(x - base);
-        sum = sum * f + p[kHeads * D + h * 2 + 1] * k;
-        o = o * f + *reinterpret_cast<const v4f*>(p + h * D + d) * k;
-        m = top;
-      }
-      const float inv = 1.0f / sum;
-      r = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-    }
-    *reinterpret_cast<uint2*>(out + h * D + d) = r;
   }
 }
 
@@ -399,7 +366,7 @@ uint32_t head_blocks_of(int32_t G) { return static_cast<uint32_t>((G + kHeads - 
 template <int D, bool FP8>
 void launch(const DecodeArgs& a, uint32_t groups, hipStream_t stream) {
   hipLaunchKernelGGL((attn_decode_kernel<D, FP8>), dim3(groups), dim3(kThreads), 0, stream, a);
-  hipLaunchKernelGGL((attn_decode_join_kernel<D>), dim3(a.B * a.streams), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((attn_join_kernel<D, kTile, kHeads>), dim3(a.B * a.H), dim3(kJoinThreads), 0, stream, a);
 }
 
 size_t plan_bytes(int64_t B) { return (static_cast<size_t>(B) + 1 + 3) / 4 * 16; }

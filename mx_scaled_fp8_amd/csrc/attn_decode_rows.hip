@@ -13,6 +13,7 @@ namespace mx {
 namespace {
 
 constexpr int kRows = 128;             // query heads of a stream
+constexpr int kMinTokens = 256;        // of a share: its part is up to 128 rows of FP32, as much as 500 cached tokens
 
 template <int D>
 constexpr int key_tile() { return D <= 128 ? 64 : 32; }
@@ -40,7 +41,7 @@ __global__ __launch_bounds__(threads_of<D>(), 2) void attn_decode_rows_kernel(De
   const int group = wave & 3, half = wave >> 2;
   const uint32_t tok = threadIdx.x / CPR, chunk = threadIdx.x % CPR;   // of the thread's first chunk
 
-  Share sh = find_share<KT, THREADS>(a);
+  Share sh = find_share<KT, kMinTokens / KT>(a);
   while (sh.t < sh.end) {
     const Piece pc = piece_of<KT, kRows>(a, sh);
     const uint32_t len = tokens_of(a, sh.b);
@@ -177,44 +178,6 @@ __global__ __launch_bounds__(threads_of<D>(), 2) void attn_decode_rows_kernel(De
   }
 }
 
-constexpr int kJoinRows = 16, kJoinThreads = 256;
-
-// A workgroup takes kJoinRows rows of a stream: joins the parts that the workgroups left of it, in their order; zeros for a
-// sequence of no tokens.  A stream that one workgroup covered is done already.
-template <int D>
-__global__ __launch_bounds__(kJoinThreads) void attn_decode_rows_join_kernel(DecodeArgs a) {
-  constexpr int KT = key_tile<D>();
-  const uint32_t r0 = blockIdx.y * kJoinRows;
-  const uint32_t b = blockIdx.x / a.streams, s = blockIdx.x - b * a.streams;
-  const uint32_t nt = (tokens_of(a, b) + KT - 1) / KT;
-  const uint32_t kvh = s / a.head_blocks, h0 = kvh * a.G + (s - kvh * a.head_blocks) * kRows;
-  const uint32_t heads = min(static_cast<uint32_t>(kRows), (kvh + 1) * a.G - h0);
-  const uint32_t share = a.plan[0], t0 = a.plan[1 + b] + s * nt;
-  const uint32_t w0 = t0 / share, w1 = nt ? (t0 + nt - 1) / share : w0;
-  if (nt != 0 && w0 == w1) return;
-  for (uint32_t e = threadIdx.x * 4; e < kJoinRows * D; e += kJoinThreads * 4) {
-    const uint32_t r = r0 + e / D, d = e % D;
-    if (r >= heads) break;
-    uint2 o = make_uint2(0, 0);
-    if (nt != 0) {
-      float m = -INFINITY, l = 0.0f;
-      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (uint32_t w = w0; w <= w1; ++w) {
-        const float* p = part_of(a, w, w == w0, kRows * (D + 2));
-        const float y = p[kRows * D + r], top = fmaxf(m, y), base = top == -INFINITY ? 0.0f : top;
-        const float f = __builtin_amdgcn_exp2f(m - base), g = __builtin_amdgcn_exp2f(y - base);
-        const float4 v = *reinterpret_cast<const float4*>(p + r * D + d);
-        l = l * f + p[kRows * D + kRows + r] * g;
-        x = make_float4(x.x * f + v.x * g, x.y * f + v.y * g, x.z * f + v.z * g, x.w * f + v.w * g);
-        m = top;
-      }
-      const float inv = 1.0f / l;
-      o = make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-    }
-    *reinterpret_cast<uint2*>(a.out + (static_cast<size_t>(b) * a.H + h0 + r) * D + d) = o;
-  }
-}
-
 uint32_t head_blocks_of(int32_t G) { return static_cast<uint32_t>((G + kRows - 1) / kRows); }
 
 // Workgroups: as many as run at once, and no more than there can be tiles.
@@ -231,9 +194,7 @@ void launch(const DecodeArgs& a, uint32_t groups, hipStream_t stream) {
   } else if constexpr (D < 512) {
     hipLaunchKernelGGL((attn_decode_rows_kernel<D, FP8, false>), dim3(groups), block, 0, stream, a);
   }
-  const uint32_t rows = std::min<uint32_t>(a.G, kRows);
-  hipLaunchKernelGGL((attn_decode_rows_join_kernel<D>), dim3(a.B * a.streams, (rows + kJoinRows - 1) / kJoinRows),
-                     dim3(kJoinThreads), 0, stream, a);
+  hipLaunchKernelGGL((attn_join_kernel<D, key_tile<D>(), kRows>), dim3(a.B * a.H), dim3(kJoinThreads), 0, stream, a);
 }
 
 }  // namespace

@@ -30,29 +30,6 @@ __device__ __forceinline__ uint32_t tokens_of(const DecodeArgs& a, uint32_t b) {
   return min(static_cast<uint32_t>(max(a.lens[b], 0)), a.c.max_pages << a.c.page_shift);
 }
 
-// Sum over the workgroup of the threads' v, and the sum of those before this thread.
-template <int THREADS>
-__device__ __forceinline__ uint32_t scan(uint32_t v, uint32_t* buf, uint32_t& before) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t x = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t y = __shfl_up(x, d);
-    if (lane >= d) x += y;
-  }
-  __syncthreads();
-  if (lane == 63) buf[wave] = x;
-  __syncthreads();
-  uint32_t sum = 0, base = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 64; ++w) {
-    if (w < wave) base += buf[w];
-    sum += buf[w];
-  }
-  before = base + x - v;
-  return sum;
-}
-
 // A workgroup's share: tiles t .. end - 1, the first of them of sequence b, whose tiles begin at `first`.
 struct Share {
   uint32_t t, end, b, first;
@@ -64,47 +41,53 @@ struct Piece {
   uint32_t tile0, tiles, of; // of the stream's `of`
 };
 
-// All threads of the workgroup; t == end: nothing to do.
-template <int TILE, int THREADS>
+// Every wave finds its workgroup's share by itself, 64 sequences at a time, without a barrier; t == end: nothing to do.
+// A share is at least MIN tiles.  Workgroup 0 leaves the plan for the second kernel.
+template <int TILE, int MIN>
 __device__ __forceinline__ Share find_share(const DecodeArgs& a) {
-  __shared__ uint32_t buf[THREADS / 64], found[2];
+  const uint32_t lane = threadIdx.x & 63;
   auto tiles = [&](uint32_t b) { return b < a.B ? (tokens_of(a, b) + TILE - 1) / TILE : 0u; };
-  uint32_t total = 0;
-  for (uint32_t b0 = 0; b0 < a.B; b0 += THREADS) {
-    const uint32_t b = b0 + threadIdx.x;
-    uint32_t before;
-    const uint32_t sum = scan<THREADS>(tiles(b), buf, before);
-    if (blockIdx.x == 0 && b < a.B) a.plan[1 + b] = (total + before) * a.streams;
-    total += sum;
+  auto scan = [&](uint32_t x) {                        // sums up to and with each lane
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t y = __shfl_up(x, d);
+      if (lane >= static_cast<uint32_t>(d)) x += y;
+    }
+    return x;
+  };
+  uint32_t total = 0, n = 0, upto = 0;
+  for (uint32_t b0 = 0; b0 < a.B; b0 += 64) {
+    n = tiles(b0 + lane);
+    upto = scan(n);
+    if (blockIdx.x == 0 && threadIdx.x < 64 && b0 + lane < a.B) a.plan[1 + b0 + lane] = (total + upto - n) * a.streams;
+    total += __builtin_amdgcn_readlane(upto, 63);
   }
-  total *= a.streams;
-  const uint32_t share = max((total + gridDim.x - 1) / gridDim.x, 1u);
+  const uint32_t all = total * a.streams;
+  const uint32_t share = max((all + gridDim.x - 1) / gridDim.x, static_cast<uint32_t>(MIN));
   if (blockIdx.x == 0 && threadIdx.x == 0) a.plan[0] = share;
   Share s;
   s.t = blockIdx.x * share;
-  s.end = min(s.t + share, total);
-  if (s.t >= total) {
+  s.end = min(s.t + share, all);
+  s.b = s.first = 0;
+  if (s.t >= all) {
     s.end = s.t;
     return s;
   }
   uint32_t done = 0;
-  for (uint32_t b0 = 0; b0 < a.B; b0 += THREADS) {
-    const uint32_t b = b0 + threadIdx.x;
-    uint32_t before;
-    const uint32_t n = tiles(b);
-    const uint32_t sum = scan<THREADS>(n, buf, before);
-    const uint32_t first = (done + before) * a.streams;
-    if (s.t >= first && s.t < first + n * a.streams) {
-      found[0] = b;
-      found[1] = first;
+  for (uint32_t b0 = 0;; b0 += 64) {                   // ends: s.t is below the sum of all
+    if (a.B > 64) {                                    // of up to 64 sequences n and upto are still there
+      n = tiles(b0 + lane);
+      upto = scan(n);
     }
-    done += sum;
-    if (s.t < done * a.streams) break;
+    const uint64_t behind = __ballot(s.t < (done + upto) * a.streams);
+    if (behind != 0) {
+      const int at = __builtin_ctzll(behind);
+      s.b = b0 + at;
+      s.first = (done + __builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(n, at)) * a.streams;
+      return s;
+    }
+    done += __builtin_amdgcn_readlane(upto, 63);
   }
-  __syncthreads();
-  s.b = __builtin_amdgcn_readfirstlane(found[0]);
-  s.first = __builtin_amdgcn_readfirstlane(found[1]);
-  return s;
 }
 
 // The piece at s.t, with HEADS query heads a block.
@@ -133,6 +116,80 @@ __device__ __forceinline__ void advance(const DecodeArgs& a, Share& s, const Pie
 // Where the part of a piece that is not its stream's whole goes.
 __device__ __forceinline__ float* part_of(const DecodeArgs& a, uint32_t group, bool begins, uint32_t size) {
   return a.parts + (static_cast<size_t>(group) * 2 + (begins ? 1 : 0)) * size;
+}
+
+constexpr int kJoinThreads = 256;
+
+// A workgroup joins the parts of one query head (blockIdx.x: sequence and head) that the workgroups left of its stream,
+// zeros for a sequence of no tokens.  A stream that one workgroup covered is done already.  D / 4 threads take a part at a
+// time, four of them under way, the others every so many-th of the others; their sums meet in LDS, in a fixed order.
+template <int D, int TILE, int HEADS>
+__global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(DecodeArgs a) {
+  constexpr uint32_t DT = D / 4, LANES = kJoinThreads / DT, SIZE = HEADS * (D + 2);
+  __shared__ __attribute__((aligned(16))) float sum[LANES][D];
+  __shared__ float tops[LANES], weights[LANES];
+  const uint32_t b = blockIdx.x / a.H, h = blockIdx.x - b * a.H;
+  const uint32_t kvh = h / a.G, block = (h - kvh * a.G) / HEADS, r = (h - kvh * a.G) - block * HEADS;
+  const uint32_t share = a.plan[0], begin = a.plan[1 + b];
+  const uint32_t nt = (tokens_of(a, b) + TILE - 1) / TILE;
+  const uint32_t lane = threadIdx.x / DT, d = threadIdx.x % DT * 4;
+  uint2* out = reinterpret_cast<uint2*>(a.out + (static_cast<size_t>(b) * a.H + h) * D + d);
+  if (nt == 0) {
+    if (lane == 0) *out = make_uint2(0, 0);
+    return;
+  }
+  const uint32_t t0 = begin + (kvh * a.head_blocks + block) * nt;
+  const uint32_t w0 = t0 / share, w1 = (t0 + nt - 1) / share;
+  if (w0 == w1) return;
+  float m = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (uint32_t w = w0 + lane; w <= w1; w += 4 * LANES) {
+    float4 x[4];
+    float pm[4], pl[4], top = m;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool some = w + k * LANES <= w1;
+      const float* p = part_of(a, some ? w + k * LANES : w, w + k * LANES == w0 || (!some && w == w0), SIZE);
+      x[k] = *reinterpret_cast<const float4*>(p + r * D + d);
+      pm[k] = some ? p[HEADS * D + r] : -INFINITY;
+      pl[k] = p[HEADS * D + HEADS + r];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = fmaxf(top, pm[k]);
+    const float base = top == -INFINITY ? 0.0f : top, f = __builtin_amdgcn_exp2f(m - base);
+    l *= f;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (w + k * LANES <= w1) {
+        const float g = __builtin_amdgcn_exp2f(pm[k] - base);
+        l += pl[k] * g;
+        o = make_float4(o.x + x[k].x * g, o.y + x[k].y * g, o.z + x[k].z * g, o.w + x[k].w * g);
+      }
+    m = top;
+  }
+  *reinterpret_cast<float4*>(&sum[lane][d]) = o;
+  if (d == 0) {
+    tops[lane] = m;
+    weights[lane] = l;
+  }
+  __syncthreads();
+  if (lane != 0) return;
+  float top = -INFINITY;
+#pragma unroll
+  for (uint32_t k = 0; k < LANES; ++k) top = fmaxf(top, tops[k]);
+  const float base = top == -INFINITY ? 0.0f : top;
+  l = 0.0f;
+  o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (uint32_t k = 0; k < LANES; ++k) {
+    const float4 x = *reinterpret_cast<const float4*>(&sum[k][d]);
+    const float f = __builtin_amdgcn_exp2f(tops[k] - base);
+    l += weights[k] * f;
+    o = make_float4(o.x + x.x * f, o.y + x.y * f, o.z + x.z * f, o.w + x.w * f);
+  }
+  const float inv = 1.0f / l;
+  *out = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
 
 }  // namespace mx
