@@ -485,13 +485,15 @@ def _result(t, name, shape, dtype, like, dtypes):
 
 # torch.cuda.current_stream() builds a Stream object, 2 us of a call that takes 6; the handle alone is a lookup
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# as torch.cuda.current_device() without its look whether the GPU is initialised: a tensor is there already
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _on_device(fn, ref, *args):
     """fn(*args, stream) with the device of `ref` as the current one, on its current stream."""
     index = ref.get_device()
     stream = _raw_stream(index) if _raw_stream else _stream(ref)
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         return _check(fn(*args, stream))
     with torch.cuda.device(index):
         return _check(fn(*args, stream))
@@ -613,79 +615,112 @@ def mx_moe_combine(y, slot_row, weights, shared=None, out=None):
 
 # ------------------------------------------ key-value cache and attention
 
-def _rows(t, name, heads=None, D=None):
+_BYTES = frozenset(_E4M3)
+_HALVES = frozenset(_BF16)
+_E8M0 = frozenset((torch.uint8, torch.float8_e8m0fnu))
+_INT32 = frozenset((torch.int32,))
+_INT64 = frozenset((torch.int64,))
+
+
+def _gpu(t, name):
+    """The index of the GPU that a tensor is on."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return index
+
+
+def _dense(t, name, shape, dtypes, index):
+    """The pointer of a contiguous tensor of this shape (or, an int, so many elements), one of these types, on this GPU:
+    one pass of cheap checks, since the checks of a small call take longer than its kernel."""
+    if (isinstance(t, torch.Tensor) and (t.numel() == shape if isinstance(shape, int) else t.shape == shape)
+            and t.dtype in dtypes and t.get_device() == index and t.is_contiguous()):
+        return t.data_ptr()
+    _gpu(t, name)
+    if isinstance(shape, int):
+        _numel(t, shape, name)
+    else:
+        _shape(t, shape, name)
+    _dtype(t, tuple(dtypes), name)
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    return _dev(t, name)
+
+
+def _rows(t, name, heads, D, index):
     """(pointer, row stride) of a BF16 tensor [rows, heads, D] whose heads are dense; the rows may be strided."""
+    _gpu(t, name)
     if t.dim() != 3:
         raise ValueError(f"{name} must be [rows, heads, D] (got shape {tuple(t.shape)})")
     n, h, d = t.shape
     if (heads is not None and h != heads) or (D is not None and d != D):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [rows, {heads}, {D}]")
-    _dtype(t, _BF16, name)
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if n == 0 or h == 0:
-        return t.data_ptr(), h * d
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    if t.dtype not in _HALVES:
+        _dtype(t, _BF16, name)
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    row, head, element = t.stride()
+    if (d > 1 and element != 1) or (h > 1 and head != d and n > 0):
         raise ValueError(f"{name} must have dense heads (strides {t.stride()})")
-    return t.data_ptr(), t.stride(0) if n > 1 else h * d
+    return t.data_ptr(), row if n > 1 else h * d
 
 
-def _cache_args(k_cache, v_cache, k_scale, v_scale):
+def _cache_args(k_cache, v_cache, k_scale, v_scale, index):
     """(kind, k, k_scale, v, v_scale, pages, page_size, Hkv, D) of a paged cache."""
-    if k_cache.dim() != 4:
-        raise ValueError(f"k_cache must be [pages, Hkv, page_size, D] (got shape {tuple(k_cache.shape)})")
-    pages, heads, page_size, D = k_cache.shape
+    _gpu(k_cache, "k_cache")
+    shape = k_cache.shape
+    if len(shape) != 4:
+        raise ValueError(f"k_cache must be [pages, Hkv, page_size, D] (got shape {tuple(shape)})")
+    pages, heads, page_size, D = shape
     kind = MX_CACHE_MXFP8 if k_cache.element_size() == 1 else MX_CACHE_BF16
-    _dtype(k_cache, _E4M3 + _BF16, "k_cache")
+    types = _BYTES if kind == MX_CACHE_MXFP8 else _HALVES
+    scales = (pages, heads, page_size, D // MX_CACHE_BLOCK)
+    at = [_dense(k_cache, "k_cache", shape, types, index), None, None, None]
     if v_cache is not None:
-        _shape(v_cache, k_cache.shape, "v_cache")
-        _dtype(v_cache, _E4M3 if kind == MX_CACHE_MXFP8 else _BF16, "v_cache")
-    for name, c, s in (("k_scale", k_cache, k_scale), ("v_scale", v_cache, v_scale)):
-        if (s is None) != (c is None or kind == MX_CACHE_BF16):
+        at[2] = _dense(v_cache, "v_cache", shape, types, index)
+    for i, name, cache, scale in ((1, "k_scale", k_cache, k_scale), (3, "v_scale", v_cache, v_scale)):
+        if (scale is None) != (cache is None or kind == MX_CACHE_BF16):
             raise ValueError(f"{name}: an MXFP8 cache has scales [pages, Hkv, page_size, D/32], a BF16 cache none")
-        _shape(s, (pages, heads, page_size, D // MX_CACHE_BLOCK), name)
-        _dtype(s, (torch.uint8, torch.float8_e8m0fnu), name)
-    _same_device(k_cache, ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale))
-    at = lambda t, name: _dev(t, name) if t is not None else None  # noqa: E731
-    return (kind, at(k_cache, "k_cache"), at(k_scale, "k_scale"), at(v_cache, "v_cache"), at(v_scale, "v_scale"),
-            pages, page_size, heads, D)
+        if scale is not None:
+            at[i] = _dense(scale, name, scales, _E8M0, index)
+    return (kind, *at, pages, page_size, heads, D)
 
 
-def _table_args(block_table):
-    if block_table.dim() != 2:
-        raise ValueError(f"block_table must be [B, max_pages] (got shape {tuple(block_table.shape)})")
-    _dtype(block_table, (torch.int32,), "block_table")
-    return _dev(block_table, "block_table"), block_table.shape[0], block_table.shape[1]
+def _table_args(block_table, index):
+    """(pointer, B, max_pages) of a block table."""
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    shape = block_table.shape
+    return _dense(block_table, "block_table", shape, _INT32, index), shape[0], shape[1]
 
 
 def mx_kv_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None):
     """k, v BF16 [T,Hkv,D] (rows may be strided) into rows ``slots`` (int64 [T], page * page_size + row, -1 to skip a
     token) of the cache [pages,Hkv,page_size,D]: MXFP8 uint8 with uint8 scales [pages,Hkv,page_size,D/32], or BF16.
     ``v`` and ``v_cache`` None: a latent cache.  Writes the caches in place."""
-    kind, kc, ks, vc, vs, pages, page_size, heads, D = _cache_args(k_cache, v_cache, k_scale, v_scale)
-    kp, k_stride = _rows(k, "k", heads, D)
+    index = _gpu(k, "k")
+    kind, kc, ks, vc, vs, pages, page_size, heads, D = _cache_args(k_cache, v_cache, k_scale, v_scale, index)
+    kp, k_stride = _rows(k, "k", heads, D, index)
     T = k.shape[0]
     if (v is None) != (v_cache is None):
         raise ValueError("v and v_cache go together")
     vp, v_stride = None, 0
     if v is not None:
-        vp, v_stride = _rows(v, "v", heads, D)
+        vp, v_stride = _rows(v, "v", heads, D, index)
         _shape(v, k.shape, "v")
-    _dtype(slots, (torch.int64,), "slots")
-    _numel(slots, T, "slots")
-    _same_device(k, ("v", v), ("slots", slots), ("k_cache", k_cache))
-    _on_device(lib().mx_kv_cache_write, k, kp, k_stride, vp, v_stride, T, heads, D, _dev(slots, "slots"), kind, kc, ks,
-               vc, vs, pages, page_size)
+    _on_device(lib().mx_kv_cache_write, k, kp, k_stride, vp, v_stride, T, heads, D, _dense(slots, "slots", T, _INT64, index),
+               kind, kc, ks, vc, vs, pages, page_size)
 
 
 def mx_kv_cache_read(k_cache, v_cache, block_table, offsets, rows, k_scale=None, v_scale=None, k=None, v=None):
     """The sequences of a cache as packed BF16 rows: (k [rows,Hkv,D], v [rows,Hkv,D] or None).  Token i of sequence b
-    is row offsets[b] + i (offsets int32 [B+1]), from page block_table[b, i // page_size] (int32 [B,max_pages])."""
-    kind, kc, ks, vc, vs, pages, page_size, heads, D = _cache_args(k_cache, v_cache, k_scale, v_scale)
-    table, B, max_pages = _table_args(block_table)
-    _dtype(offsets, (torch.int32,), "offsets")
-    _numel(offsets, B + 1, "offsets")
-    _same_device(k_cache, ("block_table", block_table), ("offsets", offsets))
+    is row offsets[b] + i (offsets int32 [B+1]), from page block_table[b, i // page_size] (int32 [B,max_pages]).  Rows that
+    no sequence owns keep what k and v held."""
+    index = _gpu(k_cache, "k_cache")
+    kind, kc, ks, vc, vs, pages, page_size, heads, D = _cache_args(k_cache, v_cache, k_scale, v_scale, index)
+    table, B, max_pages = _table_args(block_table, index)
     if rows < 0:
         raise ValueError(f"rows = {rows} must not be negative")
     k, kp = _result(k, "k", (rows, heads, D), torch.bfloat16, k_cache, _BF16)
@@ -695,7 +730,7 @@ def mx_kv_cache_read(k_cache, v_cache, block_table, offsets, rows, k_scale=None,
     elif v is not None:
         raise ValueError("a latent cache has no values of its own: v must be None")
     _on_device(lib().mx_kv_cache_read, k_cache, kind, kc, ks, vc, vs, pages, page_size, heads, D, table, B, max_pages,
-               _dev(offsets, "offsets"), rows, kp, vp)
+               _dense(offsets, "offsets", B + 1, _INT32, index), rows, kp, vp)
     return k, v
 
 
@@ -708,20 +743,21 @@ def mx_attn_decode(q, k_cache, v_cache, block_table, lens, k_scale=None, v_scale
     """Attention of one new token for each sequence over its first lens[b] cached tokens: q BF16 [B,H,D] (rows may be
     strided), cache and block_table as in mx_kv_cache_read, lens int32 [B] -> BF16 [B,H,D].  Query head h reads key
     head h // (H // Hkv).  ``scale`` is 1 / sqrt(D) unless given."""
-    kind, kc, ks, vc, vs, pages, page_size, heads, D = _cache_args(k_cache, v_cache, k_scale, v_scale)
-    table, B, max_pages = _table_args(block_table)
-    qp, q_stride = _rows(q, "q", None, D)
-    H = q.shape[1]
-    if q.shape[0] != B:
-        raise ValueError(f"q has {q.shape[0]} rows, block_table {B}")
-    _dtype(lens, (torch.int32,), "lens")
-    _numel(lens, B, "lens")
-    _same_device(q, ("k_cache", k_cache), ("block_table", block_table), ("lens", lens), ("workspace", workspace))
+    index = _gpu(q, "q")
+    kind, kc, ks, vc, vs, pages, page_size, heads, D = _cache_args(k_cache, v_cache, k_scale, v_scale, index)
+    table, B, max_pages = _table_args(block_table, index)
+    qp, q_stride = _rows(q, "q", None, D, index)
+    n, H, _ = q.shape
+    if n != B:
+        raise ValueError(f"q has {n} rows, block_table {B}")
+    lp = _dense(lens, "lens", B, _INT32, index)
     out, op = _result(out, "out", (B, H, D), torch.bfloat16, q, _BF16)
-    need = mx_attn_decode_workspace_bytes(B, H, heads, D, max_pages, page_size)
-    workspace, wp, wb = _workspace(workspace, need, q)
-    _on_device(lib().mx_attn_decode, q, qp, q_stride, B, H, heads, D, kind, kc, ks, vc, vs, pages, page_size, table,
-               max_pages, _dev(lens, "lens"), D ** -0.5 if scale is None else scale, op, wp, wb)
+    L = lib()
+    if workspace is not None:
+        _same_device(q, ("workspace", workspace))
+    workspace, wp, wb = _workspace(workspace, L.mx_attn_decode_workspace_bytes(B, H, heads, D, max_pages, page_size), q)
+    _on_device(L.mx_attn_decode, q, qp, q_stride, B, H, heads, D, kind, kc, ks, vc, vs, pages, page_size, table,
+               max_pages, lp, D ** -0.5 if scale is None else scale, op, wp, wb)
     return out
 
 
@@ -733,23 +769,26 @@ def mx_attn_prefill(q, k, v, q_offsets, k_offsets, scale=None, out=None, workspa
     """Causal attention over packed prompts: q BF16 [Tq,H,D], k and v BF16 [Tk,Hkv,D] (rows may be strided),
     q_offsets and k_offsets int32 [B+1] -> BF16 [Tq,H,D].  Rows q_offsets[b]..q_offsets[b+1] are the last of the
     tokens whose keys are rows k_offsets[b]..k_offsets[b+1].  ``scale`` is 1 / sqrt(D) unless given."""
-    qp, q_stride = _rows(q, "q")
+    index = _gpu(q, "q")
+    qp, q_stride = _rows(q, "q", None, None, index)
     Tq, H, D = q.shape
-    kp, k_stride = _rows(k, "k", None, D)
-    Tk, heads = k.shape[:2]
-    vp, v_stride = _rows(v, "v", heads, D)
-    _shape(v, k.shape, "v")
-    for name, t in (("q_offsets", q_offsets), ("k_offsets", k_offsets)):
-        _dtype(t, (torch.int32,), name)
+    kp, k_stride = _rows(k, "k", None, D, index)
+    Tk, heads, _ = k.shape
+    vp, v_stride = (kp, k_stride) if v is k else _rows(v, "v", heads, D, index)
+    if v is not k:
+        _shape(v, k.shape, "v")
+    _gpu(q_offsets, "q_offsets")
     B = q_offsets.numel() - 1
     if B < 0:
         raise ValueError("q_offsets must hold B + 1 values")
-    _numel(k_offsets, B + 1, "k_offsets")
-    _same_device(q, ("k", k), ("v", v), ("q_offsets", q_offsets), ("k_offsets", k_offsets), ("workspace", workspace))
+    qo, ko = _dense(q_offsets, "q_offsets", B + 1, _INT32, index), _dense(k_offsets, "k_offsets", B + 1, _INT32, index)
     out, op = _result(out, "out", (Tq, H, D), torch.bfloat16, q, _BF16)
-    workspace, wp, wb = _workspace(workspace, mx_attn_prefill_workspace_bytes(B, Tq, Tk, H, heads, D), q)
-    _on_device(lib().mx_attn_prefill, q, qp, q_stride, kp, k_stride, vp, v_stride, _dev(q_offsets, "q_offsets"),
-               _dev(k_offsets, "k_offsets"), B, Tq, Tk, H, heads, D, D ** -0.5 if scale is None else scale, op, wp, wb)
+    L = lib()
+    if workspace is not None:
+        _same_device(q, ("workspace", workspace))
+    workspace, wp, wb = _workspace(workspace, L.mx_attn_prefill_workspace_bytes(B, Tq, Tk, H, heads, D), q)
+    _on_device(L.mx_attn_prefill, q, qp, q_stride, kp, k_stride, vp, v_stride, qo, ko, B, Tq, Tk, H, heads, D,
+               D ** -0.5 if scale is None else scale, op, wp, wb)
     return out
 
 
