@@ -28,8 +28,7 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
-constexpr int kThreads = 256;
-constexpr int kTile = 128;             // tokens of a tile
+constexpr int kTile = 128;             // tokens of a tile of a share: 32 for each of four waves
 constexpr int kHeads = 16;             // query heads of a stream: one (sequence, key head, group of up to 16 query heads)
 
 __device__ __forceinline__ float across_groups_max(float x) {
@@ -56,7 +55,10 @@ struct Shape {
   static constexpr bool WIDE = SB <= 4;                 // V's scales of 4 tokens by one load of all their bytes
   // As many registers as one wave's loads of a tile take; two tiles are held where two waves a SIMD still have room.
   static constexpr int REGS = 2 * 4 * KP + 8 * NP * VW + (FP8 ? 2 * SW + (WIDE ? 2 * SB : 8 * NP) : 0);
-  static constexpr bool AHEAD = 2 * REGS + D / 4 + D / 8 <= 190;
+  static constexpr bool AHEAD = 2 * REGS + D / 4 + D / 8 <= 170;
+  // Rows of 512 fill the registers with O and Q: the second 16 rows of K are loaded when the first are used up, V after
+  // that.  (All of a tile at once spilled registers.)
+  static constexpr bool LATE = D >= 512;
 };
 
 // What a wave reads of 32 tokens.
@@ -82,19 +84,16 @@ __device__ __forceinline__ void load_words(uint32_t* to, const uint8_t* from) {
 }
 
 template <int D, bool FP8>
-__device__ __forceinline__ void load_k(const KvCache& c, Tokens<D, FP8>& x) {
+__device__ __forceinline__ void load_k(const KvCache& c, int u, Tokens<D, FP8>& x) {
   using S = Shape<D, FP8>;
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+  const uint8_t* kp = c.k + (x.rows[u] + col) * (D * S::EB) + g * 16;
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const uint8_t* kp = c.k + (x.rows[u] + col) * (D * S::EB) + g * 16;
-#pragma unroll
-    for (int j = 0; j < S::KP; ++j) x.k[u][j] = *reinterpret_cast<const v4u*>(kp + j * 64);
-    if constexpr (FP8) {
-      const uint8_t* sp = c.ks + (x.rows[u] + col) * S::SB;
-      if constexpr (S::SB == 2) x.ks[u][0] = *reinterpret_cast<const uint16_t*>(sp);
-      else load_words<S::SW>(x.ks[u], sp);
-    }
+  for (int j = 0; j < S::KP; ++j) x.k[u][j] = *reinterpret_cast<const v4u*>(kp + j * 64);
+  if constexpr (FP8) {
+    const uint8_t* sp = c.ks + (x.rows[u] + col) * S::SB;
+    if constexpr (S::SB == 2) x.ks[u][0] = *reinterpret_cast<const uint16_t*>(sp);
+    else load_words<S::SW>(x.ks[u], sp);
   }
 }
 
@@ -120,19 +119,39 @@ __device__ __forceinline__ void load_v(const KvCache& c, int p, Tokens<D, FP8>& 
   }
 }
 
-template <int D, bool FP8>
-__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_decode_kernel(DecodeArgs a) {
+// WHOLE: every workgroup takes one stream from end to end, nothing is left to join.
+template <int D, bool WHOLE>
+constexpr int waves_of() { return WHOLE && D <= 256 ? 8 : 4; }
+
+template <int D, bool FP8, bool WHOLE>
+__global__ __launch_bounds__((64 * waves_of<D, WHOLE>()), D <= 128 ? 2 : 1) void attn_decode_kernel(DecodeArgs a) {
   using S = Shape<D, FP8>;
+  constexpr int WAVES = waves_of<D, WHOLE>(), TILE = 32 * WAVES;
   constexpr int DPL = S::DPL, NP = S::NP, PANEL = S::PANEL;
-  __shared__ float sml[4][kHeads][2];
-  __shared__ __attribute__((aligned(16))) float sacc[4][kHeads][D + 4];   // + 4: the columns' rows in different banks
+  __shared__ float sml[WAVES][kHeads][2];
+  __shared__ __attribute__((aligned(16))) float sacc[WAVES][kHeads][D + 4];   // + 4: the columns' rows in different banks
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
 
-  Share sh = find_share<kTile, 1>(a);
+  Share sh;
+  if constexpr (WHOLE) {                                // tiles numbered from this sequence's first
+    sh.b = blockIdx.x / a.streams;
+    const uint32_t of = (tokens_of(a, sh.b) + TILE - 1) / TILE, s = blockIdx.x - sh.b * a.streams;
+    sh.first = 0;
+    sh.t = s * of;
+    sh.end = sh.t + of;
+    if (of == 0) {
+      const uint32_t kvh = s / a.head_blocks, h0 = kvh * a.G + (s - kvh * a.head_blocks) * kHeads;
+      const uint32_t heads = min(static_cast<uint32_t>(kHeads), (kvh + 1) * a.G - h0);
+      for (uint32_t e = threadIdx.x * 4; e < heads * D; e += 64 * WAVES * 4)
+        *reinterpret_cast<uint2*>(a.out + (static_cast<size_t>(sh.b) * a.H + h0) * D + e) = make_uint2(0, 0);
+    }
+  } else {
+    sh = find_share<TILE, 1>(a);
+  }
   while (sh.t < sh.end) {
-    const Piece pc = piece_of<kTile, kHeads>(a, sh);
+    const Piece pc = piece_of<TILE, kHeads>(a, sh);
     const uint32_t b = sh.b, kvh = pc.kvh, h0 = pc.h0, heads = pc.heads, tile0 = pc.tile0, n = pc.tiles;
-    const bool whole = n == pc.of;
+    const bool whole = WHOLE || n == pc.of;
     const uint32_t len = tokens_of(a, b);
     bool bad = a.lens[b] > static_cast<int32_t>(len);   // longer than its table
 
@@ -156,7 +175,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_decode_kernel
     const int32_t* table = a.c.table + static_cast<int64_t>(b) * a.c.max_pages;
     // The wave's tokens of tile i of the piece, if there are any, and the rows of its two groups of 16, each inside one
     // page; a group past the end reads the first one again.
-    auto token = [&](uint32_t i) { return (tile0 + i) * kTile + static_cast<uint32_t>(wave) * 32; };
+    auto token = [&](uint32_t i) { return (tile0 + i) * TILE + static_cast<uint32_t>(wave) * 32; };
     auto some = [&](uint32_t i) { return i < n && token(i) < len; };
     uint32_t page[2] = {0, 0};
     auto find_pages = [&](uint32_t i) {
@@ -176,8 +195,11 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_decode_kernel
         }
         x.rows[u] = ((static_cast<int64_t>(page[u]) * a.c.Hkv + kvh) << a.c.page_shift) + ((u ? t1 : t0) & ((1u << a.c.page_shift) - 1));
       }
-      load_k<D, FP8>(a.c, x);
-      load_v<D, FP8>(a.c, 0, x);
+      load_k<D, FP8>(a.c, 0, x);
+      if constexpr (!S::LATE) {
+        load_k<D, FP8>(a.c, 1, x);
+        load_v<D, FP8>(a.c, 0, x);
+      }
     };
     auto compute = [&](uint32_t i, Tokens<D, FP8>& x) {
       const uint32_t tok0 = token(i);
@@ -203,6 +225,11 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_decode_kernel
           }
         }
         s2[u] = y;
+        if constexpr (S::LATE) {
+          asm volatile("" ::: "memory");               // not before the products
+          if (u == 0) load_k<D, FP8>(a.c, 1, x);
+          else load_v<D, FP8>(a.c, 0, x);
+        }
       }
       const bool tail = tok0 + 32 > len;
       float top = -INFINITY;
@@ -306,7 +333,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_decode_kernel
       }
     }
 
-    // the four waves' parts into one
+    // the waves' parts into one
     l = across_groups_sum(l);
     if (bad) l = __builtin_nanf("");
     __syncthreads();                                      // the last stream's parts have been read
@@ -324,16 +351,16 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_decode_kernel
               v4f{acc[p][i][r], acc[p][i + 1][r], acc[p][i + 2][r], acc[p][i + 3][r]};
     __syncthreads();
     float* part = part_of(a, blockIdx.x, tile0 == 0, kHeads * (D + 2));
-    for (uint32_t e = threadIdx.x * 4; e < heads * D; e += kThreads * 4) {
+    for (uint32_t e = threadIdx.x * 4; e < heads * D; e += 64 * WAVES * 4) {
       const uint32_t h = e / D, d = e % D;
       float top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) top = fmaxf(top, sml[w][h][0]);
+      for (int w = 0; w < WAVES; ++w) top = fmaxf(top, sml[w][h][0]);
       const float base = top == -INFINITY ? 0.0f : top;
       float sum = 0.0f;
       v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < WAVES; ++w) {
         const float f = __builtin_amdgcn_exp2f(sml[w][h][0] - base);
         sum += sml[w][h][1] * f;
         o += *reinterpret_cast<const v4f*>(&sacc[w][h][d]) * f;
@@ -350,6 +377,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_decode_kernel
         }
       }
     }
+    if constexpr (WHOLE) return;
     advance(a, sh, pc);
   }
 }
@@ -363,9 +391,19 @@ uint32_t groups_of(int64_t B, uint32_t streams, int32_t D, int64_t max_tokens) {
 
 uint32_t head_blocks_of(int32_t G) { return static_cast<uint32_t>((G + kHeads - 1) / kHeads); }
 
+// Whether streams are short enough for one workgroup each, which saves the second kernel.  (8 key heads of 128, MXFP8, in a
+// graph: one sequence of 300 tokens 6.8 us whole and 8.3 in shares, of 1000 tokens 12.5 and 8.9; 64 sequences up to 1000
+// tokens 25.4 and 28.0, up to 2000 39.2 and 37.8.)
+bool short_streams(int64_t streams, int64_t max_tokens) { return max_tokens <= (streams >= 512 ? 1024 : 512); }
+
 template <int D, bool FP8>
-void launch(const DecodeArgs& a, uint32_t groups, hipStream_t stream) {
-  hipLaunchKernelGGL((attn_decode_kernel<D, FP8>), dim3(groups), dim3(kThreads), 0, stream, a);
+void launch(const DecodeArgs& a, int64_t max_tokens, hipStream_t stream) {
+  if (short_streams(static_cast<int64_t>(a.B) * a.streams, max_tokens)) {
+    hipLaunchKernelGGL((attn_decode_kernel<D, FP8, true>), dim3(a.B * a.streams), dim3(64 * waves_of<D, true>()), 0, stream, a);
+    return;
+  }
+  const uint32_t groups = groups_of(a.B, a.streams, D, max_tokens);
+  hipLaunchKernelGGL((attn_decode_kernel<D, FP8, false>), dim3(groups), dim3(64 * waves_of<D, false>()), 0, stream, a);
   hipLaunchKernelGGL((attn_join_kernel<D, kTile, kHeads>), dim3(a.B * a.H), dim3(kJoinThreads), 0, stream, a);
 }
 
@@ -400,12 +438,11 @@ mx_status launch_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t
   } else {
     a.head_blocks = head_blocks_of(static_cast<int32_t>(a.G));
     a.streams = c.Hkv * a.head_blocks;
-    const uint32_t groups = groups_of(B, a.streams, D, max_tokens);
     switch (D) {
-      case 64: fp8 ? launch<64, true>(a, groups, stream) : launch<64, false>(a, groups, stream); break;
-      case 128: fp8 ? launch<128, true>(a, groups, stream) : launch<128, false>(a, groups, stream); break;
-      case 256: fp8 ? launch<256, true>(a, groups, stream) : launch<256, false>(a, groups, stream); break;
-      default: fp8 ? launch<512, true>(a, groups, stream) : launch<512, false>(a, groups, stream); break;
+      case 64: fp8 ? launch<64, true>(a, max_tokens, stream) : launch<64, false>(a, max_tokens, stream); break;
+      case 128: fp8 ? launch<128, true>(a, max_tokens, stream) : launch<128, false>(a, max_tokens, stream); break;
+      case 256: fp8 ? launch<256, true>(a, max_tokens, stream) : launch<256, false>(a, max_tokens, stream); break;
+      default: fp8 ? launch<512, true>(a, max_tokens, stream) : launch<512, false>(a, max_tokens, stream); break;
     }
   }
   return launch_status("mx_attn_decode");
