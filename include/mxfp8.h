@@ -588,7 +588,7 @@ mx_status mx_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t H, 
  *           split over workgroups, written before they are read.  Calls that may
  *           overlap need one each.
  * Requires: B, Tq, Tk >= 0 (B or Tq 0 is a no-op), B < 2^24, Tq, Tk < 2^31, D 64, 128, 256 or 512, Hkv >= 1,
- * H % Hkv == 0, H <= 2^16, (Tq / 128 + B) * H < 2^24, q_stride, k_stride and v_stride multiples of 8 and at least a dense
+ * H % Hkv == 0, H <= 2^16, (Tq / 64 + B) * H < 2^23, q_stride, k_stride and v_stride multiples of 8 and at least a dense
  * row, q_stride below 2^31, the others below 2^22, scale finite and > 0, q, k, v and out 16-byte, offsets 4-byte aligned;
  * out and the workspace overlap no input and not each other.
  */

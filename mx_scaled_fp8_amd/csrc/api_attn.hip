@@ -237,7 +237,7 @@ mx_status mx_attn_prefill(const void* q, int64_t q_stride, const void* k, int64_
   if (st != MX_OK) return st;
   MX_CHECK(B >= 0 && B < (int64_t(1) << 24) && Tq >= 0 && Tq < k31 && Tk >= 0 && Tk < k31,
            "%s: B = %lld, Tq = %lld, Tk = %lld out of range", fn, (long long)B, (long long)Tq, (long long)Tk);
-  MX_CHECK((Tq / 128 + B) * H < (int64_t(1) << 24), "%s: Tq = %lld rows of H = %d heads too large", fn, (long long)Tq, H);
+  MX_CHECK((Tq / 64 + B) * H < (int64_t(1) << 23), "%s: Tq = %lld rows of H = %d heads too large", fn, (long long)Tq, H);
   if (B == 0 || Tq == 0) { clear_error(); return MX_OK; }
   MX_CHECK(q && q_offsets && k_offsets && out && ((k && v) || Tk == 0), "%s: null tensor pointer", fn);
   const int64_t qw = int64_t(H) * D, kw = int64_t(Hkv) * D, most = int64_t(1) << 22;

@@ -16,7 +16,6 @@ namespace mx {
 
 namespace {
 
-constexpr int kRows = 128;             // query rows of a workgroup
 constexpr int kMinTiles = 4;           // fewest key tiles of a split
 
 struct PrefillArgs {
@@ -27,7 +26,7 @@ struct PrefillArgs {
   const int32_t* q_offsets;
   const int32_t* k_offsets;
   uint16_t* out;
-  float* parts;              // [row tile, head, split][O: kRows x D, m, l: kRows each], FP32
+  float* parts;              // [row tile, head, split][O: rows x D, m, l: a row each], FP32
   float scale;               // times log2(e)
   uint32_t B, Tq, Tk, H, Hkv, G;
   uint32_t tiles;            // bound on the row tiles of all prompts
@@ -48,12 +47,13 @@ struct RowTile {
   bool any;                  // the tile has rows
 };
 
+template <int ROWS>
 __device__ __forceinline__ RowTile row_tile(const PrefillArgs& a, uint32_t rt) {
-  // prompt b's row tiles are numbered from offsets[b] / kRows + b, which leaves room for every ragged end
+  // prompt b's row tiles are numbered from offsets[b] / ROWS + b, which leaves room for every ragged end
   uint32_t lo = 0, hi = a.B;
   while (hi - lo > 1) {
     const uint32_t mid = (lo + hi) >> 1;
-    if (cut(a.q_offsets, mid, a.Tq) / kRows + mid <= rt) lo = mid; else hi = mid;
+    if (cut(a.q_offsets, mid, a.Tq) / ROWS + mid <= rt) lo = mid; else hi = mid;
   }
   RowTile t;
   t.q0 = cut(a.q_offsets, lo, a.Tq);
@@ -61,10 +61,10 @@ __device__ __forceinline__ RowTile row_tile(const PrefillArgs& a, uint32_t rt) {
   const uint32_t q1 = cut(a.q_offsets, lo + 1, a.Tq), k1 = cut(a.k_offsets, lo + 1, a.Tk);
   t.Lq = q1 > t.q0 ? static_cast<int32_t>(q1 - t.q0) : 0;
   t.Lk = k1 > t.k0 ? static_cast<int32_t>(k1 - t.k0) : 0;
-  const uint32_t first = (rt - (t.q0 / kRows + lo)) * kRows;
+  const uint32_t first = (rt - (t.q0 / ROWS + lo)) * ROWS;
   t.any = first < static_cast<uint32_t>(t.Lq);
   t.first = static_cast<int32_t>(first);
-  t.keys = t.any ? max(min(t.Lk, t.Lk - t.Lq + min(t.first + kRows, t.Lq)), 0) : 0;
+  t.keys = t.any ? max(min(t.Lk, t.Lk - t.Lq + min(t.first + ROWS, t.Lq)), 0) : 0;
   return t;
 }
 
@@ -82,10 +82,13 @@ __device__ __forceinline__ uint32_t split_tiles(int32_t keys, uint32_t splits, u
 
 template <int D>
 constexpr int halves_of() { return D >= 512 ? 2 : 1; }
+// Query rows of a workgroup.
+template <int D, bool SAME>
+constexpr int rows_of() { return D >= 512 && SAME ? 64 : 128; }
 
 template <int D, bool SAME>
-__global__ __launch_bounds__(256 * halves_of<D>(), 2) void attn_prefill_kernel(PrefillArgs a) {
-  constexpr int HALVES = halves_of<D>(), WAVES = 4 * HALVES;
+__global__ __launch_bounds__((2 * rows_of<D, SAME>() * halves_of<D>()), 2) void attn_prefill_kernel(PrefillArgs a) {
+  constexpr int HALVES = halves_of<D>(), ROWS = rows_of<D, SAME>(), GROUPS = ROWS / 32, WAVES = GROUPS * HALVES;
   constexpr int KT = key_tile<D>();
   constexpr int CH = D / 8;                             // 16-byte chunks of a row
   constexpr int TB = KT * D * 2;                        // bytes of a tile
@@ -95,7 +98,7 @@ __global__ __launch_bounds__(256 * halves_of<D>(), 2) void attn_prefill_kernel(P
   __shared__ __attribute__((aligned(1024))) uint8_t kbuf0[TB], kbuf1[TB], vbuf0[SAME ? 16 : TB], vbuf1[SAME ? 16 : TB];
   __shared__ __attribute__((aligned(16))) uint8_t partial[HALVES == 1 ? 16 : WAVES * SUB * 4096];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31;
-  const int group = wave & 3, half = wave >> 2;         // which 32 rows, which half of D
+  const int group = wave % GROUPS, half = wave / GROUPS;         // which 32 rows, which half of D
 
   // (row tile, head, split): key heads fastest, so that with workgroups dealt to the XCDs in turn an XCD's L2 serves few
   // key heads; last row tiles first, which have the most keys.
@@ -105,7 +108,7 @@ __global__ __launch_bounds__(256 * halves_of<D>(), 2) void attn_prefill_kernel(P
   const uint32_t head = kvh * a.G + id % a.G;
   id /= a.G;
   const uint32_t split = id % a.splits, rt = a.tiles - 1 - id / a.splits;
-  const RowTile t = row_tile(a, rt);
+  const RowTile t = row_tile<ROWS>(a, rt);
   uint32_t used;
   const uint32_t per = split_tiles<D>(t.keys, a.splits, used);
   if (!t.any || split >= used) return;
@@ -158,7 +161,7 @@ __global__ __launch_bounds__(256 * halves_of<D>(), 2) void attn_prefill_kernel(P
     w.hide_bases();
     if (active) w.scores(kt, s);
     if constexpr (HALVES == 2)
-      Tile::exchange(s, partial + wave * SUB * 4096, partial + (wave ^ 4) * SUB * 4096, active);
+      Tile::exchange(s, partial + wave * SUB * 4096, partial + (wave ^ GROUPS) * SUB * 4096, active);
   };
   auto step = [&](int32_t tile, const uint8_t* kt, const uint8_t* vt, uint8_t* knext, uint8_t* vnext) {
     turn();
@@ -202,7 +205,7 @@ __global__ __launch_bounds__(256 * halves_of<D>(), 2) void attn_prefill_kernel(P
 
   w.l += __shfl_xor(w.l, 32);
   if (used > 1) {
-    float* part = a.parts + (static_cast<size_t>(rt * a.H + head) * a.splits + split) * kRows * (D + 2);
+    float* part = a.parts + (static_cast<size_t>(rt * a.H + head) * a.splits + split) * ROWS * (D + 2);
     float* row = part + (group * 32 + col) * D + half * Tile::DH + w.hf * 4;
 #pragma unroll
     for (int d = 0; d < Tile::DT; ++d)
@@ -211,8 +214,8 @@ __global__ __launch_bounds__(256 * halves_of<D>(), 2) void attn_prefill_kernel(P
         *reinterpret_cast<float4*>(row + d * 32 + r * 8) =
             make_float4(w.acc[d][4 * r], w.acc[d][4 * r + 1], w.acc[d][4 * r + 2], w.acc[d][4 * r + 3]);
     if (w.hf == 0 && half == 0) {
-      part[kRows * D + group * 32 + col] = w.m;
-      part[kRows * D + kRows + group * 32 + col] = w.l;
+      part[ROWS * D + group * 32 + col] = w.m;
+      part[ROWS * D + ROWS + group * 32 + col] = w.l;
     }
     return;
   }
@@ -230,17 +233,17 @@ __global__ __launch_bounds__(256 * halves_of<D>(), 2) void attn_prefill_kernel(P
 
 // A workgroup takes kJoinRows rows of a row tile and head: the splits' parts joined in their order.
 constexpr int kJoinRows = 16, kJoinThreads = 256;
-template <int D>
+template <int D, int ROWS>
 __global__ __launch_bounds__(kJoinThreads) void attn_prefill_join_kernel(PrefillArgs a) {
   uint32_t id = blockIdx.x;
-  const uint32_t r0 = id % (kRows / kJoinRows) * kJoinRows;
-  id /= kRows / kJoinRows;
+  const uint32_t r0 = id % (ROWS / kJoinRows) * kJoinRows;
+  id /= ROWS / kJoinRows;
   const uint32_t head = id % a.H, rt = id / a.H;
-  const RowTile t = row_tile(a, rt);
+  const RowTile t = row_tile<ROWS>(a, rt);
   uint32_t used;
   split_tiles<D>(t.keys, a.splits, used);
   if (!t.any || used == 1) return;
-  const float* parts = a.parts + static_cast<size_t>(rt * a.H + head) * a.splits * kRows * (D + 2);
+  const float* parts = a.parts + static_cast<size_t>(rt * a.H + head) * a.splits * ROWS * (D + 2);
   for (uint32_t e = threadIdx.x * 4; e < kJoinRows * D; e += kJoinThreads * 4) {
     const uint32_t r = r0 + e / D, d = e % D;
     const int32_t i = t.first + static_cast<int32_t>(r);
@@ -248,11 +251,11 @@ __global__ __launch_bounds__(kJoinThreads) void attn_prefill_join_kernel(Prefill
     float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (uint32_t s = 0; s < used; ++s) {
-      const float* p = parts + static_cast<size_t>(s) * kRows * (D + 2);
-      const float x = p[kRows * D + r], top = fmaxf(m, x), base = top == -INFINITY ? 0.0f : top;
+      const float* p = parts + static_cast<size_t>(s) * ROWS * (D + 2);
+      const float x = p[ROWS * D + r], top = fmaxf(m, x), base = top == -INFINITY ? 0.0f : top;
       const float f = __builtin_amdgcn_exp2f(m - base), g = __builtin_amdgcn_exp2f(x - base);
       const float4 v = *reinterpret_cast<const float4*>(p + r * D + d);
-      l = l * f + p[kRows * D + kRows + r] * g;
+      l = l * f + p[ROWS * D + ROWS + r] * g;
       o = make_float4(o.x * f + v.x * g, o.y * f + v.y * g, o.z * f + v.z * g, o.w * f + v.w * g);
       m = top;
     }
@@ -262,36 +265,53 @@ __global__ __launch_bounds__(kJoinThreads) void attn_prefill_join_kernel(Prefill
   }
 }
 
-uint32_t row_tiles(int64_t B, int64_t Tq) { return static_cast<uint32_t>(Tq / kRows + B); }
+bool same(const void* k, int64_t k_stride, const void* v, int64_t v_stride) { return k == v && k_stride == v_stride; }
+
+// Query rows of a workgroup (rows_of, of a call).
+int rows_of_call(int32_t D, bool latent) { return D >= 512 && latent ? 64 : 128; }
+
+uint32_t row_tiles(int64_t B, int64_t Tq, int rows) { return static_cast<uint32_t>(Tq / rows + B); }
 
 // How many workgroups share the keys of one row tile and head.  `slots` run at once; with fewer (row tile, head) pairs
 // than that, a split leaves fewer of them idle, as long as every part has some tiles of keys.
-uint32_t split_count(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t D) {
-  const int64_t units = static_cast<int64_t>(row_tiles(B, Tq)) * H, slots = D >= 512 ? 256 : 512;
+uint32_t split_count(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t D, int rows) {
+  const int64_t units = static_cast<int64_t>(row_tiles(B, Tq, rows)) * H, slots = D >= 512 && rows == 128 ? 256 : 512;
   const int64_t tiles = (Tk / B + 63) / 64;             // of an average prompt
   return static_cast<uint32_t>(std::max<int64_t>(1, std::min(slots / units, tiles / kMinTiles)));
 }
 
-template <int D>
+size_t part_bytes(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t D, int rows) {
+  const size_t splits = split_count(B, Tq, Tk, H, D, rows);
+  return splits == 1 ? 0 : splits * row_tiles(B, Tq, rows) * H * rows * (D + 2) * 4;
+}
+
+template <int D, bool SAME>
 void launch(const PrefillArgs& a, hipStream_t stream) {
-  const dim3 grid(a.tiles * a.H * a.splits), block(256 * halves_of<D>());
-  if (a.k == a.v && a.k_stride == a.v_stride) hipLaunchKernelGGL((attn_prefill_kernel<D, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((attn_prefill_kernel<D, false>), grid, block, 0, stream, a);
+  constexpr int ROWS = rows_of<D, SAME>();
+  hipLaunchKernelGGL((attn_prefill_kernel<D, SAME>), dim3(a.tiles * a.H * a.splits), dim3(2 * ROWS * halves_of<D>()), 0, stream, a);
   if (a.splits > 1)
-    hipLaunchKernelGGL(attn_prefill_join_kernel<D>, dim3(a.tiles * a.H * (kRows / kJoinRows)), dim3(kJoinThreads), 0, stream, a);
+    hipLaunchKernelGGL((attn_prefill_join_kernel<D, ROWS>), dim3(a.tiles * a.H * (ROWS / kJoinRows)), dim3(kJoinThreads), 0, stream, a);
+}
+
+template <int D>
+void launch(const PrefillArgs& a, bool latent, hipStream_t stream) {
+  if (latent) launch<D, true>(a, stream);
+  else launch<D, false>(a, stream);
 }
 
 }  // namespace
 
+// Of either kind of call: the sizes do not say whether v is k.
 size_t prefill_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t, int32_t D) {
-  const size_t splits = split_count(B, Tq, Tk, H, D);
-  return splits == 1 ? 0 : splits * row_tiles(B, Tq) * H * kRows * (D + 2) * 4;
+  return std::max(part_bytes(B, Tq, Tk, H, D, rows_of_call(D, false)), part_bytes(B, Tq, Tk, H, D, rows_of_call(D, true)));
 }
 
 mx_status launch_attn_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                               int64_t v_stride, const int32_t* q_offsets, const int32_t* k_offsets, int64_t B,
                               int64_t Tq, int64_t Tk, int32_t H, int32_t Hkv, int32_t D, float scale, void* out,
                               void* workspace, hipStream_t stream) {
+  const bool latent = same(k, k_stride, v, v_stride);
+  const int rows = rows_of_call(D, latent);
   PrefillArgs a;
   a.q = static_cast<const uint16_t*>(q);
   a.k = static_cast<const uint16_t*>(k);
@@ -310,13 +330,13 @@ mx_status launch_attn_prefill(const void* q, int64_t q_stride, const void* k, in
   a.H = static_cast<uint32_t>(H);
   a.Hkv = static_cast<uint32_t>(Hkv);
   a.G = a.H / a.Hkv;
-  a.tiles = row_tiles(B, Tq);
-  a.splits = split_count(B, Tq, Tk, H, D);
+  a.tiles = row_tiles(B, Tq, rows);
+  a.splits = split_count(B, Tq, Tk, H, D, rows);
   switch (D) {
-    case 64: launch<64>(a, stream); break;
-    case 128: launch<128>(a, stream); break;
-    case 256: launch<256>(a, stream); break;
-    default: launch<512>(a, stream); break;
+    case 64: launch<64>(a, latent, stream); break;
+    case 128: launch<128>(a, latent, stream); break;
+    case 256: launch<256>(a, latent, stream); break;
+    default: launch<512>(a, latent, stream); break;
   }
   return launch_status("mx_attn_prefill");
 }
