@@ -134,13 +134,15 @@ __global__ __launch_bounds__((64 * waves_of<D, WHOLE>()), D <= 128 ? 2 : 1) void
 
   Share sh;
   if constexpr (WHOLE) {                                // tiles numbered from this sequence's first
-    sh.b = blockIdx.x / a.streams;
-    const uint32_t of = (tokens_of(a, sh.b) + TILE - 1) / TILE, s = blockIdx.x - sh.b * a.streams;
-    sh.first = 0;
-    sh.t = s * of;
+    const uint32_t x = blockIdx.x / a.head_blocks;
+    sh.block = blockIdx.x - x * a.head_blocks;
+    sh.b = x / a.c.Hkv;
+    const uint32_t of = (tokens_of(a, sh.b) + TILE - 1) / TILE, kvh = x - sh.b * a.c.Hkv;
+    sh.group = sh.first = 0;
+    sh.t = kvh * of;
     sh.end = sh.t + of;
     if (of == 0) {
-      const uint32_t kvh = s / a.head_blocks, h0 = kvh * a.G + (s - kvh * a.head_blocks) * kHeads;
+      const uint32_t h0 = kvh * a.G + sh.block * kHeads;
       const uint32_t heads = min(static_cast<uint32_t>(kHeads), (kvh + 1) * a.G - h0);
       for (uint32_t e = threadIdx.x * 4; e < heads * D; e += 64 * WAVES * 4)
         *reinterpret_cast<uint2*>(a.out + (static_cast<size_t>(sh.b) * a.H + h0) * D + e) = make_uint2(0, 0);
@@ -350,7 +352,7 @@ __global__ __launch_bounds__((64 * waves_of<D, WHOLE>()), D <= 128 ? 2 : 1) void
           *reinterpret_cast<v4f*>(&sacc[wave][col][p * PANEL + (g * 4 + r) * DPL + i]) =
               v4f{acc[p][i][r], acc[p][i + 1][r], acc[p][i + 2][r], acc[p][i + 3][r]};
     __syncthreads();
-    float* part = part_of(a, blockIdx.x, tile0 == 0, kHeads * (D + 2));
+    float* part = part_of(a, sh.group, sh.block, tile0 == 0, kHeads * (D + 2));
     for (uint32_t e = threadIdx.x * 4; e < heads * D; e += 64 * WAVES * 4) {
       const uint32_t h = e / D, d = e % D;
       float top = -INFINITY;
@@ -382,11 +384,9 @@ __global__ __launch_bounds__((64 * waves_of<D, WHOLE>()), D <= 128 ? 2 : 1) void
   }
 }
 
-// Workgroups of a call: as many as run at once (by registers and LDS), and no more than there can be tiles.
-uint32_t groups_of(int64_t B, uint32_t streams, int32_t D, int64_t max_tokens) {
-  const int64_t tiles = B * streams * ((max_tokens + kTile - 1) / kTile);
-  const int64_t most = D >= 512 ? 256 : 512;
-  return static_cast<uint32_t>(std::min<int64_t>(most, tiles));
+// Groups of a call: as many as run at once (by registers and LDS), and no more than there can be tiles.
+uint32_t groups_of(int64_t B, int32_t Hkv, uint32_t head_blocks, int32_t D, int64_t max_tokens) {
+  return decode_groups(B * Hkv * ((max_tokens + kTile - 1) / kTile), (D >= 512 ? 256 : 512) / head_blocks);
 }
 
 uint32_t head_blocks_of(int32_t G) { return static_cast<uint32_t>((G + kHeads - 1) / kHeads); }
@@ -397,13 +397,13 @@ uint32_t head_blocks_of(int32_t G) { return static_cast<uint32_t>((G + kHeads - 
 bool short_streams(int64_t streams, int64_t max_tokens) { return max_tokens <= (streams >= 512 ? 1024 : 512); }
 
 template <int D, bool FP8>
-void launch(const DecodeArgs& a, int64_t max_tokens, hipStream_t stream) {
-  if (short_streams(static_cast<int64_t>(a.B) * a.streams, max_tokens)) {
-    hipLaunchKernelGGL((attn_decode_kernel<D, FP8, true>), dim3(a.B * a.streams), dim3(64 * waves_of<D, true>()), 0, stream, a);
+void launch(DecodeArgs a, int64_t max_tokens, hipStream_t stream) {
+  if (short_streams(static_cast<int64_t>(a.B) * a.c.Hkv * a.head_blocks, max_tokens)) {
+    hipLaunchKernelGGL((attn_decode_kernel<D, FP8, true>), dim3(a.B * a.c.Hkv * a.head_blocks), dim3(64 * waves_of<D, true>()), 0, stream, a);
     return;
   }
-  const uint32_t groups = groups_of(a.B, a.streams, D, max_tokens);
-  hipLaunchKernelGGL((attn_decode_kernel<D, FP8, false>), dim3(groups), dim3(64 * waves_of<D, false>()), 0, stream, a);
+  a.groups = groups_of(a.B, static_cast<int32_t>(a.c.Hkv), a.head_blocks, D, max_tokens);
+  hipLaunchKernelGGL((attn_decode_kernel<D, FP8, false>), dim3(a.groups * a.head_blocks), dim3(64 * waves_of<D, false>()), 0, stream, a);
   hipLaunchKernelGGL((attn_join_kernel<D, kTile, kHeads>), dim3(a.B * a.H), dim3(kJoinThreads), 0, stream, a);
 }
 
@@ -412,8 +412,8 @@ size_t plan_bytes(int64_t B) { return (static_cast<size_t>(B) + 1 + 3) / 4 * 16;
 }  // namespace
 
 size_t decode_workspace_bytes(int64_t B, int32_t H, int32_t Hkv, int32_t D, int64_t max_tokens) {
-  const uint32_t streams = static_cast<uint32_t>(Hkv) * head_blocks_of(H / Hkv);
-  const size_t few = static_cast<size_t>(groups_of(B, streams, D, max_tokens)) * 2 * kHeads * (D + 2) * 4;
+  const uint32_t blocks = head_blocks_of(H / Hkv);
+  const size_t few = static_cast<size_t>(groups_of(B, Hkv, blocks, D, max_tokens)) * blocks * 2 * kHeads * (D + 2) * 4;
   return plan_bytes(B) + std::max(few, decode_rows_part_bytes(B, H, Hkv, D, max_tokens));
 }
 
@@ -437,7 +437,6 @@ mx_status launch_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t
     launch_decode_rows(a, D, fp8, max_tokens, stream);
   } else {
     a.head_blocks = head_blocks_of(static_cast<int32_t>(a.G));
-    a.streams = c.Hkv * a.head_blocks;
     switch (D) {
       case 64: fp8 ? launch<64, true>(a, max_tokens, stream) : launch<64, false>(a, max_tokens, stream); break;
       case 128: fp8 ? launch<128, true>(a, max_tokens, stream) : launch<128, false>(a, max_tokens, stream); break;

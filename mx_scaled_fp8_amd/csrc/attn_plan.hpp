@@ -1,10 +1,11 @@
 // How the attention of one new token for each sequence is shared among workgroups (gfx950; not part of the ABI).
 //
-// A stream is one (sequence, key head, block of its query heads).  Its keys are cut into tiles, the tiles of all streams
-// are numbered, sequence by sequence, and every workgroup takes an equal share of consecutive ones: a long sequence is
-// spread over many workgroups, many short ones share one.  A stream that a workgroup does not cover whole leaves its
-// part (O, m, l) in the workspace, at most two of them for a workgroup: in place 0 where the share begins inside the stream,
-// in place 1 where it ends inside one that it holds from its first tile.  A second kernel joins the parts.
+// A stream is one (sequence, key head).  Its keys are cut into tiles, the tiles of all streams are numbered, sequence by
+// sequence, and every group takes an equal share of consecutive ones: a long sequence is spread over many groups, many
+// short ones share one.  A group is as many workgroups as a key head has blocks of query heads; they read the same keys,
+// and are dealt to the same XCD, whose L2 then has them for all.  A stream that a group does not cover whole leaves its part
+// (O, m, l) in the workspace, at most two of them for a group: in place 0 where the share begins inside the stream, in
+// place 1 where it ends inside one that it holds from its first tile.  A second kernel joins the parts.
 #pragma once
 
 #include "kv_cache.hpp"
@@ -17,11 +18,11 @@ struct DecodeArgs {
   int64_t q_stride;
   const int32_t* lens;
   uint16_t* out;
-  float* parts;              // [groups][2][O: heads x D, then m and l]
+  float* parts;              // [group][head block][2][O: heads x D, then m and l]
   uint32_t* plan;            // [0] share, [1 + b] first tile of sequence b
   float scale;               // times log2(e)
   uint32_t B, H, G;          // G query heads a key head
-  uint32_t streams;          // a sequence's: Hkv * head_blocks
+  uint32_t groups;           // up to 8 or a multiple of 8
   uint32_t head_blocks;
 };
 
@@ -30,9 +31,10 @@ __device__ __forceinline__ uint32_t tokens_of(const DecodeArgs& a, uint32_t b) {
   return min(static_cast<uint32_t>(max(a.lens[b], 0)), a.c.max_pages << a.c.page_shift);
 }
 
-// A workgroup's share: tiles t .. end - 1, the first of them of sequence b, whose tiles begin at `first`.
+// A workgroup's share: tiles t .. end - 1, the first of them of sequence b, whose tiles begin at `first`, for one block of
+// heads.
 struct Share {
-  uint32_t t, end, b, first;
+  uint32_t t, end, b, first, group, block;
 };
 
 // One stream's stretch of a share.
@@ -59,14 +61,18 @@ __device__ __forceinline__ Share find_share(const DecodeArgs& a) {
   for (uint32_t b0 = 0; b0 < a.B; b0 += 64) {
     n = tiles(b0 + lane);
     upto = scan(n);
-    if (blockIdx.x == 0 && threadIdx.x < 64 && b0 + lane < a.B) a.plan[1 + b0 + lane] = (total + upto - n) * a.streams;
+    if (blockIdx.x == 0 && threadIdx.x < 64 && b0 + lane < a.B) a.plan[1 + b0 + lane] = (total + upto - n) * a.c.Hkv;
     total += __builtin_amdgcn_readlane(upto, 63);
   }
-  const uint32_t all = total * a.streams;
-  const uint32_t share = max((all + gridDim.x - 1) / gridDim.x, static_cast<uint32_t>(MIN));
+  const uint32_t all = total * a.c.Hkv;
+  const uint32_t share = max((all + a.groups - 1) / a.groups, static_cast<uint32_t>(MIN));
   if (blockIdx.x == 0 && threadIdx.x == 0) a.plan[0] = share;
+  // consecutive workgroups go to the XCDs in turn: the blocks of one group are 8 apart
+  const uint32_t side = min(a.groups, 8u), x = blockIdx.x / side;
   Share s;
-  s.t = blockIdx.x * share;
+  s.block = x % a.head_blocks;
+  s.group = x / a.head_blocks * side + blockIdx.x % side;
+  s.t = s.group * share;
   s.end = min(s.t + share, all);
   s.b = s.first = 0;
   if (s.t >= all) {
@@ -79,11 +85,11 @@ __device__ __forceinline__ Share find_share(const DecodeArgs& a) {
       n = tiles(b0 + lane);
       upto = scan(n);
     }
-    const uint64_t behind = __ballot(s.t < (done + upto) * a.streams);
+    const uint64_t behind = __ballot(s.t < (done + upto) * a.c.Hkv);
     if (behind != 0) {
       const int at = __builtin_ctzll(behind);
       s.b = b0 + at;
-      s.first = (done + __builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(n, at)) * a.streams;
+      s.first = (done + __builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(n, at)) * a.c.Hkv;
       return s;
     }
     done += __builtin_amdgcn_readlane(upto, 63);
@@ -98,8 +104,8 @@ __device__ __forceinline__ Piece piece_of(const DecodeArgs& a, const Share& s) {
   const uint32_t x = (s.t - s.first) / p.of;
   p.tile0 = (s.t - s.first) - x * p.of;
   p.tiles = min(p.of - p.tile0, s.end - s.t);
-  p.kvh = x / a.head_blocks;
-  p.h0 = p.kvh * a.G + (x - p.kvh * a.head_blocks) * HEADS;
+  p.kvh = x;
+  p.h0 = x * a.G + s.block * HEADS;
   p.heads = min(static_cast<uint32_t>(HEADS), (p.kvh + 1) * a.G - p.h0);
   return p;
 }
@@ -107,15 +113,15 @@ __device__ __forceinline__ Piece piece_of(const DecodeArgs& a, const Share& s) {
 // Past the piece, to the next sequence that has tokens if this one's streams are done and the share is not.
 __device__ __forceinline__ void advance(const DecodeArgs& a, Share& s, const Piece& p) {
   s.t += p.tiles;
-  if (s.t == s.first + p.of * a.streams && s.t < s.end) {
+  if (s.t == s.first + p.of * a.c.Hkv && s.t < s.end) {
     s.first = s.t;
     do ++s.b; while (tokens_of(a, s.b) == 0);            // a tile is left, so a sequence that has one
   }
 }
 
 // Where the part of a piece that is not its stream's whole goes.
-__device__ __forceinline__ float* part_of(const DecodeArgs& a, uint32_t group, bool begins, uint32_t size) {
-  return a.parts + (static_cast<size_t>(group) * 2 + (begins ? 1 : 0)) * size;
+__device__ __forceinline__ float* part_of(const DecodeArgs& a, uint32_t group, uint32_t block, bool begins, uint32_t size) {
+  return a.parts + ((static_cast<size_t>(group) * a.head_blocks + block) * 2 + (begins ? 1 : 0)) * size;
 }
 
 constexpr int kJoinThreads = 256;
@@ -138,7 +144,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(DecodeArgs a) {
     if (lane == 0) *out = make_uint2(0, 0);
     return;
   }
-  const uint32_t t0 = begin + (kvh * a.head_blocks + block) * nt;
+  const uint32_t t0 = begin + kvh * nt;
   const uint32_t w0 = t0 / share, w1 = (t0 + nt - 1) / share;
   if (w0 == w1) return;
   float m = -INFINITY, l = 0.0f;
@@ -149,7 +155,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(DecodeArgs a) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const bool some = w + k * LANES <= w1;
-      const float* p = part_of(a, some ? w + k * LANES : w, w + k * LANES == w0 || (!some && w == w0), SIZE);
+      const float* p = part_of(a, some ? w + k * LANES : w, block, w + k * LANES == w0 || (!some && w == w0), SIZE);
       x[k] = *reinterpret_cast<const float4*>(p + r * D + d);
       pm[k] = some ? p[HEADS * D + r] : -INFINITY;
       pl[k] = p[HEADS * D + HEADS + r];

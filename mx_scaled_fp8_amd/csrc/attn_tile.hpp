@@ -32,6 +32,11 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t from, uint8_t* to, 
   __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void_t*)to, 16, offset, 0, 0, 0);
 }
 
+// The same from an address of each lane.
+__device__ __forceinline__ void dma16_at(const uint8_t* from, uint8_t* to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from, (lds_void_t*)to, 16, 0, 0);
+}
+
 __device__ __forceinline__ v2u read_transposed(const uint8_t* at) {
   return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)at));
 }
