@@ -15,15 +15,14 @@ namespace {
 
 constexpr int kMinTokens = 256;        // of a share: its part is up to 128 rows of FP32, as much as 500 cached tokens
 
+constexpr int kRows = 128;             // query heads of a workgroup: 32 or 16 for each wave
 template <int D>
-constexpr int key_tile() { return D <= 128 ? 64 : 32; }
-template <int D>
-constexpr int halves_of() { return D >= 512 ? 2 : 1; }
-constexpr int kRows = 128;             // query heads of a workgroup: 32 for each wave, or two waves
+constexpr int threads_of() { return kRows / TileOf<D>::type::ROWS * 64; }
 
 template <int D, bool FP8, bool SAME>
-__global__ __launch_bounds__(256 * halves_of<D>(), 2) void attn_decode_rows_kernel(DecodeArgs a) {
-  constexpr int HALVES = halves_of<D>(), WAVES = 4 * HALVES, KT = key_tile<D>();
+__global__ __launch_bounds__(threads_of<D>(), 2) void attn_decode_rows_kernel(DecodeArgs a) {
+  using Tile = typename TileOf<D>::type;
+  constexpr int WAVES = kRows / Tile::ROWS, KT = key_tile<D>();
   constexpr int TB = KT * D * 2;                        // bytes of a tile in LDS
   constexpr int EB = FP8 ? 1 : 2;
   constexpr int RPI = 1024 / (D * EB);                  // rows of one DMA instruction: at most 16, so of one page
@@ -31,13 +30,10 @@ __global__ __launch_bounds__(256 * halves_of<D>(), 2) void attn_decode_rows_kern
   constexpr int NI = KT / RPI / WAVES;                  // a wave's instructions for one tile
   constexpr int KV = SAME ? 1 : 2;
   constexpr int RAW = FP8 ? KT * D : 16;
-  using Tile = AttnTile<D, KT, HALVES>;
-  constexpr int SUB = Tile::SUB;
   static_assert(NI >= 1 && RPI <= 16, "every wave has its share of a tile");
   __shared__ __attribute__((aligned(1024))) uint8_t buf0[KV][TB], buf1[KV][TB], raw[KV][RAW];
-  __shared__ __attribute__((aligned(16))) uint8_t partial[HALVES == 1 ? 16 : WAVES * SUB * 4096];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31;
-  const int group = wave & 3, half = wave >> 2;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t r = wave * Tile::ROWS + Tile::row();   // the lane's row
 
   Share sh = find_share<KT, kMinTokens / KT>(a);
   while (sh.t < sh.end) {
@@ -45,12 +41,11 @@ __global__ __launch_bounds__(256 * halves_of<D>(), 2) void attn_decode_rows_kern
     const uint32_t len = tokens_of(a, sh.b);
     const bool bad = a.lens[sh.b] > static_cast<int32_t>(len);   // longer than its table
     const int32_t* table = a.c.table + static_cast<int64_t>(sh.b) * a.c.max_pages;
-    const bool active = static_cast<uint32_t>(group * 32) < pc.heads;   // the wave has heads
+    const bool active = static_cast<uint32_t>(wave * Tile::ROWS) < pc.heads;   // the wave has heads
 
     Tile w;
-    w.begin(half);
-    w.load_q(a.q + static_cast<int64_t>(sh.b) * a.q_stride + (pc.h0 + min(static_cast<uint32_t>(group * 32 + col), pc.heads - 1)) * D +
-             half * Tile::DH);
+    w.begin();
+    w.load_q(a.q + static_cast<int64_t>(sh.b) * a.q_stride + (pc.h0 + min(r, pc.heads - 1)) * D);
 
     // Instruction x of a wave has rows (wave + x WAVES) RPI .. of the tile.  Its page's number is looked up two turns
     // ahead.  Rows of a page outside the cache are read from page 0 and made NaN (`lost`); rows past the end are zeros.
@@ -102,7 +97,7 @@ __global__ __launch_bounds__(256 * halves_of<D>(), 2) void attn_decode_rows_kern
       const uint32_t lane = hidden();
 #pragma unroll
       for (int x = 0; x < NI; ++x) {
-        const uint32_t r = (wave + x * WAVES) * RPI + lane / CPR, c = lane % CPR;
+        const uint32_t r = (wave + x * WAVES) * RPI + lane / CPR, c = lane % CPR;   // row of the tile, chunk
         const bool out = tile * KT + r >= len, nans = (lost >> x) & 1;
         const uint32_t fill = nans ? 0x7FC07FC0u : 0u;
 #pragma unroll
@@ -154,21 +149,14 @@ __global__ __launch_bounds__(256 * halves_of<D>(), 2) void attn_decode_rows_kern
         load(tile + 1, next);
         pages(tile + 2);
       }
-      v16f s[SUB];
-      w.hide_bases();
-      if (active) w.scores(now[0], s);
-      if constexpr (HALVES == 2) Tile::exchange(s, partial + wave * SUB * 4096, partial + (wave ^ 4) * SUB * 4096, active);
       if (!active) return;
+      typename Tile::Scores s;
+      typename Tile::Weights p;
+      w.scores(now[0], s);
       const int32_t seen = static_cast<int32_t>(len - tile * KT);
-      if (seen < KT) {
-#pragma unroll
-        for (int u = 0; u < SUB; ++u)
-#pragma unroll
-          for (int x = 0; x < 16; ++x) s[u][x] = u * 32 + w.key_of(x) < seen ? s[u][x] : -INFINITY;
-      }
-      v8bf pf[SUB][2];
-      w.weights(s, a.scale, pf);
-      w.values(now[KV - 1], pf);
+      if (seen < KT) w.mask(s, seen);
+      w.weights(s, a.scale, p);
+      w.values(now[KV - 1], p);
     };
 
     uint32_t tile = pc.tile0;
@@ -189,33 +177,29 @@ __global__ __launch_bounds__(256 * halves_of<D>(), 2) void attn_decode_rows_kern
       if (tile + 1 < last) step(tile + 1, buf1, buf0);
     }
 
-    const float2 sums = halves(w.l);
-    w.l = sums.x + sums.y;
-    if (bad) w.l = __builtin_nanf("");
-    const uint32_t r = group * 32 + col;
+    float l = w.sum();
+    if (bad) l = __builtin_nanf("");
     if (active && r < pc.heads) {
       if (pc.tiles == pc.of) {
-        const float inv = 1.0f / w.l;
-        uint16_t* row = a.out + (static_cast<size_t>(sh.b) * a.H + pc.h0 + r) * D + half * Tile::DH + w.hf * 4;
+        const float inv = 1.0f / l;
+        uint16_t* row = a.out + (static_cast<size_t>(sh.b) * a.H + pc.h0 + r) * D;
 #pragma unroll
-        for (int d = 0; d < Tile::DT; ++d)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            *reinterpret_cast<uint2*>(row + d * 32 + x * 8) =
-                make_uint2(pack_bf16x2(w.acc[d][4 * x] * inv, w.acc[d][4 * x + 1] * inv),
-                           pack_bf16x2(w.acc[d][4 * x + 2] * inv, w.acc[d][4 * x + 3] * inv));
+        for (int x = 0; x < Tile::QUADS; ++x) {
+          int d;
+          const float4 o = w.quad(x, d);
+          *reinterpret_cast<uint2*>(row + d) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        }
       } else {
         float* part = part_of(a, sh.group, sh.block, pc.tile0 == 0, kRows * (D + 2));
-        float* row = part + r * D + half * Tile::DH + w.hf * 4;
 #pragma unroll
-        for (int d = 0; d < Tile::DT; ++d)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            *reinterpret_cast<float4*>(row + d * 32 + x * 8) =
-                make_float4(w.acc[d][4 * x], w.acc[d][4 * x + 1], w.acc[d][4 * x + 2], w.acc[d][4 * x + 3]);
-        if (w.hf == 0 && half == 0) {
+        for (int x = 0; x < Tile::QUADS; ++x) {
+          int d;
+          const float4 o = w.quad(x, d);
+          *reinterpret_cast<float4*>(part + r * D + d) = o;
+        }
+        if (Tile::first_lane()) {
           part[kRows * D + r] = w.m;
-          part[kRows * D + kRows + r] = w.l;
+          part[kRows * D + kRows + r] = l;
         }
       }
     }
@@ -233,7 +217,7 @@ uint32_t groups_of(int64_t B, int32_t Hkv, uint32_t head_blocks, int32_t D, int6
 
 template <int D, bool FP8>
 void launch(const DecodeArgs& a, hipStream_t stream) {
-  const dim3 grid(a.groups * a.head_blocks), block(256 * halves_of<D>());
+  const dim3 grid(a.groups * a.head_blocks), block(threads_of<D>());
   if (D >= 512 || (a.c.k == a.c.v && a.c.ks == a.c.vs)) {
     hipLaunchKernelGGL((attn_decode_rows_kernel<D, FP8, true>), grid, block, 0, stream, a);
   } else if constexpr (D < 512) {

@@ -1,7 +1,7 @@
 // Causal attention over packed prompts (gfx950).
 //
-// A workgroup takes 128 query rows of one prompt and head, 32 for each of its four waves (attn_tile.hpp; for rows of 512
-// there are eight, two of which share 32 rows), and runs over the keys in tiles of KT.  K and V tiles go from global memory to LDS by buffer-load DMA, the next one while this one is
+// A workgroup takes 128 query rows of one prompt and head (64 in rows of 512 that are keys and values), 32 or 16 for each
+// wave (attn_tile.hpp), and runs over the keys in tiles of KT.  K and V tiles go from global memory to LDS by buffer-load DMA, the next one while this one is
 // used; rows past the end are zeros by the buffer's bound.  Tiles that every row sees whole run first, two to a turn of
 // the loop, so that each of the two buffers is an object of its own and the compiler waits for no DMA but what a read
 // needs; the last few, which hold the diagonal and the ragged end, go through a loop with masks.
@@ -68,9 +68,6 @@ __device__ __forceinline__ RowTile row_tile(const PrefillArgs& a, uint32_t rt) {
   return t;
 }
 
-template <int D>
-constexpr int key_tile() { return D <= 128 ? 64 : 32; }
-
 // Splits that a row tile with so many keys is really cut into, and the tiles of each.
 template <int D>
 __device__ __forceinline__ uint32_t split_tiles(int32_t keys, uint32_t splits, uint32_t& used) {
@@ -80,25 +77,22 @@ __device__ __forceinline__ uint32_t split_tiles(int32_t keys, uint32_t splits, u
   return per;
 }
 
-template <int D>
-constexpr int halves_of() { return D >= 512 ? 2 : 1; }
-// Query rows of a workgroup.
+// Query rows of a workgroup.  Four waves are half of what a compute unit runs: two workgroups, which know nothing of each
+// other's barriers, fill it.  (Rows of 512 whose K and V both need LDS: one of eight waves.)
 template <int D, bool SAME>
 constexpr int rows_of() { return D >= 512 && SAME ? 64 : 128; }
+template <int D, bool SAME>
+constexpr int threads_of() { return rows_of<D, SAME>() / TileOf<D>::type::ROWS * 64; }
 
 template <int D, bool SAME>
-__global__ __launch_bounds__((2 * rows_of<D, SAME>() * halves_of<D>()), 2) void attn_prefill_kernel(PrefillArgs a) {
-  constexpr int HALVES = halves_of<D>(), ROWS = rows_of<D, SAME>(), GROUPS = ROWS / 32, WAVES = GROUPS * HALVES;
-  constexpr int KT = key_tile<D>();
+__global__ __launch_bounds__((threads_of<D, SAME>()), 2) void attn_prefill_kernel(PrefillArgs a) {
+  using Tile = typename TileOf<D>::type;
+  constexpr int ROWS = rows_of<D, SAME>(), WAVES = ROWS / Tile::ROWS, KT = key_tile<D>();
   constexpr int CH = D / 8;                             // 16-byte chunks of a row
   constexpr int TB = KT * D * 2;                        // bytes of a tile
   constexpr int ND = TB / 1024 / WAVES;                 // a wave's DMA instructions for one tile
-  using Tile = AttnTile<D, KT, HALVES>;
-  constexpr int SUB = Tile::SUB;
   __shared__ __attribute__((aligned(1024))) uint8_t kbuf0[TB], kbuf1[TB], vbuf0[SAME ? 16 : TB], vbuf1[SAME ? 16 : TB];
-  __shared__ __attribute__((aligned(16))) uint8_t partial[HALVES == 1 ? 16 : WAVES * SUB * 4096];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31;
-  const int group = wave % GROUPS, half = wave / GROUPS;         // which 32 rows, which half of D
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
   // (row tile, head, split): key heads fastest, so that with workgroups dealt to the XCDs in turn an XCD's L2 serves few
   // key heads; last row tiles first, which have the most keys.
@@ -113,16 +107,16 @@ __global__ __launch_bounds__((2 * rows_of<D, SAME>() * halves_of<D>()), 2) void 
   const uint32_t per = split_tiles<D>(t.keys, a.splits, used);
   if (!t.any || split >= used) return;
   const int32_t hidden = t.Lk - t.Lq;                              // row i sees keys 0 .. hidden + i
-  const int32_t i0 = t.first + group * 32, i = i0 + col;            // the wave's first row, the lane's
-  const int32_t w_keys = i0 < t.Lq ? min(t.Lk, hidden + min(i0 + 32, t.Lq)) : 0;   // keys that some row of the wave sees
+  const int32_t i0 = t.first + wave * Tile::ROWS, i = i0 + Tile::row();            // the wave's first row, the lane's
+  const int32_t w_keys = i0 < t.Lq ? min(t.Lk, hidden + min(i0 + Tile::ROWS, t.Lq)) : 0;   // keys that some row of the wave sees
   const int32_t n_tiles = min((t.keys + KT - 1) / KT, static_cast<int32_t>((split + 1) * per));
   const int32_t begin = split * per;
   // whole tiles: those that the workgroup's first row sees whole; an even number of them
   const int32_t whole = max(min(n_tiles, (hidden + t.first + 1) / KT) - begin, 0) & ~1;
 
   Tile w;
-  w.begin(half);
-  w.load_q(a.q + static_cast<int64_t>(t.q0 + min(i, t.Lq - 1)) * a.q_stride + head * D + half * Tile::DH);
+  w.begin();
+  w.load_q(a.q + static_cast<int64_t>(t.q0 + min(i, t.Lq - 1)) * a.q_stride + head * D);
 
   // DMA: an instruction fills 1024 bytes of LDS, RPI rows, in lane order.  The swizzle repeats after 16 rows, so that a
   // wave's PAT instructions of one PERIOD of rows serve all of them.
@@ -157,20 +151,14 @@ __global__ __launch_bounds__((2 * rows_of<D, SAME>() * halves_of<D>()), 2) void 
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
     asm volatile("s_barrier" ::: "memory");
   };
-  auto scores = [&](const uint8_t* kt, v16f (&s)[SUB], bool active) {
-    w.hide_bases();
-    if (active) w.scores(kt, s);
-    if constexpr (HALVES == 2)
-      Tile::exchange(s, partial + wave * SUB * 4096, partial + (wave ^ GROUPS) * SUB * 4096, active);
-  };
   auto step = [&](int32_t tile, const uint8_t* kt, const uint8_t* vt, uint8_t* knext, uint8_t* vnext) {
     turn();
     if (tile + 1 < n_tiles) dma(tile + 1, knext, vnext);
-    v16f s[SUB];
-    v8bf pf[SUB][2];
-    scores(kt, s, true);
-    w.weights(s, a.scale, pf);
-    w.values(SAME ? kt : vt, pf);
+    typename Tile::Scores s;
+    typename Tile::Weights p;
+    w.scores(kt, s);
+    w.weights(s, a.scale, p);
+    w.values(SAME ? kt : vt, p);
   };
 
   int32_t tile = begin;
@@ -185,50 +173,44 @@ __global__ __launch_bounds__((2 * rows_of<D, SAME>() * halves_of<D>()), 2) void 
     turn();
     if (tile + 1 < n_tiles) dma(tile + 1, second ? kbuf0 : kbuf1, second ? vbuf0 : vbuf1);
     const int32_t t0 = tile * KT;
-    const bool active = t0 < w_keys;
-    if (HALVES == 1 && !active) continue;
+    if (t0 >= w_keys) continue;
     const uint8_t* kt = second ? kbuf1 : kbuf0;
     const uint8_t* vt = SAME ? kt : second ? vbuf1 : vbuf0;
     const int32_t seen = hidden + i + 1 - t0;           // keys of the tile that the lane's row sees (rows past Lq: more than
                                                         // there are, zeros; nobody reads their results)
-    v16f s[SUB];
-    v8bf pf[SUB][2];
-    scores(kt, s, active);
-    if (!active) continue;
-#pragma unroll
-    for (int u = 0; u < SUB; ++u)
-#pragma unroll
-      for (int x = 0; x < 16; ++x) s[u][x] = u * 32 + w.key_of(x) < seen ? s[u][x] : -INFINITY;
-    w.weights(s, a.scale, pf);
-    w.values_masked(vt, pf, seen);
+    typename Tile::Scores s;
+    typename Tile::Weights p;
+    w.scores(kt, s);
+    w.mask(s, seen);
+    w.weights(s, a.scale, p);
+    w.values_masked(vt, p, seen);
   }
 
-  w.l += __shfl_xor(w.l, 32);
+  const float l = w.sum();
   if (used > 1) {
     float* part = a.parts + (static_cast<size_t>(rt * a.H + head) * a.splits + split) * ROWS * (D + 2);
-    float* row = part + (group * 32 + col) * D + half * Tile::DH + w.hf * 4;
+    const int r = wave * Tile::ROWS + Tile::row();
 #pragma unroll
-    for (int d = 0; d < Tile::DT; ++d)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        *reinterpret_cast<float4*>(row + d * 32 + r * 8) =
-            make_float4(w.acc[d][4 * r], w.acc[d][4 * r + 1], w.acc[d][4 * r + 2], w.acc[d][4 * r + 3]);
-    if (w.hf == 0 && half == 0) {
-      part[ROWS * D + group * 32 + col] = w.m;
-      part[ROWS * D + ROWS + group * 32 + col] = w.l;
+    for (int x = 0; x < Tile::QUADS; ++x) {
+      int d;
+      const float4 o = w.quad(x, d);
+      *reinterpret_cast<float4*>(part + r * D + d) = o;
+    }
+    if (Tile::first_lane()) {
+      part[ROWS * D + r] = w.m;
+      part[ROWS * D + ROWS + r] = l;
     }
     return;
   }
   if (i >= t.Lq) return;
-  const float inv = t.Lk > 0 && hidden + i >= 0 ? 1.0f / w.l : 0.0f;
-  uint16_t* row = a.out + (static_cast<int64_t>(t.q0 + i) * a.H + head) * D + half * Tile::DH + w.hf * 4;
+  const float inv = t.Lk > 0 && hidden + i >= 0 ? 1.0f / l : 0.0f;
+  uint16_t* row = a.out + (static_cast<int64_t>(t.q0 + i) * a.H + head) * D;
 #pragma unroll
-  for (int d = 0; d < Tile::DT; ++d)
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      *reinterpret_cast<uint2*>(row + d * 32 + r * 8) =
-          make_uint2(pack_bf16x2(w.acc[d][4 * r] * inv, w.acc[d][4 * r + 1] * inv),
-                     pack_bf16x2(w.acc[d][4 * r + 2] * inv, w.acc[d][4 * r + 3] * inv));
+  for (int x = 0; x < Tile::QUADS; ++x) {
+    int d;
+    const float4 o = w.quad(x, d);
+    *reinterpret_cast<uint2*>(row + d) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  }
 }
 
 // A workgroup takes kJoinRows rows of a row tile and head: the splits' parts joined in their order.
@@ -288,7 +270,7 @@ size_t part_bytes(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t D, int r
 template <int D, bool SAME>
 void launch(const PrefillArgs& a, hipStream_t stream) {
   constexpr int ROWS = rows_of<D, SAME>();
-  hipLaunchKernelGGL((attn_prefill_kernel<D, SAME>), dim3(a.tiles * a.H * a.splits), dim3(2 * ROWS * halves_of<D>()), 0, stream, a);
+  hipLaunchKernelGGL((attn_prefill_kernel<D, SAME>), dim3(a.tiles * a.H * a.splits), dim3(threads_of<D, SAME>()), 0, stream, a);
   if (a.splits > 1)
     hipLaunchKernelGGL((attn_prefill_join_kernel<D, ROWS>), dim3(a.tiles * a.H * (ROWS / kJoinRows)), dim3(kJoinThreads), 0, stream, a);
 }
