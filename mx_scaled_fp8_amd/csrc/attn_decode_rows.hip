@@ -15,14 +15,15 @@ namespace {
 
 constexpr int kMinTokens = 256;        // of a share: its part is up to 128 rows of FP32, as much as 500 cached tokens
 
-constexpr int kRows = 128;             // query heads of a workgroup: 32 or 16 for each wave
-template <int D>
-constexpr int threads_of() { return kRows / TileOf<D>::type::ROWS * 64; }
+// Query heads of a workgroup: 32 or 16 for each of four waves, half of what a compute unit runs, so that two workgroups,
+// which know nothing of each other's barriers, fill it.
+constexpr int rows_of(int D) { return D >= 512 ? 64 : 128; }
+constexpr int kThreads = 256;
 
 template <int D, bool FP8, bool SAME>
-__global__ __launch_bounds__(threads_of<D>(), 2) void attn_decode_rows_kernel(DecodeArgs a) {
+__global__ __launch_bounds__(kThreads, 2) void attn_decode_rows_kernel(DecodeArgs a) {
   using Tile = typename TileOf<D>::type;
-  constexpr int WAVES = kRows / Tile::ROWS, KT = key_tile<D>();
+  constexpr int ROWS = rows_of(D), WAVES = ROWS / Tile::ROWS, KT = key_tile<D>();
   constexpr int TB = KT * D * 2;                        // bytes of a tile in LDS
   constexpr int EB = FP8 ? 1 : 2;
   constexpr int RPI = 1024 / (D * EB);                  // rows of one DMA instruction: at most 16, so of one page
@@ -37,7 +38,7 @@ __global__ __launch_bounds__(threads_of<D>(), 2) void attn_decode_rows_kernel(De
 
   Share sh = find_share<KT, kMinTokens / KT>(a);
   while (sh.t < sh.end) {
-    const Piece pc = piece_of<KT, kRows>(a, sh);
+    const Piece pc = piece_of<KT, ROWS>(a, sh);
     const uint32_t len = tokens_of(a, sh.b);
     const bool bad = a.lens[sh.b] > static_cast<int32_t>(len);   // longer than its table
     const int32_t* table = a.c.table + static_cast<int64_t>(sh.b) * a.c.max_pages;
@@ -190,7 +191,7 @@ __global__ __launch_bounds__(threads_of<D>(), 2) void attn_decode_rows_kernel(De
           *reinterpret_cast<uint2*>(row + d) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
         }
       } else {
-        float* part = part_of(a, sh.group, sh.block, pc.tile0 == 0, kRows * (D + 2));
+        float* part = part_of(a, sh.group, sh.block, pc.tile0 == 0, ROWS * (D + 2));
 #pragma unroll
         for (int x = 0; x < Tile::QUADS; ++x) {
           int d;
@@ -198,8 +199,8 @@ __global__ __launch_bounds__(threads_of<D>(), 2) void attn_decode_rows_kernel(De
           *reinterpret_cast<float4*>(part + r * D + d) = o;
         }
         if (Tile::first_lane()) {
-          part[kRows * D + r] = w.m;
-          part[kRows * D + kRows + r] = l;
+          part[ROWS * D + r] = w.m;
+          part[ROWS * D + ROWS + r] = l;
         }
       }
     }
@@ -207,23 +208,23 @@ __global__ __launch_bounds__(threads_of<D>(), 2) void attn_decode_rows_kernel(De
   }
 }
 
-uint32_t head_blocks_of(int32_t G) { return static_cast<uint32_t>((G + kRows - 1) / kRows); }
+uint32_t head_blocks_of(int32_t G, int32_t D) { return static_cast<uint32_t>((G + rows_of(D) - 1) / rows_of(D)); }
 
 // Groups: as many as run at once, and no more than there can be tiles.
 uint32_t groups_of(int64_t B, int32_t Hkv, uint32_t head_blocks, int32_t D, int64_t max_tokens) {
   const int64_t kt = D <= 128 ? 64 : 32;
-  return decode_groups(B * Hkv * ((max_tokens + kt - 1) / kt), (D >= 512 ? 256 : 512) / head_blocks);
+  return decode_groups(B * Hkv * ((max_tokens + kt - 1) / kt), 512 / head_blocks);
 }
 
 template <int D, bool FP8>
 void launch(const DecodeArgs& a, hipStream_t stream) {
-  const dim3 grid(a.groups * a.head_blocks), block(threads_of<D>());
+  const dim3 grid(a.groups * a.head_blocks), block(kThreads);
   if (D >= 512 || (a.c.k == a.c.v && a.c.ks == a.c.vs)) {
     hipLaunchKernelGGL((attn_decode_rows_kernel<D, FP8, true>), grid, block, 0, stream, a);
   } else if constexpr (D < 512) {
     hipLaunchKernelGGL((attn_decode_rows_kernel<D, FP8, false>), grid, block, 0, stream, a);
   }
-  hipLaunchKernelGGL((attn_join_kernel<D, key_tile<D>(), kRows>), dim3(a.B * a.H), dim3(kJoinThreads), 0, stream, a);
+  hipLaunchKernelGGL((attn_join_kernel<D, key_tile<D>(), rows_of(D)>), dim3(a.B * a.H), dim3(kJoinThreads), 0, stream, a);
 }
 
 }  // namespace
@@ -235,12 +236,12 @@ bool decode_by_rows(int32_t G, int32_t D, bool latent) { return G >= 32 && (D < 
 size_t decode_rows_part_bytes(int64_t B, int32_t H, int32_t Hkv, int32_t D, int64_t max_tokens) {
   const int32_t G = H / Hkv;
   if (!decode_by_rows(G, D, true)) return 0;
-  const uint32_t blocks = head_blocks_of(G);
-  return static_cast<size_t>(groups_of(B, Hkv, blocks, D, max_tokens)) * blocks * 2 * kRows * (D + 2) * 4;
+  const uint32_t blocks = head_blocks_of(G, D);
+  return static_cast<size_t>(groups_of(B, Hkv, blocks, D, max_tokens)) * blocks * 2 * rows_of(D) * (D + 2) * 4;
 }
 
 void launch_decode_rows(DecodeArgs a, int32_t D, bool fp8, int64_t max_tokens, hipStream_t stream) {
-  a.head_blocks = head_blocks_of(static_cast<int32_t>(a.G));
+  a.head_blocks = head_blocks_of(static_cast<int32_t>(a.G), D);
   a.groups = groups_of(a.B, static_cast<int32_t>(a.c.Hkv), a.head_blocks, D, max_tokens);
   switch (D) {
     case 64: fp8 ? launch<64, true>(a, stream) : launch<64, false>(a, stream); break;

@@ -49,7 +49,9 @@ __device__ __forceinline__ v2u read_transposed(const uint8_t* at) {
 // 64 elements, two rows are, and they have 8 chunks to spread, by row / 2.
 template <int D>
 __device__ __forceinline__ uint32_t swizzled(uint32_t c, uint32_t row) {
-  if constexpr (D >= 512) return c ^ (((row & 7) << 1) | ((row >> 3) & 1));        // V: 2 chunks of 8 rows at a time
+  // V: 2 chunks of 8 rows at a time.  K: a chunk of 16 rows, but the banks serve rows 0..3, 12..15 of one chunk together
+  // with rows 4..11 of the next, so that row / 4 % 2, not row / 8, tells rows 8 apart.
+  if constexpr (D >= 512) return c ^ (((row & 7) << 1) | ((row >> 2) & 1));
   else if constexpr (D >= 128) return c ^ (((row & 3) << 2) | ((row >> 2) & 3));   // 4 chunks of 4 rows
   else return c ^ ((((row >> 1) & 1) << 2) | ((row >> 2) & 3));
 }
