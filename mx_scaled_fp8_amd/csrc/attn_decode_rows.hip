@@ -6,6 +6,8 @@
 // a turn ahead, where the wave that asked for them makes BF16 of them (exact) under the other waves' products and writes
 // it to the buffer that the last turn read; registers hold O and Q and have no room for codes under way.
 // Work is shared as attn_plan.hpp says.
+#include <type_traits>
+
 #include "attn_decode.hpp"
 #include "attn_tile.hpp"
 
@@ -22,16 +24,18 @@ constexpr int kThreads = 256;
 
 template <int D, bool FP8, bool SAME>
 __global__ __launch_bounds__(kThreads, 2) void attn_decode_rows_kernel(DecodeArgs a) {
-  using Tile = typename TileOf<D>::type;
+  using Tile = typename TileOf<D, 4>::type;              // (6 ahead: no registers, and the compiler reads none ahead)
   constexpr int ROWS = rows_of(D), WAVES = ROWS / Tile::ROWS, KT = key_tile<D>();
   constexpr int TB = KT * D * 2;                        // bytes of a tile in LDS
   constexpr int EB = FP8 ? 1 : 2;
-  constexpr int RPI = 1024 / (D * EB);                  // rows of one DMA instruction: at most 16, so of one page
+  constexpr int RW = KT / WAVES;                        // rows that a wave brings: of one page
+  constexpr int RPI = 1024 / (D * EB);                  // of one DMA instruction
   constexpr int CPR = D * EB / 16;                      // 16-byte chunks of a row in the cache
-  constexpr int NI = KT / RPI / WAVES;                  // a wave's instructions for one tile
+  constexpr int NI = RW / RPI;                          // instructions
+  constexpr int SB = D / 32;                            // scale bytes of a row
   constexpr int KV = SAME ? 1 : 2;
   constexpr int RAW = FP8 ? KT * D : 16;
-  static_assert(NI >= 1 && RPI <= 16, "every wave has its share of a tile");
+  static_assert(NI >= 1 && 16 % RW == 0 && RW * SB <= 256, "a wave's rows are of one page, their scales a word a lane");
   __shared__ __attribute__((aligned(1024))) uint8_t buf0[KV][TB], buf1[KV][TB], raw[KV][RAW];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t r = wave * Tile::ROWS + Tile::row();   // the lane's row
@@ -48,17 +52,17 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_rows_kernel(DecodeArg
     w.begin();
     w.load_q(a.q + static_cast<int64_t>(sh.b) * a.q_stride + (pc.h0 + min(r, pc.heads - 1)) * D);
 
-    // Instruction x of a wave has rows (wave + x WAVES) RPI .. of the tile.  Its page's number is looked up two turns
-    // ahead.  Rows of a page outside the cache are read from page 0 and made NaN (`lost`); rows past the end are zeros.
+    // A wave brings rows wave * RW .. of a tile.  Rows of a page outside the cache are read from page 0 and made NaN
+    // (`lost`); rows past the end are zeros.
     const uint32_t last = pc.tile0 + pc.tiles;
-    uint32_t page[NI], scale[KV][NI], lost = 0, lost_next = 0;
-    auto first_token = [&](uint32_t tile, int x) { return tile * KT + static_cast<uint32_t>(wave + x * WAVES) * RPI; };
-    auto pages = [&](uint32_t tile) {
-#pragma unroll
-      for (int x = 0; x < NI; ++x) {
-        const uint32_t at = first_token(tile, x);
-        page[x] = tile < last && at < len ? static_cast<uint32_t>(table[at >> a.c.page_shift]) : 0u;
-      }
+    uint32_t page = 0, scale[KV];                         // scale: the rows' scale bytes, four a lane
+    bool lost = false, lost_next = false;
+    auto first_token = [&](uint32_t tile) { return tile * KT + static_cast<uint32_t>(wave) * RW; };
+    // The page's number by a scalar load (nothing writes the table meanwhile), which holds no vector register and does not
+    // wait behind the DMA; past the end, the last token's page again.
+    const auto* numbers = (const __attribute__((address_space(4))) int32_t*)table;
+    auto find_page = [&](uint32_t tile) {
+      page = static_cast<uint32_t>(numbers[__builtin_amdgcn_readfirstlane(min(first_token(tile), len - 1) >> a.c.page_shift)]);
     };
     // The lane's number as the compiler cannot see through: addresses are formed where they are used, and not held in
     // registers that a wide row needs.
@@ -70,64 +74,74 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_rows_kernel(DecodeArg
     auto load = [&](uint32_t tile, uint8_t (&to)[KV][TB]) {
       if (tile >= last) return;
       const uint32_t lane = hidden();
-      lost_next = 0;
+      lost_next = page >= a.c.pages;
+      const uint32_t at = lost_next ? 0u : page;
+      const int64_t row = ((static_cast<int64_t>(at) * a.c.Hkv + pc.kvh) << a.c.page_shift) +
+                          (min(first_token(tile), len - 1) & ((1u << a.c.page_shift) - 1) & ~(RW - 1));
 #pragma unroll
-      for (int x = 0; x < NI; ++x) {
-        if (page[x] >= a.c.pages) {
-          lost_next |= 1u << x;
-          page[x] = 0;
-        }
-        const uint32_t r0 = (wave + x * WAVES) * RPI;
-        const int64_t row = ((static_cast<int64_t>(page[x]) * a.c.Hkv + pc.kvh) << a.c.page_shift) +
-                            (first_token(tile, x) & ((1u << a.c.page_shift) - 1));
+      for (int i = 0; i < KV; ++i) {
+        const uint8_t* from = (i == 0 ? a.c.k : a.c.v) + row * (D * EB);
 #pragma unroll
-        for (int i = 0; i < KV; ++i) {
-          const uint8_t* from = (i == 0 ? a.c.k : a.c.v) + row * (D * EB);
-          if constexpr (FP8) {
-            dma16_at(from + lane * 16, &raw[i][r0 * D]);
-            scale[i][x] = (i == 0 ? a.c.ks : a.c.vs)[(row + lane / CPR) * (D / 32) + lane % CPR / 2];
-          } else {
-            dma16_at(from + lane / CPR * (D * 2) + (swizzled<D>(lane % CPR, r0 + lane / CPR) << 4), &to[i][r0 * D * 2]);
-          }
+        for (int x = 0; x < NI; ++x) {
+          const uint32_t r0 = wave * RW + x * RPI;
+          if constexpr (FP8) dma16_at(from + x * 1024 + lane * 16, &raw[i][r0 * D]);
+          else dma16_at(from + x * 1024 + lane / CPR * (D * 2) + (swizzled<D>(lane % CPR, r0 + lane / CPR) << 4), &to[i][r0 * D * 2]);
         }
+        if constexpr (FP8)
+          scale[i] = *reinterpret_cast<const uint32_t*>((i == 0 ? a.c.ks : a.c.vs) + row * SB + lane * 4 % (RW * SB));
       }
     };
     // The wave's codes, which are there, to BF16.
-    auto convert = [&](uint32_t tile, uint8_t (&to)[KV][TB]) {
-      if (tile >= last) return;
-      const uint32_t lane = hidden();
+    auto convert_rows = [&](auto EDGE, uint32_t tile, uint8_t (&to)[KV][TB]) {
+      const uint32_t lane = hidden(), c = lane % CPR;
 #pragma unroll
-      for (int x = 0; x < NI; ++x) {
-        const uint32_t r = (wave + x * WAVES) * RPI + lane / CPR, c = lane % CPR;   // row of the tile, chunk
-        const bool out = tile * KT + r >= len, nans = (lost >> x) & 1;
-        const uint32_t fill = nans ? 0x7FC07FC0u : 0u;
+      for (int i = 0; i < KV; ++i) {
+        v4u v[NI];
+        uint32_t sc[NI];
 #pragma unroll
-        for (int i = 0; i < KV; ++i) {
-          const v4u v = *reinterpret_cast<const v4u*>(&raw[i][(wave + x * WAVES) * 1024 + lane * 16]);
-          const float sb = __uint_as_float(scale[i][x] << 23);
-          const uint32_t nan = nan_codes(scale[i][x]);
+        for (int x = 0; x < NI; ++x) {
+          const uint32_t byte = (x * RPI + lane / CPR) * SB + c / 2;
+          v[x] = *reinterpret_cast<const v4u*>(&raw[i][(wave * RW + x * RPI) * D + lane * 16]);
+          sc[x] = __shfl(scale[i], byte / 4) >> (8 * (byte & 3)) & 0xFFu;
+        }
+        asm volatile("" ::: "memory");                  // all reads under way before the first is used
+#pragma unroll
+        for (int x = 0; x < NI; ++x) {
+          const uint32_t r = wave * RW + x * RPI + lane / CPR;   // row of the tile
+          const float sb = __uint_as_float(sc[x] << 23);
+          const uint32_t nan = nan_codes(sc[x]);
+          // half of the lanes write their second eight elements first, so that 16 lanes meet all banks
+          const uint32_t turned = (c >> 3) & 1;
+          if (turned) v[x] = v4u{v[x][2], v[x][3], v[x][0], v[x][1]};
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t w0 = v[2 * h] | nan, w1 = v[2 * h + 1] | nan;
+            const uint32_t w0 = v[x][2 * h] | nan, w1 = v[x][2 * h + 1] | nan;
             v4u o = {dequant_pair<false>(w0, sb), dequant_pair<true>(w0, sb), dequant_pair<false>(w1, sb), dequant_pair<true>(w1, sb)};
-            if (out || nans) o = v4u{fill, fill, fill, fill};
-            *reinterpret_cast<v4u*>(&to[i][r * D * 2 + (swizzled<D>(c * 2 + h, r) << 4)]) = o;
+            if constexpr (EDGE) {
+              const uint32_t fill = lost ? 0x7FC07FC0u : 0u;
+              if (lost || tile * KT + r >= len) o = v4u{fill, fill, fill, fill};
+            }
+            *reinterpret_cast<v4u*>(&to[i][r * D * 2 + (swizzled<D>(c * 2 + (h ^ turned), r) << 4)]) = o;
           }
         }
       }
     };
+    auto convert = [&](uint32_t tile, uint8_t (&to)[KV][TB]) {
+      if (tile >= last) return;
+      if (lost || (tile + 1) * KT > len) convert_rows(std::true_type{}, tile, to);
+      else convert_rows(std::false_type{}, tile, to);
+    };
     // The wave's BF16 rows, which are there: those past the end to zeros, those of a lost page to NaN.
     auto mend = [&](uint32_t tile, uint8_t (&at)[KV][TB]) {
-      if (lost == 0 && (tile + 1) * KT <= len) return;
+      if (!lost && (tile + 1) * KT <= len) return;
       const uint32_t lane = hidden();
 #pragma unroll
       for (int x = 0; x < NI; ++x) {
-        const uint32_t r = (wave + x * WAVES) * RPI + lane / CPR;
-        const bool out = tile * KT + r >= len, nans = (lost >> x) & 1;
-        const uint32_t fill = nans ? 0x7FC07FC0u : 0u;
+        const uint32_t r0 = wave * RW + x * RPI;
+        const uint32_t fill = lost ? 0x7FC07FC0u : 0u;
 #pragma unroll
         for (int i = 0; i < KV; ++i)
-          if (out || nans) *reinterpret_cast<v4u*>(&at[i][(wave + x * WAVES) * 1024 + lane * 16]) = v4u{fill, fill, fill, fill};
+          if (lost || tile * KT + r0 + lane / CPR >= len) *reinterpret_cast<v4u*>(&at[i][r0 * D * 2 + lane * 16]) = v4u{fill, fill, fill, fill};
       }
     };
     // What this wave asked for is there.
@@ -136,46 +150,52 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_rows_kernel(DecodeArg
       __builtin_amdgcn_s_waitcnt(wait_vm(0));
       asm volatile("" ::: "memory");
     };
-    auto step = [&](uint32_t tile, uint8_t (&now)[KV][TB], uint8_t (&next)[KV][TB]) {
+    auto step = [&](auto RAGGED, uint32_t tile, uint8_t (&now)[KV][TB], uint8_t (&next)[KV][TB]) {
       landed();
       lost = lost_next;
+      find_page(tile + (FP8 ? 2 : 1));
       if constexpr (!FP8) mend(tile, now);
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // the tile is whole; everyone has read `next`
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(kWaitLgkmOnly);
+      asm volatile("s_barrier" ::: "memory");           // the tile is whole; everyone has read `next`
       if constexpr (FP8) {
         convert(tile + 1, next);
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the codes are read, their place is free
-        load(tile + 2, next);
-        pages(tile + 3);
-      } else {
-        load(tile + 1, next);
-        pages(tile + 2);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(kWaitLgkmOnly);      // the codes are read, their place is free
       }
+      load(tile + (FP8 ? 2 : 1), next);
       if (!active) return;
       typename Tile::Scores s;
       typename Tile::Weights p;
       w.scores(now[0], s);
-      const int32_t seen = static_cast<int32_t>(len - tile * KT);
-      if (seen < KT) w.mask(s, seen);
+      if constexpr (RAGGED) w.mask(s, static_cast<int32_t>(len - tile * KT));
       w.weights(s, a.scale, p);
       w.values(now[KV - 1], p);
     };
 
     uint32_t tile = pc.tile0;
     __syncthreads();                                    // the last piece's tiles have been read
-    pages(tile);
+    find_page(tile);
     load(tile, buf0);
-    pages(tile + 1);
     if constexpr (FP8) {
+      find_page(tile + 1);
       landed();
       lost = lost_next;
       convert(tile, buf0);
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(kWaitLgkmOnly);
       load(tile + 1, buf1);
-      pages(tile + 2);
     }
-    for (; tile < last; tile += 2) {
-      step(tile, buf0, buf1);
-      if (tile + 1 < last) step(tile + 1, buf1, buf0);
+    // Whole tiles two to a turn of the loop, so that each buffer is an object of its own; then what is left, an odd one and
+    // the one with the end.
+    const uint32_t pairs = pc.tile0 + ((last - (last * KT > len ? 1 : 0) - pc.tile0) & ~1u);
+    for (; tile < pairs; tile += 2) {
+      step(std::false_type{}, tile, buf0, buf1);
+      step(std::false_type{}, tile + 1, buf1, buf0);
+    }
+#pragma unroll 1
+    for (; tile < last; ++tile) {
+      const bool second = ((tile - pc.tile0) & 1) != 0;
+      step(std::true_type{}, tile, second ? buf1 : buf0, second ? buf0 : buf1);
     }
 
     float l = w.sum();

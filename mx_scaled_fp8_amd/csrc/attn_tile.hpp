@@ -289,7 +289,8 @@ struct AttnTile {
   }
 };
 
-template <int D, int KT>
+// AHEAD: see read_ahead(); what a kernel has registers for.
+template <int D, int KT, int AHEAD>
 struct AttnTile16 {
   static_assert(D % 256 == 0 && KT == 32, "rows of whole 256 bytes, one operand of weights");
   static constexpr int ROWS = 16, KS = D / 32, DT = D / 16, QUADS = DT;
@@ -333,7 +334,7 @@ struct AttnTile16 {
         const v8bf kf = *reinterpret_cast<const v8bf*>(kt + (kbase ^ (j % 4 << 6)) + u * 16 * D * 2 + (j / 4) * 256);
         x.s[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[j], x.s[u], 0, 0, 0);
       }
-    read_ahead<1, KS * 2, 6>();
+    read_ahead<1, KS * 2, AHEAD>();
   }
 
   __device__ __forceinline__ void mask(Scores& x, int seen) const {
@@ -375,7 +376,7 @@ struct AttnTile16 {
 #pragma unroll
     for (int d = 0; d < DT; ++d)
       acc[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, v_operand(vt, d)), y.p, acc[d], 0, 0, 0);
-    read_ahead<2, DT, 6>();
+    read_ahead<2, DT, AHEAD>();
   }
 
   __device__ __forceinline__ void values_masked(const uint8_t* vt, const Weights& y, int seen) {
@@ -417,10 +418,10 @@ struct AttnTile16 {
 };
 
 // The tile of rows of D, and its keys.
-template <int D>
+template <int D, int AHEAD = 6>
 struct TileOf { using type = AttnTile<D, D <= 128 ? 64 : 32>; };
-template <>
-struct TileOf<512> { using type = AttnTile16<512, 32>; };
+template <int AHEAD>
+struct TileOf<512, AHEAD> { using type = AttnTile16<512, 32, AHEAD>; };
 template <int D>
 constexpr int key_tile() { return D <= 128 ? 64 : 32; }
 
