@@ -19,11 +19,11 @@ constexpr int kMinTokens = 256;        // of a share: its part is up to 128 rows
 
 // Query heads of a workgroup: 32 or 16 for each of four waves, half of what a compute unit runs, so that two workgroups,
 // which know nothing of each other's barriers, fill it.
-constexpr int rows_of(int D) { return D >= 512 ? 64 : 128; }
-constexpr int kThreads = 256;
+constexpr int rows_of(int) { return 128; }
+constexpr int threads_of(int D) { return D >= 512 ? 512 : 256; }
 
 template <int D, bool FP8, bool SAME>
-__global__ __launch_bounds__(kThreads, 2) void attn_decode_rows_kernel(DecodeArgs a) {
+__global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(DecodeArgs a) {
   using Tile = typename TileOf<D, 4>::type;              // (6 ahead: no registers, and the compiler reads none ahead)
   constexpr int ROWS = rows_of(D), WAVES = ROWS / Tile::ROWS, KT = key_tile<D>();
   constexpr int TB = KT * D * 2;                        // bytes of a tile in LDS
@@ -233,12 +233,12 @@ uint32_t head_blocks_of(int32_t G, int32_t D) { return static_cast<uint32_t>((G 
 // Groups: as many as run at once, and no more than there can be tiles.
 uint32_t groups_of(int64_t B, int32_t Hkv, uint32_t head_blocks, int32_t D, int64_t max_tokens) {
   const int64_t kt = D <= 128 ? 64 : 32;
-  return decode_groups(B * Hkv * ((max_tokens + kt - 1) / kt), 512 / head_blocks);
+  return decode_groups(B * Hkv * ((max_tokens + kt - 1) / kt), (D >= 512 ? 256 : 512) / head_blocks);
 }
 
 template <int D, bool FP8>
 void launch(const DecodeArgs& a, hipStream_t stream) {
-  const dim3 grid(a.groups * a.head_blocks), block(kThreads);
+  const dim3 grid(a.groups * a.head_blocks), block(threads_of(D));
   if (D >= 512 || (a.c.k == a.c.v && a.c.ks == a.c.vs)) {
     hipLaunchKernelGGL((attn_decode_rows_kernel<D, FP8, true>), grid, block, 0, stream, a);
   } else if constexpr (D < 512) {
