@@ -1,7 +1,9 @@
 // Causal attention over packed prompts (gfx950).
 //
-// A workgroup takes 128 query rows of one prompt and head (64 in rows of 512 that are keys and values), 32 or 16 for each
-// wave (attn_tile.hpp), and runs over the keys in tiles of KT.  K and V tiles go from global memory to LDS by buffer-load DMA, the next one while this one is
+// The query rows of a prompt and head are its tokens; in prompts of few tokens, the tokens' `pack` heads that share a key
+// head: row f is head f % pack of token f / pack, so that they read the keys once and fill a row tile.  A workgroup
+// takes 128 rows (64 in rows of 512 that are keys and values), 32 or 16 for each wave (attn_tile.hpp), and runs over the
+// keys in tiles of KT.  K and V tiles go from global memory to LDS by buffer-load DMA, the next one while this one is
 // used; rows past the end are zeros by the buffer's bound.  Tiles that every row sees whole run first, two to a turn of
 // the loop, so that each of the two buffers is an object of its own and the compiler waits for no DMA but what a read
 // needs; the last few, which hold the diagonal and the ragged end, go through a loop with masks.
@@ -26,9 +28,10 @@ struct PrefillArgs {
   const int32_t* q_offsets;
   const int32_t* k_offsets;
   uint16_t* out;
-  float* parts;              // [row tile, head, split][O: rows x D, m, l: a row each], FP32
+  float* parts;              // [row tile, pack of heads, split][O: rows x D, m, l: a row each], FP32
   float scale;               // times log2(e)
-  uint32_t B, Tq, Tk, H, Hkv, G;
+  uint32_t B, Tq, Tk, H, Hkv;
+  uint32_t pack, packs;      // heads of a row tile; packs of a key head
   uint32_t tiles;            // bound on the row tiles of all prompts
   uint32_t splits;
 };
@@ -41,19 +44,25 @@ __device__ __forceinline__ uint32_t cut(const int32_t* offsets, uint32_t b, uint
 // A row tile: its prompt's rows and keys, and which of them it has.
 struct RowTile {
   uint32_t q0, k0;           // where the prompt's rows and keys begin
-  int32_t Lq, Lk;
+  int32_t Lq, Lk;            // tokens, keys
+  int32_t rows;              // Lq * pack
   int32_t first;             // row of the prompt
   int32_t keys;              // keys that some row of the tile sees
   bool any;                  // the tile has rows
 };
 
+// Keys that row f of the prompt, or its last row, sees.
+__device__ __forceinline__ int32_t keys_of(const PrefillArgs& a, const RowTile& t, int32_t f) {
+  return max(t.Lk - t.Lq + min(static_cast<int32_t>(static_cast<uint32_t>(f) / a.pack), t.Lq - 1) + 1, 0);
+}
+
 template <int ROWS>
 __device__ __forceinline__ RowTile row_tile(const PrefillArgs& a, uint32_t rt) {
-  // prompt b's row tiles are numbered from offsets[b] / ROWS + b, which leaves room for every ragged end
+  // prompt b's row tiles are numbered from offsets[b] * pack / ROWS + b, which leaves room for every ragged end
   uint32_t lo = 0, hi = a.B;
   while (hi - lo > 1) {
     const uint32_t mid = (lo + hi) >> 1;
-    if (cut(a.q_offsets, mid, a.Tq) / ROWS + mid <= rt) lo = mid; else hi = mid;
+    if (cut(a.q_offsets, mid, a.Tq) * a.pack / ROWS + mid <= rt) lo = mid; else hi = mid;
   }
   RowTile t;
   t.q0 = cut(a.q_offsets, lo, a.Tq);
@@ -61,10 +70,11 @@ __device__ __forceinline__ RowTile row_tile(const PrefillArgs& a, uint32_t rt) {
   const uint32_t q1 = cut(a.q_offsets, lo + 1, a.Tq), k1 = cut(a.k_offsets, lo + 1, a.Tk);
   t.Lq = q1 > t.q0 ? static_cast<int32_t>(q1 - t.q0) : 0;
   t.Lk = k1 > t.k0 ? static_cast<int32_t>(k1 - t.k0) : 0;
-  const uint32_t first = (rt - (t.q0 / ROWS + lo)) * ROWS;
-  t.any = first < static_cast<uint32_t>(t.Lq);
+  const uint32_t first = (rt - (t.q0 * a.pack / ROWS + lo)) * ROWS;
+  t.rows = t.Lq * static_cast<int32_t>(a.pack);
+  t.any = first < static_cast<uint32_t>(t.rows);
   t.first = static_cast<int32_t>(first);
-  t.keys = t.any ? max(min(t.Lk, t.Lk - t.Lq + min(t.first + ROWS, t.Lq)), 0) : 0;
+  t.keys = t.any ? keys_of(a, t, t.first + ROWS - 1) : 0;
   return t;
 }
 
@@ -94,29 +104,42 @@ __global__ __launch_bounds__((threads_of<D, SAME>()), 2) void attn_prefill_kerne
   __shared__ __attribute__((aligned(1024))) uint8_t kbuf0[TB], kbuf1[TB], vbuf0[SAME ? 16 : TB], vbuf1[SAME ? 16 : TB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-  // (row tile, head, split): key heads fastest, so that with workgroups dealt to the XCDs in turn an XCD's L2 serves few
-  // key heads; last row tiles first, which have the most keys.
+  // (row tile, split, pack, key head): key heads fastest, so that with workgroups dealt to the XCDs in turn an XCD's L2
+  // serves few key heads; last row tiles first, which have the most keys.
   uint32_t id = blockIdx.x;
   const uint32_t kvh = id % a.Hkv;
   id /= a.Hkv;
-  const uint32_t head = kvh * a.G + id % a.G;
-  id /= a.G;
+  const uint32_t head0 = (kvh * a.packs + id % a.packs) * a.pack;   // the first of the pack
+  id /= a.packs;
   const uint32_t split = id % a.splits, rt = a.tiles - 1 - id / a.splits;
   const RowTile t = row_tile<ROWS>(a, rt);
   uint32_t used;
   const uint32_t per = split_tiles<D>(t.keys, a.splits, used);
   if (!t.any || split >= used) return;
-  const int32_t hidden = t.Lk - t.Lq;                              // row i sees keys 0 .. hidden + i
-  const int32_t i0 = t.first + wave * Tile::ROWS, i = i0 + Tile::row();            // the wave's first row, the lane's
-  const int32_t w_keys = i0 < t.Lq ? min(t.Lk, hidden + min(i0 + Tile::ROWS, t.Lq)) : 0;   // keys that some row of the wave sees
+  // the wave's first row, and the lane's: its number, token, head and the keys that it sees
+  const int32_t f0 = t.first + wave * Tile::ROWS;
+  struct Row { int32_t f, token; uint32_t head; int32_t sees; };
+  auto lane_row = [&](int32_t in_wave) {
+    Row r;
+    r.f = f0 + in_wave;
+    const int32_t at = min(r.f, t.rows - 1);
+    r.token = static_cast<int32_t>(static_cast<uint32_t>(at) / a.pack);
+    r.head = head0 + (at - r.token * static_cast<int32_t>(a.pack));
+    r.sees = keys_of(a, t, at);
+    return r;
+  };
+  const int32_t w_keys = f0 < t.rows ? keys_of(a, t, f0 + Tile::ROWS - 1) : 0;   // that some row of the wave sees
   const int32_t n_tiles = min((t.keys + KT - 1) / KT, static_cast<int32_t>((split + 1) * per));
   const int32_t begin = split * per;
   // whole tiles: those that the workgroup's first row sees whole; an even number of them
-  const int32_t whole = max(min(n_tiles, (hidden + t.first + 1) / KT) - begin, 0) & ~1;
+  const int32_t whole = max(min(n_tiles, keys_of(a, t, t.first) / KT) - begin, 0) & ~1;
 
   Tile w;
   w.begin();
-  w.load_q(a.q + static_cast<int64_t>(t.q0 + min(i, t.Lq - 1)) * a.q_stride + head * D);
+  {
+    const Row r = lane_row(Tile::row());
+    w.load_q(a.q + static_cast<int64_t>(t.q0 + r.token) * a.q_stride + r.head * D);
+  }
 
   // DMA: an instruction fills 1024 bytes of LDS, RPI rows, in lane order.  The swizzle repeats after 16 rows, so that a
   // wave's PAT instructions of one PERIOD of rows serve all of them.
@@ -167,6 +190,10 @@ __global__ __launch_bounds__((threads_of<D, SAME>()), 2) void attn_prefill_kerne
     step(tile, kbuf0, vbuf0, kbuf1, vbuf1);
     step(tile + 1, kbuf1, vbuf1, kbuf0, vbuf0);
   }
+  // (found again rather than held in registers, of which rows of 512 leave none)
+  int32_t in_wave = Tile::row();
+  asm volatile("" : "+v"(in_wave));
+  const Row row = lane_row(in_wave);
 #pragma unroll 1
   for (; tile < n_tiles; ++tile) {
     const bool second = ((tile - begin) & 1) != 0;
@@ -176,8 +203,7 @@ __global__ __launch_bounds__((threads_of<D, SAME>()), 2) void attn_prefill_kerne
     if (t0 >= w_keys) continue;
     const uint8_t* kt = second ? kbuf1 : kbuf0;
     const uint8_t* vt = SAME ? kt : second ? vbuf1 : vbuf0;
-    const int32_t seen = hidden + i + 1 - t0;           // keys of the tile that the lane's row sees (rows past Lq: more than
-                                                        // there are, zeros; nobody reads their results)
+    const int32_t seen = row.sees - t0;                     // of the tile
     typename Tile::Scores s;
     typename Tile::Weights p;
     w.scores(kt, s);
@@ -188,8 +214,9 @@ __global__ __launch_bounds__((threads_of<D, SAME>()), 2) void attn_prefill_kerne
 
   const float l = w.sum();
   if (used > 1) {
-    float* part = a.parts + (static_cast<size_t>(rt * a.H + head) * a.splits + split) * ROWS * (D + 2);
-    const int r = wave * Tile::ROWS + Tile::row();
+    const size_t unit = static_cast<size_t>(rt) * (a.H / a.pack) + head0 / a.pack;
+    float* part = a.parts + (unit * a.splits + split) * ROWS * (D + 2);
+    const int r = wave * Tile::ROWS + in_wave;
 #pragma unroll
     for (int x = 0; x < Tile::QUADS; ++x) {
       int d;
@@ -202,34 +229,35 @@ __global__ __launch_bounds__((threads_of<D, SAME>()), 2) void attn_prefill_kerne
     }
     return;
   }
-  if (i >= t.Lq) return;
-  const float inv = t.Lk > 0 && hidden + i >= 0 ? 1.0f / l : 0.0f;
-  uint16_t* row = a.out + (static_cast<int64_t>(t.q0 + i) * a.H + head) * D;
+  if (row.f >= t.rows) return;
+  const float inv = row.sees > 0 ? 1.0f / l : 0.0f;
+  uint16_t* to = a.out + (static_cast<int64_t>(t.q0 + row.token) * a.H + row.head) * D;
 #pragma unroll
   for (int x = 0; x < Tile::QUADS; ++x) {
     int d;
     const float4 o = w.quad(x, d);
-    *reinterpret_cast<uint2*>(row + d) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    *reinterpret_cast<uint2*>(to + d) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
   }
 }
 
-// A workgroup takes kJoinRows rows of a row tile and head: the splits' parts joined in their order.
+// A workgroup takes kJoinRows rows of a row tile and pack: the splits' parts joined in their order.
 constexpr int kJoinRows = 16, kJoinThreads = 256;
 template <int D, int ROWS>
 __global__ __launch_bounds__(kJoinThreads) void attn_prefill_join_kernel(PrefillArgs a) {
   uint32_t id = blockIdx.x;
   const uint32_t r0 = id % (ROWS / kJoinRows) * kJoinRows;
   id /= ROWS / kJoinRows;
-  const uint32_t head = id % a.H, rt = id / a.H;
+  const uint32_t heads = a.H / a.pack, pack = id % heads, rt = id / heads;
   const RowTile t = row_tile<ROWS>(a, rt);
   uint32_t used;
   split_tiles<D>(t.keys, a.splits, used);
   if (!t.any || used == 1) return;
-  const float* parts = a.parts + static_cast<size_t>(rt * a.H + head) * a.splits * ROWS * (D + 2);
+  const float* parts = a.parts + (static_cast<size_t>(rt) * heads + pack) * a.splits * ROWS * (D + 2);
   for (uint32_t e = threadIdx.x * 4; e < kJoinRows * D; e += kJoinThreads * 4) {
     const uint32_t r = r0 + e / D, d = e % D;
-    const int32_t i = t.first + static_cast<int32_t>(r);
-    if (i >= t.Lq) break;
+    const int32_t f = t.first + static_cast<int32_t>(r);
+    if (f >= t.rows) break;
+    const uint32_t i = static_cast<uint32_t>(f) / a.pack, head = pack * a.pack + (f - i * a.pack);
     float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (uint32_t s = 0; s < used; ++s) {
@@ -241,7 +269,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_prefill_join_kernel(Prefill
       o = make_float4(o.x * f + v.x * g, o.y * f + v.y * g, o.z * f + v.z * g, o.w * f + v.w * g);
       m = top;
     }
-    const float inv = t.Lk - t.Lq + i >= 0 ? 1.0f / l : 0.0f;
+    const float inv = keys_of(a, t, f) > 0 ? 1.0f / l : 0.0f;
     *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(t.q0 + i) * a.H + head) * D + d) =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
   }
@@ -252,28 +280,40 @@ bool same(const void* k, int64_t k_stride, const void* v, int64_t v_stride) { re
 // Query rows of a workgroup (rows_of, of a call).
 int rows_of_call(int32_t D, bool latent) { return D >= 512 && latent ? 64 : 128; }
 
-uint32_t row_tiles(int64_t B, int64_t Tq, int rows) { return static_cast<uint32_t>(Tq / rows + B); }
+// Heads of a row tile: those that share a key head where an average prompt has fewer tokens than a row tile has rows.  (7
+// rows of 4 prompts over 30000 tokens, 4 heads a key head: 147 us with, 263 without.  With full row tiles of their own the
+// heads were as fast or faster: 8192 rows 534 and 529 us, latent rows of 512 314 and 283.)
+int32_t pack_of(int64_t B, int64_t Tq, int32_t H, int32_t Hkv, int rows) { return Tq / B < rows ? H / Hkv : 1; }
 
-// How many workgroups share the keys of one row tile and head.  512 run at once; up to twice as many, as long as every
-// part has some tiles of keys, keep them busy and let those that run together read the same keys.  (4096 rows over 30011
-// earlier tokens, 8 heads: 613 us with no split of its 256 pairs, 671 with 2, 528 with 4, 540 with 8, 593 with 16.)
-uint32_t split_count(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int rows) {
-  const int64_t units = static_cast<int64_t>(row_tiles(B, Tq, rows)) * H, slots = 1024;
+// Bound on the row tiles of all prompts.
+uint32_t row_tiles(int64_t B, int64_t Tq, int32_t pack, int rows) { return static_cast<uint32_t>(Tq * pack / rows + B); }
+
+// How many workgroups share the keys of one row tile and pack.  512 run at once; up to twice as many, as long as every part
+// has some tiles of keys, keep them busy and let those that run together read the same keys.  (4096 rows over 30011 earlier
+// tokens, 8 heads: 613 us with no split of its 256 pairs, 671 with 2, 528 with 4, 540 with 8, 593 with 16.)
+uint32_t split_count(int64_t B, int64_t Tk, int64_t units) {
   const int64_t tiles = (Tk / B + 63) / 64;             // of an average prompt
-  return static_cast<uint32_t>(std::max<int64_t>(1, std::min(slots / units, tiles / kMinTiles)));
+  return static_cast<uint32_t>(std::max<int64_t>(1, std::min(1024 / units, tiles / kMinTiles)));
 }
 
-size_t part_bytes(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t D, int rows) {
-  const size_t splits = split_count(B, Tq, Tk, H, rows);
-  return splits == 1 ? 0 : splits * row_tiles(B, Tq, rows) * H * rows * (D + 2) * 4;
+// (row tile, pack) pairs.
+int64_t units_of(int64_t B, int64_t Tq, int32_t H, int32_t Hkv, int rows) {
+  const int32_t pack = pack_of(B, Tq, H, Hkv, rows);
+  return static_cast<int64_t>(row_tiles(B, Tq, pack, rows)) * (H / pack);
+}
+
+size_t part_bytes(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t Hkv, int32_t D, int rows) {
+  const size_t units = units_of(B, Tq, H, Hkv, rows), splits = split_count(B, Tk, units);
+  return splits == 1 ? 0 : splits * units * rows * (D + 2) * 4;
 }
 
 template <int D, bool SAME>
 void launch(const PrefillArgs& a, hipStream_t stream) {
   constexpr int ROWS = rows_of<D, SAME>();
-  hipLaunchKernelGGL((attn_prefill_kernel<D, SAME>), dim3(a.tiles * a.H * a.splits), dim3(threads_of<D, SAME>()), 0, stream, a);
+  const uint32_t units = a.tiles * (a.H / a.pack);
+  hipLaunchKernelGGL((attn_prefill_kernel<D, SAME>), dim3(units * a.splits), dim3(threads_of<D, SAME>()), 0, stream, a);
   if (a.splits > 1)
-    hipLaunchKernelGGL((attn_prefill_join_kernel<D, ROWS>), dim3(a.tiles * a.H * (ROWS / kJoinRows)), dim3(kJoinThreads), 0, stream, a);
+    hipLaunchKernelGGL((attn_prefill_join_kernel<D, ROWS>), dim3(units * (ROWS / kJoinRows)), dim3(kJoinThreads), 0, stream, a);
 }
 
 template <int D>
@@ -285,8 +325,9 @@ void launch(const PrefillArgs& a, bool latent, hipStream_t stream) {
 }  // namespace
 
 // Of either kind of call: the sizes do not say whether v is k.
-size_t prefill_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t, int32_t D) {
-  return std::max(part_bytes(B, Tq, Tk, H, D, rows_of_call(D, false)), part_bytes(B, Tq, Tk, H, D, rows_of_call(D, true)));
+size_t prefill_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t Hkv, int32_t D) {
+  return std::max(part_bytes(B, Tq, Tk, H, Hkv, D, rows_of_call(D, false)),
+                  part_bytes(B, Tq, Tk, H, Hkv, D, rows_of_call(D, true)));
 }
 
 mx_status launch_attn_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
@@ -312,9 +353,10 @@ mx_status launch_attn_prefill(const void* q, int64_t q_stride, const void* k, in
   a.Tk = static_cast<uint32_t>(Tk);
   a.H = static_cast<uint32_t>(H);
   a.Hkv = static_cast<uint32_t>(Hkv);
-  a.G = a.H / a.Hkv;
-  a.tiles = row_tiles(B, Tq, rows);
-  a.splits = split_count(B, Tq, Tk, H, rows);
+  a.pack = static_cast<uint32_t>(pack_of(B, Tq, H, Hkv, rows));
+  a.packs = a.H / a.Hkv / a.pack;
+  a.tiles = row_tiles(B, Tq, static_cast<int32_t>(a.pack), rows);
+  a.splits = split_count(B, Tk, units_of(B, Tq, H, Hkv, rows));
   switch (D) {
     case 64: launch<64>(a, latent, stream); break;
     case 128: launch<128>(a, latent, stream); break;
