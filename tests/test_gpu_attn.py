@@ -204,3 +204,338 @@ def test_prefill(lens, past, Hkv, G, D):
 @pytest.mark.parametrize("D", [128, 512])
 def test_prefill_latent(D):
     _prefill(np.random.default_rng(D), [90, 200], [0, 33], 1, 16, D, same=True, scale=0.07)
+
+
+# ------------------------------------------- values that hide, and do not
+
+def _poison_behind(c, table, lens, fp8):
+    """NaN, Inf and the largest values in every cache row that no sequence owns."""
+    pages, Hkv, page, D = c["k"].shape
+    owned = np.zeros((pages, page), bool)
+    for b, n in enumerate(lens):
+        for i in range(n):
+            owned[table[b, i // page], i % page] = True
+    where = np.broadcast_to(~owned[:, None, :], (pages, Hkv, page))
+    for name in ("k", "v"):
+        if c[name] is None:
+            continue
+        if fp8:
+            c[name][where] = 0x7F
+            c[name + "s"][where] = 0xFF
+        else:
+            c[name][where] = np.resize(np.array([0x7FC0, 0x7F80, 0xFF80, 0x7F7F], np.uint16), D)
+
+
+@pytest.mark.parametrize("Hkv,G,D,page,latent", [(2, 4, 128, 16, False), (2, 3, 64, 64, False), (1, 5, 512, 16, False), (1, 2, 256, 32, True),
+                                                 (1, 64, 512, 64, True), (1, 40, 128, 16, False), (1, 33, 256, 64, True), (2, 32, 64, 16, False)])
+@KINDS
+def test_decode_ignores_what_lies_behind_the_end(Hkv, G, D, page, latent, fp8):
+    rng = np.random.default_rng(G)
+    lens = [1, 15, 33, 70, 0, 129, 600]
+    c, table = make_cache(rng, lens, Hkv, D, page, fp8, latent)
+    _poison_behind(c, table, lens, fp8)
+    q = normal(rng, len(lens), Hkv * G, D)
+    say("decode behind the end", Hkv, G, D, page, latent, fp8)
+    out = mx.mx_attn_decode(on_gpu(q), on_gpu(c["k"]), on_gpu(c["v"]), _i32(table), _i32(lens), k_scale=on_gpu(c["ks"]),
+                            v_scale=on_gpu(c["vs"]))
+    torch.cuda.synchronize()
+    check(host_u16(out), *decode_oracle(q, c, table, lens, D ** -0.5), D, max(lens))
+
+
+@pytest.mark.parametrize("Hkv,G,D,latent", [(2, 4, 128, False), (1, 64, 512, True), (1, 40, 128, False), (1, 3, 512, False)])
+@KINDS
+def test_decode_bad_pages_and_lengths(Hkv, G, D, latent, fp8):
+    """A sequence with a page outside the cache or longer than its table has NaN outputs, its neighbours are untouched."""
+    rng = np.random.default_rng(G)
+    lens = [700, 300, 90, 40, 512]
+    c, table = make_cache(rng, lens, Hkv, D, 32, fp8, latent)
+    q = normal(rng, len(lens), Hkv * G, D)
+    table[1, 5], table[3, 1] = c["k"].shape[0], -3
+    say("decode bad pages", Hkv, G, D, latent, fp8)
+    asked = [700, 300, 90, 40, table.shape[1] * 32 + 1]
+    out = mx.mx_attn_decode(on_gpu(q), on_gpu(c["k"]), on_gpu(c["v"]), _i32(table), _i32(asked), k_scale=on_gpu(c["ks"]),
+                            v_scale=on_gpu(c["vs"]))
+    torch.cuda.synchronize()
+    got = host_u16(out)
+    assert np.isnan(F.bf16_to_f64(got[[1, 3, 4]])).all()
+    ref = [x[[0, 2]] for x in decode_oracle(q, c, table, lens, D ** -0.5)]
+    check(got[[0, 2]], *ref, D, 700)
+
+
+@pytest.mark.parametrize("G,D,latent", [(4, 128, False), (64, 512, True), (2, 512, False)])
+@KINDS
+def test_decode_values_that_are_not_finite_count(G, D, latent, fp8):
+    """A NaN or Inf that a sequence does see reaches its outputs, and no other sequence's."""
+    rng = np.random.default_rng(G)
+    lens = [100, 100, 40]
+    c, table = make_cache(rng, lens, 1, D, 16, fp8, latent)
+    name = "k" if latent else "v"
+    if fp8:
+        c[name + "s"][table[1, 2], 0, 3, 1] = 0xFF                  # token 35, elements 32..63
+    else:
+        c[name][table[1, 2], 0, 3, 40] = 0x7F80 if not latent else 0x7FC0
+    q = normal(rng, 3, G, D)
+    say("decode not finite", G, D, latent, fp8)
+    out = mx.mx_attn_decode(on_gpu(q), on_gpu(c["k"]), on_gpu(c["v"]), _i32(table), _i32(lens), k_scale=on_gpu(c["ks"]),
+                            v_scale=on_gpu(c["vs"]))
+    torch.cuda.synchronize()
+    ref = decode_oracle(q, c, table, lens, D ** -0.5)
+    assert not np.isfinite(ref[0][1]).all() and np.isfinite(ref[0][[0, 2]]).all()
+    check(host_u16(out), *ref, D, 100)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+@pytest.mark.parametrize("same", [False, True])
+@pytest.mark.parametrize("G", [1, 4])
+def test_prefill_keys_and_values_that_a_row_does_not_see(D, same, G):
+    """NaN and infinities in keys and values reach the rows that see them, each as itself, and no other row."""
+    rng = np.random.default_rng(D + G)
+    Lq = 150
+    q, k = normal(rng, Lq, G, D), normal(rng, Lq, 1, D)
+    v = k if same else normal(rng, Lq, 1, D)
+    v[140, 0, 3] = 0x7FC0
+    if not same:
+        v[60, 0, :40] = 0x7F80                       # +Inf
+        v[61, 0, 5] = 0xFF80                         # -Inf, seen from row 61 on: with +Inf, NaN
+        v[97, 0, D - 1] = 0xFF80
+        k[120] = 0x7F80                              # scores of +-Inf or NaN
+    say("prefill not finite", D, same, G)
+    dk = on_gpu(k)
+    out = mx.mx_attn_prefill(on_gpu(q), dk, dk if same else on_gpu(v), _i32([0, Lq]), _i32([0, Lq]))
+    torch.cuda.synchronize()
+    f = F.bf16_to_f64
+    ref = A.attend(f(q), f(k), f(v), D ** -0.5)
+    assert np.isfinite(ref[0][:60]).all() and np.isnan(ref[0][140:]).any()
+    check(host_u16(out), *ref, D, Lq)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+def test_prefill_scores_that_grow(D):
+    """Maxima that move in steps above and below what lets the weights stand, and scores far apart."""
+    Lk = 400
+    q = np.zeros((Lk, 1, D), np.float32)
+    k = np.zeros((Lk, 1, D), np.float32)
+    q[:, 0, 0] = 1
+    steps = np.concatenate([np.arange(100) * 0.9, 90 + np.arange(100) * 7.0, 790 - np.arange(100) * 11.0, np.full(100, -300.0)])
+    k[:, 0, 0] = steps
+    v = np.random.default_rng(D).standard_normal((Lk, 1, D)).astype(np.float32)
+    q, k, v = (workloads.to_bf16_bits(x) for x in (q, k, v))
+    say("prefill growing scores", D)
+    out = mx.mx_attn_prefill(on_gpu(q), on_gpu(k), on_gpu(v), _i32([0, Lk]), _i32([0, Lk]), scale=1.0)
+    c = {"k": k.reshape(25, 1, 16, D), "v": v.reshape(25, 1, 16, D), "ks": None, "vs": None}
+    table = np.arange(25, dtype=np.int32)[None]
+    dec = mx.mx_attn_decode(on_gpu(q[:1]), on_gpu(c["k"]), on_gpu(c["v"]), _i32(table), _i32([Lk]), scale=1.0)
+    torch.cuda.synchronize()
+    f = F.bf16_to_f64
+    ref = A.attend(f(q), f(k), f(v), 1.0)
+    check(host_u16(out), *ref, D, Lk)
+    check(host_u16(dec), *decode_oracle(q[:1], c, table, [Lk], 1.0), D, Lk)
+
+
+# ------------------------------------ strides, rows left alone, repetition
+
+@pytest.mark.parametrize("D", [64, 512])
+def test_strided_rows_and_rows_that_no_prompt_owns(D):
+    """q, k and v as slices of one fused projection; rows before the first and behind the last prompt stay as they were."""
+    rng = np.random.default_rng(D)
+    H, Hkv, before, lens, behind = 4, 2, 5, [33, 0, 140], 9
+    T = before + sum(lens) + behind
+    fused = normal(rng, T, H + 2 * Hkv + 1, D)
+    offsets = before + np.concatenate([[0], np.cumsum(lens)])
+    d = on_gpu(fused)
+    out = on_gpu(np.full((T, H, D), 0x1234, np.uint16))
+    say("prefill strided", D)
+    mx.mx_attn_prefill(d[:, :H], d[:, H:H + Hkv], d[:, H + Hkv:H + 2 * Hkv], _i32(offsets), _i32(offsets), out=out)
+    torch.cuda.synchronize()
+    got, f = host_u16(out), F.bf16_to_f64(fused)
+    assert np.all(got[:before] == 0x1234) and np.all(got[T - behind:] == 0x1234)
+    for b in range(len(lens)):
+        x = slice(offsets[b], offsets[b + 1])
+        if lens[b]:
+            check(got[x], *A.attend(f[x, :H], f[x, H:H + Hkv], f[x, H + Hkv:H + 2 * Hkv], D ** -0.5), D, lens[b])
+
+
+@KINDS
+def test_decode_strided_queries_and_given_output(fp8):
+    rng = np.random.default_rng(1)
+    lens, Hkv, G, D = [200, 3], 2, 4, 128
+    c, table = make_cache(rng, lens, Hkv, D, 16, fp8)
+    fused = normal(rng, 2, 3 * Hkv * G, D)
+    out = torch.zeros((2, Hkv * G * D), dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((mx.mx_attn_decode_workspace_bytes(2, Hkv * G, Hkv, D, table.shape[1], 16),), 0xFF, dtype=torch.uint8, device="cuda")
+    say("decode strided", fp8)
+    got = mx.mx_attn_decode(on_gpu(fused)[:, 4:4 + Hkv * G], on_gpu(c["k"]), on_gpu(c["v"]), _i32(table), _i32(lens),
+                            k_scale=on_gpu(c["ks"]), v_scale=on_gpu(c["vs"]), out=out, workspace=ws)
+    torch.cuda.synchronize()
+    assert got is out
+    ref = decode_oracle(fused[:, 4:4 + Hkv * G], c, table, lens, D ** -0.5)
+    check(host_u16(out).reshape(2, Hkv * G, D), *ref, D, 200)
+
+
+def _chain(rng, fp8):
+    lens, Hkv, G, D = [900, 1500, 64], 2, 8, 128
+    c, table = make_cache(rng, lens, Hkv, D, 64, fp8)
+    q = on_gpu(normal(rng, 3, Hkv * G, D)).view(torch.bfloat16)
+    return [q] + [on_gpu(c[n]) for n in ("k", "v", "ks", "vs")] + [_i32(table), _i32(lens)]
+
+
+@KINDS
+def test_repetition_other_streams_and_stale_workspaces(fp8):
+    """The same call gives the same bits whatever the workspace held, on any stream, two at once."""
+    q, k, v, ks, vs, table, lens = _chain(np.random.default_rng(2), fp8)
+    call = lambda **kw: mx.mx_attn_decode(q, k, v, table, lens, k_scale=ks, v_scale=vs, **kw)  # noqa: E731
+    need = mx.mx_attn_decode_workspace_bytes(3, 16, 2, 128, table.shape[1], 64)
+    say("decode repeated", fp8)
+    first = call()
+    dirty = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            outs += [call(workspace=dirty.clone()) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(first.view(torch.int16), o.view(torch.int16)) for o in outs)
+    rows = 700
+    x = on_gpu(normal(np.random.default_rng(3), rows, 16, 128))
+    kk = on_gpu(normal(np.random.default_rng(4), 9000, 2, 128))
+    qo, ko = _i32([0, rows]), _i32([0, 9000])
+    a = mx.mx_attn_prefill(x, kk, kk.clone(), qo, ko)
+    w = torch.full((max(1, mx.mx_attn_prefill_workspace_bytes(1, rows, 9000, 16, 2, 128)),), 0xFF, dtype=torch.uint8, device="cuda")
+    b = mx.mx_attn_prefill(x, kk, kk.clone(), qo, ko, workspace=w)
+    torch.cuda.synchronize()
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@KINDS
+def test_graph_step_by_step(fp8):
+    """A decode step (write the new token, attend) and a prompt captured once and replayed with other contents: every
+    replay equals the eager calls."""
+    rng = np.random.default_rng(5)
+    B, Hkv, G, D, page = 3, 2, 4, 128, 16
+    c, table = make_cache(rng, [200] * B, Hkv, D, page, fp8)
+    k, v, ks, vs = (on_gpu(c[n]) for n in ("k", "v", "ks", "vs"))
+    table_d, lens, slots = _i32(table), _i32([5, 60, 130]), dev_i64([0] * B)
+    rows = on_gpu(normal(rng, B, (G + 2) * Hkv, D))
+    prompt = on_gpu(normal(rng, 90, Hkv * G, D))
+    keys = on_gpu(normal(rng, 4000, Hkv, D))
+    qo, ko = _i32([0, 30, 90]), _i32([0, 3000, 4000])
+
+    def step():
+        mx.mx_kv_cache_write(rows[:, G * Hkv:(G + 1) * Hkv], rows[:, (G + 1) * Hkv:], slots, k, v, k_scale=ks, v_scale=vs)
+        return (mx.mx_attn_decode(rows[:, :G * Hkv], k, v, table_d, lens, k_scale=ks, v_scale=vs),
+                mx.mx_attn_prefill(prompt, keys, keys, qo, ko))
+
+    say("graph", fp8)
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = step()
+    for n in range(4):
+        at = [5 + n, 60 + 3 * n, 130 + n]
+        lens.copy_(_i32([x + 1 for x in at]))
+        slots.copy_(dev_i64([int(table[b, at[b] // page]) * page + at[b] % page for b in range(B)]))
+        rows.copy_(on_gpu(normal(rng, B, (G + 2) * Hkv, D)))
+        prompt.copy_(on_gpu(normal(rng, 90, Hkv * G, D)))
+        ko.copy_(_i32([0, 2000 + 17 * n, 4000 - n]))
+        g.replay()
+        torch.cuda.synchronize()
+        got = [h.clone() for h in held]
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(got, want)), n
+
+
+# ------------------------------------------------------------- used together
+
+def test_prompt_in_chunks_then_tokens_then_the_output_projection():
+    """A prompt in two chunks through an MXFP8 cache: write, read back, attend; then new tokens; then the inverse rotation
+    and quantisation of the output projection.  Each step against the oracle on what the cache then holds."""
+    rng = np.random.default_rng(6)
+    H, Hkv, D, page, first, second = 8, 2, 128, 16, 70, 50
+    n = first + second
+    pages = 12
+    k, v = (torch.zeros((pages, Hkv, page, D), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros((pages, Hkv, page, D // 32), dtype=torch.uint8, device="cuda") for _ in range(2))
+    table = rng.permutation(pages)[None, :9].astype(np.int32)
+    slot = lambda i: int(table[0, i // page]) * page + i % page  # noqa: E731
+    f = F.bf16_to_f64
+    host = lambda: {"k": host_u8(k), "v": host_u8(v), "ks": host_u8(ks), "vs": host_u8(vs)}  # noqa: E731
+    say("chunks")
+    for begin, end in ((0, first), (first, n)):
+        rows = normal(rng, end - begin, H + 2 * Hkv, D)
+        d = on_gpu(rows)
+        mx.mx_kv_cache_write(d[:, H:H + Hkv], d[:, H + Hkv:], dev_i64([slot(i) for i in range(begin, end)]), k, v, k_scale=ks, v_scale=vs)
+        kk, vv = mx.mx_kv_cache_read(k, v, _i32(table), _i32([0, end]), end, k_scale=ks, v_scale=vs)
+        out = mx.mx_attn_prefill(d[:, :H], kk, vv, _i32([0, end - begin]), _i32([0, end]))
+        torch.cuda.synchronize()
+        c = host()
+        ref = A.attend(f(rows[:, :H]), A.sequence(c["k"], c["ks"], table[0], end), A.sequence(c["v"], c["vs"], table[0], end), D ** -0.5)
+        check(host_u16(out), *ref, D, end, "chunk")
+    for i in range(n, n + 3):
+        rows = normal(rng, 1, H + 2 * Hkv, D)
+        d = on_gpu(rows)
+        mx.mx_kv_cache_write(d[:, H:H + Hkv], d[:, H + Hkv:], dev_i64([slot(i)]), k, v, k_scale=ks, v_scale=vs)
+        out = mx.mx_attn_decode(d[:, :H], k, v, _i32(table), _i32([i + 1]), k_scale=ks, v_scale=vs)
+        torch.cuda.synchronize()
+        check(host_u16(out), *decode_oracle(rows[:, :H], host(), table, [i + 1], D ** -0.5), D, i + 1, "token")
+    cos, sin = workloads.rope_tables(rows=256)
+    q, s = mx.mx_inv_rope_group_quant(out.view(1, H * D), dev_i64([n + 2]), on_gpu(cos), on_gpu(sin), H, D, 64)
+    torch.cuda.synchronize()
+    from oracle.quant import inv_rope_group_quant
+    rq, rs = inv_rope_group_quant(host_u16(out).reshape(1, H * D), np.array([n + 2]), cos, sin, H, D, 64)
+    assert np.array_equal(host_u8(s), rs) and (host_u8(q) != rq).sum() <= 1
+
+
+# ------------------------------------------------------- behind 32-bit offsets
+
+@KINDS
+def test_pages_behind_4_gb(fp8):
+    """A cache of more than 2^32 bytes whose sequences are in its last pages (and its first)."""
+    rng = np.random.default_rng(7)
+    Hkv, G, D, page = 8, 2, 128, 64
+    per_page = Hkv * page * D * (1 if fp8 else 2)
+    pages = (9 << 30) // 2 // per_page
+    dtype = torch.uint8 if fp8 else torch.bfloat16
+    k = torch.empty((pages, Hkv, page, D), dtype=dtype, device="cuda")
+    v = torch.empty((pages, Hkv, page, D), dtype=dtype, device="cuda")
+    ks, vs = (torch.empty((pages, Hkv, page, D // 32), dtype=torch.uint8, device="cuda") if fp8 else None for _ in range(2))
+    lens = [100, 300]
+    table = np.array([[pages - 1, 0, 0, 0, 0], [pages - 2, 1, pages - 7, pages // 2, pages - 3]], np.int32)
+    rows = normal(rng, sum(lens), (2 + G) * Hkv, D)
+    d = on_gpu(rows).view(torch.bfloat16)
+    slots = [int(table[b, i // page]) * page + i % page for b, n in enumerate(lens) for i in range(n)]
+    say("behind 4 GB", fp8)
+    mx.mx_kv_cache_write(d[:, :Hkv], d[:, Hkv:2 * Hkv], dev_i64(slots), k, v, k_scale=ks, v_scale=vs)
+    q = d[:2, 2 * Hkv:]
+    out = mx.mx_attn_decode(q, k, v, _i32(table), _i32(lens), k_scale=ks, v_scale=vs)
+    offsets = [0, 100, 400]
+    kk, vv = mx.mx_kv_cache_read(k, v, _i32(table), _i32(offsets), 400, k_scale=ks, v_scale=vs)
+    torch.cuda.synchronize()
+    kh, vh = F.bf16_to_f64(host_u16(kk)), F.bf16_to_f64(host_u16(vv))
+    if not fp8:
+        assert np.array_equal(host_u16(kk), rows[:, :Hkv]) and np.array_equal(host_u16(vv), rows[:, Hkv:2 * Hkv])
+    else:
+        codes, sc = A.group_quant(rows[:, :Hkv].reshape(-1, D), 32, F.OCP)
+        assert np.array_equal(kh, A.values(codes, sc).reshape(400, Hkv, D))
+    qh = F.bf16_to_f64(rows[:2, 2 * Hkv:])
+    parts = [A.attend(qh[b:b + 1], kh[offsets[b]:offsets[b + 1]], vh[offsets[b]:offsets[b + 1]], D ** -0.5) for b in range(2)]
+    check(host_u16(out), *(np.concatenate([p[i] for p in parts]) for i in range(3)), D, 300)
+
+
+def test_prompt_rows_behind_4_gb():
+    """q, k, v and out rows whose offsets pass 2^32 bytes."""
+    rng = np.random.default_rng(8)
+    D, Hkv, H, T = 128, 2, 4, 600000
+    k = torch.zeros((T, 16, Hkv, D), dtype=torch.bfloat16, device="cuda")[:, 3]       # rows 8 KiB apart
+    q = torch.zeros((T, 8, H, D), dtype=torch.bfloat16, device="cuda")[:, 5]
+    n = 200
+    rows, keys = normal(rng, n, H, D), normal(rng, n, Hkv, D)
+    q[T - n:], k[T - n:] = on_gpu(rows).view(torch.bfloat16), on_gpu(keys).view(torch.bfloat16)
+    offsets = _i32([T - n, T])
+    say("prompt behind 4 GB")
+    out = mx.mx_attn_prefill(q, k, k, offsets, offsets)
+    torch.cuda.synchronize()
+    f = F.bf16_to_f64
+    check(host_u16(out[T - n:]), *A.attend(f(rows), f(keys), f(keys), D ** -0.5), D, n)
