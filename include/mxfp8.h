@@ -504,8 +504,8 @@ mx_status mx_moe_combine(const void* y, int64_t rows, int64_t N, const int32_t* 
  * NaN/Inf gets scale 0xFF and NaN codes.  (The MXFP8 quantiser of mx_linear.)
  * Requires: T >= 0 (0 is a no-op), Hkv >= 1, D % 32 == 0, 32 <= D <= 1024,
  * Hkv * D <= 2^20, T * Hkv * D < 2^34, strides >= Hkv * D and multiples of 8 (below 2^31), pages
- * >= 1 and < 2^31, k, v and the caches 16-byte, slots 8-byte aligned; caches and scales
- * overlap neither each other nor k, v and slots.
+ * >= 1 and < 2^31, pages * page_size * Hkv * D < 2^46, k, v, the caches and scales 16-byte, slots 8-byte aligned;
+ * caches and scales overlap neither each other nor k, v and slots.
  */
 mx_status mx_kv_cache_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                             int64_t T, int32_t Hkv, int32_t D, const int64_t* slots, int32_t kind,
@@ -542,7 +542,7 @@ mx_status mx_kv_cache_read(int32_t kind, const void* k_cache, const uint8_t* k_s
  * q         device BF16 [B, H, D], sequence b at b * q_stride elements.
  * lens      device int32 [B].  lens[b] <= 0: out[b] is 0.  A sequence that is
  *           longer than its table (lens[b] > max_pages * page_size), or with a
- *           page outside [0, pages), has NaN outputs; the cache is not read there.
+ *           page outside [0, pages), has NaN outputs; nothing outside the cache is read.
  * scale     finite and > 0 (1 / sqrt(D) as a rule).
  * out       device BF16 [B, H, D], FP32 scores, statistics and sums; probabilities
  *           are rounded to BF16 for the second product.  The result does not depend
@@ -552,7 +552,7 @@ mx_status mx_kv_cache_read(int32_t kind, const void* k_cache, const uint8_t* k_s
  *           page_size), 16-byte aligned: parts of long sequences, written before
  *           they are read.  Calls that may overlap need one each.
  * Requires: B >= 0 (0 is a no-op), B < 2^24, D 64, 128, 256 or 512, Hkv >= 1, H % Hkv == 0, H <= 2^16,
- * max_pages >= 1, max_pages * page_size < 2^31, pages >= 1 and < 2^31,
+ * max_pages >= 1, max_pages * page_size < 2^31, the cache's sizes as for mx_kv_cache_write,
  * B * H < 2^24, B * Hkv * ceil(H / Hkv / 16) times ceil(max_pages * page_size / 32)
  * < 2^31, q_stride >= H * D and a multiple of 8, q, caches and out 16-byte, scales 16-byte,
  * block_table and lens 4-byte aligned; out and the workspace overlap no input

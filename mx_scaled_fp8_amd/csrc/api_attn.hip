@@ -57,6 +57,7 @@ mx_status check_cache(const char* fn, int32_t kind, const void* k, const void* k
   MX_CHECK(pages >= 1 && pages < k31, "%s: pages = %lld out of range", fn, (long long)pages);
   MX_CHECK(Hkv >= 1 && D >= 32 && D <= 1024 && D % MX_CACHE_BLOCK == 0 && int64_t(Hkv) * D <= (int64_t(1) << 20),
            "%s: Hkv = %d, D = %d (D a multiple of %d up to 1024, Hkv * D up to 2^20)", fn, Hkv, D, MX_CACHE_BLOCK);
+  MX_CHECK(pages * page_size * Hkv * D < (int64_t(1) << 46), "%s: %lld pages too large", fn, (long long)pages);
   MX_CHECK(k, "%s: null k_cache", fn);
   MX_CHECK(aligned(k, 16) && aligned(v, 16) && aligned(ks, 16) && aligned(vs, 16),
            "%s: caches and scales must be 16-byte aligned", fn);
@@ -176,7 +177,9 @@ mx_status mx_kv_cache_read(int32_t kind, const void* k_cache, const uint8_t* k_s
 
 size_t mx_attn_decode_workspace_bytes(int64_t B, int32_t H, int32_t Hkv, int32_t D, int64_t max_pages,
                                       int32_t page_size) {
-  if (B <= 0 || Hkv <= 0 || H < Hkv || D <= 0 || max_pages <= 0 || page_size <= 0) return 0;
+  if (B <= 0 || B >= (int64_t(1) << 24) || Hkv <= 0 || H < Hkv || H > 65536 || D <= 0 || D > 1024 || max_pages <= 0 ||
+      max_pages >= k31 || page_size <= 0 || page_size > MX_CACHE_MAX_PAGE || max_pages * page_size >= k31)
+    return 0;                                          // sizes that a call refuses
   return decode_workspace_bytes(B, H, Hkv, D, max_pages * page_size);
 }
 
@@ -224,7 +227,9 @@ mx_status mx_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t H, 
 }
 
 size_t mx_attn_prefill_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t Hkv, int32_t D) {
-  if (B <= 0 || Tq <= 0 || Tk < 0 || Hkv <= 0 || H < Hkv || D <= 0) return 0;
+  if (B <= 0 || B >= (int64_t(1) << 24) || Tq <= 0 || Tq >= k31 || Tk < 0 || Tk >= k31 || Hkv <= 0 || H < Hkv ||
+      H > 65536 || D <= 0 || D > 1024)
+    return 0;
   return prefill_workspace_bytes(B, Tq, Tk, H, Hkv, D);
 }
 

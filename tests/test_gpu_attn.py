@@ -539,3 +539,81 @@ def test_prompt_rows_behind_4_gb():
     torch.cuda.synchronize()
     f = F.bf16_to_f64
     check(host_u16(out[T - n:]), *A.attend(f(rows), f(keys), f(keys), D ** -0.5), D, n)
+
+
+# ------------------------------------------------- refusals of the binding
+
+def _z(*shape, dtype=torch.uint8):
+    return torch.zeros(shape, dtype=dtype, device="cuda")
+
+
+def _raises(match, f, *a, **kw):
+    with pytest.raises((ValueError, TypeError, mx.MxError), match=match):
+        f(*a, **kw)
+
+
+def test_binding_refusals():
+    bf, i32, i64 = torch.bfloat16, torch.int32, torch.int64
+    kc, sc, kb = _z(4, 2, 16, 64), _z(4, 2, 16, 2), _z(4, 2, 16, 64, dtype=bf)
+    rows, slots, table, lens = _z(3, 2, 64, dtype=bf), _z(3, dtype=i64), _z(3, 2, dtype=i32), _z(3, dtype=i32)
+    say("refusals")
+    w = mx.mx_kv_cache_write
+    _raises("k must be", w, _z(6, 64, dtype=bf), rows, slots, kc, kc, sc, sc)
+    _raises("k has shape", w, _z(3, 1, 64, dtype=bf), rows, slots, kc, kc, sc, sc)
+    _raises("k must be", w, rows.float(), rows, slots, kc, kc, sc, sc)
+    _raises("dense heads", w, _z(3, 64, 2, dtype=bf).transpose(1, 2), rows, slots, kc, kc, sc, sc)
+    _raises("v has shape", w, rows, rows[:2], slots, kc, kc, sc, sc)
+    _raises("go together", w, rows, None, slots, kc, kc.clone(), sc, sc.clone())
+    _raises("slots has", w, rows, rows, slots[:2], kc, kc, sc, sc)
+    _raises("slots must be", w, rows, rows, slots.int(), kc, kc, sc, sc)
+    _raises("k_cache must be", w, rows, rows, slots, kc[0], kc, sc, sc)
+    _raises("v_cache has shape", w, rows, rows, slots, kc, kc[:3], sc, sc)
+    _raises("k_scale", w, rows, rows, slots, kc, kc, None, sc)
+    _raises("v_scale", w, rows, rows, slots, kc, kc, sc, None)
+    _raises("k_scale", w, rows, rows, slots, kb, kb, sc, sc)
+    _raises("k_scale has shape", w, rows, rows, slots, kc, kc, _z(4, 2, 16, 4), sc)
+    _raises("contiguous", w, rows, rows, slots, _z(4, 2, 16, 128)[..., :64], kc, sc, sc)
+    _raises("overlaps", w, rows, rows, slots, kc, kc, sc, sc.clone())
+    r = mx.mx_kv_cache_read
+    _raises("block_table must be", r, kb, kb, table[0], lens, 3)
+    _raises("block_table must be", r, kb, kb, table.long(), lens, 3)
+    _raises("offsets has", r, kb, kb, table, lens, 3)
+    _raises("negative", r, kb, kb, table, _z(4, dtype=i32), -1)
+    _raises("k has", r, kb, kb, table, _z(4, dtype=i32), 3, k=rows[:2])
+    _raises("v must be None", r, kb, None, table, _z(4, dtype=i32), 3, v=rows)
+    d = mx.mx_attn_decode
+    q = _z(3, 4, 64, dtype=bf)
+    _raises("q has 2 rows", d, q[:2], kb, kb, table, lens)
+    _raises("q has shape", d, _z(3, 4, 128, dtype=bf), kb, kb, table, lens)
+    _raises("lens has", d, q, kb, kb, table, lens[:2])
+    _raises("lens must be", d, q, kb, kb, table, lens.long())
+    _raises("query heads", d, _z(3, 3, 64, dtype=bf), kb, kb, table, lens)
+    _raises("scale", d, q, kb, kb, table, lens, scale=0.0)
+    _raises("workspace", d, q, kb, kb, table, lens, workspace=_z(16))
+    _raises("out has", d, q, kb, kb, table, lens, out=q[:2])
+    _raises("out overlaps q", d, q, kb, kb, table, lens, out=q)
+    p = mx.mx_attn_prefill
+    o = torch.tensor([0, 3], dtype=i32, device="cuda")
+    _raises("v has shape", p, q, rows, rows[:2], o, o)
+    _raises("k has shape", p, q, _z(3, 2, 128, dtype=bf), rows, o, o)
+    _raises("q_offsets must hold", p, q, rows, rows, o[:0], o)
+    _raises("k_offsets has", p, q, rows, rows, o, o[:1])
+    _raises("q_offsets must be", p, q, rows, rows, o.long(), o)
+    _raises("D = 32", p, _z(3, 4, 32, dtype=bf), _z(3, 2, 32, dtype=bf), _z(3, 2, 32, dtype=bf), o, o)
+    _raises("out overlaps", p, rows, rows.clone(), rows, o, o, out=rows)
+    torch.cuda.synchronize()
+
+
+def test_shared_pages_and_one_table_for_all():
+    """Sequences that share their first pages, and a head that is broadcast: the same page many times."""
+    rng = np.random.default_rng(9)
+    lens, D = [100, 90, 64, 17], 128
+    c, table = make_cache(rng, lens, 1, D, 16, True)
+    table[1:, :4] = table[0, :4]
+    table[3, :2] = table[0, 1]
+    q = normal(rng, 4, 6, D)
+    say("shared pages")
+    out = mx.mx_attn_decode(on_gpu(q), on_gpu(c["k"]), on_gpu(c["v"]), _i32(table), _i32(lens), k_scale=on_gpu(c["ks"]),
+                            v_scale=on_gpu(c["vs"]))
+    torch.cuda.synchronize()
+    check(host_u16(out), *decode_oracle(q, c, table, lens, D ** -0.5), D, 100)
