@@ -7,6 +7,7 @@
 // it to the buffer that the last turn read; registers hold O and Q and have no room for codes under way.
 // Work is shared as attn_plan.hpp says.
 #include <type_traits>
+#include <utility>
 
 #include "attn_decode.hpp"
 #include "attn_tile.hpp"
@@ -22,9 +23,140 @@ constexpr int kMinTokens = 256;        // of a share: its part is up to 128 rows
 constexpr int rows_of(int) { return 128; }
 constexpr int threads_of(int D) { return D >= 512 ? 512 : 256; }
 
+typedef int v8i __attribute__((ext_vector_type(8)));
+
+// Rows of 512 over MXFP8 codes: S comes from the codes themselves, by v_mfma_scale_f32_16x16x128_f8f6f4 with their block
+// scales, and from Q as the sum of two MXFP8 numbers.  A BF16 number has 8 significant bits, an e4m3 code 4: with e the
+// scale of the block, hi = e4m3(q 2^-e) leaves at most 8 steps of q's last bit, which lo = e4m3((q - hi 2^e) 2^(4-e)) holds.
+// So Q is exact but for elements below 2^-14 of their block's largest, which are off by up to 2^-21 of that: what a sum of
+// FP32 products over the block loses too.  The two products take the time of one in BF16, but K is half as many bytes to read
+// from LDS, which is what the matrix cores wait for; the BF16 copy is V alone.
+struct CodesTile : AttnTile16<512, 32, 3> {
+  static constexpr int D = 512, J = D / 128;
+  static constexpr int KN = 2, VN = 5;                  // operands of K and V under way
+  v8i hi[J], lo[J];
+  uint32_t qs, cbase, sbase;                            // qs: byte j is the scale byte of block 4 j + g of the lane's row
+
+  // The operand layout: lane row + 16 g holds bytes 16 g .. + 15 and 64 + 16 g .. + 15 of 128, and the scale of block g of
+  // 32.  In LDS, chunk c of row r of the codes is at c ^ r % 16.
+  __device__ __forceinline__ void begin() {
+    uint32_t lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));                      // found again for each piece: no registers for what never changes
+    AttnTile16::begin(lane);
+    const uint32_t r = lane & 15;
+    cbase = r * D + ((static_cast<uint32_t>(g) ^ r) << 4);
+    sbase = r * (D / 32) + g * 4;
+  }
+
+  __device__ __forceinline__ void load_q(const uint16_t* q) {
+    uint32_t lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const uint32_t g = lane >> 4;
+    qs = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      uint32_t bytes = 0;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint4* at = reinterpret_cast<const uint4*>(q + j * 128 + half * 64 + g * 16);
+        const uint4 a = at[0], b = at[1];
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+        top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));   // the block's other half
+        const bool finite = top < 0x7F80u;
+        const int e = max(e8m0_exponent<8>(finite ? top : 0), -123);
+        const float se = __uint_as_float(static_cast<uint32_t>(e + 127) << 23), sl = __uint_as_float(static_cast<uint32_t>(e + 123) << 23);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          typedef short v2s __attribute__((ext_vector_type(2)));
+          typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+          v2s h = {0, 0}, l = {0, 0};
+          uint32_t back[2], rest[2];
+          h = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(h, __builtin_bit_cast(v2bf, w[2 * i]), se, false);
+          h = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(h, __builtin_bit_cast(v2bf, w[2 * i + 1]), se, true);
+          back[0] = dequant_pair<false>(__builtin_bit_cast(uint32_t, h), se);
+          back[1] = dequant_pair<true>(__builtin_bit_cast(uint32_t, h), se);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)                   // exact, in FP32 and in BF16
+            rest[k] = pack_bf16x2(__uint_as_float(w[2 * i + k] << 16) - __uint_as_float(back[k] << 16),
+                                  __uint_as_float(w[2 * i + k] & 0xFFFF0000u) - __uint_as_float(back[k] & 0xFFFF0000u));
+          l = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(l, __builtin_bit_cast(v2bf, rest[0]), sl, false);
+          l = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(l, __builtin_bit_cast(v2bf, rest[1]), sl, true);
+          hi[j][half * 4 + i] = __builtin_bit_cast(int, h);
+          lo[j][half * 4 + i] = __builtin_bit_cast(int, l);
+        }
+        bytes |= (finite ? static_cast<uint32_t>(e + 127) : 0xFFu) << (8 * half);
+      }
+      // blocks 0, 1 are the first halves of lanes g 0 and 2, blocks 2, 3 their second
+      bytes = static_cast<uint32_t>(__shfl(static_cast<int>(bytes), (lane & 15) + 32 * (g & 1)));
+      qs |= (bytes >> (8 * (g >> 1)) & 0xFFu) << (8 * j);
+    }
+  }
+
+  __device__ __forceinline__ v8i codes_of(const uint8_t* codes, int j, int u) const {
+    const uint8_t* row = codes + u * 16 * D + (j / 2) * 256;
+    const v4u a = *reinterpret_cast<const v4u*>(row + (cbase ^ ((j % 2 * 8) << 4)));
+    const v4u b = *reinterpret_cast<const v4u*>(row + (cbase ^ ((j % 2 * 8 + 4) << 4)));
+    return v8i{static_cast<int>(a[0]), static_cast<int>(a[1]), static_cast<int>(a[2]), static_cast<int>(a[3]),
+               static_cast<int>(b[0]), static_cast<int>(b[1]), static_cast<int>(b[2]), static_cast<int>(b[3])};
+  }
+
+  template <int N>
+  __device__ __forceinline__ void products(const v8i& k, uint32_t ks, uint32_t qlo, Scores& x) {
+    x.s[N % 2] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, hi[N / 2], x.s[N % 2], 0, 0, N / 2, ks, N / 2, qs);
+    x.s[N % 2] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, lo[N / 2], x.s[N % 2], 0, 0, N / 2, ks, N / 2, qlo);
+  }
+
+  // Of the codes of a tile and their scale bytes, [row][g][j].  Eight times two products; the codes are read KN times
+  // ahead, and between() is other work to do under the n-th products.
+  template <class F>
+  __device__ __forceinline__ void scores(const uint8_t* codes, const uint8_t* scales, Scores& x, F between) {
+    asm volatile("" : "+v"(cbase), "+v"(sbase), "+v"(kbase), "+v"(vbase));
+    x.s[0] = x.s[1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const uint32_t qlo = qs - 0x04040404u;              // no byte is below 4; of a NaN block, one NaN is enough
+    const uint32_t ks[2] = {*reinterpret_cast<const uint32_t*>(scales + sbase),
+                            *reinterpret_cast<const uint32_t*>(scales + sbase + 16 * (D / 32))};
+    v8i k[KN + 1];
+#pragma unroll
+    for (int n = 0; n < KN; ++n) k[n] = codes_of(codes, n / 2, n % 2);
+    each(std::make_integer_sequence<int, 8>{}, [&](auto N) {
+      constexpr int n = N;
+      if constexpr (n + KN < 8) k[(n + KN) % (KN + 1)] = codes_of(codes, (n + KN) / 2, (n + KN) % 2);
+      between(N);
+      products<n>(k[n % (KN + 1)], ks[n % 2], qlo, x);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  }
+
+  // O += P V, V's operands read VN products ahead; between() as above.
+  template <class F>
+  __device__ __forceinline__ void values(const uint8_t* vt, const Weights& y, F between) {
+    v4u f[VN];
+#pragma unroll
+    for (int d = 0; d < VN; ++d) f[d] = v_operand(vt, d);
+    __builtin_amdgcn_sched_barrier(0);
+    each(std::make_integer_sequence<int, DT>{}, [&](auto N) {
+      constexpr int d = N;
+      acc[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, f[d % VN]), y.p, acc[d], 0, 0, 0);
+      if constexpr (d + VN < DT) f[d % VN] = v_operand(vt, d + VN);
+      between(N);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  }
+
+  template <int... N, class F>
+  __device__ __forceinline__ static void each(std::integer_sequence<int, N...>, F f) {
+    (f(std::integral_constant<int, N>{}), ...);
+  }
+};
+
 template <int D, bool FP8, bool SAME>
 __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(DecodeArgs a) {
-  using Tile = typename TileOf<D, 4>::type;              // (6 ahead: no registers, and the compiler reads none ahead)
+  constexpr bool CODES = FP8 && D == 512;               // S by the codes themselves
+  using Tile = std::conditional_t<CODES, CodesTile, typename TileOf<D, 4>::type>;   // (6 ahead: no registers, and the
+                                                                                    // compiler reads none ahead)
   constexpr int ROWS = rows_of(D), WAVES = ROWS / Tile::ROWS, KT = key_tile<D>();
   constexpr int TB = KT * D * 2;                        // bytes of a tile in LDS
   constexpr int EB = FP8 ? 1 : 2;
@@ -36,9 +168,18 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
   constexpr int KV = SAME ? 1 : 2;
   constexpr int RAW = FP8 ? KT * D : 16;
   static_assert(NI >= 1 && 16 % RW == 0 && RW * SB <= 256, "a wave's rows are of one page, their scales a word a lane");
-  __shared__ __attribute__((aligned(1024))) uint8_t buf0[KV][TB], buf1[KV][TB], raw[KV][RAW];
+  // Codes that S reads stay until all waves have read them, those of the next tile are converted meanwhile, and those of the
+  // one after it are on their way: three places in turn.
+  constexpr bool TURNS = D == 512;
+  constexpr int MORE = TURNS ? TB : 16, SCALES = CODES ? KT * SB : 16;
+  __shared__ __attribute__((aligned(1024))) uint8_t buf0[KV][TB], buf1[KV][TB], buf2[KV][MORE], raw0[KV][RAW], raw1[CODES ? KV : 1][RAW],
+      raw2[CODES ? KV : 1][RAW], scales0[SCALES], scales1[SCALES], scales2[SCALES];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t r = wave * Tile::ROWS + Tile::row();   // the lane's row
+  auto lane_row = [&]() {                               // of the workgroup's rows; found where it is used
+    uint32_t x = Tile::row();
+    if constexpr (D >= 512) asm volatile("" : "+v"(x));
+    return wave * Tile::ROWS + x;
+  };
 
   Share sh = find_share<KT, kMinTokens / KT>(a);
   while (sh.t < sh.end) {
@@ -50,7 +191,7 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
 
     Tile w;
     w.begin();
-    w.load_q(a.q + static_cast<int64_t>(sh.b) * a.q_stride + (pc.h0 + min(r, pc.heads - 1)) * D);
+    w.load_q(a.q + static_cast<int64_t>(sh.b) * a.q_stride + (pc.h0 + min(lane_row(), pc.heads - 1)) * D);
 
     // A wave brings rows wave * RW .. of a tile.  Rows of a page outside the cache are read from page 0 and made NaN
     // (`lost`); rows past the end are zeros.
@@ -61,9 +202,6 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
     // The page's number by a scalar load (nothing writes the table meanwhile), which holds no vector register and does not
     // wait behind the DMA; past the end, the last token's page again.
     const auto* numbers = (const __attribute__((address_space(4))) int32_t*)table;
-    auto find_page = [&](uint32_t tile) {
-      page = static_cast<uint32_t>(numbers[__builtin_amdgcn_readfirstlane(min(first_token(tile), len - 1) >> a.c.page_shift)]);
-    };
     // The lane's number as the compiler cannot see through: addresses are formed where they are used, and not held in
     // registers that a wide row needs.
     auto hidden = [&]() {
@@ -71,8 +209,18 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
       if constexpr (D >= 256) asm volatile("" : "+v"(x));
       return x;
     };
-    auto load = [&](uint32_t tile, uint8_t (&to)[KV][TB]) {
-      if (tile >= last) return;
+    // The codes of CODES: a lane's place in the cache among the wave's first two rows, and its place in the tile, where its
+    // first eight elements go, or its second, as write_half() has it.  For the next two rows both differ by what is added below.
+    const uint32_t lane0 = hidden(), row0 = wave * RW + lane0 / 32, chunk0 = lane0 % 32 ^ (row0 & 15);
+    uint32_t chunk = lane0 / 32 * 512 + chunk0 * 16;
+    uint32_t put = row0 * D * 2 + (swizzled<D>(chunk0 * 2 + (chunk0 >> 3 & 1), row0) << 4);
+    auto hide_places = [&]() {                          // as hidden() does
+      if constexpr (CODES) asm volatile("" : "+v"(chunk), "+v"(put));
+    };
+    auto find_page = [&](uint32_t tile) {
+      page = static_cast<uint32_t>(numbers[__builtin_amdgcn_readfirstlane(min(first_token(tile), len - 1) >> a.c.page_shift)]);
+    };
+    auto load_rows = [&](uint32_t tile, uint8_t (&to)[KV][TB], uint8_t (*raw)[RAW]) {
       const uint32_t lane = hidden();
       lost_next = page >= a.c.pages;
       const uint32_t at = lost_next ? 0u : page;
@@ -84,52 +232,73 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
 #pragma unroll
         for (int x = 0; x < NI; ++x) {
           const uint32_t r0 = wave * RW + x * RPI;
-          if constexpr (FP8) dma16_at(from + x * 1024 + lane * 16, &raw[i][r0 * D]);
+          if constexpr (CODES) {
+            const uint32_t at = (chunk ^ (x << 5)) + x * 1024;          // row + 2 x: two bits of the row's number
+            dma16_at(from + at, &raw[i][r0 * D]);
+          } else if constexpr (FP8) dma16_at(from + x * 1024 + lane * 16, &raw[i][r0 * D]);
           else dma16_at(from + x * 1024 + lane / CPR * (D * 2) + (swizzled<D>(lane % CPR, r0 + lane / CPR) << 4), &to[i][r0 * D * 2]);
         }
         if constexpr (FP8)
           scale[i] = *reinterpret_cast<const uint32_t*>((i == 0 ? a.c.ks : a.c.vs) + row * SB + lane * 4 % (RW * SB));
       }
     };
-    // The wave's codes, which are there, to BF16.
-    auto convert_rows = [&](auto EDGE, uint32_t tile, uint8_t (&to)[KV][TB]) {
-      const uint32_t lane = hidden(), c = lane % CPR;
+    auto load = [&](uint32_t tile, uint8_t (&to)[KV][TB], uint8_t (*raw)[RAW]) {
+      if (tile < last) load_rows(tile, to, raw);
+    };
+    // The wave's codes, which are there, to BF16.  One DMA instruction's codes of cache i, and their scales:
+    auto read_codes = [&](int i, int x, const uint8_t (*raw)[RAW], uint32_t scale, v4u& v, uint32_t& sc) {
+      if constexpr (CODES) {
+        v = *reinterpret_cast<const v4u*>(&raw[i][(wave * RW + x * RPI) * D + hidden() * 16]);
+        // the scale byte is number chunk / 32 of the first two rows', or its neighbour of the next two
+        const uint32_t byte = chunk / 32, word = __builtin_amdgcn_ds_bpermute((byte & ~3u) + x * 2 * SB, scale);
+        sc = word >> ((byte & 3) * 8 ^ x << 3) & 0xFFu;
+      } else {
+        const uint32_t lane = hidden(), byte = (x * RPI + lane / CPR) * SB + lane % CPR / 2;
+        v = *reinterpret_cast<const v4u*>(&raw[i][(wave * RW + x * RPI) * D + lane * 16]);
+        sc = __shfl(scale, byte / 4) >> (8 * (byte & 3)) & 0xFFu;
+      }
+    };
+    // Half h of them to the tile.  Half of the lanes write their second eight elements first, so that 16 lanes meet all banks.
+    auto write_half = [&](auto EDGE, uint32_t tile, int x, int h, const v4u& v, uint32_t sc, uint8_t* to) {
+      const uint32_t lane = CODES ? 0 : hidden(), c = lane % CPR;
+      const uint32_t r = wave * RW + x * RPI + (CODES && EDGE ? hidden() : lane) / CPR;   // row of the tile
+      const uint32_t turned = (CODES ? chunk >> 7 : c >> 3) & 1;
+      const float sb = __uint_as_float(sc << 23);
+      const uint32_t a0 = v[0], a1 = v[1], b0 = v[2], b1 = v[3], nan = nan_codes(sc);
+      const bool second = (turned ^ h) != 0;
+      const uint32_t w0 = (second ? b0 : a0) | nan, w1 = (second ? b1 : a1) | nan;
+      v4u o = {dequant_pair<false>(w0, sb), dequant_pair<true>(w0, sb), dequant_pair<false>(w1, sb), dequant_pair<true>(w1, sb)};
+      if constexpr (EDGE) {
+        if (tile * KT + r >= len) o = v4u{0, 0, 0, 0};
+      }
+      const uint32_t at = CODES ? (put ^ (h << 4)) + x * 2 * D * 2 : r * D * 2 + (swizzled<D>(c * 2 + (h ^ turned), r) << 4);
+      *reinterpret_cast<v4u*>(&to[at]) = o;
+    };
+    auto convert_rows = [&](auto EDGE, uint32_t tile, uint8_t (&to)[KV][TB], const uint8_t (*raw)[RAW], const uint32_t (&scale)[KV]) {
 #pragma unroll
       for (int i = 0; i < KV; ++i) {
         v4u v[NI];
         uint32_t sc[NI];
 #pragma unroll
-        for (int x = 0; x < NI; ++x) {
-          const uint32_t byte = (x * RPI + lane / CPR) * SB + c / 2;
-          v[x] = *reinterpret_cast<const v4u*>(&raw[i][(wave * RW + x * RPI) * D + lane * 16]);
-          sc[x] = __shfl(scale[i], byte / 4) >> (8 * (byte & 3)) & 0xFFu;
-        }
+        for (int x = 0; x < NI; ++x) read_codes(i, x, raw, scale[i], v[x], sc[x]);
         asm volatile("" ::: "memory");                  // all reads under way before the first is used
 #pragma unroll
         for (int x = 0; x < NI; ++x) {
-          const uint32_t r = wave * RW + x * RPI + lane / CPR;   // row of the tile
-          const float sb = __uint_as_float(sc[x] << 23);
-          const uint32_t nan = nan_codes(sc[x]);
-          // half of the lanes write their second eight elements first, so that 16 lanes meet all banks
-          const uint32_t turned = (c >> 3) & 1;
-          if (turned) v[x] = v4u{v[x][2], v[x][3], v[x][0], v[x][1]};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t w0 = v[x][2 * h] | nan, w1 = v[x][2 * h + 1] | nan;
-            v4u o = {dequant_pair<false>(w0, sb), dequant_pair<true>(w0, sb), dequant_pair<false>(w1, sb), dequant_pair<true>(w1, sb)};
-            if constexpr (EDGE) {
-              const uint32_t fill = lost ? 0x7FC07FC0u : 0u;
-              if (lost || tile * KT + r >= len) o = v4u{fill, fill, fill, fill};
-            }
-            *reinterpret_cast<v4u*>(&to[i][r * D * 2 + (swizzled<D>(c * 2 + (h ^ turned), r) << 4)]) = o;
-          }
+          write_half(EDGE, tile, x, 0, v[x], sc[x], to[i]);
+          write_half(EDGE, tile, x, 1, v[x], sc[x], to[i]);
         }
       }
     };
-    auto convert = [&](uint32_t tile, uint8_t (&to)[KV][TB]) {
-      if (tile >= last) return;
-      if (lost || (tile + 1) * KT > len) convert_rows(std::true_type{}, tile, to);
-      else convert_rows(std::false_type{}, tile, to);
+    // Their scale bytes to LDS, [row][g][j]: of the four that a lane has, of blocks 4 j + g.
+    auto keep_scales = [&](uint8_t* to, uint32_t bytes) {
+      const uint32_t lane = hidden() % (RW * SB / 4);   // (the others have the same)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        to[wave * RW * SB + lane / (SB / 4) * SB + g * (SB / 4) + lane % (SB / 4)] = static_cast<uint8_t>(bytes >> (8 * g));
+    };
+    auto convert = [&](uint32_t tile, uint8_t (&to)[KV][TB], const uint8_t (*raw)[RAW], const uint32_t (&scale)[KV]) {
+      if ((tile + 1) * KT > len) convert_rows(std::true_type{}, tile, to, raw, scale);
+      else convert_rows(std::false_type{}, tile, to, raw, scale);
     };
     // The wave's BF16 rows, which are there: those past the end to zeros, those of a lost page to NaN.
     auto mend = [&](uint32_t tile, uint8_t (&at)[KV][TB]) {
@@ -150,54 +319,153 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
       __builtin_amdgcn_s_waitcnt(wait_vm(0));
       asm volatile("" ::: "memory");
     };
-    auto step = [&](auto RAGGED, uint32_t tile, uint8_t (&now)[KV][TB], uint8_t (&next)[KV][TB]) {
-      landed();
-      lost = lost_next;
-      find_page(tile + (FP8 ? 2 : 1));
-      if constexpr (!FP8) mend(tile, now);
+    // The next codes are there: those of a lost page are NaN by their scales.
+    auto scales_landed = [&]() {
+#pragma unroll
+      for (int i = 0; i < KV; ++i) scale[i] = lost_next ? 0xFFFFFFFFu : scale[i];
+    };
+    auto all_here = [&]() {
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_waitcnt(kWaitLgkmOnly);
-      asm volatile("s_barrier" ::: "memory");           // the tile is whole; everyone has read `next`
+      asm volatile("s_barrier" ::: "memory");           // the tile is whole; everyone has read what comes next's place
+    };
+    auto step = [&](auto RAGGED, uint32_t tile, uint8_t (&now)[KV][TB], uint8_t (&next)[KV][TB]) {
+      landed();
+      if constexpr (FP8) scales_landed();
+      else lost = lost_next;
+      if constexpr (!FP8) mend(tile, now);
+      all_here();
       if constexpr (FP8) {
-        convert(tile + 1, next);
+        if (tile + 1 < last) convert(tile + 1, next, raw0, scale);
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(kWaitLgkmOnly);      // the codes are read, their place is free
       }
-      load(tile + (FP8 ? 2 : 1), next);
+      load(tile + (FP8 ? 2 : 1), next, raw0);
+      find_page(tile + (FP8 ? 3 : 2));                  // a turn ahead: a scalar load is long
       if (!active) return;
       typename Tile::Scores s;
       typename Tile::Weights p;
-      w.scores(now[0], s);
+      if constexpr (!CODES) w.scores(now[0], s);
       if constexpr (RAGGED) w.mask(s, static_cast<int32_t>(len - tile * KT));
       w.weights(s, a.scale, p);
-      w.values(now[KV - 1], p);
+      if constexpr (!CODES) w.values(now[KV - 1], p);
+    };
+    // In turns.  The codes of the next tile are converted under the products with V.
+    auto turn = [&](auto RAGGED, uint32_t tile, const uint8_t* before, uint8_t (&now)[KV][TB], uint8_t (&next)[KV][TB],
+                    const uint8_t (*codes)[RAW], const uint8_t (*codes_next)[RAW], uint8_t (*codes_after)[RAW],
+                    const uint8_t* scales, uint8_t* scales_next) {
+      landed();
+      if constexpr (FP8) scales_landed();
+      else lost = lost_next;
+      if constexpr (!FP8) mend(tile, now);
+      const uint32_t sc[KV] = {scale[0]};
+      hide_places();
+      all_here();
+      auto load_after = [&]() {
+        load(tile + (FP8 ? 2 : 1), next, codes_after);
+        find_page(tile + (FP8 ? 3 : 2));                // a turn ahead: a scalar load is long
+      };
+      auto convert_next = [&]() {
+        if constexpr (CODES) {
+          if (tile + 1 >= last) return;
+          keep_scales(scales_next, sc[0]);
+          convert(tile + 1, next, codes_next, sc);
+        }
+      };
+      if (!active) {
+        load_after();
+        convert_next();
+        return;
+      }
+      typename Tile::Scores s;
+      typename Tile::Weights p;
+      if constexpr (CODES) {
+        if constexpr (RAGGED) {
+          load_after();
+          convert_next();
+          w.scores(codes[0], scales, s, [](auto) {});
+          w.mask(s, static_cast<int32_t>(len - tile * KT));
+          w.weights(s, a.scale, p);
+          w.values(now[0], p, [](auto) {});
+        } else {
+          w.scores(codes[0], scales, s, [&](auto N) {
+            if constexpr (N == 1) {                     // also past the last tile: no harm, and no branch among the products
+              load_rows(tile + 2, next, codes_after);
+              find_page(tile + 3);
+            }
+          });
+          w.weights(s, a.scale, p);
+          v4u v;
+          uint32_t vs;
+          w.values(now[0], p, [&](auto N) {             // the next tile's conversion, in pieces
+            constexpr int n = N;
+            static_assert(NI == 2 || !CODES, "two to each");
+            if constexpr (n == 0) keep_scales(scales_next, sc[0]);
+            if constexpr (n == 1 || n == 13) read_codes(0, n / 13, codes_next, sc[0], v, vs);
+            if constexpr (n == 8 || n == 11 || n == 20 || n == 23) write_half(std::false_type{}, tile + 1, n / 13, n % 12 / 11, v, vs, next[0]);
+          });
+        }
+      } else {
+        load_after();
+        w.scores(now[0], s);
+        if constexpr (RAGGED) w.mask(s, static_cast<int32_t>(len - tile * KT));
+        w.weights(s, a.scale, p);
+        w.values(now[0], p);
+      }
     };
 
     uint32_t tile = pc.tile0;
-    __syncthreads();                                    // the last piece's tiles have been read
+    landed();                                           // what the last piece asked for past its end
+    __syncthreads();                                    // its tiles have been read
     find_page(tile);
-    load(tile, buf0);
+    load(tile, buf0, raw0);
+    find_page(tile + 1);
     if constexpr (FP8) {
-      find_page(tile + 1);
       landed();
-      lost = lost_next;
-      convert(tile, buf0);
+      scales_landed();
+      if constexpr (CODES) keep_scales(scales0, scale[0]);
+      convert(tile, buf0, raw0, scale);
       __builtin_amdgcn_s_waitcnt(kWaitLgkmOnly);
-      load(tile + 1, buf1);
+      if constexpr (CODES) load(tile + 1, buf1, raw1);
+      else load(tile + 1, buf1, raw0);
+      find_page(tile + 2);
     }
-    // Whole tiles two to a turn of the loop, so that each buffer is an object of its own; then what is left, an odd one and
-    // the one with the end.
-    const uint32_t pairs = pc.tile0 + ((last - (last * KT > len ? 1 : 0) - pc.tile0) & ~1u);
-    for (; tile < pairs; tile += 2) {
-      step(std::false_type{}, tile, buf0, buf1);
-      step(std::false_type{}, tile + 1, buf1, buf0);
-    }
+    // Tiles that are whole (and the next one too, with CODES), as many to a turn of the loop as there are places, so that each
+    // is an object of its own; then what is left.
+    const uint32_t rest = (last * KT > len ? 1 : 0) + (CODES ? 1 : 0);
+    const uint32_t whole = pc.tile0 + (pc.tiles > rest ? pc.tiles - rest : 0);
+    if constexpr (TURNS) {
+      while (tile < whole) {
+        turn(std::false_type{}, tile, buf2[0], buf0, buf1, raw0, CODES ? raw1 : raw0, CODES ? raw2 : raw0, scales0, scales1);
+        if (++tile == whole) break;
+        turn(std::false_type{}, tile, buf0[0], buf1, buf2, raw1, raw2, raw0, scales1, scales2);
+        if (++tile == whole) break;
+        turn(std::false_type{}, tile, buf1[0], buf2, buf0, raw2, raw0, raw1, scales2, scales0);
+        ++tile;
+      }
 #pragma unroll 1
-    for (; tile < last; ++tile) {
-      const bool second = ((tile - pc.tile0) & 1) != 0;
-      step(std::true_type{}, tile, second ? buf1 : buf0, second ? buf0 : buf1);
+      for (; tile < last; ++tile) {
+        const uint32_t n = (tile - pc.tile0) % 3;
+        turn(std::true_type{}, tile, n == 0 ? buf2[0] : n == 1 ? buf0[0] : buf1[0], n == 0 ? buf0 : n == 1 ? buf1 : buf2,
+             n == 0 ? buf1 : n == 1 ? buf2 : buf0, n == 0 ? raw0 : n == 1 ? raw1 : raw2, n == 0 ? raw1 : n == 1 ? raw2 : raw0,
+             n == 0 ? raw2 : n == 1 ? raw0 : raw1, n == 0 ? scales0 : n == 1 ? scales1 : scales2,
+             n == 0 ? scales1 : n == 1 ? scales2 : scales0);
+      }
+    } else {
+      while (tile < whole) {
+        step(std::false_type{}, tile, buf0, buf1);
+        if (++tile == whole) break;
+        step(std::false_type{}, tile, buf1, buf0);
+        ++tile;
+      }
+#pragma unroll 1
+      for (; tile < last; ++tile) {
+        const bool odd = ((tile - pc.tile0) & 1) != 0;
+        step(std::true_type{}, tile, odd ? buf1 : buf0, odd ? buf0 : buf1);
+      }
     }
 
+    const uint32_t r = lane_row();
     float l = w.sum();
     if (bad) l = __builtin_nanf("");
     if (active && r < pc.heads) {

@@ -305,8 +305,8 @@ struct AttnTile16 {
   __device__ __forceinline__ static int row() { return threadIdx.x & 15; }
   __device__ __forceinline__ static bool first_lane() { return (threadIdx.x & 48) == 0; }
 
-  __device__ __forceinline__ void begin() {
-    const uint32_t lane = threadIdx.x & 63, col = lane & 15;
+  __device__ __forceinline__ void begin(uint32_t lane = threadIdx.x & 63) {
+    const uint32_t col = lane & 15;
     g = lane >> 4;
     // K: row col of 16, chunk 4 j + g.  V: row 4 g + (lane % 16) / 4 of 16, columns 4 (lane % 4) of 16.
     kbase = col * (D * 2) + (swizzled<D>(g, col) << 4);
