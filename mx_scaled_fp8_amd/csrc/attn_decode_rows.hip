@@ -170,8 +170,7 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
   static_assert(NI >= 1 && 16 % RW == 0 && RW * SB <= 256, "a wave's rows are of one page, their scales a word a lane");
   // Codes that S reads stay until all waves have read them, those of the next tile are converted meanwhile, and those of the
   // one after it are on their way: three places in turn.
-  constexpr bool TURNS = D == 512;
-  constexpr int MORE = TURNS ? TB : 16, SCALES = CODES ? KT * SB : 16;
+  constexpr int MORE = CODES ? TB : 16, SCALES = CODES ? KT * SB : 16;
   __shared__ __attribute__((aligned(1024))) uint8_t buf0[KV][TB], buf1[KV][TB], buf2[KV][MORE], raw0[KV][RAW], raw1[CODES ? KV : 1][RAW],
       raw2[CODES ? KV : 1][RAW], scales0[SCALES], scales1[SCALES], scales2[SCALES];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -191,7 +190,6 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
 
     Tile w;
     w.begin();
-    w.load_q(a.q + static_cast<int64_t>(sh.b) * a.q_stride + (pc.h0 + min(lane_row(), pc.heads - 1)) * D);
 
     // A wave brings rows wave * RW .. of a tile.  Rows of a page outside the cache are read from page 0 and made NaN
     // (`lost`); rows past the end are zeros.
@@ -246,22 +244,21 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
       if (tile < last) load_rows(tile, to, raw);
     };
     // The wave's codes, which are there, to BF16.  One DMA instruction's codes of cache i, and their scales:
-    auto read_codes = [&](int i, int x, const uint8_t (*raw)[RAW], uint32_t scale, v4u& v, uint32_t& sc) {
+    auto read_codes = [&](uint32_t lane, int i, int x, const uint8_t (*raw)[RAW], uint32_t scale, v4u& v, uint32_t& sc) {
       if constexpr (CODES) {
-        v = *reinterpret_cast<const v4u*>(&raw[i][(wave * RW + x * RPI) * D + hidden() * 16]);
+        v = *reinterpret_cast<const v4u*>(&raw[i][(wave * RW + x * RPI) * D + lane * 16]);
         // the scale byte is number chunk / 32 of the first two rows', or its neighbour of the next two
         const uint32_t byte = chunk / 32, word = __builtin_amdgcn_ds_bpermute((byte & ~3u) + x * 2 * SB, scale);
         sc = word >> ((byte & 3) * 8 ^ x << 3) & 0xFFu;
       } else {
-        const uint32_t lane = hidden(), byte = (x * RPI + lane / CPR) * SB + lane % CPR / 2;
+        const uint32_t byte = (x * RPI + lane / CPR) * SB + lane % CPR / 2;
         v = *reinterpret_cast<const v4u*>(&raw[i][(wave * RW + x * RPI) * D + lane * 16]);
         sc = __shfl(scale, byte / 4) >> (8 * (byte & 3)) & 0xFFu;
       }
     };
     // Half h of them to the tile.  Half of the lanes write their second eight elements first, so that 16 lanes meet all banks.
-    auto write_half = [&](auto EDGE, uint32_t tile, int x, int h, const v4u& v, uint32_t sc, uint8_t* to) {
-      const uint32_t lane = CODES ? 0 : hidden(), c = lane % CPR;
-      const uint32_t r = wave * RW + x * RPI + (CODES && EDGE ? hidden() : lane) / CPR;   // row of the tile
+    auto write_half = [&](auto EDGE, uint32_t lane, uint32_t tile, int x, int h, const v4u& v, uint32_t sc, uint8_t* to) {
+      const uint32_t c = lane % CPR, r = wave * RW + x * RPI + lane / CPR;   // row of the tile
       const uint32_t turned = (CODES ? chunk >> 7 : c >> 3) & 1;
       const float sb = __uint_as_float(sc << 23);
       const uint32_t a0 = v[0], a1 = v[1], b0 = v[2], b1 = v[3], nan = nan_codes(sc);
@@ -277,15 +274,16 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
     auto convert_rows = [&](auto EDGE, uint32_t tile, uint8_t (&to)[KV][TB], const uint8_t (*raw)[RAW], const uint32_t (&scale)[KV]) {
 #pragma unroll
       for (int i = 0; i < KV; ++i) {
+        const uint32_t lane = hidden();
         v4u v[NI];
         uint32_t sc[NI];
 #pragma unroll
-        for (int x = 0; x < NI; ++x) read_codes(i, x, raw, scale[i], v[x], sc[x]);
+        for (int x = 0; x < NI; ++x) read_codes(lane, i, x, raw, scale[i], v[x], sc[x]);
         asm volatile("" ::: "memory");                  // all reads under way before the first is used
 #pragma unroll
         for (int x = 0; x < NI; ++x) {
-          write_half(EDGE, tile, x, 0, v[x], sc[x], to[i]);
-          write_half(EDGE, tile, x, 1, v[x], sc[x], to[i]);
+          write_half(EDGE, lane, tile, x, 0, v[x], sc[x], to[i]);
+          write_half(EDGE, lane, tile, x, 1, v[x], sc[x], to[i]);
         }
       }
     };
@@ -333,6 +331,7 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
       landed();
       if constexpr (FP8) scales_landed();
       else lost = lost_next;
+      find_page(tile + (FP8 ? 2 : 1));
       if constexpr (!FP8) mend(tile, now);
       all_here();
       if constexpr (FP8) {
@@ -341,7 +340,6 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
         __builtin_amdgcn_s_waitcnt(kWaitLgkmOnly);      // the codes are read, their place is free
       }
       load(tile + (FP8 ? 2 : 1), next, raw0);
-      find_page(tile + (FP8 ? 3 : 2));                  // a turn ahead: a scalar load is long
       if (!active) return;
       typename Tile::Scores s;
       typename Tile::Weights p;
@@ -351,26 +349,22 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
       if constexpr (!CODES) w.values(now[KV - 1], p);
     };
     // In turns.  The codes of the next tile are converted under the products with V.
-    auto turn = [&](auto RAGGED, uint32_t tile, const uint8_t* before, uint8_t (&now)[KV][TB], uint8_t (&next)[KV][TB],
+    auto turn = [&](auto RAGGED, uint32_t tile, uint8_t (&now)[KV][TB], uint8_t (&next)[KV][TB],
                     const uint8_t (*codes)[RAW], const uint8_t (*codes_next)[RAW], uint8_t (*codes_after)[RAW],
                     const uint8_t* scales, uint8_t* scales_next) {
       landed();
-      if constexpr (FP8) scales_landed();
-      else lost = lost_next;
-      if constexpr (!FP8) mend(tile, now);
+      scales_landed();
       const uint32_t sc[KV] = {scale[0]};
       hide_places();
       all_here();
       auto load_after = [&]() {
-        load(tile + (FP8 ? 2 : 1), next, codes_after);
-        find_page(tile + (FP8 ? 3 : 2));                // a turn ahead: a scalar load is long
+        load(tile + 2, next, codes_after);
+        find_page(tile + 3);                            // a turn ahead: a scalar load is long
       };
       auto convert_next = [&]() {
-        if constexpr (CODES) {
-          if (tile + 1 >= last) return;
-          keep_scales(scales_next, sc[0]);
-          convert(tile + 1, next, codes_next, sc);
-        }
+        if (tile + 1 >= last) return;
+        keep_scales(scales_next, sc[0]);
+        convert(tile + 1, next, codes_next, sc);
       };
       if (!active) {
         load_after();
@@ -379,38 +373,31 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
       }
       typename Tile::Scores s;
       typename Tile::Weights p;
-      if constexpr (CODES) {
-        if constexpr (RAGGED) {
-          load_after();
-          convert_next();
-          w.scores(codes[0], scales, s, [](auto) {});
-          w.mask(s, static_cast<int32_t>(len - tile * KT));
-          w.weights(s, a.scale, p);
-          w.values(now[0], p, [](auto) {});
-        } else {
-          w.scores(codes[0], scales, s, [&](auto N) {
-            if constexpr (N == 1) {                     // also past the last tile: no harm, and no branch among the products
-              load_rows(tile + 2, next, codes_after);
-              find_page(tile + 3);
-            }
-          });
-          w.weights(s, a.scale, p);
-          v4u v;
-          uint32_t vs;
-          w.values(now[0], p, [&](auto N) {             // the next tile's conversion, in pieces
-            constexpr int n = N;
-            static_assert(NI == 2 || !CODES, "two to each");
-            if constexpr (n == 0) keep_scales(scales_next, sc[0]);
-            if constexpr (n == 1 || n == 13) read_codes(0, n / 13, codes_next, sc[0], v, vs);
-            if constexpr (n == 8 || n == 11 || n == 20 || n == 23) write_half(std::false_type{}, tile + 1, n / 13, n % 12 / 11, v, vs, next[0]);
-          });
-        }
-      } else {
+      if constexpr (!CODES) return;
+      else if constexpr (RAGGED) {
         load_after();
-        w.scores(now[0], s);
-        if constexpr (RAGGED) w.mask(s, static_cast<int32_t>(len - tile * KT));
+        convert_next();
+        w.scores(codes[0], scales, s, [](auto) {});
+        w.mask(s, static_cast<int32_t>(len - tile * KT));
         w.weights(s, a.scale, p);
-        w.values(now[0], p);
+        w.values(now[0], p, [](auto) {});
+      } else {
+        w.scores(codes[0], scales, s, [&](auto N) {
+          if constexpr (N == 1) {                       // also past the last tile: no harm, and no branch among the products
+            load_rows(tile + 2, next, codes_after);
+            find_page(tile + 3);
+          }
+        });
+        w.weights(s, a.scale, p);
+        v4u v;
+        uint32_t vs;
+        w.values(now[0], p, [&](auto N) {               // the next tile's conversion, in pieces
+          constexpr int n = N;
+          static_assert(NI == 2 || !CODES, "two to each");
+          if constexpr (n == 0) keep_scales(scales_next, sc[0]);
+          if constexpr (n == 1 || n == 13) read_codes(hidden(), 0, n / 13, codes_next, sc[0], v, vs);
+          if constexpr (n == 8 || n == 11 || n == 20 || n == 23) write_half(std::false_type{}, 0, tile + 1, n / 13, n % 12 / 11, v, vs, next[0]);
+        });
       }
     };
 
@@ -419,8 +406,9 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
     __syncthreads();                                    // its tiles have been read
     find_page(tile);
     load(tile, buf0, raw0);
-    find_page(tile + 1);
+    w.load_q(a.q + static_cast<int64_t>(sh.b) * a.q_stride + (pc.h0 + min(lane_row(), pc.heads - 1)) * D);
     if constexpr (FP8) {
+      find_page(tile + 1);
       landed();
       scales_landed();
       if constexpr (CODES) keep_scales(scales0, scale[0]);
@@ -428,35 +416,33 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
       __builtin_amdgcn_s_waitcnt(kWaitLgkmOnly);
       if constexpr (CODES) load(tile + 1, buf1, raw1);
       else load(tile + 1, buf1, raw0);
-      find_page(tile + 2);
+      if constexpr (CODES) find_page(tile + 2);
     }
     // Tiles that are whole (and the next one too, with CODES), as many to a turn of the loop as there are places, so that each
     // is an object of its own; then what is left.
     const uint32_t rest = (last * KT > len ? 1 : 0) + (CODES ? 1 : 0);
     const uint32_t whole = pc.tile0 + (pc.tiles > rest ? pc.tiles - rest : 0);
-    if constexpr (TURNS) {
+    if constexpr (CODES) {
       while (tile < whole) {
-        turn(std::false_type{}, tile, buf2[0], buf0, buf1, raw0, CODES ? raw1 : raw0, CODES ? raw2 : raw0, scales0, scales1);
+        turn(std::false_type{}, tile, buf0, buf1, raw0, raw1, raw2, scales0, scales1);
         if (++tile == whole) break;
-        turn(std::false_type{}, tile, buf0[0], buf1, buf2, raw1, raw2, raw0, scales1, scales2);
+        turn(std::false_type{}, tile, buf1, buf2, raw1, raw2, raw0, scales1, scales2);
         if (++tile == whole) break;
-        turn(std::false_type{}, tile, buf1[0], buf2, buf0, raw2, raw0, raw1, scales2, scales0);
+        turn(std::false_type{}, tile, buf2, buf0, raw2, raw0, raw1, scales2, scales0);
         ++tile;
       }
 #pragma unroll 1
       for (; tile < last; ++tile) {
         const uint32_t n = (tile - pc.tile0) % 3;
-        turn(std::true_type{}, tile, n == 0 ? buf2[0] : n == 1 ? buf0[0] : buf1[0], n == 0 ? buf0 : n == 1 ? buf1 : buf2,
+        turn(std::true_type{}, tile, n == 0 ? buf0 : n == 1 ? buf1 : buf2,
              n == 0 ? buf1 : n == 1 ? buf2 : buf0, n == 0 ? raw0 : n == 1 ? raw1 : raw2, n == 0 ? raw1 : n == 1 ? raw2 : raw0,
              n == 0 ? raw2 : n == 1 ? raw0 : raw1, n == 0 ? scales0 : n == 1 ? scales1 : scales2,
              n == 0 ? scales1 : n == 1 ? scales2 : scales0);
       }
     } else {
-      while (tile < whole) {
+      for (; tile + 2 <= whole; tile += 2) {
         step(std::false_type{}, tile, buf0, buf1);
-        if (++tile == whole) break;
-        step(std::false_type{}, tile, buf1, buf0);
-        ++tile;
+        step(std::false_type{}, tile + 1, buf1, buf0);
       }
 #pragma unroll 1
       for (; tile < last; ++tile) {
