@@ -545,9 +545,11 @@ mx_status mx_kv_cache_read(int32_t kind, const void* k_cache, const uint8_t* k_s
  *           page outside [0, pages), has NaN outputs; nothing outside the cache is read.
  * scale     finite and > 0 (1 / sqrt(D) as a rule).
  * out       device BF16 [B, H, D], FP32 scores, statistics and sums; probabilities
- *           are rounded to BF16 for the second product.  The result does not depend
- *           on timing, but on B and max_pages, which decide where a long sequence is
- *           cut.
+ *           are rounded to BF16 for the second product.  (A latent MXFP8 cache of D = 512
+ *           under 32 heads or more takes q as the sum of two MXFP8 numbers: exact, but
+ *           for elements below 2^-14 of the largest of their 32, which are off by up to
+ *           2^-21 of that.)  The result does not depend on timing, but on B and
+ *           max_pages, which decide where a long sequence is cut.
  * workspace device, at least mx_attn_decode_workspace_bytes(B, H, Hkv, D, max_pages,
  *           page_size), 16-byte aligned: parts of long sequences, written before
  *           they are read.  Calls that may overlap need one each.

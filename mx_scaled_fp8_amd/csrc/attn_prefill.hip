@@ -10,6 +10,11 @@
 //
 // Few row tiles with many keys are split along the keys over `splits` workgroups, whose parts (O, m, l) a second
 // kernel joins.
+//
+// What bounds it is the matrix cores and, beside them, the issue of what the softmax needs: of 8192 tokens, 32 heads of 128, the
+// products alone take 357 us at the clock that the power allows, the kernel 511 to 540 (1.02 to 1.07 PFLOP/s; a library product
+// of 8192^3 reaches 1.2 to 1.45).  P is rounded to BF16 for the second product; m, the sum of the unrounded P, S and O
+// are FP32, parts too.
 #include <algorithm>
 
 #include "attn_tile.hpp"
@@ -281,8 +286,8 @@ bool same(const void* k, int64_t k_stride, const void* v, int64_t v_stride) { re
 int rows_of_call(int32_t D, bool latent) { return D >= 512 && latent ? 64 : 128; }
 
 // Heads of a row tile: those that share a key head where an average prompt has fewer tokens than a row tile has rows.  (7
-// rows of 4 prompts over 30000 tokens, 4 heads a key head: 147 us with, 263 without.  With full row tiles of their own the
-// heads were as fast or faster: 8192 rows 534 and 529 us, latent rows of 512 314 and 283.)
+// rows of 4 prompts over 30000 tokens, 4 heads a key head: 142 us with, 268 without.  With full row tiles of their own the
+// heads are as fast unpacked: 8192 rows 534 us packed, 529 not.)
 int32_t pack_of(int64_t B, int64_t Tq, int32_t H, int32_t Hkv, int rows) { return Tq / B < rows ? H / Hkv : 1; }
 
 // Bound on the row tiles of all prompts.

@@ -1,7 +1,9 @@
 // Writing the tokens' keys and values into the paged cache, and reading sequences back (gfx950).
 //
 // Both are one pass over the data and bound by HBM: the write reads 2 and writes 1 + 1/32 bytes an element (2 for a BF16
-// cache), the read the other way round.
+// cache), the read the other way round.  (8192 tokens of 8 heads of 128, keys and values, to MXFP8: 10.9 us, 4.7 TB/s; 91,807
+// cached tokens of them read back as BF16: 119 us for 570 MB, 4.8 TB/s; 64 new tokens 3 us, a launch.  A copy
+// reaches 5.1 TB/s.)
 #include <algorithm>
 
 #include "kv_cache.hpp"

@@ -617,3 +617,53 @@ def test_shared_pages_and_one_table_for_all():
                             v_scale=on_gpu(c["vs"]))
     torch.cuda.synchronize()
     check(host_u16(out), *decode_oracle(q, c, table, lens, D ** -0.5), D, 100)
+
+
+@pytest.mark.parametrize("exponent", [0, 40, -60, -130])
+def test_decode_queries_of_all_magnitudes(exponent):
+    """Latent rows of 512 in MXFP8, whose queries the kernel splits into two MXFP8 numbers: elements of one block spread over
+    2^30, blocks of zeros, the range's ends.  An element below 2^-14 of its block's largest is off by up to 2^-21 of that; a
+    weight moves by the scores' error, and the weights' sum too, so that the bound gains 2 err size."""
+    rng = np.random.default_rng(10)
+    H, D, lens = 48, 512, [70, 1, 300]
+    c, table = make_cache(rng, lens, 1, D, 16, True, True)
+    x = rng.standard_normal((3, H, D)) * 2.0 ** rng.integers(-30, 1, (3, H, D))
+    x[:, ::3] = rng.standard_normal((3, H // 3, D)) * 2.0 ** rng.integers(-8, 1, (3, H // 3, D))
+    x[:, 1, 64:96] = 0
+    x[:, 2] = 0
+    q = workloads.to_bf16_bits((x * 2.0 ** exponent).astype(np.float32))
+    scale = D ** -0.5 * 2.0 ** min(-exponent, 100)
+    say("decode all magnitudes", exponent)
+    out = mx.mx_attn_decode(on_gpu(q), on_gpu(c["k"]), None, _i32(table), _i32(lens), k_scale=on_gpu(c["ks"]), scale=scale)
+    torch.cuda.synchronize()
+    ref, size, spread = decode_oracle(q, c, table, lens, scale)
+    qf = F.bf16_to_f64(q).reshape(3, H, D // 32, 32)
+    for b, n in enumerate(lens):
+        k = np.abs(A.sequence(c["k"], c["ks"], table[b], n)).reshape(n, D // 32, 32).sum(-1).max(0)      # a block's largest sum
+        err = scale * 2.0 ** -21 * (np.abs(qf[b]).max(-1) * k).sum(-1)
+        spread[b] += err * 2.0 ** 24 / (D + 4)
+    check(host_u16(out), ref, size, spread, D, max(lens))
+
+
+@pytest.mark.parametrize("G,D,latent", [(4, 128, False), (40, 128, False), (64, 512, True), (3, 512, False)])
+@pytest.mark.parametrize("what", [0x7F80, 0xFF80, 0x7FC0])
+@KINDS
+def test_queries_that_are_not_finite(G, D, latent, what, fp8):
+    """An infinity or NaN in a head's query makes that head NaN, and no other."""
+    rng = np.random.default_rng(G)
+    lens = [300, 1]
+    c, table = make_cache(rng, lens, 1, D, 16, fp8, latent)
+    q = normal(rng, 2, G, D)
+    q[0, 1, 37], q[1, G - 1, D - 1], q[1, 0, 0] = what, what, what
+    say("query not finite", G, D, latent, hex(what), fp8)
+    out = mx.mx_attn_decode(on_gpu(q), on_gpu(c["k"]), on_gpu(c["v"]), _i32(table), _i32(lens), k_scale=on_gpu(c["ks"]),
+                            v_scale=on_gpu(c["vs"]))
+    keys = normal(rng, 400, 1, D)
+    dk = on_gpu(keys)
+    pre = mx.mx_attn_prefill(on_gpu(q), dk, dk, _i32([0, 2]), _i32([0, 400]))
+    torch.cuda.synchronize()
+    bad = np.zeros((2, G), bool)
+    bad[0, 1] = bad[1, G - 1] = bad[1, 0] = True
+    for got in (host_u16(out), host_u16(pre)):
+        f = F.bf16_to_f64(got)
+        assert np.isnan(f[bad]).all() and np.isfinite(f[~bad]).all()
