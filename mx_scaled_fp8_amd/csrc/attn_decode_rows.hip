@@ -22,7 +22,10 @@ namespace mx {
 
 namespace {
 
-constexpr int kMinTokens = 256;        // of a share: its part is up to 128 rows of FP32, as much as 500 cached tokens
+// Of a share: its part is up to 128 rows of FP32, as much as 500 cached tokens.  (Us of 64, 128 and 256: one sequence of 1000
+// tokens, 128 heads of 512 27, 28 and 35, of 6566 42, 38 and 40; 4 of 2000, 64 heads of 256 21, 23 and 29; 2 of 30,000, 32 heads of
+// 128 22.5, 22.7 and 21.)
+constexpr int kMinTokens = 128;
 
 // Query heads of a workgroup: 32 for each of four waves, half of what a compute unit runs, so that two workgroups, which know
 // nothing of each other's barriers, fill it; in rows of 512, 16 for each of eight, so that codes are converted once for all 128

@@ -23,7 +23,10 @@ namespace mx {
 
 namespace {
 
-constexpr int kMinTiles = 4;           // fewest key tiles of a split
+// Fewest keys of a split, in 64s: its parts, O in FP32, are written and read again.  (Us of 4, 8 and 16: 64 rows over 8000 tokens, 16
+// heads of 512 on one 119, 78 and 73; 4 prompts of 17 rows over 3972, 6 heads of 128 on each of 4 31, 26 and 36; 200 rows over
+// 3000, 4 heads of 128 on each of 2 28, 26 and 31.)
+constexpr int kMinTiles = 8;
 
 struct PrefillArgs {
   const uint16_t* q;
