@@ -440,10 +440,11 @@ mx_status launch_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t
   a.H = static_cast<uint32_t>(H);
   a.G = a.H / c.Hkv;
   const int64_t max_tokens = static_cast<int64_t>(c.max_pages) << c.page_shift;
-  if (decode_by_rows(static_cast<int32_t>(a.G), D, c.k == c.v && c.ks == c.vs)) {
+  if (decode_by_rows(static_cast<int32_t>(a.G), D, c.k == c.v && c.ks == c.vs, fp8)) {
     launch_decode_rows(a, D, fp8, max_tokens, stream);
   } else {
     a.head_blocks = head_blocks_of(static_cast<int32_t>(a.G));
+    a.part_heads = kHeads;
     switch (D) {
       case 64: fp8 ? launch<64, true>(a, max_tokens, stream) : launch<64, false>(a, max_tokens, stream); break;
       case 128: fp8 ? launch<128, true>(a, max_tokens, stream) : launch<128, false>(a, max_tokens, stream); break;

@@ -476,7 +476,7 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
           *reinterpret_cast<uint2*>(row + d) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
         }
       } else {
-        float* part = part_of(a, sh.group, sh.block, pc.tile0 == 0, ROWS * (D + 2));
+        float* part = part_of(a, sh.group, sh.block, pc.tile0 == 0, a.part_heads * (D + 2));
 #pragma unroll
         for (int x = 0; x < Tile::QUADS; ++x) {
           int d;
@@ -484,8 +484,8 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
           *reinterpret_cast<float4*>(part + r * D + d) = o;
         }
         if (Tile::first_lane()) {
-          part[ROWS * D + r] = w.m;
-          part[ROWS * D + ROWS + r] = l;
+          part[a.part_heads * D + r] = w.m;
+          part[a.part_heads * D + a.part_heads + r] = l;
         }
       }
     }
@@ -494,6 +494,9 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
 }
 
 uint32_t head_blocks_of(int32_t G, int32_t D) { return static_cast<uint32_t>((G + rows_of(D) - 1) / rows_of(D)); }
+
+// Heads of a part: a multiple of 4, so that every part is 16-byte aligned.
+int32_t part_heads_of(int32_t G, int32_t D) { return std::min((G + 3) / 4 * 4, rows_of(D)); }
 
 // Groups: as many as run at once, and no more than there can be tiles.
 uint32_t groups_of(int64_t B, int32_t Hkv, uint32_t head_blocks, int32_t D, int64_t max_tokens) {
@@ -515,18 +518,23 @@ void launch(const DecodeArgs& a, hipStream_t stream) {
 }  // namespace
 
 // From 32 heads on the rows fill at least one wave's products, and the cache is read once, not once for each 16 heads.
-// Rows of 512 have no room in LDS for values of their own.
-bool decode_by_rows(int32_t G, int32_t D, bool latent) { return G >= 32 && (D < 512 || latent); }
+// Rows of 512 have no room in LDS for values of their own.  A latent BF16 row of 512, read twice by the other kernel, which has no
+// registers to read ahead, is always better here (64 sequences up to 8192 tokens: one head 55 us here, 64 there, 16 heads 62 and 76;
+// 2 up to 2000, 4 heads 15.9 and 15.4); in MXFP8 one head is 68 and 50, 20 heads 75 and 96 but over 2 times 2000 tokens 26 and 16.
+bool decode_by_rows(int32_t G, int32_t D, bool latent, bool fp8) {
+  return D == 512 ? latent && (G >= 32 || !fp8) : G >= 32;
+}
 
 size_t decode_rows_part_bytes(int64_t B, int32_t H, int32_t Hkv, int32_t D, int64_t max_tokens) {
   const int32_t G = H / Hkv;
-  if (!decode_by_rows(G, D, true)) return 0;
+  if (!decode_by_rows(G, D, true, false)) return 0;
   const uint32_t blocks = head_blocks_of(G, D);
-  return static_cast<size_t>(groups_of(B, Hkv, blocks, D, max_tokens)) * blocks * 2 * rows_of(D) * (D + 2) * 4;
+  return static_cast<size_t>(groups_of(B, Hkv, blocks, D, max_tokens)) * blocks * 2 * part_heads_of(G, D) * (D + 2) * 4;
 }
 
 void launch_decode_rows(DecodeArgs a, int32_t D, bool fp8, int64_t max_tokens, hipStream_t stream) {
   a.head_blocks = head_blocks_of(static_cast<int32_t>(a.G), D);
+  a.part_heads = static_cast<uint32_t>(part_heads_of(static_cast<int32_t>(a.G), D));
   a.groups = groups_of(a.B, static_cast<int32_t>(a.c.Hkv), a.head_blocks, D, max_tokens);
   switch (D) {
     case 64: fp8 ? launch<64, true>(a, stream) : launch<64, false>(a, stream); break;

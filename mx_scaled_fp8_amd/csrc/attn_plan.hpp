@@ -18,12 +18,13 @@ struct DecodeArgs {
   int64_t q_stride;
   const int32_t* lens;
   uint16_t* out;
-  float* parts;              // [group][head block][2][O: heads x D, then m and l]
+  float* parts;              // [group][head block][2][O: part_heads x D, then m and l]
   uint32_t* plan;            // [0] share, [1 + b] first tile of sequence b
   float scale;               // times log2(e)
   uint32_t B, H, G;          // G query heads a key head
   uint32_t groups;           // up to 8 or a multiple of 8
   uint32_t head_blocks;
+  uint32_t part_heads;       // up to a block's heads
 };
 
 // Tokens of sequence b, cut to what its table holds.
@@ -131,12 +132,12 @@ constexpr int kJoinThreads = 256;
 // time, four of them under way, the others every so many-th of the others; their sums meet in LDS, in a fixed order.
 template <int D, int TILE, int HEADS>
 __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(DecodeArgs a) {
-  constexpr uint32_t DT = D / 4, LANES = kJoinThreads / DT, SIZE = HEADS * (D + 2);
+  constexpr uint32_t DT = D / 4, LANES = kJoinThreads / DT;
   __shared__ __attribute__((aligned(16))) float sum[LANES][D];
   __shared__ float tops[LANES], weights[LANES];
   const uint32_t b = blockIdx.x / a.H, h = blockIdx.x - b * a.H;
   const uint32_t kvh = h / a.G, block = (h - kvh * a.G) / HEADS, r = (h - kvh * a.G) - block * HEADS;
-  const uint32_t share = a.plan[0], begin = a.plan[1 + b];
+  const uint32_t heads = a.part_heads, share = a.plan[0], begin = a.plan[1 + b];
   const uint32_t nt = (tokens_of(a, b) + TILE - 1) / TILE;
   const uint32_t lane = threadIdx.x / DT, d = threadIdx.x % DT * 4;
   uint2* out = reinterpret_cast<uint2*>(a.out + (static_cast<size_t>(b) * a.H + h) * D + d);
@@ -155,10 +156,10 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(DecodeArgs a) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const bool some = w + k * LANES <= w1;
-      const float* p = part_of(a, some ? w + k * LANES : w, block, w + k * LANES == w0 || (!some && w == w0), SIZE);
+      const float* p = part_of(a, some ? w + k * LANES : w, block, w + k * LANES == w0 || (!some && w == w0), heads * (D + 2));
       x[k] = *reinterpret_cast<const float4*>(p + r * D + d);
-      pm[k] = some ? p[HEADS * D + r] : -INFINITY;
-      pl[k] = p[HEADS * D + HEADS + r];
+      pm[k] = some ? p[heads * D + r] : -INFINITY;
+      pl[k] = p[heads * D + heads + r];
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) top = fmaxf(top, pm[k]);

@@ -667,3 +667,16 @@ def test_queries_that_are_not_finite(G, D, latent, what, fp8):
     for got in (host_u16(out), host_u16(pre)):
         f = F.bf16_to_f64(got)
         assert np.isnan(f[bad]).all() and np.isfinite(f[~bad]).all()
+
+
+@pytest.mark.parametrize("G", [1, 5, 17, 33])
+def test_decode_latent_bf16_of_few_heads_in_parts(G):
+    """Any number of heads over a latent BF16 row of 512, streams that are cut into parts and ones that are not."""
+    rng = np.random.default_rng(G)
+    lens = [2000, 0, 3, 129, 700]
+    c, table = make_cache(rng, lens, 1, 512, 32, False, True)
+    q = normal(rng, len(lens), G, 512)
+    say("decode latent bf16", G)
+    out = mx.mx_attn_decode(on_gpu(q), on_gpu(c["k"]), None, _i32(table), _i32(lens))
+    torch.cuda.synchronize()
+    check(host_u16(out), *decode_oracle(q, c, table, lens, 512 ** -0.5), 512, 2000)
