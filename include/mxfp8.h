@@ -523,7 +523,7 @@ mx_status mx_kv_cache_write(const void* k, int64_t k_stride, const void* v, int6
  *           elements, exact wherever BF16 holds them (2^-133 and above; nearest
  *           even below).  A row whose page is outside [0, pages), or beyond
  *           max_pages, is NaN; the cache is not read for it.
- * Requires: B >= 0, rows >= 0 (either 0 is a no-op), rows < 2^31, max_pages >= 1, the cache's
+ * Requires: B >= 0, rows >= 0 (either 0 is a no-op), rows < 2^28, max_pages >= 1, the cache's
  * sizes as for mx_kv_cache_write, rows * Hkv * D < 2^34, tensors 16-byte, block_table and offsets
  * 4-byte aligned; k and v overlap neither each other nor an input.
  */
@@ -555,7 +555,7 @@ mx_status mx_kv_cache_read(int32_t kind, const void* k_cache, const uint8_t* k_s
  *           they are read.  Calls that may overlap need one each.
  * Requires: B >= 0 (0 is a no-op), B < 2^24, D 64, 128, 256 or 512, Hkv >= 1, H % Hkv == 0, H <= 2^16,
  * max_pages >= 1, max_pages * page_size < 2^31, the cache's sizes as for mx_kv_cache_write,
- * B * H < 2^24, B * Hkv * ceil(H / Hkv / 16) times ceil(max_pages * page_size / 32)
+ * B * H < 2^23, B * Hkv * ceil(H / Hkv / 16) times ceil(max_pages * page_size / 32)
  * < 2^31, q_stride >= H * D and a multiple of 8, q, caches and out 16-byte, scales 16-byte,
  * block_table and lens 4-byte aligned; out and the workspace overlap no input
  * and not each other.
@@ -589,7 +589,7 @@ mx_status mx_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t H, 
  *           16-byte aligned (may be NULL when that is 0): parts of rows whose keys are
  *           split over workgroups, written before they are read.  Calls that may
  *           overlap need one each.
- * Requires: B, Tq, Tk >= 0 (B or Tq 0 is a no-op), B < 2^24, Tq, Tk < 2^31, D 64, 128, 256 or 512, Hkv >= 1,
+ * Requires: B, Tq, Tk >= 0 (B or Tq 0 is a no-op), B < 2^24, Tq < 2^31, Tk < 2^31 - 64, D 64, 128, 256 or 512, Hkv >= 1,
  * H % Hkv == 0, H <= 2^16, (Tq / 64 + B) * H < 2^23, q_stride, k_stride and v_stride multiples of 8 and at least a dense
  * row, q_stride below 2^31, the others below 2^22, scale finite and > 0, q, k, v and out 16-byte, offsets 4-byte aligned;
  * out and the workspace overlap no input and not each other.

@@ -149,7 +149,7 @@ mx_status mx_kv_cache_read(int32_t kind, const void* k_cache, const uint8_t* k_s
   const mx_status ok = check_cache(fn, kind, k_cache, k_scale, v_cache, v_scale, pages, page_size, Hkv, D);
   if (ok != MX_OK) return ok;
   const int64_t width = int64_t(Hkv) * D;
-  MX_CHECK(B >= 0 && B < k31 && rows >= 0 && rows < k31 && rows * width < (int64_t(1) << 34),
+  MX_CHECK(B >= 0 && B < k31 && rows >= 0 && rows < (int64_t(1) << 28) && rows * width < (int64_t(1) << 34),
            "%s: B = %lld, rows = %lld of %lld out of range", fn, (long long)B, (long long)rows, (long long)width);
   MX_CHECK(max_pages >= 1 && max_pages < k31, "%s: max_pages = %lld out of range", fn, (long long)max_pages);
   MX_CHECK((v != nullptr) == (v_cache != nullptr) || rows == 0 || B == 0,
@@ -199,7 +199,7 @@ mx_status mx_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t H, 
   const int64_t streams = B * Hkv * ((H / Hkv + 15) / 16);
   MX_CHECK(streams < (int64_t(1) << 24) && streams * ((max_pages * page_size + 31) / 32) < k31,
            "%s: B = %lld x Hkv = %d x %lld tokens too large", fn, (long long)B, Hkv, (long long)(max_pages * page_size));
-  MX_CHECK(B * H < (int64_t(1) << 24), "%s: B = %lld x H = %d too large", fn, (long long)B, H);
+  MX_CHECK(B * H < (int64_t(1) << 23), "%s: B = %lld x H = %d too large", fn, (long long)B, H);
   if (B == 0) { clear_error(); return MX_OK; }
   MX_CHECK(q && block_table && lens && out, "%s: null tensor pointer", fn);
   MX_CHECK(q_stride >= int64_t(H) * D && q_stride % 8 == 0 && q_stride < k31,
@@ -227,7 +227,7 @@ mx_status mx_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t H, 
 }
 
 size_t mx_attn_prefill_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t Hkv, int32_t D) {
-  if (B <= 0 || B >= (int64_t(1) << 24) || Tq <= 0 || Tq >= k31 || Tk < 0 || Tk >= k31 || Hkv <= 0 || H < Hkv ||
+  if (B <= 0 || B >= (int64_t(1) << 24) || Tq <= 0 || Tq >= k31 || Tk < 0 || Tk >= k31 - 64 || Hkv <= 0 || H < Hkv ||
       H > 65536 || D <= 0 || D > 1024)
     return 0;
   return prefill_workspace_bytes(B, Tq, Tk, H, Hkv, D);
@@ -240,7 +240,7 @@ mx_status mx_attn_prefill(const void* q, int64_t q_stride, const void* k, int64_
   const char* fn = "mx_attn_prefill";
   mx_status st = check_heads(fn, H, Hkv, D, scale);
   if (st != MX_OK) return st;
-  MX_CHECK(B >= 0 && B < (int64_t(1) << 24) && Tq >= 0 && Tq < k31 && Tk >= 0 && Tk < k31,
+  MX_CHECK(B >= 0 && B < (int64_t(1) << 24) && Tq >= 0 && Tq < k31 && Tk >= 0 && Tk < k31 - 64,
            "%s: B = %lld, Tq = %lld, Tk = %lld out of range", fn, (long long)B, (long long)Tq, (long long)Tk);
   MX_CHECK((Tq / 64 + B) * H < (int64_t(1) << 23), "%s: Tq = %lld rows of H = %d heads too large", fn, (long long)Tq, H);
   if (B == 0 || Tq == 0) { clear_error(); return MX_OK; }

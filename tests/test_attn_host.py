@@ -68,7 +68,7 @@ def test_read_validation(dry):
     assert _read(vc=None, vcs=None, v=None) == mx.MX_OK
     assert _read(B=0, table=None, offsets=None, k=None, v=None) == mx.MX_OK
     assert _read(rows=0, table=None, offsets=None, k=None, v=None) == mx.MX_OK
-    _refused(_read, BAD_CACHES + [dict(B=-1), dict(B=1 << 31), dict(rows=-1), dict(rows=1 << 31), dict(rows=1 << 25), dict(max_pages=0),
+    _refused(_read, BAD_CACHES + [dict(B=-1), dict(B=1 << 31), dict(rows=-1), dict(rows=1 << 31), dict(rows=1 << 28, Hkv=1, D=32), dict(rows=1 << 25), dict(max_pages=0),
                                   dict(max_pages=1 << 31), dict(k=None), dict(v=None), dict(table=None), dict(offsets=None),
                                   dict(k=FAKE + 8), dict(v=FAKE + 8), dict(table=FAKE + 2), dict(offsets=FAKE + 1), dict(D=48)])
 
@@ -91,7 +91,7 @@ def test_decode_validation(dry):
     assert need and _decode(wb=need) == mx.MX_OK
     nan, inf = float("nan"), float("inf")
     _refused(_decode, BAD_CACHES + [dict(D=96), dict(D=1024, qs=8192), dict(H=6), dict(H=0), dict(H=65540), dict(B=-1), dict(B=1 << 24),
-                                    dict(B=1 << 21), dict(scale=0.0), dict(scale=-1.0), dict(scale=nan), dict(scale=inf),
+                                    dict(B=1 << 21), dict(B=1 << 20), dict(scale=0.0), dict(scale=-1.0), dict(scale=nan), dict(scale=inf),
                                     dict(max_pages=0), dict(max_pages=1 << 31), dict(max_pages=1 << 25), dict(q=None), dict(table=None),
                                     dict(lens=None), dict(out=None), dict(qs=1016), dict(qs=1028), dict(qs=1 << 31), dict(q=FAKE + 2),
                                     dict(out=FAKE + 8), dict(table=FAKE + 2), dict(lens=FAKE + 2), dict(ws=None), dict(ws=FAKE + 8),
@@ -117,7 +117,7 @@ def test_prefill_validation(dry):
     assert need and _prefill(**split, wb=need) == mx.MX_OK
     nan, inf = float("nan"), float("inf")
     _refused(_prefill, [dict(D=32), dict(D=96), dict(H=6), dict(H=0), dict(Hkv=0), dict(Hkv=-4), dict(H=65540), dict(B=-1), dict(B=1 << 24),
-                        dict(Tq=-1), dict(Tq=1 << 31), dict(Tk=-1), dict(Tk=1 << 31), dict(Tq=1 << 30), dict(scale=0.0),
+                        dict(Tq=-1), dict(Tq=1 << 31), dict(Tk=-1), dict(Tk=1 << 31), dict(Tk=(1 << 31) - 64), dict(Tq=1 << 30), dict(scale=0.0),
                         dict(scale=nan), dict(scale=inf), dict(q=None), dict(k=None), dict(v=None), dict(qo=None), dict(ko=None),
                         dict(out=None), dict(qs=1016), dict(qs=1028), dict(qs=1 << 31), dict(ks=504), dict(ks=516), dict(ks=1 << 22),
                         dict(vs=504), dict(vs=516), dict(vs=1 << 22), dict(q=FAKE + 8), dict(k=FAKE + 8), dict(v=FAKE + 8),
