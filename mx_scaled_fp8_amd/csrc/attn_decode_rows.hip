@@ -40,7 +40,8 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 // scale of the block, hi = e4m3(q 2^-e) leaves at most 8 steps of q's last bit, which lo = e4m3((q - hi 2^e) 2^(4-e)) holds.
 // So Q is exact but for elements below 2^-14 of their block's largest, which are off by up to 2^-21 of that: what a sum of
 // FP32 products over the block loses too.  The two products take the time of one in BF16, but K is half as many bytes to read
-// from LDS, which is what the matrix cores wait for; the BF16 copy is V alone.
+// from LDS, and its reads need not wait for the conversion, which only V's do.  (64 sequences up to 32,768 tokens, 128 heads: 376
+// us by the BF16 copy, 338 so.)
 struct CodesTile : AttnTile16<512, 32, 3> {
   static constexpr int D = 512, J = D / 128;
   // Operands of K and V under way (us: 1 and 4 365, 2 and 4 363, 2 and 5 348, 2 and 6, which spills in the loop, 354).
@@ -300,10 +301,12 @@ __global__ __launch_bounds__(threads_of(D), 2) void attn_decode_rows_kernel(Deco
     };
     // Their scale bytes to LDS, [row][g][j]: of the four that a lane has, of blocks 4 j + g.
     auto keep_scales = [&](uint8_t* to, uint32_t bytes) {
-      const uint32_t lane = hidden() % (RW * SB / 4);   // (the others have the same)
+      if constexpr (CODES) {
+        const uint32_t lane = hidden() % (RW * SB / 4); // (the others have the same)
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
-        to[wave * RW * SB + lane / (SB / 4) * SB + g * (SB / 4) + lane % (SB / 4)] = static_cast<uint8_t>(bytes >> (8 * g));
+        for (int g = 0; g < 4; ++g)
+          to[wave * RW * SB + lane / (SB / 4) * SB + g * (SB / 4) + lane % (SB / 4)] = static_cast<uint8_t>(bytes >> (8 * g));
+      }
     };
     auto convert = [&](uint32_t tile, uint8_t (&to)[KV][TB], const uint8_t (*raw)[RAW], const uint32_t (&scale)[KV]) {
       if ((tile + 1) * KT > len) convert_rows(std::true_type{}, tile, to, raw, scale);
