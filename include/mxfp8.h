@@ -551,8 +551,9 @@ mx_status mx_kv_cache_read(int32_t kind, const void* k_cache, const uint8_t* k_s
  *           2^-21 of that.)  The result does not depend on timing, but on B and
  *           max_pages, which decide where a long sequence is cut.
  * workspace device, at least mx_attn_decode_workspace_bytes(B, H, Hkv, D, max_pages,
- *           page_size), 16-byte aligned: parts of long sequences, written before
- *           they are read.  Calls that may overlap need one each.
+ *           page_size) (0 for sizes that the call refuses), 16-byte aligned: parts of
+ *           long sequences, written before they are read.  Calls that may overlap
+ *           need one each.
  * Requires: B >= 0 (0 is a no-op), B < 2^24, D 64, 128, 256 or 512, Hkv >= 1, H % Hkv == 0, H <= 2^16,
  * max_pages >= 1, max_pages * page_size < 2^31, the cache's sizes as for mx_kv_cache_write,
  * B * H < 2^23, B * Hkv * ceil(H / Hkv / 16) times ceil(max_pages * page_size / 32)
@@ -585,8 +586,8 @@ mx_status mx_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t H, 
  * out       device BF16 [Tq, H, D], dense.  FP32 scores, statistics and sums;
  *           probabilities are rounded to BF16 for the second product.  Keys and
  *           values that a row does not see take no part in it, NaN or not.
- * workspace device, at least mx_attn_prefill_workspace_bytes(B, Tq, Tk, H, Hkv, D),
- *           16-byte aligned (may be NULL when that is 0): parts of rows whose keys are
+ * workspace device, at least mx_attn_prefill_workspace_bytes(B, Tq, Tk, H, Hkv, D) (0 for
+ *           sizes that the call refuses), 16-byte aligned (may be NULL when that is 0): parts of rows whose keys are
  *           split over workgroups, written before they are read.  Calls that may
  *           overlap need one each.
  * Requires: B, Tq, Tk >= 0 (B or Tq 0 is a no-op), B < 2^24, Tq < 2^31, Tk < 2^31 - 64, D 64, 128, 256 or 512, Hkv >= 1,

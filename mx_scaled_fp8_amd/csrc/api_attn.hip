@@ -48,15 +48,34 @@ size_t extent(int64_t n, int64_t stride, int64_t width) {
   return n > 0 ? (static_cast<size_t>(n - 1) * stride + width) * 2 : 0;
 }
 
+bool head_dim(int32_t D) { return D == 64 || D == 128 || D == 256 || D == 512; }
+bool heads_fit(int32_t H, int32_t Hkv) { return Hkv >= 1 && H >= 1 && H <= 65536 && H % Hkv == 0; }
+bool page_fits(int32_t page_size) {
+  return page_size >= 16 && page_size <= MX_CACHE_MAX_PAGE && (page_size & (page_size - 1)) == 0;
+}
+bool row_fits(int32_t Hkv, int32_t D) {
+  return Hkv >= 1 && D >= 32 && D <= 1024 && D % MX_CACHE_BLOCK == 0 && int64_t(Hkv) * D <= (int64_t(1) << 20);
+}
+
+// The sizes of a call, each and their products, of heads (and pages) that fit: what the call and the query of its workspace
+// agree on, and what keeps the launchers' arithmetic in range.
+bool decode_fits(int64_t B, int32_t H, int32_t Hkv, int64_t max_pages, int32_t page_size) {
+  if (B < 0 || B >= (int64_t(1) << 24) || max_pages < 1 || max_pages >= k31 || max_pages * page_size >= k31) return false;
+  const int64_t streams = B * Hkv * ((H / Hkv + 15) / 16);
+  return streams < (int64_t(1) << 24) && streams * ((max_pages * page_size + 31) / 32) < k31 && B * H < (int64_t(1) << 23);
+}
+bool prefill_fits(int64_t B, int64_t Tq, int64_t Tk, int32_t H) {
+  return B >= 0 && B < (int64_t(1) << 24) && Tq >= 0 && Tq < k31 && Tk >= 0 && Tk < k31 - 64 &&
+         (Tq / 64 + B) * H < (int64_t(1) << 23);
+}
+
 // The cache's sizes and pointers.
 mx_status check_cache(const char* fn, int32_t kind, const void* k, const void* ks, const void* v, const void* vs,
                       int64_t pages, int32_t page_size, int32_t Hkv, int32_t D) {
   MX_CHECK(kind == MX_CACHE_MXFP8 || kind == MX_CACHE_BF16, "%s: unknown cache kind %d", fn, kind);
-  MX_CHECK(page_size >= 16 && page_size <= MX_CACHE_MAX_PAGE && (page_size & (page_size - 1)) == 0,
-           "%s: page_size = %d (a power of two, 16 to %d)", fn, page_size, MX_CACHE_MAX_PAGE);
+  MX_CHECK(page_fits(page_size), "%s: page_size = %d (a power of two, 16 to %d)", fn, page_size, MX_CACHE_MAX_PAGE);
   MX_CHECK(pages >= 1 && pages < k31, "%s: pages = %lld out of range", fn, (long long)pages);
-  MX_CHECK(Hkv >= 1 && D >= 32 && D <= 1024 && D % MX_CACHE_BLOCK == 0 && int64_t(Hkv) * D <= (int64_t(1) << 20),
-           "%s: Hkv = %d, D = %d (D a multiple of %d up to 1024, Hkv * D up to 2^20)", fn, Hkv, D, MX_CACHE_BLOCK);
+  MX_CHECK(row_fits(Hkv, D), "%s: Hkv = %d, D = %d (D a multiple of %d up to 1024, Hkv * D up to 2^20)", fn, Hkv, D, MX_CACHE_BLOCK);
   MX_CHECK(pages * page_size * Hkv * D < (int64_t(1) << 46), "%s: %lld pages too large", fn, (long long)pages);
   MX_CHECK(k, "%s: null k_cache", fn);
   MX_CHECK(aligned(k, 16) && aligned(v, 16) && aligned(ks, 16) && aligned(vs, 16),
@@ -94,12 +113,9 @@ KvCache view(const void* k, const uint8_t* ks, const void* v, const uint8_t* vs,
   return c;
 }
 
-bool head_dim(int32_t D) { return D == 64 || D == 128 || D == 256 || D == 512; }
-
 mx_status check_heads(const char* fn, int32_t H, int32_t Hkv, int32_t D, float scale) {
   MX_CHECK(head_dim(D), "%s: D = %d (64, 128, 256 or 512)", fn, D);
-  MX_CHECK(Hkv >= 1 && H >= 1 && H <= 65536 && H % Hkv == 0, "%s: H = %d query heads over Hkv = %d key heads", fn, H,
-           Hkv);
+  MX_CHECK(heads_fit(H, Hkv), "%s: H = %d query heads over Hkv = %d key heads", fn, H, Hkv);
   MX_CHECK(std::isfinite(scale) && scale > 0.0f, "%s: scale = %g (finite, above 0)", fn, static_cast<double>(scale));
   return MX_OK;
 }
@@ -177,9 +193,9 @@ mx_status mx_kv_cache_read(int32_t kind, const void* k_cache, const uint8_t* k_s
 
 size_t mx_attn_decode_workspace_bytes(int64_t B, int32_t H, int32_t Hkv, int32_t D, int64_t max_pages,
                                       int32_t page_size) {
-  if (B <= 0 || B >= (int64_t(1) << 24) || Hkv <= 0 || H < Hkv || H > 65536 || D <= 0 || D > 1024 || max_pages <= 0 ||
-      max_pages >= k31 || page_size <= 0 || page_size > MX_CACHE_MAX_PAGE || max_pages * page_size >= k31)
-    return 0;                                          // sizes that a call refuses
+  if (B == 0 || !head_dim(D) || !heads_fit(H, Hkv) || !row_fits(Hkv, D) || !page_fits(page_size) ||
+      !decode_fits(B, H, Hkv, max_pages, page_size))
+    return 0;                                          // nothing to do, or sizes that a call refuses
   return decode_workspace_bytes(B, H, Hkv, D, max_pages * page_size);
 }
 
@@ -193,13 +209,9 @@ mx_status mx_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t H, 
   if (st != MX_OK) return st;
   st = check_cache(fn, kind, k_cache, k_scale, v_cache, v_scale, pages, page_size, Hkv, D);
   if (st != MX_OK) return st;
-  MX_CHECK(B >= 0 && B < (int64_t(1) << 24), "%s: B = %lld out of range", fn, (long long)B);
-  MX_CHECK(max_pages >= 1 && max_pages < k31 && max_pages * page_size < k31, "%s: max_pages = %lld of %d tokens out of range",
-           fn, (long long)max_pages, page_size);
-  const int64_t streams = B * Hkv * ((H / Hkv + 15) / 16);
-  MX_CHECK(streams < (int64_t(1) << 24) && streams * ((max_pages * page_size + 31) / 32) < k31,
-           "%s: B = %lld x Hkv = %d x %lld tokens too large", fn, (long long)B, Hkv, (long long)(max_pages * page_size));
-  MX_CHECK(B * H < (int64_t(1) << 23), "%s: B = %lld x H = %d too large", fn, (long long)B, H);
+  MX_CHECK(decode_fits(B, H, Hkv, max_pages, page_size),
+           "%s: B = %lld, H = %d, Hkv = %d, max_pages = %lld of %d tokens out of range", fn, (long long)B, H, Hkv,
+           (long long)max_pages, page_size);
   if (B == 0) { clear_error(); return MX_OK; }
   MX_CHECK(q && block_table && lens && out, "%s: null tensor pointer", fn);
   MX_CHECK(q_stride >= int64_t(H) * D && q_stride % 8 == 0 && q_stride < k31,
@@ -227,9 +239,7 @@ mx_status mx_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t H, 
 }
 
 size_t mx_attn_prefill_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t Hkv, int32_t D) {
-  if (B <= 0 || B >= (int64_t(1) << 24) || Tq <= 0 || Tq >= k31 || Tk < 0 || Tk >= k31 - 64 || Hkv <= 0 || H < Hkv ||
-      H > 65536 || D <= 0 || D > 1024)
-    return 0;
+  if (B == 0 || Tq == 0 || !head_dim(D) || !heads_fit(H, Hkv) || !prefill_fits(B, Tq, Tk, H)) return 0;
   return prefill_workspace_bytes(B, Tq, Tk, H, Hkv, D);
 }
 
@@ -240,9 +250,8 @@ mx_status mx_attn_prefill(const void* q, int64_t q_stride, const void* k, int64_
   const char* fn = "mx_attn_prefill";
   mx_status st = check_heads(fn, H, Hkv, D, scale);
   if (st != MX_OK) return st;
-  MX_CHECK(B >= 0 && B < (int64_t(1) << 24) && Tq >= 0 && Tq < k31 && Tk >= 0 && Tk < k31 - 64,
-           "%s: B = %lld, Tq = %lld, Tk = %lld out of range", fn, (long long)B, (long long)Tq, (long long)Tk);
-  MX_CHECK((Tq / 64 + B) * H < (int64_t(1) << 23), "%s: Tq = %lld rows of H = %d heads too large", fn, (long long)Tq, H);
+  MX_CHECK(prefill_fits(B, Tq, Tk, H), "%s: B = %lld, Tq = %lld, Tk = %lld, H = %d out of range", fn, (long long)B,
+           (long long)Tq, (long long)Tk, H);
   if (B == 0 || Tq == 0) { clear_error(); return MX_OK; }
   MX_CHECK(q && q_offsets && k_offsets && out && ((k && v) || Tk == 0), "%s: null tensor pointer", fn);
   const int64_t qw = int64_t(H) * D, kw = int64_t(Hkv) * D, most = int64_t(1) << 22;

@@ -294,7 +294,7 @@ int rows_of_call(int32_t D, bool latent) { return D >= 512 && latent ? 64 : 128;
 int32_t pack_of(int64_t B, int64_t Tq, int32_t H, int32_t Hkv, int rows) { return Tq / B < rows ? H / Hkv : 1; }
 
 // Bound on the row tiles of all prompts.
-uint32_t row_tiles(int64_t B, int64_t Tq, int32_t pack, int rows) { return static_cast<uint32_t>(Tq * pack / rows + B); }
+int64_t row_tiles(int64_t B, int64_t Tq, int32_t pack, int rows) { return Tq * pack / rows + B; }
 
 // How many workgroups share the keys of one row tile and pack.  512 run at once; up to twice as many, as long as every part
 // has some tiles of keys, keep them busy and let those that run together read the same keys.  (4096 rows over 30011 earlier
@@ -307,7 +307,7 @@ uint32_t split_count(int64_t B, int64_t Tk, int64_t units) {
 // (row tile, pack) pairs.
 int64_t units_of(int64_t B, int64_t Tq, int32_t H, int32_t Hkv, int rows) {
   const int32_t pack = pack_of(B, Tq, H, Hkv, rows);
-  return static_cast<int64_t>(row_tiles(B, Tq, pack, rows)) * (H / pack);
+  return row_tiles(B, Tq, pack, rows) * (H / pack);
 }
 
 size_t part_bytes(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t Hkv, int32_t D, int rows) {
@@ -363,7 +363,7 @@ mx_status launch_attn_prefill(const void* q, int64_t q_stride, const void* k, in
   a.Hkv = static_cast<uint32_t>(Hkv);
   a.pack = static_cast<uint32_t>(pack_of(B, Tq, H, Hkv, rows));
   a.packs = a.H / a.Hkv / a.pack;
-  a.tiles = row_tiles(B, Tq, static_cast<int32_t>(a.pack), rows);
+  a.tiles = static_cast<uint32_t>(row_tiles(B, Tq, static_cast<int32_t>(a.pack), rows));
   a.splits = split_count(B, Tk, units_of(B, Tq, H, Hkv, rows));
   switch (D) {
     case 64: launch<64>(a, latent, stream); break;

@@ -23,3 +23,22 @@ def test_attn_host_code_under_address_sanitizer(tmp_path):
     r = subprocess.run([exe], capture_output=True, text=True, timeout=600, env=env)
     assert r.returncode == 0 and "all checks passed" in r.stdout, r.stdout + r.stderr
     assert "AddressSanitizer" not in r.stderr, r.stderr
+
+
+def test_attn_workspace_sizes_under_sanitizers(tmp_path):
+    """The real size arithmetic (only the launchers' host code is compiled: no device code, no HIP runtime)."""
+    san = ["-fsanitize=address,undefined", "-fno-sanitize-recover=undefined", "-g", "-O1", "-fPIC"]
+    objs, binaries = [], []
+    for name in ("api_attn", "attn_decode", "attn_decode_rows", "attn_prefill", "kv_cache"):
+        objs.append(str(tmp_path / f"{name}.o"))
+        _run([HIPCC, "--offload-arch=gfx950", "--cuda-host-only", "-std=c++17", f"-I{INC}", f"-I{CSRC}",
+              *[a for f in san for a in ("-Xarch_host", f)], "-c", os.path.join(CSRC, f"{name}.hip"), "-o", objs[-1]])
+        undefined = _run(["nm", "-u", objs[-1]]).stdout.split()
+        binaries += [f"-Wl,--defsym={s}=0" for s in undefined if s.startswith("__hip_fatbin")]      # the device code
+    drv, exe = str(tmp_path / "driver.o"), str(tmp_path / "sizes_driver")
+    _run([CLANG, "-std=c++17", *san, f"-I{INC}", "-c", os.path.join(ROOT, "tests", "asan", "attn_sizes_driver.cpp"), "-o", drv])
+    _run([CLANG, "-fsanitize=address,undefined", *objs, drv, *binaries, "-o", exe])
+    env = dict(os.environ, ASAN_OPTIONS="detect_leaks=0:abort_on_error=0")
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=600, env=env)
+    assert r.returncode == 0 and "all checks passed" in r.stdout, r.stdout[-3000:] + r.stderr[-3000:]
+    assert "Sanitizer" not in r.stderr and "runtime error" not in r.stderr, r.stderr

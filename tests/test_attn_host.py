@@ -195,3 +195,16 @@ def test_binding_wants_gpu_tensors():
     _raises("q must be a GPU tensor", mx.mx_attn_decode, z(1, 4, 64, dtype=i16), kc, kc, z(1, 2, dtype=i32), z(1, dtype=i32), sc, sc)
     _raises("q must be a GPU tensor", mx.mx_attn_prefill, rows, rows, rows, z(2, dtype=i32), z(2, dtype=i32))
     _raises("k must be a torch tensor", mx.mx_kv_cache_write, [1], rows, z(3, dtype=i64), kc, kc, sc, sc)
+
+
+def test_sizes_that_a_call_refuses_have_no_workspace(dry):
+    """The queries are public and come before the call that refuses: one of them divided by a product that had wrapped to 0."""
+    d, p = mx.mx_attn_decode_workspace_bytes, mx.mx_attn_prefill_workspace_bytes
+    for B, Tq, Tk, H, Hkv, D in ((1 << 23, (1 << 24) - (1 << 14), 1 << 20, 65536, 1, 128), ((1 << 24) - 1, (1 << 31) - 1, 100, 65536, 1, 64),
+                                 (1, 100, 100, 6, 4, 128), (1, 100, 100, 8, 4, 96), (1, 1 << 30, 100, 8, 4, 128)):
+        assert p(B, Tq, Tk, H, Hkv, D) == 0
+        assert _prefill(B=B, Tq=Tq, Tk=Tk, H=H, Hkv=Hkv, D=D, qs=H * D, ks=Hkv * D, vs=Hkv * D) == mx.MX_ERR_INVALID_ARG
+    for B, H, Hkv, D, n, page in (((1 << 24) - 1, 65536, 65536, 512, 1 << 18, 4096), (5, 6, 4, 128, 7, 64), (5, 8, 4, 96, 7, 64),
+                                  (5, 8, 4, 128, 7, 48), (1 << 20, 8, 4, 128, 7, 64), (1, 4096, 4096, 512, 7, 64)):
+        assert d(B, H, Hkv, D, n, page) == 0
+        assert _decode(B=B, H=H, Hkv=Hkv, D=D, max_pages=n, page=page, qs=H * D) == mx.MX_ERR_INVALID_ARG
