@@ -523,7 +523,7 @@ mx_status mx_kv_cache_write(const void* k, int64_t k_stride, const void* v, int6
  *           elements, exact wherever BF16 holds them (2^-133 and above; nearest
  *           even below).  A row whose page is outside [0, pages), or beyond
  *           max_pages, is NaN; the cache is not read for it.
- * Requires: B >= 0, rows >= 0 (either 0 is a no-op), rows < 2^28, max_pages >= 1, the cache's
+ * Requires: B >= 0, rows >= 0 (either 0 is a no-op), rows <= 2^28 - 16, max_pages >= 1, the cache's
  * sizes as for mx_kv_cache_write, rows * Hkv * D < 2^34, tensors 16-byte, block_table and offsets
  * 4-byte aligned; k and v overlap neither each other nor an input.
  */

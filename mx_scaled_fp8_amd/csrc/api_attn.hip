@@ -165,7 +165,8 @@ mx_status mx_kv_cache_read(int32_t kind, const void* k_cache, const uint8_t* k_s
   const mx_status ok = check_cache(fn, kind, k_cache, k_scale, v_cache, v_scale, pages, page_size, Hkv, D);
   if (ok != MX_OK) return ok;
   const int64_t width = int64_t(Hkv) * D;
-  MX_CHECK(B >= 0 && B < k31 && rows >= 0 && rows < (int64_t(1) << 28) && rows * width < (int64_t(1) << 34),
+  // (rows: 16 to a workgroup of 256, a launch has fewer than 2^32 threads)
+  MX_CHECK(B >= 0 && B < k31 && rows >= 0 && rows <= (int64_t(1) << 28) - 16 && rows * width < (int64_t(1) << 34),
            "%s: B = %lld, rows = %lld of %lld out of range", fn, (long long)B, (long long)rows, (long long)width);
   MX_CHECK(max_pages >= 1 && max_pages < k31, "%s: max_pages = %lld out of range", fn, (long long)max_pages);
   MX_CHECK((v != nullptr) == (v_cache != nullptr) || rows == 0 || B == 0,

@@ -208,3 +208,9 @@ def test_sizes_that_a_call_refuses_have_no_workspace(dry):
                                   (5, 8, 4, 128, 7, 48), (1 << 20, 8, 4, 128, 7, 64), (1, 4096, 4096, 512, 7, 64)):
         assert d(B, H, Hkv, D, n, page) == 0
         assert _decode(B=B, H=H, Hkv=Hkv, D=D, max_pages=n, page=page, qs=H * D) == mx.MX_ERR_INVALID_ARG
+
+
+def test_read_of_as_many_rows_as_a_launch_has_threads_for(dry):
+    """16 rows to a workgroup of 256 threads: 2^28 - 15 rows would be 2^32 threads."""
+    assert _read(rows=(1 << 28) - 16, Hkv=1, D=32) == mx.MX_OK
+    _refused(_read, [dict(rows=(1 << 28) - 15, Hkv=1, D=32), dict(rows=(1 << 28) - 1, Hkv=1, D=32)])
