@@ -543,7 +543,7 @@ mx_status mx_kv_cache_read(int32_t kind, const void* k_cache, const uint8_t* k_s
  * lens      device int32 [B].  lens[b] <= 0: out[b] is 0.  A sequence that is
  *           longer than its table (lens[b] > max_pages * page_size), or with a
  *           page outside [0, pages), has NaN outputs; nothing outside the cache is read.
- * scale     finite and > 0 (1 / sqrt(D) as a rule).
+ * scale     > 0, scale * log2(e) finite in FP32 (1 / sqrt(D) as a rule).
  * out       device BF16 [B, H, D], FP32 scores, statistics and sums; probabilities
  *           are rounded to BF16 for the second product.  (A latent MXFP8 cache of D = 512
  *           under 32 heads or more takes q as the sum of two MXFP8 numbers: exact, but
@@ -592,7 +592,7 @@ mx_status mx_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t H, 
  *           overlap need one each.
  * Requires: B, Tq, Tk >= 0 (B or Tq 0 is a no-op), B < 2^24, Tq < 2^31, Tk < 2^31 - 64, D 64, 128, 256 or 512, Hkv >= 1,
  * H % Hkv == 0, H <= 2^16, (Tq / 64 + B) * H < 2^23, q_stride, k_stride and v_stride multiples of 8 and at least a dense
- * row, q_stride below 2^31, the others below 2^22, scale finite and > 0, q, k, v and out 16-byte, offsets 4-byte aligned;
+ * row, q_stride below 2^31, the others below 2^22, scale as above, q, k, v and out 16-byte, offsets 4-byte aligned;
  * out and the workspace overlap no input and not each other.
  */
 size_t mx_attn_prefill_workspace_bytes(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t Hkv,

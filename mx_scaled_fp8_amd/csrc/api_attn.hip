@@ -116,7 +116,9 @@ KvCache view(const void* k, const uint8_t* ks, const void* v, const uint8_t* vs,
 mx_status check_heads(const char* fn, int32_t H, int32_t Hkv, int32_t D, float scale) {
   MX_CHECK(head_dim(D), "%s: D = %d (64, 128, 256 or 512)", fn, D);
   MX_CHECK(heads_fit(H, Hkv), "%s: H = %d query heads over Hkv = %d key heads", fn, H, Hkv);
-  MX_CHECK(std::isfinite(scale) && scale > 0.0f, "%s: scale = %g (finite, above 0)", fn, static_cast<double>(scale));
+  // (the kernels multiply scores by scale * log2(e))
+  MX_CHECK(scale > 0.0f && std::isfinite(scale * kLog2E), "%s: scale = %g (above 0, scale * log2(e) finite)", fn,
+           static_cast<double>(scale));
   return MX_OK;
 }
 

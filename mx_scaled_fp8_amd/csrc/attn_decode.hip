@@ -435,7 +435,7 @@ mx_status launch_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t
   a.out = static_cast<uint16_t*>(out);
   a.plan = static_cast<uint32_t*>(workspace);
   a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan_bytes(B));
-  a.scale = scale * 1.44269504088896340736f;
+  a.scale = scale * kLog2E;
   a.B = static_cast<uint32_t>(B);
   a.H = static_cast<uint32_t>(H);
   a.G = a.H / c.Hkv;

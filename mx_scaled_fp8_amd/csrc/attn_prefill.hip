@@ -355,7 +355,7 @@ mx_status launch_attn_prefill(const void* q, int64_t q_stride, const void* k, in
   a.k_offsets = k_offsets;
   a.out = static_cast<uint16_t*>(out);
   a.parts = static_cast<float*>(workspace);
-  a.scale = scale * 1.44269504088896340736f;
+  a.scale = scale * kLog2E;
   a.B = static_cast<uint32_t>(B);
   a.Tq = static_cast<uint32_t>(Tq);
   a.Tk = static_cast<uint32_t>(Tk);

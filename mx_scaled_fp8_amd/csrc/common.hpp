@@ -50,6 +50,8 @@ enum Counter {
 };
 void count(Counter c);
 
+constexpr float kLog2E = 1.44269504088896340736f;
+
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Unsigned 32-bit division by a run-time constant d >= 1 through a 64-bit

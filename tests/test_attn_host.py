@@ -214,3 +214,10 @@ def test_read_of_as_many_rows_as_a_launch_has_threads_for(dry):
     """16 rows to a workgroup of 256 threads: 2^28 - 15 rows would be 2^32 threads."""
     assert _read(rows=(1 << 28) - 16, Hkv=1, D=32) == mx.MX_OK
     _refused(_read, [dict(rows=(1 << 28) - 15, Hkv=1, D=32), dict(rows=(1 << 28) - 1, Hkv=1, D=32)])
+
+
+def test_scales_that_leave_fp32_in_powers_of_two(dry):
+    """The kernels take scale * log2(e): infinite, it would make NaN of scores of 0."""
+    for call in (_decode, _prefill):
+        assert call(scale=2.0 ** 127) == mx.MX_OK and call(scale=2.0 ** -149) == mx.MX_OK
+        _refused(call, [dict(scale=2.4e38), dict(scale=3.4e38), dict(scale=1e39), dict(scale=-2.0 ** -149)])
