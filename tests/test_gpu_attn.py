@@ -7,7 +7,7 @@ import torch
 
 import mx_scaled_fp8_amd as mx
 import workloads
-from attn_cases import check, decode_oracle, make_cache, normal, on_gpu
+from attn_cases import check, decode_oracle, make_cache, normal, on_gpu, random_cache, sampled_oracle, spread_lens
 from helpers import dev_i64, host_u16, host_u8, requires_gpu, say
 from oracle import attn as A
 from oracle import formats as F
@@ -680,3 +680,56 @@ def test_decode_latent_bf16_of_few_heads_in_parts(G):
     out = mx.mx_attn_decode(on_gpu(q), on_gpu(c["k"]), None, _i32(table), _i32(lens))
     torch.cuda.synchronize()
     check(host_u16(out), *decode_oracle(q, c, table, lens, 512 ** -0.5), 512, 2000)
+
+
+# --------------------------------------- shares of many tiles, long histories
+
+def _shares(rng, B, Hkv, G, D, page, fp8, latent, tile, groups, tiles, heads):
+    """Enough tokens for shares of `tiles` tiles in every one of `groups` groups: shares that end one stream, pass empty sequences and
+    begin another, several in one stream, and one that its stream does not fill.  Scores have a deviation of 3, so that a
+    sequence's output is that of few of its keys, and a tile that is left out or counted twice shows."""
+    lens = spread_lens(rng, B, int(tiles * groups * tile / Hkv * 1.1))
+    c, table = random_cache(rng, lens, Hkv, D, page, fp8, latent)
+    H = Hkv * G
+    q = normal(rng, B, H, D)
+    some = A.values(c["k"][0], None if c["ks"] is None else c["ks"][0])
+    scale = 3 / float(np.sqrt(D * np.mean(some ** 2)))
+    ws = torch.zeros(mx.mx_attn_decode_workspace_bytes(B, H, Hkv, D, table.shape[1], page), dtype=torch.uint8, device="cuda")
+    say("decode shares", B, Hkv, G, D, page, fp8, latent, sum(lens), max(lens))
+    out = mx.mx_attn_decode(on_gpu(q), on_gpu(c["k"]), on_gpu(c["v"]), _i32(table), _i32(lens), k_scale=on_gpu(c["ks"]),
+                            v_scale=on_gpu(c["vs"]), scale=scale, workspace=ws)
+    torch.cuda.synchronize()
+    assert int(ws[:4].view(torch.int32)) >= tiles                   # the plan begins with the share
+    got = host_u16(out)
+    assert not got[np.array(lens) == 0].any() and np.isfinite(F.bf16_to_f64(got)).all()
+    check(got[:, heads], *sampled_oracle(q, c, table, lens, scale, heads), D, max(lens))
+
+
+@pytest.mark.parametrize("B,Hkv,G,D,fp8,latent", [(70, 8, 4, 128, True, False), (300, 8, 2, 64, True, False), (300, 4, 3, 128, False, False),
+                                                  (70, 8, 5, 64, False, False), (70, 6, 5, 256, True, False), (300, 4, 2, 256, False, False),
+                                                  (70, 2, 17, 128, True, False), (70, 2, 3, 512, True, False), (70, 2, 3, 512, False, False),
+                                                  (300, 1, 16, 512, True, True)])
+def test_decode_shares_of_several_tiles(B, Hkv, G, D, fp8, latent):
+    rng = np.random.default_rng(B + G + D)
+    groups = (512 if D < 512 else 256) // -(-G // 16)
+    heads = sorted({0, G - 1, Hkv * G // 2, Hkv * G - 1, *(int(h) for h in rng.integers(0, Hkv * G, 4))})
+    _shares(rng, B, Hkv, G, D, 64, fp8, latent, 128, groups, 3, heads)
+
+
+@pytest.mark.parametrize("B,Hkv,G,D,fp8,latent", [(70, 2, 40, 128, True, False), (300, 1, 130, 64, True, False), (70, 1, 130, 64, False, False),
+                                                  (70, 1, 130, 128, False, True), (70, 1, 40, 256, True, True), (70, 1, 130, 256, False, False),
+                                                  (300, 1, 33, 512, True, True), (70, 1, 128, 512, True, True), (70, 1, 128, 512, False, True),
+                                                  (300, 1, 4, 512, False, True)])
+def test_decode_shares_of_many_tiles_with_heads_as_rows(B, Hkv, G, D, fp8, latent):
+    rng = np.random.default_rng(B + G + D)
+    groups = (512 if D < 512 else 256) // -(-G // 128)
+    heads = sorted({0, G - 1, min(127, G - 1), Hkv * G - 1, *(int(h) for h in rng.integers(0, Hkv * G, 3))})
+    _shares(rng, B, Hkv, G, D, 32, fp8, latent, 64 if D <= 128 else 32, groups, 9, heads)
+
+
+@pytest.mark.parametrize("lens,past,Hkv,G", [([200, 1], [9000, 5003], 2, 2), ([3, 7, 1], [8001, 30, 6000], 1, 5), ([1300], [77], 1, 1)])
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+@pytest.mark.parametrize("same", [False, True])
+def test_prefill_over_long_keys(lens, past, Hkv, G, D, same):
+    """Keys split over workgroups, many tiles in each split, and rows that are not split."""
+    _prefill(np.random.default_rng(sum(lens) + D), lens, past, Hkv, G, D, same=same)
