@@ -60,6 +60,14 @@ struct CodesTile : AttnTile16<512, 32, 3> {
     sbase = r * (D / 32) + g * 4;
   }
 
+  // Of the two BF16 numbers in w: what hi is made of.  Above 240 2^120 the nearest code is 2^128, which has no remainder in FP32; 240
+  // leaves up to 15 2^120, which lo holds.
+  __device__ __forceinline__ static uint32_t below_top(uint32_t w) {
+    typedef uint16_t v2u16 __attribute__((ext_vector_type(2)));
+    const v2u16 size = __builtin_elementwise_min(__builtin_bit_cast(v2u16, w & 0x7FFF7FFFu), (v2u16{0x7F70, 0x7F70}));
+    return __builtin_bit_cast(uint32_t, size) | (w & 0x80008000u);
+  }
+
   __device__ __forceinline__ void load_q(const uint16_t* q) {
     uint32_t lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));
@@ -86,8 +94,8 @@ struct CodesTile : AttnTile16<512, 32, 3> {
           typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
           v2s h = {0, 0}, l = {0, 0};
           uint32_t back[2], rest[2];
-          h = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(h, __builtin_bit_cast(v2bf, w[2 * i]), se, false);
-          h = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(h, __builtin_bit_cast(v2bf, w[2 * i + 1]), se, true);
+          h = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(h, __builtin_bit_cast(v2bf, below_top(w[2 * i])), se, false);
+          h = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(h, __builtin_bit_cast(v2bf, below_top(w[2 * i + 1])), se, true);
           back[0] = dequant_pair<false>(__builtin_bit_cast(uint32_t, h), se);
           back[1] = dequant_pair<true>(__builtin_bit_cast(uint32_t, h), se);
 #pragma unroll

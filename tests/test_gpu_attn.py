@@ -733,3 +733,31 @@ def test_decode_shares_of_many_tiles_with_heads_as_rows(B, Hkv, G, D, fp8, laten
 def test_prefill_over_long_keys(lens, past, Hkv, G, D, same):
     """Keys split over workgroups, many tiles in each split, and rows that are not split."""
     _prefill(np.random.default_rng(sum(lens) + D), lens, past, Hkv, G, D, same=same)
+
+
+@pytest.mark.parametrize("H", [40, 130])
+def test_decode_queries_at_the_top_of_the_range(H):
+    """The same split of queries up to the largest BF16 number, whose nearest MXFP8 number is 2^128, over keys so small that
+    scores are about 1: scores and outputs are as finite as the formula's, bounds as above."""
+    rng = np.random.default_rng(11)
+    D, lens = 512, [70, 1, 300]
+    c, table = make_cache(rng, lens, 1, D, 16, True, True)
+    c["ks"] -= 20                                                   # keys times 2^-20
+    x = rng.integers(0x7F00, 0x7F80, (3, H, D)) | (rng.integers(0, 2, (3, H, D)) << 15)      # 2^127 and above, either sign
+    x[:, 1] = np.where(rng.random((3, D)) < 0.5, 0x7F7F, 0xFF7F)
+    x[:, 2, 1::2] -= 0x0300                                         # and times 2^-6 between them
+    x[:, 3, :] -= 0x0100                                            # the next powers of two down
+    x[:, 4, :] -= 0x0080
+    q = x.astype(np.uint16)
+    scale = D ** -0.5 * 2.0 ** -107
+    say("decode top of the range", H)
+    out = mx.mx_attn_decode(on_gpu(q), on_gpu(c["k"]), None, _i32(table), _i32(lens), k_scale=on_gpu(c["ks"]), scale=scale)
+    torch.cuda.synchronize()
+    ref, size, spread = decode_oracle(q, c, table, lens, scale)
+    assert np.isfinite(ref).all() and spread.max() < 64
+    qf = F.bf16_to_f64(q).reshape(3, H, D // 32, 32)
+    for b, n in enumerate(lens):
+        k = np.abs(A.sequence(c["k"], c["ks"], table[b], n)).reshape(n, D // 32, 32).sum(-1).max(0)      # a block's largest sum
+        err = scale * 2.0 ** -21 * (np.abs(qf[b]).max(-1) * k).sum(-1)
+        spread[b] += err * 2.0 ** 24 / (D + 4)
+    check(host_u16(out), ref, size, spread, D, max(lens))
