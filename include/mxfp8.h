@@ -521,7 +521,8 @@ mx_status mx_kv_cache_write(const void* k, int64_t k_stride, const void* v, int6
  *           sequence owns keep what the outputs held.
  * k, v      device BF16 [rows, Hkv, D], dense (v NULL with a latent cache): the
  *           elements, exact wherever BF16 holds them (2^-133 and above; nearest
- *           even below).  A row whose page is outside [0, pages), or beyond
+ *           even below, and infinite from 2^128 on, which is what the MXFP8 rule makes
+ *           of numbers of 248 2^120 and more).  A row whose page is outside [0, pages), or beyond
  *           max_pages, is NaN; the cache is not read for it.
  * Requires: B >= 0, rows >= 0 (either 0 is a no-op), rows <= 2^28 - 16, max_pages >= 1, the cache's
  * sizes as for mx_kv_cache_write, rows * Hkv * D < 2^34, tensors 16-byte, block_table and offsets
@@ -548,8 +549,13 @@ mx_status mx_kv_cache_read(int32_t kind, const void* k_cache, const uint8_t* k_s
  *           are rounded to BF16 for the second product.  (A latent MXFP8 cache of D = 512
  *           under 32 heads or more takes q as the sum of two MXFP8 numbers: exact, but
  *           for elements below 2^-14 of the largest of their 32, which are off by up to
- *           2^-21 of that.)  The result does not depend on timing, but on B and
- *           max_pages, which decide where a long sequence is cut.
+ *           2^-21 of that.)  The result does not depend on timing.  Where a sequence is
+ *           cut into parts follows from B, max_pages and the lengths of all sequences of
+ *           the call: with the same of them bits are equal, but when another sequence
+ *           grows, a sequence's last bits may change.
+ *           An infinite value that a sequence sees makes Inf, or NaN where its weight is
+ *           too small for FP32; sums of the values, each up to 2^8 times as large, have
+ *           to be finite in FP32 before they are divided by the weights' sum.
  * workspace device, at least mx_attn_decode_workspace_bytes(B, H, Hkv, D, max_pages,
  *           page_size) (0 for sizes that the call refuses), 16-byte aligned: parts of
  *           long sequences, written before they are read.  Calls that may overlap
@@ -585,7 +591,10 @@ mx_status mx_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t H, 
  *           [0, Tk].  Rows of out that no prompt owns keep what out held.
  * out       device BF16 [Tq, H, D], dense.  FP32 scores, statistics and sums;
  *           probabilities are rounded to BF16 for the second product.  Keys and
- *           values that a row does not see take no part in it, NaN or not.
+ *           values that a row does not see take no part in it, NaN or not; infinite
+ *           values that it sees and large sums as in mx_attn_decode.  The result does
+ *           not depend on timing; where keys are split over workgroups follows from
+ *           B, Tq, Tk and the offsets, and a row's last bits with it.
  * workspace device, at least mx_attn_prefill_workspace_bytes(B, Tq, Tk, H, Hkv, D) (0 for
  *           sizes that the call refuses), 16-byte aligned (may be NULL when that is 0): parts of rows whose keys are
  *           split over workgroups, written before they are read.  Calls that may
