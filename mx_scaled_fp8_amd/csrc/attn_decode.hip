@@ -391,9 +391,12 @@ __global__ __launch_bounds__((64 * waves_of<D, WHOLE>()), D <= 128 ? 2 : 1) void
   }
 }
 
-// Groups of a call: as many as run at once (by registers and LDS), and no more than there can be tiles.
+// Groups of a call: as many as run at once, and no more than there can be tiles.  Heads of 64 and 128 leave registers for two
+// workgroups on a compute unit, heads of 256 and 512 for one.  (256 groups and 512, heads of 256: 3 sequences up to 50,021 tokens, 2 x
+// 7 heads, MXFP8 31.2 us and 38.9, BF16 45.5 and 52.6; 8 up to 2000, 4 x 4 heads, BF16 15.0 and 18.7; 64 up to 8192, MXFP8 131.2 and
+// 129.7.)
 uint32_t groups_of(int64_t B, int32_t Hkv, uint32_t head_blocks, int32_t D, int64_t max_tokens) {
-  return decode_groups(B * Hkv * ((max_tokens + kTile - 1) / kTile), (D >= 512 ? 256 : 512) / head_blocks);
+  return decode_groups(B * Hkv * ((max_tokens + kTile - 1) / kTile), (D >= 256 ? 256 : 512) / head_blocks);
 }
 
 uint32_t head_blocks_of(int32_t G) { return static_cast<uint32_t>((G + kHeads - 1) / kHeads); }

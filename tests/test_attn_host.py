@@ -221,3 +221,10 @@ def test_scales_that_leave_fp32_in_powers_of_two(dry):
     for call in (_decode, _prefill):
         assert call(scale=2.0 ** 127) == mx.MX_OK and call(scale=2.0 ** -149) == mx.MX_OK
         _refused(call, [dict(scale=2.4e38), dict(scale=3.4e38), dict(scale=1e39), dict(scale=-2.0 ** -149)])
+
+
+@pytest.mark.parametrize("D,groups", [(64, 512), (128, 512), (256, 256), (512, 256)])
+def test_parts_of_as_many_groups_as_run_at_once(D, groups):
+    """Two workgroups on each of 256 compute units, one of heads of 256 and more; a group leaves two parts of 16 heads (O, m, l) behind
+    the plan."""
+    assert mx.mx_attn_decode_workspace_bytes(63, 16, 4, D, 128, 64) == 64 * 4 + groups * 2 * 16 * (D + 2) * 4
