@@ -23,10 +23,12 @@ namespace mx {
 
 namespace {
 
-// Fewest keys of a split, in 64s: its parts, O in FP32, are written and read again.  (Us of 4, 8 and 16: 64 rows over 8000 tokens, 16
-// heads of 512 on one 119, 78 and 73; 4 prompts of 17 rows over 3972, 6 heads of 128 on each of 4 31, 26 and 36; 200 rows over
-// 3000, 4 heads of 128 on each of 2 28, 26 and 31.)
-constexpr int kMinTiles = 8;
+// Fewest keys of a split, of an average prompt and of any row tile: its parts, O in FP32, are written and read again.  (Us of 256,
+// 512 and 1024: 64 rows over 8000 tokens, 16 heads of 512 on one 119, 78 and 73; 4 prompts of 17 rows over 3972, 6 heads of 128 on
+// each of 4 31, 26 and 36; 200 rows over 3000, 4 heads of 128 on each of 2 28, 26 and 31.  Of a row tile alone, 256 and 512: 8192 rows,
+// 2 heads of 512 on one 252 and 231; 2 prompts of 2000, 4 heads of 256 on each of 2 68 and 62; 4096 rows, 8 heads of 256 on one 115
+// and 120.)
+constexpr int kMinKeys = 512;
 
 struct PrefillArgs {
   const uint16_t* q;
@@ -90,7 +92,7 @@ __device__ __forceinline__ RowTile row_tile(const PrefillArgs& a, uint32_t rt) {
 template <int D>
 __device__ __forceinline__ uint32_t split_tiles(int32_t keys, uint32_t splits, uint32_t& used) {
   const uint32_t n = (static_cast<uint32_t>(keys) + key_tile<D>() - 1) / key_tile<D>();
-  const uint32_t per = max((n + splits - 1) / splits, static_cast<uint32_t>(kMinTiles));
+  const uint32_t per = max((n + splits - 1) / splits, static_cast<uint32_t>(kMinKeys / key_tile<D>()));
   used = max((n + per - 1) / per, 1u);
   return per;
 }
@@ -297,11 +299,13 @@ int32_t pack_of(int64_t B, int64_t Tq, int32_t H, int32_t Hkv, int rows) { retur
 int64_t row_tiles(int64_t B, int64_t Tq, int32_t pack, int rows) { return Tq * pack / rows + B; }
 
 // How many workgroups share the keys of one row tile and pack.  512 run at once; up to twice as many, as long as every part
-// has some tiles of keys, keep them busy and let those that run together read the same keys.  (4096 rows over 30011 earlier
-// tokens, 8 heads: 613 us with no split of its 256 pairs, 671 with 2, 528 with 4, 540 with 8, 593 with 16.)
+// has some keys, keep them busy and let those that run together read the same keys.  `units` goes by the bound of row tiles, which
+// for one prompt of whole row tiles is one more than there are: 4096 rows are 33, and 8 heads of them 3 splits, not 4.  (3 and 4
+// splits: 4096 rows over 30011 earlier tokens, 8 heads of 128 520 us and 512, 2048 over 98,000 830 and 780; prompts from their
+// beginning, whose first rows have few keys to split, 8192 rows, 4 heads of 128 90 and 93, 4096 rows, 8 heads of 256 115 and 130,
+// 2048 rows, 16 heads of 512 89 and 118.)
 uint32_t split_count(int64_t B, int64_t Tk, int64_t units) {
-  const int64_t tiles = (Tk / B + 63) / 64;             // of an average prompt
-  return static_cast<uint32_t>(std::max<int64_t>(1, std::min(1024 / units, tiles / kMinTiles)));
+  return static_cast<uint32_t>(std::max<int64_t>(1, std::min(1024 / units, (Tk / B + 63) / kMinKeys)));   // (tiles of 64)
 }
 
 // (row tile, pack) pairs.

@@ -761,3 +761,23 @@ def test_decode_queries_at_the_top_of_the_range(H):
         err = scale * 2.0 ** -21 * (np.abs(qf[b]).max(-1) * k).sum(-1)
         spread[b] += err * 2.0 ** 24 / (D + 4)
     check(host_u16(out), ref, size, spread, D, max(lens))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+def test_prefill_splits_of_512_keys_at_least(D):
+    """Rows that see 512 keys or fewer are not split: their parts of the workspace, [row tile][split] of 128 rows, stay as they were;
+    rows that see 1024 leave two parts, whatever the head's size."""
+    rng = np.random.default_rng(D)
+    rows = 1024
+    q, k, v = (on_gpu(normal(rng, rows, 1, D)) for _ in range(3))
+    offsets = _i32([0, rows])
+    need = mx.mx_attn_prefill_workspace_bytes(1, rows, rows, 1, 1, D)
+    part = 128 * (D + 2) * 4
+    assert need >= 9 * 2 * part
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    say("prefill least split", D)
+    mx.mx_attn_prefill(q, k, v, offsets, offsets, workspace=ws)
+    torch.cuda.synchronize()
+    parts = host_u8(ws)[:9 * 2 * part].reshape(9, 2, part)
+    assert (parts[:4] == 0xFF).all() and (parts[8] == 0xFF).all()
+    assert (parts[4:8, :, -128 * 4:] != 0xFF).any(-1).all()
