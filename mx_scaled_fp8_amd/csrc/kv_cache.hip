@@ -81,19 +81,18 @@ struct ReadArgs {
   uint32_t B, rows;
   uint32_t C, CD;            // 8-element chunks of a row, of a head
   DivU32 c_div, cd_div;
-  uint32_t block_rows;
 };
 
-constexpr int kReadRows = 16;          // most rows of a block
+constexpr uint32_t kReadRows = 16;     // rows of a block
 
-// A block takes block_rows rows of the output.  Its first threads find each row's place in the cache (the sequence by
+// A block takes kReadRows rows of the output.  Its first threads find each row's place in the cache (the sequence by
 // bisection in the offsets, the page from the table); then all threads copy, 8 elements a thread and step, keys and
 // values together so that two loads are under way.
 template <bool FP8>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(ReadArgs a) {
   __shared__ int64_t place[kReadRows];            // the row of head 0, -1: NaN, -2: left as it is
-  const uint32_t r0 = blockIdx.x * a.block_rows;
-  if (threadIdx.x < a.block_rows) {
+  const uint32_t r0 = blockIdx.x * kReadRows;
+  if (threadIdx.x < kReadRows) {
     const uint32_t r = r0 + threadIdx.x;
     int64_t at = -2;
     if (r < a.rows && static_cast<int64_t>(r) >= a.offsets[0] && static_cast<int64_t>(r) < a.offsets[a.B]) {
@@ -113,7 +112,7 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(ReadArgs a) {
     place[threadIdx.x] = at;
   }
   __syncthreads();
-  const uint32_t units = a.block_rows * a.C;
+  const uint32_t units = kReadRows * a.C;
   const bool both = a.out[1] != nullptr;
   for (uint32_t u = threadIdx.x; u < units; u += kThreads) {
     const uint32_t t = div_u32(u, a.c_div), c = u - t * a.C;
@@ -194,8 +193,7 @@ mx_status launch_kv_read(const KvCache& c, bool fp8, int32_t D, int64_t B, const
   a.C = a.CD * c.Hkv;
   a.c_div = make_div(a.C);
   a.cd_div = make_div(a.CD);
-  a.block_rows = kReadRows;
-  const dim3 grid(static_cast<uint32_t>((rows + a.block_rows - 1) / a.block_rows));
+  const dim3 grid(static_cast<uint32_t>((rows + kReadRows - 1) / kReadRows));
   if (fp8) hipLaunchKernelGGL(kv_read_kernel<true>, grid, dim3(kThreads), 0, stream, a);
   else hipLaunchKernelGGL(kv_read_kernel<false>, grid, dim3(kThreads), 0, stream, a);
   return launch_status("mx_kv_cache_read");
