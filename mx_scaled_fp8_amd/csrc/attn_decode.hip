@@ -16,8 +16,8 @@
 //    no transposition through LDS.
 // Codes become BF16 (exact) by v_cvt_scalef32_pk_bf16_fp8 with their block's scale.
 //
-// P is rounded to BF16 for the second product, which has no wider operand at this rate: 2^-9 of each weight, against 2^-9 of the
-// result that BF16 outputs have anyway; m, the sum (of the unrounded P), S and O are FP32, the parts of a stream too.
+// P is rounded to BF16 for the second product, which has no wider operand at this rate: up to 2^-8 of each weight, against 2^-8 of
+// the result that BF16 outputs have anyway; m, the sum (of the unrounded P), S and O are FP32, the parts of a stream too.
 //
 // Work is shared as attn_plan.hpp says, in tiles of 128 tokens, 32 for each of the four waves.
 //

@@ -9,7 +9,7 @@
 // Work is shared as attn_plan.hpp says.
 //
 // (MI355X, 128 heads, 64 sequences of up to 32,768 tokens, 512 wide, MXFP8: 320 us and 17 for the join, 0.84 PFLOP/s; up to 8192
-// tokens in BF16 136 us.  A turn of 32 tokens is 4700 cycles, of them 2050 of the matrix cores; timing copies: without the
+// tokens in BF16 125 to 136 us.  A turn of 32 tokens is 4700 cycles, of them 2050 of the matrix cores; timing copies: without the
 // products with V 95 us less, without S 80, the conversion 30 to 37, DMA 27 to 40, softmax 8 to 22.  The rest is waiting:
 // registers for two waves a SIMD only, and operands that are read no further ahead than registers reach.)
 #include <type_traits>
@@ -530,8 +530,9 @@ void launch(const DecodeArgs& a, hipStream_t stream) {
 
 // From 32 heads on the rows fill at least one wave's products, and the cache is read once, not once for each 16 heads.
 // Rows of 512 have no room in LDS for values of their own.  A latent BF16 row of 512, read twice by the other kernel, which has no
-// registers to read ahead, is always better here (64 sequences up to 8192 tokens: one head 55 us here, 64 there, 16 heads 62 and 76;
-// 2 up to 2000, 4 heads 15.9 and 15.4); in MXFP8 one head is 68 and 50, 20 heads 75 and 96 but over 2 times 2000 tokens 26 and 16.
+// registers to read ahead, goes here for any number of heads (64 sequences up to 8192 tokens: one head 55 us here, 64 there, 16 heads
+// 62 and 76; 2 up to 2000, 4 heads 15.9 and 15.4, the half microsecond that short calls lose); in MXFP8 one head is 68 and 50, 20
+// heads 75 and 96 but over 2 times 2000 tokens 26 and 16.
 bool decode_by_rows(int32_t G, int32_t D, bool latent, bool fp8) {
   return D == 512 ? latent && (G >= 32 || !fp8) : G >= 32;
 }

@@ -781,3 +781,60 @@ def test_prefill_splits_of_512_keys_at_least(D):
     parts = host_u8(ws)[:9 * 2 * part].reshape(9, 2, part)
     assert (parts[:4] == 0xFF).all() and (parts[8] == 0xFF).all()
     assert (parts[4:8, :, -128 * 4:] != 0xFF).any(-1).all()
+
+
+# ------------------------------------------- nothing to do, and replays
+
+@KINDS
+def test_nothing_to_do(fp8):
+    """No tokens, no sequences, no rows, no keys: outputs of that many rows, and rows without keys are 0."""
+    rng = np.random.default_rng(12)
+    Hkv, H, D = 2, 4, 128
+    c, table = make_cache(rng, [20, 5], Hkv, D, 16, fp8)
+    k, v, ks, vs = (on_gpu(c[n]) for n in ("k", "v", "ks", "vs"))
+    kept = [t.clone() for t in (k, v, ks, vs) if t is not None]
+    none = torch.zeros((0, Hkv, D), dtype=torch.bfloat16, device="cuda")
+    q = on_gpu(normal(rng, 7, H, D)).view(torch.bfloat16)
+    say("nothing to do", fp8)
+    mx.mx_kv_cache_write(none, none, dev_i64([]), k, v, k_scale=ks, v_scale=vs)
+    mx.mx_kv_cache_write(q[:3, :2], q[:3, 2:], dev_i64([-1, -1, 1 << 40]), k, v, k_scale=ks, v_scale=vs)
+    kk, vv = mx.mx_kv_cache_read(k, v, _i32(table[:0]), _i32([0]), 0, k_scale=ks, v_scale=vs)
+    k0, v0 = mx.mx_kv_cache_read(k, v, _i32(table), _i32([0, 0, 0]), 0, k_scale=ks, v_scale=vs)
+    assert all(t.shape == (0, Hkv, D) for t in (kk, vv, k0, v0))
+    assert mx.mx_attn_decode(q[:0], k, v, _i32(table[:0]), _i32([]), k_scale=ks, v_scale=vs).shape == (0, H, D)
+    assert mx.mx_attn_prefill(q[:0], none, none, _i32([0, 0]), _i32([0, 0])).shape == (0, H, D)
+    assert mx.mx_attn_prefill(q[:0], none, none, _i32([0]), _i32([0])).shape == (0, H, D)
+    zero = [mx.mx_attn_prefill(q, none, none, _i32([0, 3, 7]), _i32([0, 0, 0])), mx.mx_attn_prefill(q, none, none.clone(), _i32([0, 3, 7]), _i32([0, 0, 0])),
+            mx.mx_attn_decode(q[:2], k, v, _i32(table), _i32([0, -3]), k_scale=ks, v_scale=vs)]
+    torch.cuda.synchronize()
+    assert all(not t.view(torch.int16).any() for t in zero)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(kept, (t for t in (k, v, ks, vs) if t is not None)))
+
+
+@pytest.mark.parametrize("D,G,latent", [(512, 128, True), (512, 5, True), (128, 40, False), (256, 4, False)])
+@KINDS
+def test_graph_of_shares(D, G, latent, fp8):
+    """Captured once and replayed over other lengths, with empty sequences among them and eager calls between: every replay equals
+    the eager call."""
+    rng = np.random.default_rng(13)
+    B, page = 5, 32
+    c, table = make_cache(rng, [1500] * B, 1, D, page, fp8, latent)
+    k, v, ks, vs = (on_gpu(c[n]) for n in ("k", "v", "ks", "vs"))
+    t, lens, q = _i32(table), _i32([1500, 0, 3, 700, 64]), on_gpu(normal(rng, B, G, D))
+    call = lambda: mx.mx_attn_decode(q, k, v, t, lens, k_scale=ks, v_scale=vs)  # noqa: E731
+    say("graph of shares", D, G, latent, fp8)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = call()
+    for at in ([1500, 0, 3, 700, 64], [0, 0, 0, 0, 1], [1, 1500, 1500, 0, 33], [0] * 5, [1500] * 5):
+        lens.copy_(_i32(at))
+        q.copy_(on_gpu(normal(rng, B, G, D)))
+        g.replay()
+        torch.cuda.synchronize()
+        got = held.clone()
+        want = call()
+        torch.cuda.synchronize()
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16)), at
+        assert not got[np.array(at) == 0].view(torch.int16).any() and torch.isfinite(got.float()).all()
