@@ -93,10 +93,8 @@ int main() {
                 continue;
               }
               ++accepted;
-              // (rows of keys 2^22 elements apart or more are refused by their stride, which the query does not know)
-              if (int64_t(Hkv) * D < (1 << 22))
-                EXPECT(call(need) == MX_OK && call(need - 1) == MX_ERR_INVALID_ARG, "prefill B %lld Tq %lld Tk %lld H %d Hkv %d D %d: %zu bytes",
-                       (long long)B, (long long)Tq, (long long)Tk, H, Hkv, D, need);
+              EXPECT(call(need) == MX_OK && call(need - 1) == MX_ERR_INVALID_ARG, "prefill B %lld Tq %lld Tk %lld H %d Hkv %d D %d: %zu bytes",
+                     (long long)B, (long long)Tq, (long long)Tk, H, Hkv, D, need);
               EXPECT(need < (size_t(1) << 36), "prefill B %lld Tq %lld Tk %lld H %d: %zu bytes", (long long)B, (long long)Tq, (long long)Tk, H, need);
             }
         }
