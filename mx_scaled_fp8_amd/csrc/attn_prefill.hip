@@ -12,7 +12,7 @@
 // kernel joins.
 //
 // What bounds it is the matrix cores and, beside them, the issue of what the softmax needs: of 8192 tokens, 32 heads of 128, the
-// products alone take 357 us at the clock that the power allows, the kernel 511 to 540 (1.02 to 1.07 PFLOP/s; a library product
+// products alone take 357 us at the clock that the power allows, the kernel 505 to 540 (1.02 to 1.09 PFLOP/s; a library product
 // of 8192^3 reaches 1.2 to 1.45).  P is rounded to BF16 for the second product; m, the sum of the unrounded P, S and O
 // are FP32, parts too.
 #include <algorithm>
